@@ -334,6 +334,100 @@ int q4k_matmul_tc_relayouted(const float *x, const void *w_tc, float *y, int inp
 int ternary_gemv(const float *x, const void *w_packed, float scale, float *y, int inputDim,
                  int outputDim, int tokens, q4mm_stream_t stream);
 
+/*
+ * ---- Microscaled (MX) tensors --------------------------------------------
+ *
+ * The block formats of the OCP Microscaling Formats (MX) specification 1.0:
+ * `rows` vectors of K values in blocks of 32 along K.  A block has one scale
+ * 2^(b - 127), kept as the byte b (E8M0; 255 stands for NaN), and 32 codes in
+ * `bits` bits:
+ *   4: E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two codes to a
+ *      byte, the even value in the low nibble;
+ *   8: E4M3 (largest magnitude 448).
+ * A value is its code times its block's scale.
+ *
+ * Layout.  K is padded with zero codes to Kp, the next multiple of 128.
+ *   codes : rows of Kp·bits/8 bytes one after another (32-byte aligned base).
+ *   scales: tiles of 128 rows x 4 blocks, 512 bytes each; tile (i, j) holds
+ *           rows 128·i .. and blocks 4·j .. and lies at 512·(i·Kp/128 + j);
+ *           in it the byte of (row r, block b) is
+ *           16·(r % 32) + 4·(r % 128 / 32) + b % 4 (16-byte aligned base).
+ *           Bytes of padding rows and blocks are written as zero by the
+ *           quantising calls; a user's own layout must not put 255 there for
+ *           padding blocks (codes zero times NaN is NaN).
+ *
+ * Quantisation of a block v: with amax = max |v|, the scale is
+ * 2^(floor(log2 amax) - emax), emax = 2 (4 bits) or 8 (8 bits), at least
+ * 2^-127 (amax = 0 gives byte 0); a code is v / scale (exact) rounded to
+ * nearest even and cut at the largest code.  A block that holds an infinity
+ * or a NaN gets scale NaN and zero codes: all 32 values become NaN.
+ *
+ * Element types of the other side are named by a q4mm_dtype.  Rows of those
+ * tensors may be strided (in elements, the values of a row adjacent); any
+ * base aligned to its element is accepted, and rows that are 16-byte aligned
+ * with K a multiple of 8 are read and written with wide accesses.
+ *
+ * rows = 0 (tokens = 0) is a call with nothing to do and returns Q4MM_OK.
+ * Every operand, weights included, may have been written by the previous
+ * kernel on the stream.  No call allocates, and nothing persists.
+ */
+typedef enum { Q4MM_F32 = 0, Q4MM_F16 = 1, Q4MM_BF16 = 2 } q4mm_dtype;
+
+#define Q4MM_MX_PADDED(K) (((size_t)(K) + 127) / 128 * 128)
+#define Q4MM_MX_CODE_BYTES(K, rows, bits) ((size_t)(rows) * (Q4MM_MX_PADDED(K) * (bits) / 8))
+#define Q4MM_MX_SCALE_BYTES(K, rows) (((size_t)(rows) + 127) / 128 * (Q4MM_MX_PADDED(K) / 128) * 512)
+
+/*
+ * mx_quantize — x [rows][K] of type dtype to MX codes and scales.
+ * codes: Q4MM_MX_CODE_BYTES(K, rows, bits); scales: Q4MM_MX_SCALE_BYTES(K, rows).
+ * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; rows >= 0; bits 4 or 8.
+ * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
+ */
+int mx_quantize(const void *x, long long x_stride, int dtype, void *codes, void *scales, int inputDim, int rows,
+                int bits, q4mm_stream_t stream);
+
+/*
+ * mx_swiglu — silu(gate)·up quantised as by mx_quantize, in one pass:
+ * gate / (1 + e^-gate) · up in fp32, rounded once, to codes.  gate and up
+ * may be two parts of one tensor's rows.  Limits and returns as mx_quantize.
+ */
+int mx_swiglu(const void *gate, long long gate_stride, const void *up, long long up_stride, int dtype, void *codes,
+              void *scales, int hiddenDim, int rows, int bits, q4mm_stream_t stream);
+
+/*
+ * mx_rmsnorm — the residual's addition, the RMS norm and its quantisation:
+ *   h = x + residual                       (residual NULL: h = x)
+ *   v = h · (mean_k h² + eps)^-1/2 · weight
+ * in fp32; v is quantised as by mx_quantize, and h is written in x's type
+ * where h is not NULL (the norm takes it before that rounding).  h may be x
+ * or residual itself (same base and stride), and overlaps nothing else.
+ * weight: K values of x's type or of Q4MM_F32.  The sum of squares is an
+ * fp32 sum in a fixed order; it overflows where h reaches about 1e19.
+ * Limits and returns as mx_quantize, and eps >= 0.
+ */
+int mx_rmsnorm(const void *x, long long x_stride, const void *residual, long long residual_stride, void *h,
+               long long h_stride, int dtype, const void *weight, int weight_dtype, float eps, void *codes,
+               void *scales, int inputDim, int rows, int bits, q4mm_stream_t stream);
+
+/*
+ * mx_dequantize — the values an MX tensor stands for, y [rows][K] of type
+ * dtype (exact in fp32; else rounded once).  Limits and returns as mx_quantize.
+ */
+int mx_dequantize(const void *codes, const void *scales, void *y, long long y_stride, int dtype, int inputDim,
+                  int rows, int bits, q4mm_stream_t stream);
+
+/*
+ * mx_matmul — y = x·Wᵀ on the tensor cores, x an MX tensor of `tokens` rows in
+ * x_bits (4 or 8) bits, W one of outputDim rows in 4 bits, both over inputDim
+ * values.  Products of codes and scales are exact; they are added in fp32.
+ * y: [tokens][outputDim] of type dtype, contiguous, overwritten, aligned to
+ * its element.
+ * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; outputDim >= 1; tokens >= 0.
+ * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
+ */
+int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void *w_codes, const void *w_scales,
+              void *y, int dtype, int inputDim, int outputDim, int tokens, q4mm_stream_t stream);
+
 /* Message for the last error returned on the calling thread ("" if none).
  * The pointer stays valid until the thread's next failing call. */
 const char *q4mm_last_error(void);

@@ -36,5 +36,17 @@ from ._binding import (  # noqa: F401
     q4k_ffn_swiglu_ptr,
     ternary_gemv,
     ternary_gemv_ptr,
+    MxTensor,
+    mx_padded,
+    mx_quantize,
+    mx_quantize_ptr,
+    mx_swiglu,
+    mx_swiglu_ptr,
+    mx_rmsnorm,
+    mx_rmsnorm_ptr,
+    mx_dequantize,
+    mx_dequantize_ptr,
+    mx_matmul,
+    mx_matmul_ptr,
     version,
 )

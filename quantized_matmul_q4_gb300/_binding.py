@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 Q4K_VALUES = 256
@@ -10,6 +11,7 @@ Q4K_BYTES = 144
 
 _SYMBOLS = ("q4k_matmul", "q4k_matmul_tc", "q4k_matmul_tc_noalloc", "q4k_relayout_tc", "q4k_matmul_tc_relayouted",
             "q4_0_gemv", "q6k_gemv", "q4k_ffn_swiglu", "ternary_gemv",
+            "mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul",
             "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait")
 
 
@@ -44,6 +46,14 @@ def _load() -> ctypes.CDLL:
     lib.q4k_ffn_swiglu.restype = i32
     lib.ternary_gemv.argtypes = [vp, vp, f32, vp, i32, i32, i32, vp]
     lib.ternary_gemv.restype = i32
+    i64 = ctypes.c_longlong
+    lib.mx_quantize.argtypes = [vp, i64, i32, vp, vp, i32, i32, i32, vp]
+    lib.mx_swiglu.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, i32, i32, vp]
+    lib.mx_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, f32, vp, vp, i32, i32, i32, vp]
+    lib.mx_dequantize.argtypes = [vp, vp, vp, i64, i32, i32, i32, i32, vp]
+    lib.mx_matmul.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp]
+    for name in ("mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul"):
+        getattr(lib, name).restype = i32
     lib.q4mm_last_error.argtypes = []
     lib.q4mm_last_error.restype = ctypes.c_char_p
     lib.q4mm_device_status.argtypes = [vp, i32]
@@ -120,6 +130,35 @@ def q4k_ffn_swiglu_ptr(x: int, w_gate: int, w_up: int, h: int, K: int, N: int, T
 def ternary_gemv_ptr(x: int, w: int, scale: float, y: int, K: int, N: int, T: int,
                      stream: int = 0) -> None:
     _check(_LIB.ternary_gemv(x, w, ctypes.c_float(scale), y, K, N, T, stream))
+
+
+# (dtype: 0 float32, 1 float16, 2 bfloat16; strides in elements.)
+
+def mx_quantize_ptr(x: int, x_stride: int, dtype: int, codes: int, scales: int, K: int, rows: int, bits: int,
+                    stream: int = 0) -> None:
+    _check(_LIB.mx_quantize(x, x_stride, dtype, codes, scales, K, rows, bits, stream))
+
+
+def mx_swiglu_ptr(gate: int, gate_stride: int, up: int, up_stride: int, dtype: int, codes: int, scales: int, K: int,
+                  rows: int, bits: int, stream: int = 0) -> None:
+    _check(_LIB.mx_swiglu(gate, gate_stride, up, up_stride, dtype, codes, scales, K, rows, bits, stream))
+
+
+def mx_rmsnorm_ptr(x: int, x_stride: int, residual: int, residual_stride: int, h: int, h_stride: int, dtype: int,
+                   weight: int, weight_dtype: int, eps: float, codes: int, scales: int, K: int, rows: int, bits: int,
+                   stream: int = 0) -> None:
+    _check(_LIB.mx_rmsnorm(x, x_stride, residual, residual_stride, h, h_stride, dtype, weight, weight_dtype, eps,
+                           codes, scales, K, rows, bits, stream))
+
+
+def mx_dequantize_ptr(codes: int, scales: int, y: int, y_stride: int, dtype: int, K: int, rows: int, bits: int,
+                      stream: int = 0) -> None:
+    _check(_LIB.mx_dequantize(codes, scales, y, y_stride, dtype, K, rows, bits, stream))
+
+
+def mx_matmul_ptr(x_codes: int, x_scales: int, x_bits: int, w_codes: int, w_scales: int, y: int, dtype: int, K: int,
+                  N: int, T: int, stream: int = 0) -> None:
+    _check(_LIB.mx_matmul(x_codes, x_scales, x_bits, w_codes, w_scales, y, dtype, K, N, T, stream))
 
 
 def arm_wait_failure(stage: int, limit_cycles: int) -> None:
@@ -255,3 +294,192 @@ def ternary_gemv(x, w, scale: float = 1.0, N: int | None = None, out=None, strea
     ternary_gemv_ptr(x2.data_ptr(), w.data_ptr(), float(scale), out.data_ptr(), K, N, T,
                      _stream_ptr(stream))
     return out.view(T, N)
+
+
+# Microscaled (MX) tensors: layouts and roundings in include/q4mm.h.
+
+MX_BLOCK, MX_TILE_ROWS, MX_TILE_BYTES = 32, 128, 512
+
+
+class MxTensor(NamedTuple):
+    """`rows` vectors of K values in MX blocks of 32.
+
+    codes:  uint8 [rows, Kp·bits/8], Kp = K rounded up to a multiple of 128
+            (E2M1, two to a byte, for 4 bits; E4M3 for 8)
+    scales: uint8 [ceil(rows/128), Kp/128, 512], E8M0 bytes in tiles of 128
+            rows x 4 blocks
+    """
+    codes: "torch.Tensor"
+    scales: "torch.Tensor"
+    K: int
+    bits: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+
+def mx_padded(K: int) -> int:
+    return -(-K // 128) * 128
+
+
+_MX_DTYPES = None
+
+
+def _mx_dtype(t, what: str) -> int:
+    global _MX_DTYPES
+    if _MX_DTYPES is None:
+        import torch
+        _MX_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    code = _MX_DTYPES.get(t)
+    if code is None:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16")
+    return code
+
+
+def _mx_rows(x, what: str):
+    """x as a CUDA matrix of rows with adjacent values, never copied."""
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if x.dim() != 2:
+        if x.dim() == 0:
+            raise ValueError(f"{what} must have at least one dimension")
+        try:
+            x = x.view(-1, x.shape[-1]) if x.numel() else x.reshape(-1, max(x.shape[-1], 1))
+        except RuntimeError:
+            raise ValueError(f"the leading dimensions of {what} must collapse into evenly spaced rows") from None
+    rows, K = x.shape
+    s0, s1 = x.stride()
+    if s1 != 1 and K > 1:
+        raise ValueError(f"the values of a row of {what} must be adjacent")
+    return x, rows, K, s0 if rows > 1 else K
+
+
+def _mx_out(rows: int, K: int, bits: int, device, out):
+    import torch
+    if bits != 4 and bits != 8:
+        raise ValueError("bits must be 4 or 8")
+    Kp = mx_padded(K)
+    if out is None:
+        return MxTensor(torch.empty((rows, Kp * bits // 8), dtype=torch.uint8, device=device),
+                        torch.empty((-(-rows // MX_TILE_ROWS), Kp // 128, MX_TILE_BYTES), dtype=torch.uint8,
+                                    device=device), K, bits)
+    _mx_check(out, "out")
+    if out.K != K or out.bits != bits or out.rows != rows:
+        raise ValueError(f"out must hold {rows} rows of {K} values in {bits} bits")
+    return out
+
+
+def _mx_check(q: MxTensor, what: str):
+    import torch
+    codes, scales, K, bits = q
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda or not scales.is_cuda:
+        raise ValueError(f"{what}: codes and scales must be uint8 CUDA tensors")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what}: codes and scales must be contiguous")
+    Kp = mx_padded(K)
+    if bits not in (4, 8) or codes.dim() != 2 or codes.shape[1] != Kp * bits // 8 or K <= 0:
+        raise ValueError(f"{what}: codes must be [rows, padded K·bits/8]")
+    if scales.numel() != -(-codes.shape[0] // MX_TILE_ROWS) * (Kp // 128) * MX_TILE_BYTES:
+        raise ValueError(f"{what}: scales must hold ceil(rows/128)·(padded K/128) tiles of 512 bytes")
+
+
+def _mx_same_device(device, *others):
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors of a call must be on one device")
+
+
+def mx_quantize(x, bits: int = 8, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """x [..., K] (float32, float16 or bfloat16) to an MX tensor of `bits` (4 or 8) bits."""
+    x, rows, K, stride = _mx_rows(x, "x")
+    out = _mx_out(rows, K, bits, x.device, out)
+    _mx_same_device(x.device, out.codes, out.scales)
+    mx_quantize_ptr(x.data_ptr(), stride, _mx_dtype(x.dtype, "x"), out.codes.data_ptr(), out.scales.data_ptr(), K,
+                    rows, bits, _stream_ptr(stream))
+    return out
+
+
+def mx_swiglu(gate, up, bits: int = 8, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """silu(gate)·up as an MX tensor, in one pass."""
+    gate, rows, K, gs = _mx_rows(gate, "gate")
+    up, urows, uK, us = _mx_rows(up, "up")
+    if (rows, K) != (urows, uK) or gate.dtype != up.dtype:
+        raise ValueError("gate and up must have the same shape and type")
+    out = _mx_out(rows, K, bits, gate.device, out)
+    _mx_same_device(gate.device, up, out.codes, out.scales)
+    mx_swiglu_ptr(gate.data_ptr(), gs, up.data_ptr(), us, _mx_dtype(gate.dtype, "gate"), out.codes.data_ptr(),
+                  out.scales.data_ptr(), K, rows, bits, _stream_ptr(stream))
+    return out
+
+
+def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: MxTensor | None = None, h_out=None,
+               stream=None):
+    """RMS norm of h = x + residual, as an MX tensor.
+
+    With a residual returns (MxTensor, h), h in x's type, written to h_out
+    where that is given (which may be x or residual itself); without one
+    returns the MxTensor alone.
+    """
+    import torch
+    x0 = x
+    x, rows, K, xs = _mx_rows(x, "x")
+    if weight.numel() != K or not weight.is_contiguous():
+        raise ValueError("weight must be contiguous and hold one value per column of x")
+    res_ptr, rs, h_ptr, hs = 0, K, 0, K
+    if residual is not None:
+        if residual.shape != x0.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and type")
+        r, _, _, rs = _mx_rows(residual, "residual")
+        res_ptr = r.data_ptr()
+        if h_out is None:
+            h_out = torch.empty(x0.shape, dtype=x.dtype, device=x.device)
+        elif h_out.shape != x0.shape or h_out.dtype != x.dtype:
+            raise ValueError("h_out must have x's shape and type")
+        h, _, _, hs = _mx_rows(h_out, "h_out")
+        h_ptr = h.data_ptr()
+    elif h_out is not None:
+        raise ValueError("h_out needs a residual: without one h is x")
+    out = _mx_out(rows, K, bits, x.device, out)
+    _mx_same_device(x.device, weight, residual, h_out, out.codes, out.scales)
+    mx_rmsnorm_ptr(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, _mx_dtype(x.dtype, "x"), weight.data_ptr(),
+                   _mx_dtype(weight.dtype, "weight"), float(eps), out.codes.data_ptr(), out.scales.data_ptr(), K, rows,
+                   bits, _stream_ptr(stream))
+    return out if residual is None else (out, h_out)
+
+
+def mx_dequantize(q: MxTensor, dtype=None, out=None, stream=None):
+    """The values [rows, K] that an MX tensor stands for (float32 unless dtype or out says otherwise)."""
+    import torch
+    _mx_check(q, "q")
+    rows, K = q.rows, q.K
+    if out is None:
+        out = torch.empty((rows, K), dtype=dtype or torch.float32, device=q.codes.device)
+    elif out.shape != (rows, K) or (dtype is not None and out.dtype != dtype):
+        raise ValueError("out must be [rows, K] of the given type")
+    _mx_same_device(q.codes.device, q.scales, out)
+    _, _, _, stride = _mx_rows(out, "out")
+    mx_dequantize_ptr(q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"), K,
+                      rows, q.bits, _stream_ptr(stream))
+    return out
+
+
+def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
+    """y[T, N] = x·wᵀ on the tensor cores: x in 4 or 8 bits, w in 4 bits,
+    y in float32 unless dtype or out says otherwise."""
+    import torch
+    _mx_check(x, "x")
+    _mx_check(w, "w")
+    if w.bits != 4:
+        raise ValueError("w must be a 4-bit MX tensor")
+    if x.K != w.K:
+        raise ValueError("x and w must have the same K")
+    T, N = x.rows, w.rows
+    if out is None:
+        out = torch.empty((T, N), dtype=dtype or torch.float32, device=x.codes.device)
+    elif out.shape != (T, N) or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
+        raise ValueError("out must be contiguous, [tokens, outputDim] of the given type")
+    _mx_same_device(x.codes.device, x.scales, w.codes, w.scales, out)
+    mx_matmul_ptr(x.codes.data_ptr(), x.scales.data_ptr(), x.bits, w.codes.data_ptr(), w.scales.data_ptr(),
+                  out.data_ptr(), _mx_dtype(out.dtype, "out"), x.K, N, T, _stream_ptr(stream))
+    return out

@@ -135,6 +135,97 @@ int check_common(const float *x, const void *w, const float *y, int K, int N, in
     return Q4MM_OK;
 }
 
+// Checks shared by the MX entry points.
+
+size_t mx_size(int dtype) { return dtype == Q4MM_F32 ? 4 : 2; }
+
+int check_mx_dims(int K, int rows, int bits, const char *rows_name) {
+    if (K <= 0 || rows < 0)
+        return fail(Q4MM_ERR_DIM, "inputDim (%d) must be positive and %s (%d) not negative", K, rows_name, rows);
+    if (K > Q4MM_MAX_INPUT_DIM) return fail(Q4MM_ERR_DIM, "inputDim %d exceeds the limit %d", K, Q4MM_MAX_INPUT_DIM);
+    if (bits != 4 && bits != 8) return fail(Q4MM_ERR_DIM, "bits (%d) must be 4 or 8", bits);
+    return Q4MM_OK;
+}
+
+int check_mx_dtype(int dtype, const char *what) {
+    if (dtype != Q4MM_F32 && dtype != Q4MM_F16 && dtype != Q4MM_BF16)
+        return fail(Q4MM_ERR_DIM, "%s type (%d) must be Q4MM_F32, Q4MM_F16 or Q4MM_BF16", what, dtype);
+    return Q4MM_OK;
+}
+
+// One buffer of a call: [p, p + bytes).
+struct Span {
+    const void *p;
+    size_t bytes;
+    const char *name;
+};
+
+// The bytes that `rows` strided rows of K values reach over.
+Span mx_rows(const void *p, long long stride, int K, int rows, size_t size, const char *name) {
+    return Span{p, ((size_t)(rows - 1) * (size_t)stride + (size_t)K) * size, name};
+}
+Span mx_codes(const void *p, int K, int rows, int bits, const char *name) {
+    return Span{p, Q4MM_MX_CODE_BYTES(K, rows, bits), name};
+}
+Span mx_scales(const void *p, int K, int rows, const char *name) {
+    return Span{p, Q4MM_MX_SCALE_BYTES(K, rows), name};
+}
+
+// Strides count elements; one row has none.  Rows that reach past 2^48
+// elements are no memory's (and would overflow the sums below).
+int check_mx_stride(long long stride, int K, int rows, const char *name) {
+    if (rows == 1) return Q4MM_OK;
+    if (stride < K) return fail(Q4MM_ERR_DIM, "the row stride of %s (%lld) is below its row of %d", name, stride, K);
+    if (stride > (1LL << 48) / (rows - 1))
+        return fail(Q4MM_ERR_DIM, "%d rows of %s %lld elements apart do not fit in memory", rows, name, stride);
+    return Q4MM_OK;
+}
+
+int check_mx_ptr(const Span &s, size_t align) {
+    if (!s.p) return fail(Q4MM_ERR_NULL, "%s must be non-NULL", s.name);
+    if (reinterpret_cast<uintptr_t>(s.p) % align)
+        return fail(Q4MM_ERR_ALIGN, "%s must be %zu-byte aligned", s.name, align);
+    return Q4MM_OK;
+}
+
+// No output may overlap an input or another output.
+int check_mx_alias(const Span *outs, int nouts, const Span *ins, int nins) {
+    for (int i = 0; i < nouts; ++i) {
+        for (int j = i + 1; j < nouts; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return fail(Q4MM_ERR_ALIAS, "%s and %s must not overlap", outs[i].name, outs[j].name);
+        for (int j = 0; j < nins; ++j)
+            if (ins[j].p && overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes))
+                return fail(Q4MM_ERR_ALIAS, "%s and %s must not overlap", outs[i].name, ins[j].name);
+    }
+    return Q4MM_OK;
+}
+
+int mx_quantize_call(const void *x, long long x_stride, const void *up, long long up_stride, bool swiglu, int dtype,
+                     void *codes, void *scales, int K, int rows, int bits, q4mm_stream_t stream) {
+    int rc = check_mx_dims(K, rows, bits, "rows");
+    if (rc || (rc = check_mx_dtype(dtype, "input"))) return rc;
+    if (rows == 0) return Q4MM_OK;
+    const size_t size = mx_size(dtype);
+    const char *xn = swiglu ? "gate" : "x";
+    if ((rc = check_mx_stride(x_stride, K, rows, xn)) ||
+        (swiglu && (rc = check_mx_stride(up_stride, K, rows, "up"))))
+        return rc;
+    const Span ins[2] = {mx_rows(x, x_stride, K, rows, size, xn), mx_rows(up, up_stride, K, rows, size, "up")};
+    const Span outs[2] = {mx_codes(codes, K, rows, bits, "codes"), mx_scales(scales, K, rows, "scales")};
+    if ((rc = check_mx_ptr(ins[0], size)) || (swiglu && (rc = check_mx_ptr(ins[1], size))) ||
+        (rc = check_mx_ptr(outs[0], 32)) || (rc = check_mx_ptr(outs[1], 16)) ||
+        (rc = check_mx_alias(outs, 2, ins, swiglu ? 2 : 1)))
+        return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxQuantizeArgs a{x, x_stride, swiglu ? up : nullptr, up_stride, static_cast<uint8_t *>(codes),
+                                 static_cast<uint8_t *>(scales), K, rows, bits};
+    const cudaError_t e = q4mm::launch_mx_quantize(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, swiglu ? "mx_swiglu launch" : "mx_quantize launch");
+    return Q4MM_OK;
+}
+
 }  // namespace
 
 namespace q4mm {
@@ -351,6 +442,103 @@ int ternary_gemv(const float *x, const void *w_packed, float scale, float *y, in
     cudaError_t e = q4mm::launch_ternary_gemv(ctx, x, static_cast<const uint8_t *>(w_packed), scale, y,
                                               inputDim, outputDim, tokens);
     if (e != cudaSuccess) return fail_cuda(e, "ternary_gemv launch");
+    return Q4MM_OK;
+}
+
+int mx_quantize(const void *x, long long x_stride, int dtype, void *codes, void *scales, int inputDim, int rows,
+                int bits, q4mm_stream_t stream) {
+    return mx_quantize_call(x, x_stride, nullptr, 0, false, dtype, codes, scales, inputDim, rows, bits, stream);
+}
+
+int mx_swiglu(const void *gate, long long gate_stride, const void *up, long long up_stride, int dtype, void *codes,
+              void *scales, int hiddenDim, int rows, int bits, q4mm_stream_t stream) {
+    return mx_quantize_call(gate, gate_stride, up, up_stride, true, dtype, codes, scales, hiddenDim, rows, bits,
+                            stream);
+}
+
+int mx_rmsnorm(const void *x, long long x_stride, const void *residual, long long residual_stride, void *h,
+               long long h_stride, int dtype, const void *weight, int weight_dtype, float eps, void *codes,
+               void *scales, int inputDim, int rows, int bits, q4mm_stream_t stream) {
+    const int K = inputDim;
+    int rc = check_mx_dims(K, rows, bits, "rows");
+    if (rc || (rc = check_mx_dtype(dtype, "input")) || (rc = check_mx_dtype(weight_dtype, "weight"))) return rc;
+    if (weight_dtype != dtype && weight_dtype != Q4MM_F32)
+        return fail(Q4MM_ERR_DIM, "the weight's type must be the input's or Q4MM_F32");
+    if (!(eps >= 0.f)) return fail(Q4MM_ERR_DIM, "eps (%g) must not be negative", (double)eps);
+    if (rows == 0) return Q4MM_OK;
+    const size_t size = mx_size(dtype), wsize = mx_size(weight_dtype);
+    if ((rc = check_mx_stride(x_stride, K, rows, "x")) ||
+        (residual && (rc = check_mx_stride(residual_stride, K, rows, "residual"))) ||
+        (h && (rc = check_mx_stride(h_stride, K, rows, "h"))))
+        return rc;
+    const Span xs = mx_rows(x, x_stride, K, rows, size, "x"), ws{weight, (size_t)K * wsize, "weight"};
+    const Span rs = mx_rows(residual, residual_stride, K, rows, size, "residual");
+    const Span hs = mx_rows(h, h_stride, K, rows, size, "h");
+    const Span outs[3] = {mx_codes(codes, K, rows, bits, "codes"), mx_scales(scales, K, rows, "scales"), hs};
+    if ((rc = check_mx_ptr(xs, size)) || (rc = check_mx_ptr(ws, wsize)) ||
+        (residual && (rc = check_mx_ptr(rs, size))) || (h && (rc = check_mx_ptr(hs, size))) ||
+        (rc = check_mx_ptr(outs[0], 32)) || (rc = check_mx_ptr(outs[1], 16)))
+        return rc;
+    const Span ins[3] = {xs, ws, rs};
+    if ((rc = check_mx_alias(outs, h ? 3 : 2, ins, 0)) || (rc = check_mx_alias(outs, 2, ins, 3))) return rc;
+    // h may be x or the residual itself (the same rows), not a part of them.
+    const Span same[2] = {xs, rs};
+    for (int i = 0; i < 2; ++i) {
+        const bool itself = same[i].p == h && (rows == 1 || (i == 0 ? x_stride : residual_stride) == h_stride);
+        if (h && same[i].p && !itself && (rc = check_mx_alias(&hs, 1, &same[i], 1))) return rc;
+    }
+    if (h && (rc = check_mx_alias(&hs, 1, &ws, 1))) return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxRmsnormArgs a{x, x_stride, residual, residual_stride, h, h_stride, weight,
+                                weight_dtype == Q4MM_F32, eps, static_cast<uint8_t *>(codes),
+                                static_cast<uint8_t *>(scales), K, rows, bits};
+    const cudaError_t e = q4mm::launch_mx_rmsnorm(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_rmsnorm launch");
+    return Q4MM_OK;
+}
+
+int mx_dequantize(const void *codes, const void *scales, void *y, long long y_stride, int dtype, int inputDim,
+                  int rows, int bits, q4mm_stream_t stream) {
+    const int K = inputDim;
+    int rc = check_mx_dims(K, rows, bits, "rows");
+    if (rc || (rc = check_mx_dtype(dtype, "output"))) return rc;
+    if (rows == 0) return Q4MM_OK;
+    if ((rc = check_mx_stride(y_stride, K, rows, "y"))) return rc;
+    const Span out = mx_rows(y, y_stride, K, rows, mx_size(dtype), "y");
+    const Span ins[2] = {mx_codes(codes, K, rows, bits, "codes"), mx_scales(scales, K, rows, "scales")};
+    if ((rc = check_mx_ptr(out, mx_size(dtype))) || (rc = check_mx_ptr(ins[0], 32)) ||
+        (rc = check_mx_ptr(ins[1], 16)) || (rc = check_mx_alias(&out, 1, ins, 2)))
+        return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxDequantizeArgs a{static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), y,
+                                   y_stride, K, rows, bits};
+    const cudaError_t e = q4mm::launch_mx_dequantize(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_dequantize launch");
+    return Q4MM_OK;
+}
+
+int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void *w_codes, const void *w_scales,
+              void *y, int dtype, int inputDim, int outputDim, int tokens, q4mm_stream_t stream) {
+    const int K = inputDim, N = outputDim, T = tokens;
+    int rc = check_mx_dims(K, T, x_bits, "tokens");
+    if (rc || (rc = check_mx_dtype(dtype, "output"))) return rc;
+    if (N <= 0) return fail(Q4MM_ERR_DIM, "outputDim (%d) must be positive", N);
+    if (T == 0) return Q4MM_OK;
+    const Span out{y, (size_t)T * N * mx_size(dtype), "y"};
+    const Span ins[4] = {mx_codes(x_codes, K, T, x_bits, "x_codes"), mx_scales(x_scales, K, T, "x_scales"),
+                         mx_codes(w_codes, K, N, 4, "w_codes"), mx_scales(w_scales, K, N, "w_scales")};
+    for (int i = 0; i < 4; ++i)
+        if ((rc = check_mx_ptr(ins[i], i % 2 ? 16 : 32))) return rc;
+    if ((rc = check_mx_ptr(out, mx_size(dtype))) || (rc = check_mx_alias(&out, 1, ins, 4))) return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx))) return rc;
+    const q4mm::MxMatmulArgs a{static_cast<const uint8_t *>(x_codes), static_cast<const uint8_t *>(x_scales),
+                               static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), y,
+                               K, N, T, x_bits};
+    const cudaError_t e = q4mm::launch_mx_matmul(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_matmul launch");
     return Q4MM_OK;
 }
 

@@ -79,6 +79,54 @@ cudaError_t launch_q4k_mm_tc_fixed_scratch(const LaunchCtx &c, const float *x, c
 cudaError_t launch_ternary_gemv(const LaunchCtx &c, const float *x, const uint8_t *W, float scale,
                                 float *y, int K, int N, int T);
 
+// Microscaled (MX) operators; layouts in mx.cuh, contracts in q4mm.h.
+enum class MxType { kF32 = 0, kF16 = 1, kBF16 = 2 };
+
+// Quantises x [rows][K] (row stride in elements), or silu(x)·up where up is
+// given, to `bits`-bit codes.
+struct MxQuantizeArgs {
+    const void *x;
+    long long x_stride;
+    const void *up;  // may be NULL
+    long long up_stride;
+    uint8_t *codes, *scales;
+    int K, rows, bits;
+};
+cudaError_t launch_mx_quantize(const LaunchCtx &c, MxType type, const MxQuantizeArgs &a);
+
+// h = x + residual, then h·(mean h² + eps)^-1/2·weight quantised; h is
+// written where it is not NULL (it may be x or residual).
+struct MxRmsnormArgs {
+    const void *x;
+    long long x_stride;
+    const void *residual;  // may be NULL
+    long long residual_stride;
+    void *h;  // may be NULL
+    long long h_stride;
+    const void *weight;
+    bool weight_f32;  // else x's type
+    float eps;
+    uint8_t *codes, *scales;
+    int K, rows, bits;
+};
+cudaError_t launch_mx_rmsnorm(const LaunchCtx &c, MxType type, const MxRmsnormArgs &a);
+
+struct MxDequantizeArgs {
+    const uint8_t *codes, *scales;
+    void *y;
+    long long y_stride;
+    int K, rows, bits;
+};
+cudaError_t launch_mx_dequantize(const LaunchCtx &c, MxType type, const MxDequantizeArgs &a);
+
+// y[T][N] = x·wᵀ on the tensor cores, x in x_bits (4 or 8), w in 4 bits.
+struct MxMatmulArgs {
+    const uint8_t *x_codes, *x_scales, *w_codes, *w_scales;
+    void *y;
+    int K, N, T, x_bits;
+};
+cudaError_t launch_mx_matmul(const LaunchCtx &c, MxType type, const MxMatmulArgs &a);
+
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device; the attribute call is made only when the limit grows, so a
 // warmed-up launch (for instance one being captured into a CUDA graph) issues
