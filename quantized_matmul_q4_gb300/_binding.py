@@ -299,6 +299,7 @@ def ternary_gemv(x, w, scale: float = 1.0, N: int | None = None, out=None, strea
 # Microscaled (MX) tensors: layouts and roundings in include/q4mm.h.
 
 MX_BLOCK, MX_TILE_ROWS, MX_TILE_BYTES = 32, 128, 512
+MX_MAX_ROWS = 2 ** 31 - 1   # rows of a call (the C ABI's int)
 
 
 class MxTensor(NamedTuple):
@@ -323,80 +324,97 @@ def mx_padded(K: int) -> int:
     return -(-K // 128) * 128
 
 
-_MX_DTYPES = None
+_MX_DTYPES = {}   # torch type -> q4mm_dtype, filled on first use
 
 
 def _mx_dtype(t, what: str) -> int:
-    global _MX_DTYPES
-    if _MX_DTYPES is None:
-        import torch
-        _MX_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
     code = _MX_DTYPES.get(t)
     if code is None:
-        raise ValueError(f"{what} must be float32, float16 or bfloat16")
+        import torch
+        _MX_DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+        code = _MX_DTYPES.get(t)
+        if code is None:
+            raise ValueError(f"{what} must be float32, float16 or bfloat16")
     return code
 
 
+def _mx_stream(stream, device: int) -> int:
+    """The given stream, or torch's current one on the tensors' device (its
+    handle alone: building a Stream object costs as much as a launch)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream_ptr(stream)
+
+
 def _mx_rows(x, what: str):
-    """x as a CUDA matrix of rows with adjacent values, never copied."""
+    """x as a CUDA matrix of rows with adjacent values, never copied: the
+    matrix, its shape and its row stride."""
     if not x.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if x.dim() != 2:
-        if x.dim() == 0:
+    shape = x.shape
+    if len(shape) != 2:
+        if not shape:
             raise ValueError(f"{what} must have at least one dimension")
         try:
-            x = x.view(-1, x.shape[-1]) if x.numel() else x.reshape(-1, max(x.shape[-1], 1))
+            x = x.view(-1, shape[-1]) if x.numel() else x.reshape(-1, max(shape[-1], 1))
         except RuntimeError:
             raise ValueError(f"the leading dimensions of {what} must collapse into evenly spaced rows") from None
-    rows, K = x.shape
+        shape = x.shape
+    rows, K = shape
+    if rows > MX_MAX_ROWS or K > MX_MAX_ROWS:
+        raise ValueError(f"{what} has more rows or columns than a call takes")
     s0, s1 = x.stride()
     if s1 != 1 and K > 1:
         raise ValueError(f"the values of a row of {what} must be adjacent")
     return x, rows, K, s0 if rows > 1 else K
 
 
-def _mx_out(rows: int, K: int, bits: int, device, out):
-    import torch
+def _mx_out(rows: int, K: int, bits: int, x, out) -> MxTensor:
+    """`out` checked, or a new MxTensor on x's device."""
     if bits != 4 and bits != 8:
         raise ValueError("bits must be 4 or 8")
-    Kp = mx_padded(K)
     if out is None:
-        return MxTensor(torch.empty((rows, Kp * bits // 8), dtype=torch.uint8, device=device),
-                        torch.empty((-(-rows // MX_TILE_ROWS), Kp // 128, MX_TILE_BYTES), dtype=torch.uint8,
-                                    device=device), K, bits)
-    _mx_check(out, "out")
-    if out.K != K or out.bits != bits or out.rows != rows:
+        import torch
+        kt = -(-K // 128)
+        u8, device = torch.uint8, x.device
+        return MxTensor(torch.empty((rows, kt * 16 * bits), dtype=u8, device=device),
+                        torch.empty((-(-rows // MX_TILE_ROWS), kt, MX_TILE_BYTES), dtype=u8, device=device), K, bits)
+    _mx_check(out, "out", x.get_device())
+    if out.K != K or out.bits != bits or out.codes.shape[0] != rows:
         raise ValueError(f"out must hold {rows} rows of {K} values in {bits} bits")
     return out
 
 
-def _mx_check(q: MxTensor, what: str):
+def _mx_check(q: MxTensor, what: str, device: int) -> int:
+    """Checks an MxTensor; returns its rows."""
     import torch
     codes, scales, K, bits = q
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not codes.is_cuda or not scales.is_cuda:
-        raise ValueError(f"{what}: codes and scales must be uint8 CUDA tensors")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{what}: codes and scales must be uint8 tensors")
+    if codes.get_device() != device or scales.get_device() != device or device < 0:
+        raise ValueError("all tensors of a call must be on one CUDA device")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: codes and scales must be contiguous")
-    Kp = mx_padded(K)
-    if bits not in (4, 8) or codes.dim() != 2 or codes.shape[1] != Kp * bits // 8 or K <= 0:
+    shape, kt = codes.shape, -(-K // 128)
+    if bits not in (4, 8) or len(shape) != 2 or shape[1] != kt * 16 * bits or K <= 0 or shape[0] > MX_MAX_ROWS:
         raise ValueError(f"{what}: codes must be [rows, padded K·bits/8]")
-    if scales.numel() != -(-codes.shape[0] // MX_TILE_ROWS) * (Kp // 128) * MX_TILE_BYTES:
+    if scales.numel() != -(-shape[0] // MX_TILE_ROWS) * kt * MX_TILE_BYTES:
         raise ValueError(f"{what}: scales must hold ceil(rows/128)·(padded K/128) tiles of 512 bytes")
+    return shape[0]
 
 
-def _mx_same_device(device, *others):
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors of a call must be on one device")
+def _mx_device(device: int, t) -> None:
+    if t.get_device() != device:
+        raise ValueError("all tensors of a call must be on one CUDA device")
 
 
 def mx_quantize(x, bits: int = 8, out: MxTensor | None = None, stream=None) -> MxTensor:
     """x [..., K] (float32, float16 or bfloat16) to an MX tensor of `bits` (4 or 8) bits."""
     x, rows, K, stride = _mx_rows(x, "x")
-    out = _mx_out(rows, K, bits, x.device, out)
-    _mx_same_device(x.device, out.codes, out.scales)
-    mx_quantize_ptr(x.data_ptr(), stride, _mx_dtype(x.dtype, "x"), out.codes.data_ptr(), out.scales.data_ptr(), K,
-                    rows, bits, _stream_ptr(stream))
+    out = _mx_out(rows, K, bits, x, out)
+    _check(_LIB.mx_quantize(x.data_ptr(), stride, _mx_dtype(x.dtype, "x"), out.codes.data_ptr(),
+                            out.scales.data_ptr(), K, rows, bits, _mx_stream(stream, x.get_device())))
     return out
 
 
@@ -404,12 +422,13 @@ def mx_swiglu(gate, up, bits: int = 8, out: MxTensor | None = None, stream=None)
     """silu(gate)·up as an MX tensor, in one pass."""
     gate, rows, K, gs = _mx_rows(gate, "gate")
     up, urows, uK, us = _mx_rows(up, "up")
-    if (rows, K) != (urows, uK) or gate.dtype != up.dtype:
+    dtype, device = gate.dtype, gate.get_device()
+    if rows != urows or K != uK or dtype != up.dtype:
         raise ValueError("gate and up must have the same shape and type")
-    out = _mx_out(rows, K, bits, gate.device, out)
-    _mx_same_device(gate.device, up, out.codes, out.scales)
-    mx_swiglu_ptr(gate.data_ptr(), gs, up.data_ptr(), us, _mx_dtype(gate.dtype, "gate"), out.codes.data_ptr(),
-                  out.scales.data_ptr(), K, rows, bits, _stream_ptr(stream))
+    _mx_device(device, up)
+    out = _mx_out(rows, K, bits, gate, out)
+    _check(_LIB.mx_swiglu(gate.data_ptr(), gs, up.data_ptr(), us, _mx_dtype(dtype, "gate"), out.codes.data_ptr(),
+                          out.scales.data_ptr(), K, rows, bits, _mx_stream(stream, device)))
     return out
 
 
@@ -421,65 +440,74 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
     where that is given (which may be x or residual itself); without one
     returns the MxTensor alone.
     """
-    import torch
-    x0 = x
+    shape, dtype = x.shape, x.dtype
     x, rows, K, xs = _mx_rows(x, "x")
+    device = x.get_device()
     if weight.numel() != K or not weight.is_contiguous():
         raise ValueError("weight must be contiguous and hold one value per column of x")
+    _mx_device(device, weight)
     res_ptr, rs, h_ptr, hs = 0, K, 0, K
     if residual is not None:
-        if residual.shape != x0.shape or residual.dtype != x.dtype:
+        if residual.shape != shape or residual.dtype != dtype:
             raise ValueError("residual must have x's shape and type")
         r, _, _, rs = _mx_rows(residual, "residual")
+        _mx_device(device, r)
         res_ptr = r.data_ptr()
         if h_out is None:
-            h_out = torch.empty(x0.shape, dtype=x.dtype, device=x.device)
-        elif h_out.shape != x0.shape or h_out.dtype != x.dtype:
-            raise ValueError("h_out must have x's shape and type")
-        h, _, _, hs = _mx_rows(h_out, "h_out")
+            import torch
+            h = h_out = torch.empty(shape, dtype=dtype, device=x.device)
+        else:
+            if h_out.shape != shape or h_out.dtype != dtype:
+                raise ValueError("h_out must have x's shape and type")
+            h, _, _, hs = _mx_rows(h_out, "h_out")
+            _mx_device(device, h)
         h_ptr = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual: without one h is x")
-    out = _mx_out(rows, K, bits, x.device, out)
-    _mx_same_device(x.device, weight, residual, h_out, out.codes, out.scales)
-    mx_rmsnorm_ptr(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, _mx_dtype(x.dtype, "x"), weight.data_ptr(),
-                   _mx_dtype(weight.dtype, "weight"), float(eps), out.codes.data_ptr(), out.scales.data_ptr(), K, rows,
-                   bits, _stream_ptr(stream))
+    out = _mx_out(rows, K, bits, x, out)
+    _check(_LIB.mx_rmsnorm(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, _mx_dtype(dtype, "x"), weight.data_ptr(),
+                           _mx_dtype(weight.dtype, "weight"), float(eps), out.codes.data_ptr(), out.scales.data_ptr(), K,
+                           rows, bits, _mx_stream(stream, device)))
     return out if residual is None else (out, h_out)
 
 
 def mx_dequantize(q: MxTensor, dtype=None, out=None, stream=None):
     """The values [rows, K] that an MX tensor stands for (float32 unless dtype or out says otherwise)."""
-    import torch
-    _mx_check(q, "q")
-    rows, K = q.rows, q.K
+    codes, scales, K, bits = q
+    device = codes.get_device()
+    rows = _mx_check(q, "q", device)
+    stride = K
     if out is None:
-        out = torch.empty((rows, K), dtype=dtype or torch.float32, device=q.codes.device)
-    elif out.shape != (rows, K) or (dtype is not None and out.dtype != dtype):
-        raise ValueError("out must be [rows, K] of the given type")
-    _mx_same_device(q.codes.device, q.scales, out)
-    _, _, _, stride = _mx_rows(out, "out")
-    mx_dequantize_ptr(q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"), K,
-                      rows, q.bits, _stream_ptr(stream))
+        import torch
+        out = torch.empty((rows, K), dtype=dtype or torch.float32, device=codes.device)
+    else:
+        if out.shape != (rows, K) or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be [rows, K] of the given type")
+        _, _, _, stride = _mx_rows(out, "out")
+        _mx_device(device, out)
+    _check(_LIB.mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"),
+                              K, rows, bits, _mx_stream(stream, device)))
     return out
 
 
 def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
     """y[T, N] = x·wᵀ on the tensor cores: x in 4 or 8 bits, w in 4 bits,
     y in float32 unless dtype or out says otherwise."""
-    import torch
-    _mx_check(x, "x")
-    _mx_check(w, "w")
-    if w.bits != 4:
+    x_codes, x_scales, K, x_bits = x
+    w_codes, w_scales, w_K, w_bits = w
+    device = x_codes.get_device()
+    T, N = _mx_check(x, "x", device), _mx_check(w, "w", device)
+    if w_bits != 4:
         raise ValueError("w must be a 4-bit MX tensor")
-    if x.K != w.K:
+    if K != w_K:
         raise ValueError("x and w must have the same K")
-    T, N = x.rows, w.rows
     if out is None:
-        out = torch.empty((T, N), dtype=dtype or torch.float32, device=x.codes.device)
-    elif out.shape != (T, N) or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
-        raise ValueError("out must be contiguous, [tokens, outputDim] of the given type")
-    _mx_same_device(x.codes.device, x.scales, w.codes, w.scales, out)
-    mx_matmul_ptr(x.codes.data_ptr(), x.scales.data_ptr(), x.bits, w.codes.data_ptr(), w.scales.data_ptr(),
-                  out.data_ptr(), _mx_dtype(out.dtype, "out"), x.K, N, T, _stream_ptr(stream))
+        import torch
+        out = torch.empty((T, N), dtype=dtype or torch.float32, device=x_codes.device)
+    else:
+        if out.shape != (T, N) or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be contiguous, [tokens, outputDim] of the given type")
+        _mx_device(device, out)
+    _check(_LIB.mx_matmul(x_codes.data_ptr(), x_scales.data_ptr(), x_bits, w_codes.data_ptr(), w_scales.data_ptr(),
+                          out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T, _mx_stream(stream, device)))
     return out

@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "mx.cuh"
+#include "mx_geometry.h"
 #include "sync.cuh"
 
 namespace q4mm {
@@ -40,25 +41,25 @@ template <bool kX8, int kTok>
 struct MmLayout {
     static constexpr int kStageK = kX8 ? 128 : 256;
     static constexpr int kScaleTiles = kStageK / 128;                 // scale tiles per 128 rows and stage
-    static constexpr int kXTiles = (kTok + kMxTileRows - 1) / kMxTileRows;
-    static constexpr uint32_t x_bytes = kTok * 128;
     // Bytes that the weight copy reports to its barrier: the unpacking copy
     // counts what it reads, half of what it lays out.
     static constexpr uint32_t w_tx = kX8 ? kMmWBytes / 2 : kMmWBytes;
     static constexpr uint32_t off_x = kMmWBytes;
-    static constexpr uint32_t off_sw = off_x + x_bytes;
+    static constexpr uint32_t off_sw = off_x + kTok * 128;
     static constexpr uint32_t off_sx = off_sw + kScaleTiles * kMxTileBytes;
-    static constexpr uint32_t stage = (off_sx + kXTiles * kScaleTiles * kMxTileBytes + 1023) / 1024 * 1024;
-    static constexpr int kStages = kTok >= 256 ? 4 : kTok >= 128 ? 6 : 8;
+    static constexpr uint32_t stage = (off_sx + kScaleTiles * kMxTileBytes + 1023) / 1024 * 1024;
+    // Two CTAs per SM: half of the 227 KB each.
+    static constexpr int kStages = (int)(112 * 1024 / stage);
     static constexpr uint32_t off_bar = kStages * stage;
     static constexpr uint32_t total = off_bar + 8 * (2 * kStages + 1) + 16 + 1024;
     // Tensor memory columns: the accumulator, then the scales of a stage.
     static constexpr int kColSw = kTok < 32 ? 32 : kTok;
     static constexpr int kColSx = kColSw + 4 * kScaleTiles;
-    static constexpr int kColsUsed = kColSx + 4 * kXTiles * kScaleTiles;
-    static constexpr int kCols = kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128 : kColsUsed <= 256 ? 256 : 512;
-    static_assert(total <= 232448, "shared memory");
-    static_assert(kColsUsed <= 512, "tensor memory");
+    static constexpr int kColsUsed = kColSx + 4 * kScaleTiles;
+    static constexpr int kCols = kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128 : 256;
+    static_assert(kStages >= 2 && 2 * (total + 1024) <= 233472, "two CTAs per SM");
+    static_assert(2 * kCols <= 512, "tensor memory of two CTAs");
+    static_assert(kTok <= kMxTileRows && kTok * kMmRows * 4 <= off_bar, "partial sums fit the ring");
 };
 
 // Shared-memory matrix descriptors: K-major rows of 128 bytes in 8-row atoms
@@ -134,11 +135,41 @@ __device__ __forceinline__ void mm_ld8(uint32_t taddr, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// Four consecutive n of one token, as the type asks; the aligned case is one
+// store.
+__device__ __forceinline__ void store_y4(void *y, MxType type, size_t at, int left, float4 v) {
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    if (type == MxType::kF32) {
+        float *p = static_cast<float *>(y) + at;
+        if (left >= 4 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+            *reinterpret_cast<float4 *>(p) = v;
+        } else {
+            for (int i = 0; i < 4 && i < left; ++i) p[i] = e[i];
+        }
+    } else if (type == MxType::kF16) {
+        __half *p = static_cast<__half *>(y) + at;
+        for (int i = 0; i < 4 && i < left; ++i) p[i] = __float2half_rn(e[i]);
+    } else {
+        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(y) + at;
+        for (int i = 0; i < 4 && i < left; ++i) p[i] = __float2bfloat16_rn(e[i]);
+    }
+}
+
+// Up to 128 tokens per tile, K split over the CTAs of a cluster: rank r of S
+// takes the stages [r·c/S, (r+1)·c/S) and puts its partial sums, [token][row],
+// into its shared memory; rank s then adds the S partial sums of rows
+// 4·(32·s/S) onwards in rank order, read over the cluster, and writes y, so
+// the result does not depend on scheduling.
 template <bool kX8, int kTok>
-__global__ void __launch_bounds__(kMmThreads, 1)
-    mx_mm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
-                 const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales, void *__restrict__ y,
-                 MxType type, int K, int N, int T, int *status, long long wait_limit, int withhold) {
+__global__ void __launch_bounds__(kMmThreads, 2)
+    mx_mm_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                       const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales,
+                       void *__restrict__ y, MxType type, int K, int N, int T, int n_mma, int *status,
+                       long long wait_limit, int withhold) {
     using L = MmLayout<kX8, kTok>;
     extern __shared__ uint8_t mm_smem_raw[];
     __shared__ volatile int abort_flag;
@@ -150,9 +181,11 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int Kp = mx_padded(K), nkt = Kp / kMxPadK;
-    const int row0 = blockIdx.x * kMmRows, tok0 = blockIdx.y * kTok;
-    const int chunks = (Kp + L::kStageK - 1) / L::kStageK;
+    const int row_tile = blockIdx.x / S, row0 = row_tile * kMmRows, tok0 = blockIdx.y * kTok;
+    const int all = (Kp + L::kStageK - 1) / L::kStageK;
+    const int c_lo = (int)((long long)rank * all / S), chunks = (int)((long long)(rank + 1) * all / S) - c_lo;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::kStages; ++s) {
@@ -162,6 +195,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         mbar_init(done, 1);
         abort_flag = 0;
         fence_mbar_init();
+        prefetch_map(&tm_w);
+        prefetch_map(&tm_x);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
@@ -190,21 +225,17 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                     break;
                 }
                 if (c == withhold) continue;  // test only: this stage never arrives
-                const int k0 = c * L::kStageK, kt = c * L::kScaleTiles;
+                const int k0 = (c_lo + c) * L::kStageK, kt = (c_lo + c) * L::kScaleTiles;
                 const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
-                // Row tiles of x scales inside the tensor (its rows are padded to 128).
-                const int xt0 = tok0 / kMxTileRows;
-                const int xtiles = min(L::kXTiles, (T + kMxTileRows - 1) / kMxTileRows - xt0);
                 uint8_t *st = smem + s * L::stage;
                 const uint32_t sa = sbase + s * L::stage;
-                mbar_arrive_expect_tx(&full[s], L::w_tx + L::x_bytes + (1 + xtiles) * sbytes);
-                const int c0 = kX8 ? k0 : k0 / 2;  // elements (4-bit in unpacked form, else bytes)
+                mbar_arrive_expect_tx(&full[s], L::w_tx + n_mma * 128 + 2 * sbytes);
+                const int c0 = kX8 ? k0 : k0 / 2;  // 8-bit codes and unpacked 4-bit ones in values, else bytes
                 mm_tma_2d(sa, &tm_w, c0, row0, &full[s]);
                 mm_tma_2d(sa + L::off_x, &tm_x, c0, tok0, &full[s]);
-                bulk_g2s(st + L::off_sw, w_scales + ((size_t)blockIdx.x * nkt + kt) * kMxTileBytes, sbytes, &full[s]);
-                for (int i = 0; i < xtiles; ++i)
-                    bulk_g2s(st + L::off_sx + i * L::kScaleTiles * kMxTileBytes,
-                             x_scales + ((size_t)(xt0 + i) * nkt + kt) * kMxTileBytes, sbytes, &full[s]);
+                bulk_g2s(st + L::off_sw, w_scales + ((size_t)row_tile * nkt + kt) * kMxTileBytes, sbytes, &full[s]);
+                bulk_g2s(st + L::off_sx, x_scales + ((size_t)(tok0 / kMxTileRows) * nkt + kt) * kMxTileBytes, sbytes,
+                         &full[s]);
             }
             // No copy may still be writing shared memory at exit.
             for (int i = max(0, c - L::kStages); i < c; ++i)
@@ -222,12 +253,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 }
                 mm_fence_after();
                 const uint32_t sa = sbase + s * L::stage;
-                const int kts = min(L::kScaleTiles, nkt - c * L::kScaleTiles);
+                const int kts = min(L::kScaleTiles, nkt - (c_lo + c) * L::kScaleTiles);
                 for (int j = 0; j < kts; ++j) {
                     scale_to_tmem(tmem + L::kColSw + 4 * j, scale_desc(sa + L::off_sw + j * kMxTileBytes));
-                    for (int i = 0; i < L::kXTiles; ++i)
-                        scale_to_tmem(tmem + L::kColSx + 4 * (j * L::kXTiles + i),
-                                      scale_desc(sa + L::off_sx + (i * L::kScaleTiles + j) * kMxTileBytes));
+                    scale_to_tmem(tmem + L::kColSx + 4 * j, scale_desc(sa + L::off_sx + j * kMxTileBytes));
                 }
                 const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + L::off_x);
                 // 32 bytes of each row per MMA: with kX8 32 values and one scale
@@ -236,8 +265,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
                 for (int m = 0; m < 4; ++m) {
                     const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
                     if (j < kts)
-                        mx_mma<kX8>(tmem, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(kTok, sf), tmem + L::kColSw + 4 * j,
-                                    tmem + L::kColSx + 4 * j * L::kXTiles + (tok0 % kMxTileRows) / 32, (c | m) != 0);
+                        mx_mma<kX8>(tmem, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(n_mma, sf), tmem + L::kColSw + 4 * j,
+                                    tmem + L::kColSx + 4 * j, (c | m) != 0);
                 }
                 mm_commit(&empty[s]);
             }
@@ -246,18 +275,32 @@ __global__ void __launch_bounds__(kMmThreads, 1)
             (void)mbar_wait_bounded(done, 0, wait_limit);
         }
         __syncwarp();
-    } else {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, wait_limit) ? 1 : 0) && !abort_flag;
-        mm_fence_after();
+    }
+    // (The producer and the issuer leave their branches through a reconverged
+    // warp; every warp takes part from here on.)
+    const bool ok = __syncthreads_and(mbar_wait_bounded(done, 0, wait_limit) ? 1 : 0) != 0 && !abort_flag;
+    mm_fence_after();
+    const int toks = min(kTok, T - tok0);
+    float *part = reinterpret_cast<float *>(smem);  // [token][128 rows], over the ring
+    if (warp >= 2) {
         const int q = warp & 3;  // tensor-memory lane quarter of this warp
-        const int n = row0 + 32 * q + lane;
-        for (int t = 0; ok && t < kTok && tok0 + t < T; t += 8) {
+        const int r = 32 * q + lane, n = row0 + r;
+        for (int t = 0; t < toks; t += 8) {
             float v[8];
-            mm_ld8(tmem + ((uint32_t)(32 * q) << 16) + t, v);
-            if (n < N) {
+            if (ok && chunks > 0) {
+                mm_ld8(tmem + ((uint32_t)(32 * q) << 16) + t, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            }
+            if (S > 1) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (t + i < toks) part[(t + i) * kMmRows + r] = v[i];
+            } else if (ok && n < N) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (tok0 + t + i >= T) break;
+                    if (t + i >= toks) break;
                     const size_t at = (size_t)(tok0 + t + i) * N + n;
                     if (type == MxType::kF32)
                         static_cast<float *>(y)[at] = v[i];
@@ -271,7 +314,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         }
         mm_fence_before();
     }
-    __syncthreads();
+    if (S > 1) {
+        cluster_sync_all();
+        const int lo = 4 * (32 * rank / S), rows4 = (4 * (32 * (rank + 1) / S) - lo) / 4;
+        for (int i = threadIdx.x; i < rows4 * toks; i += kMmThreads) {
+            const int r = lo + 4 * (i % rows4), t = i / rows4;
+            const uint32_t at = smem_addr(part + t * kMmRows + r);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < S; ++s) {
+                const float4 v = ld_cluster_v4(map_to_rank(at, (uint32_t)s));
+                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+            }
+            if (row0 + r < N) store_y4(y, type, (size_t)(tok0 + t) * N + row0 + r, N - row0 - r, acc);
+        }
+        cluster_sync_all();  // no CTA leaves while another reads its sums
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         mm_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
@@ -309,27 +368,43 @@ bool map_codes(CUtensorMap *m, const uint8_t *codes, int rows, int Kp, int bits,
 }
 
 template <bool kX8, int kTok>
-cudaError_t launch_mm(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
+cudaError_t launch_split(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
     using L = MmLayout<kX8, kTok>;
     const int Kp = mx_padded(a.K);
+    const int n_mma = a.T < kTok ? (a.T + 15) / 16 * 16 : kTok;
     alignas(64) CUtensorMap tm_w, tm_x;
     if (!map_codes(&tm_w, a.w_codes, a.N, Kp, 4, kX8, kMmRows) ||
-        !map_codes(&tm_x, a.x_codes, a.T, Kp, a.x_bits, false, kTok))
+        !map_codes(&tm_x, a.x_codes, a.T, Kp, a.x_bits, false, n_mma))
         return cudaErrorInvalidValue;
-    auto kernel = mx_mm_kernel<kX8, kTok>;
-    const cudaError_t e = ensure_smem(kernel, L::total);
+    auto kernel = mx_mm_split_kernel<kX8, kTok>;
+    cudaError_t e = ensure_smem(kernel, L::total);
     if (e != cudaSuccess) return e;
-    const dim3 grid((a.N + kMmRows - 1) / kMmRows, (a.T + kTok - 1) / kTok);
-    return launch_kernel(c, kernel, grid, dim3(kMmThreads), L::total, tm_w, tm_x, a.w_scales, a.x_scales, a.y, type,
-                         a.K, a.N, a.T, c.status, c.wait_limit, c.withhold);
+    const int row_tiles = (a.N + kMmRows - 1) / kMmRows, tok_tiles = (a.T + kTok - 1) / kTok;
+    const int stages = (Kp + L::kStageK - 1) / L::kStageK;
+    const int S = mx_split(row_tiles, tok_tiles, stages, c.num_sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(row_tiles * S, tok_tiles);
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = L::total;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_x, a.w_scales, a.x_scales, a.y, type, a.K, a.N, a.T, n_mma,
+                              c.status, c.wait_limit, c.withhold);
 }
 
 template <bool kX8>
 cudaError_t launch_mm_tokens(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
-    if (a.T <= 16) return launch_mm<kX8, 16>(c, type, a);
-    if (a.T <= 32) return launch_mm<kX8, 32>(c, type, a);
-    if (a.T <= 128) return launch_mm<kX8, 128>(c, type, a);
-    return launch_mm<kX8, 256>(c, type, a);
+    if (a.T <= 16) return launch_split<kX8, 16>(c, type, a);
+    if (a.T <= 64) return launch_split<kX8, 64>(c, type, a);
+    return launch_split<kX8, 128>(c, type, a);
 }
 
 }  // namespace

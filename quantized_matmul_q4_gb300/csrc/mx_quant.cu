@@ -255,14 +255,16 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
         }
     }
     // Zero scale bytes for the rows past the last one: the CTAs of the last
-    // 128-row block share them.
+    // 128-row block share them, a thread per word.
     const long long first = (long long)(a.rows - 1) / kMxTileRows * kMxTileRows;
     if (row >= first) {
         const int here = (int)(a.rows - first);
         uint8_t *tiles = a.scales + (size_t)(first / kMxTileRows) * nkt * kMxTileBytes;
-        for (int p = here + (int)(row - first); p < kMxTileRows; p += here)
-            for (int kt = threadIdx.x; kt < nkt; kt += blockDim.x)
-                *reinterpret_cast<uint32_t *>(tiles + (size_t)kt * kMxTileBytes + 16 * (p & 31) + 4 * (p >> 5)) = 0u;
+        const int words = (kMxTileRows - here) * nkt;
+        for (int i = (int)(row - first) * blockDim.x + threadIdx.x; i < words; i += here * blockDim.x) {
+            const int p = here + i / nkt, kt = i % nkt;
+            *reinterpret_cast<uint32_t *>(tiles + (size_t)kt * kMxTileBytes + 16 * (p & 31) + 4 * (p >> 5)) = 0u;
+        }
     }
 }
 
