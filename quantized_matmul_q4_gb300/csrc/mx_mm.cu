@@ -57,7 +57,7 @@ struct MmLayout {
     static constexpr int kColSx = kColSw + 4 * kScaleTiles;
     static constexpr int kColsUsed = kColSx + 4 * kScaleTiles;
     static constexpr int kCols = kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128 : 256;
-    static_assert(kStages >= 2 && 2 * (total + 1024) <= 233472, "two CTAs per SM");
+    static_assert(kStages >= 2 && kStages <= 8 && 2 * (total + 1024) <= 233472, "two CTAs per SM");
     static_assert(2 * kCols <= 512, "tensor memory of two CTAs");
     static_assert(kTok <= kMxTileRows && kTok * kMmRows * 4 <= off_bar, "partial sums fit the ring");
 };
@@ -73,33 +73,30 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
 }
 
-// Block-scaled instruction descriptor: E8M0 scales, K-major operands, M = 128.
+// Block-scaled instruction descriptor: E8M0 scales, K-major operands, M = m.
 // sf: which byte of a scale column's 32-bit word the instruction starts at.
 template <bool kX8>
-__device__ __forceinline__ uint32_t mx_idesc(int n, int sf) {
+__device__ __forceinline__ uint32_t mx_idesc(int n, int sf, int m = kMmRows) {
     const uint32_t a_fmt = kX8 ? 5u : 1u;  // E2M1
     const uint32_t b_fmt = kX8 ? 0u : 1u;  // E4M3 or E2M1
     return (uint32_t)sf << 4 | a_fmt << 7 | b_fmt << 10 | (uint32_t)(n >> 3) << 17 | 1u << 23 |
-           (uint32_t)(kMmRows >> 4) << 24 | (uint32_t)sf << 29;
+           (uint32_t)(m >> 4) << 24 | (uint32_t)sf << 29;
 }
 
-template <bool kX8>
+template <bool kX8, int kGroup>
 __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
                                        uint32_t accumulate) {
-    if constexpr (kX8) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-            : "memory");
-    }
+#define Q4MM_MX_MMA(group, kind, vec)                                                                             \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                  \
+                 "tcgen05.mma.cta_group::" group ".kind::" kind ".block_scale.scale_vec::" vec                       \
+                 " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                                \
+                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)                                      \
+                 : "memory")
+    if constexpr (kX8 && kGroup == 1) Q4MM_MX_MMA("1", "mxf8f6f4", "1X");
+    if constexpr (!kX8 && kGroup == 1) Q4MM_MX_MMA("1", "mxf4", "2X");
+    if constexpr (kX8 && kGroup == 2) Q4MM_MX_MMA("2", "mxf8f6f4", "1X");
+    if constexpr (!kX8 && kGroup == 2) Q4MM_MX_MMA("2", "mxf4", "2X");
+#undef Q4MM_MX_MMA
 }
 
 // A 128-row scale tile to four tensor-memory columns, repeated in the four
@@ -214,33 +211,46 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int c = 0;
-            for (; c < chunks && !abort_flag; ++c) {
-                const int s = c % L::kStages;
-                if (c >= L::kStages &&
-                    !mbar_wait_abortable(&empty[s], ((c / L::kStages) - 1) & 1, wait_limit, &abort_flag)) {
+        // Four copies per stage, one per lane: a bulk copy holds the thread
+        // that issues it for some 475 cycles (measured), but lanes that
+        // issue by one instruction do so side by side.  Copy j of a stage:
+        // weights and tokens (tensor copies), their scales (plain ones).
+        auto issue = [&](int c, int j, bool here) {
+            const int s = c % L::kStages;
+            const int k0 = (c_lo + c) * L::kStageK, kt = (c_lo + c) * L::kScaleTiles;
+            const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
+            here = here && c != withhold;  // (test only: a stage that never arrives)
+            if (here && j == 0) mbar_arrive_expect_tx(&full[s], L::w_tx + n_mma * 128 + 2 * sbytes);
+            __syncwarp();
+            const int c0 = kX8 ? k0 : k0 / 2;  // 8-bit codes and unpacked 4-bit ones in values, else bytes
+            if (here && j < 2)
+                mm_tma_2d(sbase + s * L::stage + (j ? L::off_x : 0u), j ? &tm_x : &tm_w, c0, j ? tok0 : row0, &full[s]);
+            if (here && j >= 2)
+                bulk_g2s(smem + s * L::stage + (j == 3 ? L::off_sx : L::off_sw),
+                         (j == 3 ? x_scales + (size_t)(tok0 / kMxTileRows) * nkt * kMxTileBytes
+                                 : w_scales + (size_t)row_tile * nkt * kMxTileBytes) + (size_t)kt * kMxTileBytes,
+                         sbytes, &full[s]);
+            __syncwarp();
+        };
+        const int lap = min(chunks, L::kStages);
+        issue(lane >> 2, lane & 3, (lane >> 2) < lap);
+        int c = lap;
+        for (; c < chunks; ++c) {
+            const bool ok =
+                mbar_wait_abortable(&empty[c % L::kStages], ((c / L::kStages) - 1) & 1, wait_limit, &abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) {
                     abort_flag = 1;
                     flag_timeout(status);
-                    break;
                 }
-                if (c == withhold) continue;  // test only: this stage never arrives
-                const int k0 = (c_lo + c) * L::kStageK, kt = (c_lo + c) * L::kScaleTiles;
-                const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
-                uint8_t *st = smem + s * L::stage;
-                const uint32_t sa = sbase + s * L::stage;
-                mbar_arrive_expect_tx(&full[s], L::w_tx + n_mma * 128 + 2 * sbytes);
-                const int c0 = kX8 ? k0 : k0 / 2;  // 8-bit codes and unpacked 4-bit ones in values, else bytes
-                mm_tma_2d(sa, &tm_w, c0, row0, &full[s]);
-                mm_tma_2d(sa + L::off_x, &tm_x, c0, tok0, &full[s]);
-                bulk_g2s(st + L::off_sw, w_scales + ((size_t)row_tile * nkt + kt) * kMxTileBytes, sbytes, &full[s]);
-                bulk_g2s(st + L::off_sx, x_scales + ((size_t)(tok0 / kMxTileRows) * nkt + kt) * kMxTileBytes, sbytes,
-                         &full[s]);
+                break;
             }
-            // No copy may still be writing shared memory at exit.
+            issue(c, lane, lane < 4);
+        }
+        // No copy may still be writing shared memory at exit.
+        if (lane == 0)
             for (int i = max(0, c - L::kStages); i < c; ++i)
                 if (i != withhold) (void)mbar_wait_bounded(&full[i % L::kStages], (i / L::kStages) & 1, wait_limit);
-        }
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                 for (int m = 0; m < 4; ++m) {
                     const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
                     if (j < kts)
-                        mx_mma<kX8>(tmem, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(n_mma, sf), tmem + L::kColSw + 4 * j,
+                        mx_mma<kX8, 1>(tmem, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(n_mma, sf), tmem + L::kColSw + 4 * j,
                                     tmem + L::kColSx + 4 * j, (c | m) != 0);
                 }
                 mm_commit(&empty[s]);
@@ -337,6 +347,436 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.
+// ---------------------------------------------------------------------------
+
+constexpr int kPairThreads = 480;  // operand copies, MMA issuer, 4 scale warps, 8 epilogue warps, scale copies
+constexpr int kPairEpiWarp = 6, kPairScaleProducer = 14;
+constexpr int kPairTok = 256;
+constexpr int kPairStages = 6;
+constexpr int kPairXTiles = 3;     // 128-row scale tiles that the tokens of a tile touch at most
+
+template <bool kX8>
+struct PairLayout {
+    static constexpr int kStageK = kX8 ? 128 : 256;
+    static constexpr int kScaleTiles = kStageK / 128;
+    static constexpr uint32_t w_tx = kX8 ? kMmWBytes / 2 : kMmWBytes;
+    static constexpr uint32_t off_x = kMmWBytes;
+    static constexpr uint32_t off_sw = off_x + kPairTok / 2 * 128;
+    static constexpr uint32_t off_sx = off_sw + kScaleTiles * kMxTileBytes;
+    static constexpr uint32_t stage = (off_sx + kPairXTiles * kScaleTiles * kMxTileBytes + 1023) / 1024 * 1024;
+    // Tensor memory: per 128 values of K the scales of a stage take 4 columns
+    // for w and 8 for x (256 tokens).
+    static constexpr int kScaleCols = kScaleTiles * 12;
+    static constexpr int kScaleBufs = 96 / kScaleCols < kPairStages ? 96 / kScaleCols : kPairStages;
+    static constexpr uint32_t off_bar = kPairStages * stage;
+    static constexpr int kBars = 3 * kPairStages + kScaleBufs + 5;
+    static constexpr uint32_t total = off_bar + 8 * kBars + 16 + 1024;
+    static_assert(total <= 232448, "shared memory");
+    static_assert(kScaleBufs >= 3 && kScaleBufs <= kPairStages, "scale buffers");
+};
+
+// Tensor memory of a pair's CTA: accumulators of up to 256 columns at 0 and
+// at 160, which share what reaches past 160, then the scale buffers.
+constexpr int kPairCol1 = 160;
+constexpr int kPairColScales = 416;
+
+__device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs of the pair once the
+// MMAs (and scale copies) issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Waits on a barrier that the other CTA of the pair arrives on.
+__device__ __forceinline__ bool mbar_spin_cluster(uint64_t *bar, uint32_t parity, long long limit_cycles,
+                                                  const volatile int *abort) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_addr(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort || clock64() - t0 > limit_cycles) return false;
+    }
+}
+
+__device__ __forceinline__ void mm_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One n of `count` consecutive tokens, N values apart.
+template <class T>
+__device__ __forceinline__ void store_column(T *p, int N, int count, const float (&v)[32]) {
+    if (count >= 32) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) p[(size_t)i * N] = mx_from_float<T>(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < count) p[(size_t)i * N] = mx_from_float<T>(v[i]);
+    }
+}
+
+// The tile of a running index: token tiles in groups of 8, row tiles outside
+// the group's tokens, so that the tiles in flight share operands in L2.
+struct PairTile {
+    int row0, tok0;
+};
+__device__ __forceinline__ PairTile pair_tile(long long i, int row_tiles, int tok_tiles, int tile_tok) {
+    const long long per_group = 8LL * row_tiles;
+    const int g = (int)(i / per_group), in = (int)(i % per_group);
+    const int width = min(8, tok_tiles - 8 * g);
+    return PairTile{in / width * 2 * kMmRows, (8 * g + in % width) * tile_tok};
+}
+
+// Four columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void mm_st4(uint32_t taddr, uint4 v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// A cluster of two CTAs computes 256 weight rows x tile_tok tokens with
+// instructions of M = 256: each CTA stages its 128 weight rows and its half
+// of the tokens, and holds its 128 rows of D.  Half of the operand bytes of
+// two single CTAs, both from L2 and in shared memory.  The pair takes every
+// (number of pairs)-th tile; the epilogue of a tile runs beside the MMAs of
+// the next.  All copies of both CTAs are counted on the leader's barriers,
+// and its one thread issues every MMA; completions are multicast to both.
+template <bool kX8>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    mx_mm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                      const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales,
+                      void *__restrict__ y, MxType type, int K, int N, int T, int tile_tok, int x_tiles, int row_tiles,
+                      int tok_tiles, int *status, long long wait_limit, int withhold) {
+    using L = PairLayout<kX8>;
+    extern __shared__ uint8_t mm_smem_raw[];
+    __shared__ volatile int abort_flag;
+    const uint32_t raw = smem_addr(mm_smem_raw);
+    uint8_t *smem = mm_smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_addr(smem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::off_bar), *empty = full + kPairStages;
+    uint64_t *scales_in = empty + kPairStages;               // a stage's scale tiles have landed in this CTA
+    uint64_t *scales_up = scales_in + kPairStages;           // ... and lie in both CTAs' tensor memory
+    uint64_t *acc_full = scales_up + L::kScaleBufs, *acc_free = acc_full + 2;  // one of each per accumulator
+    uint64_t *done = acc_free + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int Kp = mx_padded(K), nkt = Kp / kMxPadK;
+    const int chunks = (Kp + L::kStageK - 1) / L::kStageK;
+    const long long tiles = (long long)row_tiles * tok_tiles;
+    const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    // Blocks of 32 tokens that the two accumulators share.
+    const int blocks = tile_tok / 32, shared = max(0, blocks - kPairCol1 / 32);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&scales_in[s], 1);
+        }
+        for (int b = 0; b < L::kScaleBufs; ++b) mbar_init(&scales_up[b], 8);  // 4 scale warps of both CTAs
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_free[b], 16);  // 8 epilogue warps of both CTAs
+        }
+        mbar_init(done, 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        prefetch_map(&tm_w);
+        prefetch_map(&tm_x);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    mm_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    mm_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    if (warp == 0 || warp == kPairScaleProducer) {
+        // Two warps copy the stages in, one copy per lane and the lanes by
+        // one instruction (a copy holds the thread that issues it for some
+        // 475 cycles): the first the weights and the tokens, the other the
+        // scales of the weights (lane 0) and of the tokens (up to three).
+        const bool operands = warp == 0;
+        int s = 0;
+        uint32_t ph = 1;  // a fresh barrier's previous phase counts as done
+        long long n = 0;  // stages issued
+        bool ok = true;
+        const uint32_t tx = 2 * (L::w_tx + (uint32_t)tile_tok / 2 * 128);
+        const int w_all = (N + kMxTileRows - 1) / kMxTileRows, x_all = (T + kMxTileRows - 1) / kMxTileRows;
+        for (long long i = pair; i < tiles && ok; i += pairs) {
+            const PairTile t = pair_tile(i, row_tiles, tok_tiles, tile_tok);
+            const int wrow = t.row0 + rank * kMmRows, xrow = t.tok0 + rank * (tile_tok / 2);
+            const CUtensorMap *map = lane ? &tm_x : &tm_w;
+            const int crow = lane ? xrow : wrow;
+            // Scale tiles: this CTA's rows (none past the last row) and all
+            // of the tile's tokens.
+            const int wt = wrow / kMxTileRows, nw = wt < w_all ? 1 : 0;
+            const int xt = t.tok0 / kMxTileRows, nx = min(x_tiles, x_all - xt);
+            const uint8_t *from = lane == 0 ? w_scales + (size_t)wt * nkt * kMxTileBytes
+                                            : x_scales + (size_t)(xt + lane - 1) * nkt * kMxTileBytes;
+            const bool mine = operands ? lane < 2 : lane == 0 ? nw != 0 : lane <= nx;
+            for (int c = 0; c < chunks; ++c, ++n) {
+                ok = mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) {
+                        abort_flag = 1;
+                        flag_timeout(status);
+                    }
+                    ok = false;
+                    break;
+                }
+                const bool here = n != withhold;  // (test only: a stage that never arrives)
+                const uint32_t off = s * L::stage;
+                if (operands) {
+                    const uint32_t bar = map_to_rank(smem_addr(&full[s]), 0);  // the leader's
+                    if (here && lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                    if (here && mine)
+                        pair_tma_2d(sbase + off + (lane ? L::off_x : 0u), map,
+                                    kX8 ? c * L::kStageK : c * (L::kStageK / 2), crow, bar);
+                } else {
+                    const int kt = c * L::kScaleTiles;
+                    const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
+                    if (here && lane == 0) mbar_arrive_expect_tx(&scales_in[s], (uint32_t)(nw + nx) * sbytes);
+                    __syncwarp();
+                    if (here && mine)
+                        bulk_g2s(smem + off + (lane ? L::off_sx + (lane - 1) * L::kScaleTiles * kMxTileBytes : L::off_sw),
+                                 from + (size_t)kt * kMxTileBytes, sbytes, &scales_in[s]);
+                }
+                __syncwarp();
+                if (++s == kPairStages) s = 0, ph ^= 1u;
+            }
+        }
+        // No copy may still be writing shared memory at exit: the MMAs wait
+        // for every stage, and their completion is awaited here.  After a
+        // time-out, which leaves copies that nobody waits for, give them far
+        // longer than a copy takes.
+        for (int k = 0; k < kPairStages && ok; ++k) {
+            ok = __all_sync(0xffffffffu, mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag) ? 1 : 0) != 0;
+            if (++s == kPairStages) s = 0, ph ^= 1u;
+        }
+        if (!ok) {
+            if (lane == 0) abort_flag = 1;
+            __nanosleep(1000000);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int s = 0, buf = 0, it = 0;
+            uint32_t ph = 0, bph = 0;
+            bool ok = true;
+            for (long long i = pair; i < tiles && ok; i += pairs, ++it) {
+                const PairTile t = pair_tile(i, row_tiles, tok_tiles, tile_tok);
+                const uint32_t d = tmem + (it & 1) * kPairCol1;
+                // The epilogue frees what this accumulator shares with the
+                // previous tile's first of all; without shared columns the
+                // one two tiles back has to be free.
+                const int before = it - (shared ? 1 : 2);
+                if (before >= 0)
+                    ok = mbar_spin_cluster(&acc_free[before & 1], (before >> 1) & 1, wait_limit, &abort_flag);
+                for (int c = 0; c < chunks && ok; ++c) {
+                    ok = mbar_spin_cluster(&scales_up[buf], bph, wait_limit, &abort_flag) &&
+                         mbar_spin_abortable(&full[s], ph, wait_limit, &abort_flag);
+                    if (!ok) break;
+                    mm_fence_after();
+                    const uint32_t sa = sbase + s * L::stage;
+                    const int kts = min(L::kScaleTiles, nkt - c * L::kScaleTiles);
+                    const uint32_t sw = tmem + kPairColScales + buf * L::kScaleCols, sx = sw + 4 * L::kScaleTiles;
+                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + L::off_x);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
+                        if (j < kts)
+                            mx_mma<kX8, 2>(d, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows),
+                                           sw + 4 * j, sx + 8 * j,
+                                           (c | m) != 0);
+                    }
+                    pair_commit(&empty[s]);
+                    if (++s == kPairStages) s = 0, ph ^= 1u;
+                    if (++buf == L::kScaleBufs) buf = 0, bph ^= 1u;
+                }
+                pair_commit(&acc_full[it & 1]);
+            }
+            if (!ok) {
+                abort_flag = 1;
+                flag_timeout(status);
+            }
+            // Whatever was issued completes before tensor memory is freed.
+            pair_commit(done);
+            (void)mbar_wait_bounded(done, 0, wait_limit);
+        }
+        __syncwarp();
+    } else if (warp < kPairEpiWarp) {
+        // Scale warps: lane l of each lane quarter gets the words of rows l,
+        // l + 32, l + 64 and l + 96, 16 adjacent bytes of a tile, as four
+        // columns.  (tcgen05.cp does the same in one instruction, but for a
+        // CTA pair each takes about 128 cycles of the tensor pipe, measured,
+        // six per stage against four MMAs of about 128.)
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairColScales;
+        const uint32_t up0 = map_to_rank(smem_addr(scales_up), 0);
+        int s = 0, buf = 0;
+        uint32_t ph = 0;
+        long long n = 0;
+        int rs = 0;          // the stage whose MMAs last read this buffer
+        uint32_t rph = 0;
+        bool ok = true;
+        for (long long i = pair; i < tiles && ok; i += pairs) {
+            // Blocks of 32 tokens before the tile's first in its scale tile.
+            const int skip = pair_tile(i, row_tiles, tok_tiles, tile_tok).tok0 % kMxTileRows / 32;
+            for (int c = 0; c < chunks; ++c, ++n) {
+                ok = mbar_wait_abortable(&scales_in[s], ph, wait_limit, &abort_flag);
+                if (n >= L::kScaleBufs) {
+                    ok = ok && mbar_wait_abortable(&empty[rs], rph, wait_limit, &abort_flag);
+                    if (++rs == kPairStages) rs = 0, rph ^= 1u;
+                }
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) {
+                        abort_flag = 1;
+                        flag_timeout(status);
+                    }
+                    ok = false;
+                    break;
+                }
+                mm_fence_after();
+                const uint8_t *st = smem + s * L::stage + 16 * lane;
+                const uint32_t col = t_lane + buf * L::kScaleCols;
+#pragma unroll
+                for (int j = 0; j < L::kScaleTiles; ++j) {
+                    mm_st4(col + 4 * j, *reinterpret_cast<const uint4 *>(st + L::off_sw + j * kMxTileBytes));
+                    auto x_words = [&](int k) {
+                        return k < x_tiles ? *reinterpret_cast<const uint4 *>(
+                                                 st + L::off_sx + (k * L::kScaleTiles + j) * kMxTileBytes)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+                    };
+                    // The tile's first token goes to the first column: the
+                    // MMA takes scales from a multiple of four columns on.
+                    uint4 u = x_words(0), v = x_words(1);
+                    if (skip) {
+                        const uint4 w = x_words(2);
+                        if (skip == 1) {
+                            u = make_uint4(u.y, u.z, u.w, v.x), v = make_uint4(v.y, v.z, v.w, w.x);
+                        } else if (skip == 2) {
+                            u = make_uint4(u.z, u.w, v.x, v.y), v = make_uint4(v.z, v.w, w.x, w.y);
+                        } else {
+                            u = make_uint4(u.w, v.x, v.y, v.z), v = make_uint4(v.w, w.x, w.y, w.z);
+                        }
+                    }
+                    mm_st4(col + 4 * L::kScaleTiles + 8 * j, u);
+                    mm_st4(col + 4 * L::kScaleTiles + 8 * j + 4, v);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                mm_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(up0 + 8 * buf);
+                if (++s == kPairStages) s = 0, ph ^= 1u;
+                if (++buf == L::kScaleBufs) buf = 0;
+            }
+        }
+    } else {
+        const int q = warp & 3, half = (warp - kPairEpiWarp) >> 2;  // lane quarter; even or odd blocks of 32 tokens
+        const uint32_t free_addr = map_to_rank(smem_addr(acc_free), 0);
+        int it = 0;
+        for (long long i = pair; i < tiles; i += pairs, ++it) {
+            const PairTile t = pair_tile(i, row_tiles, tok_tiles, tile_tok);
+            const bool ok = mbar_wait_abortable(&acc_full[it & 1], (it >> 1) & 1, wait_limit, &abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) {
+                    abort_flag = 1;
+                    flag_timeout(status);
+                }
+                break;
+            }
+            mm_fence_after();
+            const uint32_t col0 = tmem + ((uint32_t)(32 * q) << 16) + (it & 1) * kPairCol1;
+            const int n = t.row0 + rank * kMmRows + 32 * q + lane;
+            // The shared columns are the last blocks of the first accumulator
+            // and the first of the second: from there on, away from them.
+            const int first = it & 1 ? 0 : blocks - 1, dir = it & 1 ? 1 : -1;
+            const int gate = shared ? shared : blocks;  // blocks to read before the next tile may be written
+            bool freed = false;
+            for (int b = 0; b < blocks; ++b) {
+                if (b >= gate && !freed) {
+                    mm_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
+                    freed = true;
+                }
+                const int blk = first + dir * b;
+                if ((blk & 1) != half) continue;
+                float v[32];
+                mm_ld32(col0 + 32 * blk, v);
+                const int tok = t.tok0 + 32 * blk, count = min(32, T - tok);
+                if (n < N && count > 0) {
+                    const size_t at = (size_t)tok * N + n;
+                    if (type == MxType::kF32)
+                        store_column(static_cast<float *>(y) + at, N, count, v);
+                    else if (type == MxType::kF16)
+                        store_column(static_cast<__half *>(y) + at, N, count, v);
+                    else
+                        store_column(static_cast<__nv_bfloat16 *>(y) + at, N, count, v);
+                }
+                __syncwarp();
+            }
+            if (!freed) {
+                mm_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
+            }
+        }
+    }
+    mm_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the other may signal it
+    if (warp == 1) {
+        mm_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 mm_encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -401,10 +841,43 @@ cudaError_t launch_split(const LaunchCtx &c, MxType type, const MxMatmulArgs &a)
 }
 
 template <bool kX8>
+cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
+    using L = PairLayout<kX8>;
+    const int Kp = mx_padded(a.K);
+    const MxPairTiles g = mx_pair_tiles(a.T, a.N);
+    alignas(64) CUtensorMap tm_w, tm_x;
+    if (!map_codes(&tm_w, a.w_codes, a.N, Kp, 4, kX8, kMmRows) ||
+        !map_codes(&tm_x, a.x_codes, a.T, Kp, a.x_bits, false, g.tile_tok / 2))
+        return cudaErrorInvalidValue;
+    auto kernel = mx_mm_pair_kernel<kX8>;
+    cudaError_t e = ensure_smem(kernel, L::total);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)g.row_tiles * g.tok_tiles;
+    const int pairs = (int)(tiles < c.num_sms / 2 ? tiles : c.num_sms / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = L::total;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tm_w, tm_x, a.w_scales, a.x_scales, a.y, type, a.K, a.N, a.T, g.tile_tok,
+                              g.x_tiles, g.row_tiles, g.tok_tiles, c.status, c.wait_limit, c.withhold);
+}
+
+template <bool kX8>
 cudaError_t launch_mm_tokens(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
     if (a.T <= 16) return launch_split<kX8, 16>(c, type, a);
     if (a.T <= 64) return launch_split<kX8, 64>(c, type, a);
-    return launch_split<kX8, 128>(c, type, a);
+    if (!mx_use_pairs(a.T, a.N, c.num_sms)) return launch_split<kX8, 128>(c, type, a);
+    return launch_pair<kX8>(c, type, a);
 }
 
 }  // namespace

@@ -355,6 +355,36 @@ def test_matmul(T, K, N, bits):
     assert _guards_ok(buf, T * N, -5.0)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("T,K,N", [
+    # Enough tiles of 256 rows for CTA pairs; the tokens split into tiles of
+    (150, 384, 10000),     # 160
+    (200, 128, 10100),     # 224, in one tile
+    (300, 1000, 5000),     # 160, from an offset of 32 in a scale tile on
+    (380, 256, 4999),      # 192
+    (420, 2048, 4900),     # 224, over three scale tiles
+    (700, 640, 3400),      # 256
+    (1200, 300, 2050),     # 256, two rows in the last row tile
+    (2500, 640, 4200),     # 256, three tiles to a pair
+    (150, 256, 50000),     # 160, three tiles to a pair
+    (420, 4224, 16001),    # 224, two tiles to a pair, an odd number of scale tiles
+])
+def test_matmul_on_cta_pairs(T, K, N, bits):
+    q, torch = _q(), _torch()
+    g = _rng(T, K, N, bits, 2)
+    x, xv = _random_mx(g, T, K, bits)
+    w, wv = _random_mx(g, N, K, 4)
+    buf, out = _guarded(T * N, torch.float32, -5.0)
+    out.fill_(float("nan"))
+    y = q.mx_matmul(x, w, out=out.view(T, N))
+    torch.cuda.synchronize()
+    q.device_status()
+    _assert_product(y, xv, wv, "float32")
+    assert _guards_ok(buf, T * N, -5.0)
+    for name in ("float16", "bfloat16"):
+        assert torch.equal(q.mx_matmul(x, w, dtype=_dtype(name)), y.to(_dtype(name)))
+
+
 @pytest.mark.parametrize("name", ["float16", "bfloat16"])
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("T,K,N", [(1, 512, 300), (5, 1000, 129), (40, 256, 255), (130, 384, 131), (300, 640, 260)])
@@ -414,7 +444,7 @@ def test_matmul_nan_scale_stays_in_its_row(T, bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("T,K,N", [(1, 4096, 520), (40, 2048, 300), (600, 1024, 700)])
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 520), (40, 2048, 300), (600, 1024, 700), (1500, 1024, 5000)])
 def test_matmul_gives_the_same_bits_again(T, K, N, bits):
     q, torch = _q(), _torch()
     g = _rng(24, T)
@@ -536,7 +566,8 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("bits", [4, 8])
-@pytest.mark.parametrize("T,K,N", [(1, 4096, 512), (24, 4096, 300), (100, 4096, 300), (300, 4096, 300)])
+@pytest.mark.parametrize("T,K,N", [(1, 4096, 512), (24, 4096, 300), (100, 4096, 300), (300, 4096, 300),
+                                   (200, 4096, 10000)])
 def test_wait_runs_out_then_next_call_is_right(T, K, N, bits):
     # One stage of weights never arrives and waits last a millisecond: the
     # kernel reports it and leaves the context usable.
