@@ -22,6 +22,13 @@ constexpr int kMxTileBytes = 512;   // bytes of a scale tile (128 rows x 4 block
 
 __host__ __device__ constexpr int mx_padded(int K) { return (K + kMxPadK - 1) / kMxPadK * kMxPadK; }
 
+// The largest of three magnitudes; a NaN stays one.
+__device__ __forceinline__ float mx_max3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Scale byte of a block whose largest magnitude has the float bits
 // `amax_bits`: biased exponent of 2^(floor(log2 amax) - emax).  The float's
 // own exponent field is floor(log2 amax) + 127 for a normal amax and 0 below,
@@ -67,18 +74,22 @@ __device__ __forceinline__ uint32_t mx_e4m3x4(float v0, float v1, float v2, floa
     return r;
 }
 
-// Two codes back to values (exact in fp16, hence in fp32).
-__device__ __forceinline__ float2 mx_from_e2m1x2(uint32_t byte) {
+// Two codes back to values (exact in fp16, hence in fp32): byte k of four
+// E2M1 pairs, or half k of two E4M3 pairs.
+template <int k>
+__device__ __forceinline__ float2 mx_from_e2m1x2(uint32_t bytes) {
     uint32_t h;
-    asm("{\n\t.reg .b8 a, b;\n\t.reg .b16 w;\n\tcvt.u16.u32 w, %1;\n\tmov.b16 {a, b}, w;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
         : "=r"(h)
-        : "r"(byte));
+        : "r"(bytes), "n"(k));
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
-__device__ __forceinline__ float2 mx_from_e4m3x2(uint32_t two_bytes) {
+template <int k>
+__device__ __forceinline__ float2 mx_from_e4m3x2(uint32_t bytes) {
     uint32_t h;
-    asm("{\n\t.reg .b16 w;\n\tcvt.u16.u32 w, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, w;\n\t}" : "=r"(h) : "r"(two_bytes));
+    asm("{\n\t.reg .b16 b0, b1;\n\tmov.b32 {b0, b1}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b%2;\n\t}"
+        : "=r"(h)
+        : "r"(bytes), "n"(k));
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
@@ -94,5 +105,19 @@ template <>
 __device__ __forceinline__ __half mx_from_float<__half>(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 mx_from_float<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two values rounded to a 16-bit type, the lower in the low half.
+template <class T>
+__device__ __forceinline__ uint32_t mx_pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t mx_pack2<__half>(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t mx_pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
 
 }  // namespace q4mm

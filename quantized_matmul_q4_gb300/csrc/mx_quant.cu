@@ -12,12 +12,17 @@
 // rounding of its conversion.  h is rounded once to its type; the norm takes
 // the unrounded sum.
 //
-// All are bound by HBM: 2 to 8 bytes read and 0.5 to 1 written per value
-// against some 20 instructions.  A lane takes 8 consecutive values (one
-// 16-byte load of 16-bit values, one 32-byte load of fp32), a block is 4
-// lanes, so the block's maximum is two shuffles and the codes of a warp's 256
-// values are one contiguous store.
+// All move 2 to 12 bytes per value and are meant to be bound by HBM.  A lane
+// takes 8 consecutive values (16 bytes of a 16-bit type, 32 of fp32), a block
+// is 4 lanes, so the block's maximum is two shuffles and the codes of a warp's
+// 256 values are one contiguous store.  What else runs per value decides
+// whether 16-bit inputs keep up with HBM (152 SMs issue some 75 lane
+// instructions per value at 2 bytes per value), hence the packed arithmetic:
+// magnitudes of 16-bit inputs are compared two at a time, products and
+// conversions run on pairs, no index is divided, and the scale bytes of four
+// rows change places by three shuffles instead of eight.
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -29,30 +34,74 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-// Eight consecutive values of a row, zeros past K.  kVec: 16-byte aligned
-// rows and K a multiple of 8, so the eight are all inside or all outside.
+// Eight consecutive values of a row as they lie in memory, zeros past K.
+// kVec: 16-byte aligned rows and K a multiple of 8, so the eight are all
+// inside or all outside.
+template <class T>
+struct Raw8 {
+    uint32_t w[4];  // pairs, the lower value in the low half
+};
+template <>
+struct Raw8<float> {
+    float v[8];
+};
+
 template <bool kVec, class T>
-__device__ __forceinline__ void load8(const T *row, int col, int K, float (&v)[8]) {
-    if constexpr (kVec) {
-        if (col < K) {
-            if constexpr (sizeof(T) == 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(row + col);
-                const float4 b = *reinterpret_cast<const float4 *>(row + col + 4);
-                v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-            } else {
-                const uint4 a = *reinterpret_cast<const uint4 *>(row + col);
-                const T *e = reinterpret_cast<const T *>(&a);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = mx_float(e[i]);
+__device__ __forceinline__ void load8(const T *row, int col, int K, Raw8<T> &r) {
+    if constexpr (sizeof(T) == 4) {
+        if (kVec) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            if (col < K) {
+                a = *reinterpret_cast<const float4 *>(row + col);
+                b = *reinterpret_cast<const float4 *>(row + col + 4);
             }
+            r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
+            r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            for (int i = 0; i < 8; ++i) r.v[i] = col + i < K ? row[col + i] : 0.f;
         }
     } else {
+        if (kVec) {
+            uint4 a = make_uint4(0u, 0u, 0u, 0u);
+            if (col < K) a = *reinterpret_cast<const uint4 *>(row + col);
+            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+        } else {
+            const unsigned short *p = reinterpret_cast<const unsigned short *>(row);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = col + i < K ? mx_float(row[col + i]) : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = col + 2 * i < K ? p[col + 2 * i] : 0u;
+                const uint32_t hi = col + 2 * i + 1 < K ? p[col + 2 * i + 1] : 0u;
+                r.w[i] = lo | hi << 16;
+            }
+        }
     }
+}
+
+__device__ __forceinline__ void to_float(const Raw8<float> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = r.v[i];
+}
+__device__ __forceinline__ void to_float(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(r.w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void to_float(const Raw8<__half> &r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+template <bool kVec, class T>
+__device__ __forceinline__ void load8(const T *row, int col, int K, float (&v)[8]) {
+    Raw8<T> r;
+    load8<kVec>(row, col, K, r);
+    to_float(r, v);
 }
 
 template <bool kVec, class T>
@@ -63,11 +112,10 @@ __device__ __forceinline__ void store8(T *row, int col, int K, const float (&v)[
                 *reinterpret_cast<float4 *>(row + col) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4 *>(row + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
             } else {
-                uint4 a;
-                T *e = reinterpret_cast<T *>(&a);
+                uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = mx_from_float<T>(v[i]);
-                *reinterpret_cast<uint4 *>(row + col) = a;
+                for (int i = 0; i < 4; ++i) w[i] = mx_pack2<T>(v[2 * i], v[2 * i + 1]);
+                *reinterpret_cast<uint4 *>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
     } else {
@@ -77,94 +125,137 @@ __device__ __forceinline__ void store8(T *row, int col, int K, const float (&v)[
     }
 }
 
-// Quantises a warp's 256 values (8 per lane from column col = c0 + 8·lane on;
-// col may lie past Kp, where nothing is stored), stores the codes of the row
-// and returns, in every lane, the scale word of its half: the four scale
-// bytes of columns c0 + 128·(lane / 16) onwards.
-__device__ __forceinline__ uint32_t quantize_warp(const float (&v)[8], int bits, uint8_t *codes_row, int col, int Kp) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    m = max(m, __shfl_xor_sync(kFull, m, 1));
-    m = max(m, __shfl_xor_sync(kFull, m, 2));
-    const uint32_t b = mx_scale_byte(m, bits == 4 ? 2 : 8);
-    const float inv = mx_inverse(b);
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = b == 255 ? 0.f : v[i] * inv;  // the codes under a NaN scale are zeros
-    if (col < Kp) {
-        if (bits == 4) {
-            *reinterpret_cast<uint32_t *>(codes_row + (col >> 1)) = mx_e2m1x8(s);
-        } else {
-            *reinterpret_cast<uint2 *>(codes_row + col) =
-                make_uint2(mx_e4m3x4(s[0], s[1], s[2], s[3]), mx_e4m3x4(s[4], s[5], s[6], s[7]));
-        }
-    }
-    const int lane = threadIdx.x & 31;
-    uint32_t w = b << (8 * ((lane >> 2) & 3));
-    w |= __shfl_xor_sync(kFull, w, 4);
-    w |= __shfl_xor_sync(kFull, w, 8);
-    return w;
+// Float bits of the largest magnitude of eight values, and of the 32 of a
+// block over its four lanes; NaN where one of them is.
+__device__ __forceinline__ uint32_t block_amax(const float (&v)[8]) {
+    const float a = mx_max3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2]));
+    const float b = mx_max3(fabsf(v[3]), fabsf(v[4]), fabsf(v[5]));
+    float m = mx_max3(a, b, fabsf(v[6]));
+    m = mx_max3(m, fabsf(v[7]), __shfl_xor_sync(kFull, mx_max3(m, fabsf(v[7]), m), 1));
+    return __float_as_uint(mx_max3(m, __shfl_xor_sync(kFull, m, 2), m));
 }
 
-// x / (1 + e^-x), by the quotient's definition; e^-x overflows to infinity
-// for x below about -88, where the quotient is -0.
-__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+template <class T>
+__device__ __forceinline__ uint32_t block_amax(const Raw8<T> &r, const float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        return block_amax(v);
+    } else {
+        // Two at a time: 16-bit magnitudes as packed numbers of their type.
+        using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+        auto mag = [&](int i) {
+            const uint32_t w = r.w[i] & 0x7FFF7FFFu;
+            return *reinterpret_cast<const T2 *>(&w);
+        };
+        T2 m = __hmax2_nan(__hmax2_nan(mag(0), mag(1)), __hmax2_nan(mag(2), mag(3)));
+        m = __hmax2_nan(m, __shfl_xor_sync(kFull, m, 1));
+        m = __hmax2_nan(m, __shfl_xor_sync(kFull, m, 2));
+        return __float_as_uint(mx_float(__hmax_nan(m.x, m.y)));
+    }
+}
+__device__ __forceinline__ uint32_t block_amax(const Raw8<float> &, const float (&v)[8]) { return block_amax(v); }
 
-// One warp per item: 256 columns of the four rows r, r + 32, r + 64, r + 96
-// of a 128-row block, whose scale words are 16 contiguous bytes of a tile
-// (four rows also keep four independent loads in flight per lane).  Rows past
-// the last one get zero scale bytes and no codes.
+// Quantises the block of `amax` (float bits) that this lane's eight values
+// belong to, stores their codes (nothing where col >= Kp) and returns the
+// block's scale byte.
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t amax, int bits, uint8_t *codes_row, int col,
+                                              int Kp) {
+    const uint32_t b = mx_scale_byte(amax, bits == 4 ? 2 : 8);
+    const float2 inv = make_float2(mx_inverse(b), mx_inverse(b));
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), inv);
+        s[2 * i] = f.x, s[2 * i + 1] = f.y;
+    }
+    if (col < Kp) {
+        // The codes under a NaN scale are zeros.
+        if (bits == 4) {
+            *reinterpret_cast<uint32_t *>(codes_row + (col >> 1)) = b == 255 ? 0u : mx_e2m1x8(s);
+        } else {
+            const uint32_t lo = mx_e4m3x4(s[0], s[1], s[2], s[3]), hi = mx_e4m3x4(s[4], s[5], s[6], s[7]);
+            *reinterpret_cast<uint2 *>(codes_row + col) = make_uint2(b == 255 ? 0u : lo, b == 255 ? 0u : hi);
+        }
+    }
+    return b;
+}
+
+// The exchange of scale bytes.  Four lanes hold a block; the four such groups
+// g = lane / 4 % 4 of a half warp hold, in byte i of `p`, the scale of their
+// block of row (or column chunk) i.  Afterwards group g holds row g's word:
+// the bytes of its four blocks in order.  p of group g ^ k comes by shuffle k;
+// byte g of it goes to byte g ^ k of the word.
+struct ByteExchange {
+    uint32_t s01, s23, s;
+    __device__ __forceinline__ explicit ByteExchange(int lane) {
+        const uint32_t g = (lane >> 2) & 3;
+        s01 = g << (4 * g) | (4 + g) << (4 * (g ^ 1));
+        s23 = g << (4 * (g ^ 2)) | (4 + g) << (4 * (g ^ 3));
+        s = g & 2 ? 0x3254u : 0x7610u;  // bytes g and g ^ 1 from the first pair
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t p) const {
+        const uint32_t a = __byte_perm(p, __shfl_xor_sync(kFull, p, 4), s01);
+        const uint32_t b = __byte_perm(__shfl_xor_sync(kFull, p, 8), __shfl_xor_sync(kFull, p, 12), s23);
+        return __byte_perm(a, b, s);
+    }
+};
+
+// x / (1 + e^-x).  The quotient is the approximate one (2 ulp); e^-x
+// overflows to infinity for x below about -88, where it gives -0.
+__device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + expf(-x)); }
+
+// One warp per 256 columns of the four rows r, r + 32, r + 64, r + 96 of a
+// 128-row block, whose scale words are 16 contiguous bytes of a tile (four
+// rows also keep four independent loads in flight per lane).  Rows past the
+// last one get zero scale bytes and no codes.  blockIdx.x: 32 row groups per
+// 128-row block; blockIdx.y and the warp: the column chunk.
 template <class T, bool kVec, bool kSwiGLU>
 __global__ void __launch_bounds__(256)
     mx_quantize_kernel(const T *__restrict__ x, long long x_stride, const T *__restrict__ up, long long up_stride,
-                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int K, int rows, int bits,
-                       long long items) {
-    const int Kp = mx_padded(K), nkt = Kp / kMxPadK, chunks = (Kp + 255) / 256;
-    const long long item = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    pdl_wait();
-    if (item >= items) return;
+                       uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int K, int rows, int bits) {
+    const int Kp = mx_padded(K), nkt = Kp / kMxPadK;
     const int lane = threadIdx.x & 31;
-    const int c = (int)(item % chunks);
-    const long long rr = item / chunks;  // 32 row groups per 128-row block
-    const int r = (int)(rr & 31);
-    const long long block = rr >> 5;
+    const int c = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int r = blockIdx.x & 31;
+    const unsigned block = blockIdx.x >> 5;
     const int col = 256 * c + 8 * lane;
     const size_t code_row = (size_t)Kp * bits / 8;
-    float v[4][8];
+    const long long row0 = (long long)block * kMxTileRows + r;
+    pdl_wait();
+    if (2 * c >= nkt) return;
+    Raw8<T> raw[4];
+    const T *px = x + row0 * x_stride;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long row = block * kMxTileRows + r + 32 * i;
-        if (row < rows) {
-            load8<kVec>(x + row * x_stride, col, K, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
-    }
+    for (int i = 0; i < 4; ++i) load8<kVec>(px + 32 * i * x_stride, col, row0 + 32 * i < rows ? K : 0, raw[i]);
+    uint32_t p = 0;
+    uint8_t *pc = codes + row0 * code_row;
     if constexpr (kSwiGLU) {
+        Raw8<T> rup[4];
+        const T *pu = up + row0 * up_stride;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load8<kVec>(pu + 32 * i * up_stride, col, row0 + 32 * i < rows ? K : 0, rup[i]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const long long row = block * kMxTileRows + r + 32 * i;
-            if (row < rows) {
-                float u[8];
-                load8<kVec>(up + row * up_stride, col, K, u);
+            float v[8], u[8];
+            to_float(raw[i], v);
+            to_float(rup[i], u);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = silu(v[i][j]) * u[j];
-            }
+            for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
+            p |= quantize8(v, block_amax(v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+                 << (8 * i);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v[8];
+            to_float(raw[i], v);
+            p |= quantize8(v, block_amax(raw[i], v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+                 << (8 * i);
         }
     }
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const long long row = block * kMxTileRows + r + 32 * i;
-        // (A row past the end passes Kp = 0: its zero block stores nothing.)
-        w[i] = quantize_warp(v[i], bits, codes + (row < rows ? row : 0) * code_row, col, row < rows ? Kp : 0);
-    }
+    const uint32_t w = ByteExchange(lane)(p);
     const int kt = 2 * c + (lane >> 4);
-    if ((lane & 15) == 0 && kt < nkt)
-        *reinterpret_cast<uint4 *>(scales + ((size_t)block * nkt + kt) * kMxTileBytes + 16 * r) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+    if ((lane & 3) == 0 && kt < nkt)
+        *reinterpret_cast<uint32_t *>(scales + ((size_t)block * nkt + kt) * kMxTileBytes + 16 * r + (lane & 12)) = w;
 }
 
 struct RmsArgs {
@@ -180,7 +271,9 @@ struct RmsArgs {
 // One CTA per row.  A thread keeps its kVals groups of 8 values of h in
 // registers between the sum of squares and the quantisation, so x and the
 // residual are read once; kVals = 0 (rows too long for that) reads and adds
-// them again, from L2.
+// them again, from L2.  More values per thread cost a single row some latency
+// and spread the fixed work (the reduction, indexes, scale words) of many
+// rows over more values.
 template <class T, bool kVec, int kVals>
 __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     __shared__ float partial[32];
@@ -192,33 +285,48 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     const T *res = a.residual ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
     T *h = a.h ? static_cast<T *>(a.h) + row * a.h_stride : nullptr;
     pdl_wait();
-    auto load_h = [&](int col, float (&v)[8]) {
-        load8<kVec>(x, col, K, v);
-        if (res) {
-            float r[8];
-            load8<kVec>(res, col, K, r);
+    constexpr int kKept = kVals > 0 ? kVals : 1;
+    // Groups are loaded four at a time at most, x and residual together.
+    auto load_h = [&](int c0, float (&v)[kKept][8]) {
+        Raw8<T> rx[kKept], rr[kKept];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += r[j];
+        for (int i = 0; i < kKept; ++i) load8<kVec>(x, c0 + i * step + 8 * threadIdx.x, K, rx[i]);
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < kKept; ++i) load8<kVec>(res, c0 + i * step + 8 * threadIdx.x, K, rr[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) {
+            to_float(rx[i], v[i]);
+            if (res) {
+                float u[8];
+                to_float(rr[i], u);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+            }
         }
     };
-    constexpr int kKept = kVals > 0 ? kVals : 1;
     float v[kKept][8];
-    float sum = 0.f;
+    float2 sums = make_float2(0.f, 0.f);
+    auto add_squares = [&]() {
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 f = make_float2(v[i][j], v[i][j + 1]);
+                sums = ffma2(f, f, sums);
+            }
+    };
     if constexpr (kVals > 0) {
-#pragma unroll
-        for (int i = 0; i < kVals; ++i) load_h(i * step + 8 * threadIdx.x, v[i]);
-#pragma unroll
-        for (int i = 0; i < kVals; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(v[i][j], v[i][j], sum);
+        load_h(0, v);
+        add_squares();
     } else {
         for (int c0 = 0; c0 < K; c0 += step) {
-            load_h(c0 + 8 * threadIdx.x, v[0]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmaf(v[0][j], v[0][j], sum);
+            load_h(c0, v);
+            add_squares();
         }
     }
-    sum = warp_sum(sum);
+    float sum = warp_sum(sums.x + sums.y);
     if (lane == 0) partial[warp] = sum;
     __syncthreads();
     // Every warp adds the partial sums in the same order: one barrier, and
@@ -229,6 +337,7 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     // Byte 16·(r % 32) + 4·(r % 128 / 32) of the row's tiles.
     uint8_t *scale_row = a.scales + (size_t)(row / kMxTileRows) * nkt * kMxTileBytes + 16 * (row & 31) +
                          4 * ((row & 127) >> 5);
+    // Writes h, quantises a group of 8 values per thread, returns its scale byte.
     auto finish = [&](int c0, float (&u)[8]) {
         const int col = c0 + 8 * threadIdx.x;
         if (h) store8<kVec>(h, col, K, u);
@@ -238,20 +347,33 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
         } else {
             load8<kVec>(static_cast<const T *>(a.weight), col, K, g);
         }
+        // Past K the values are zeros and so is the weight; an infinite norm
+        // or a NaN must not reach the padding.
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = col + j < K ? u[j] * norm * g[j] : 0.f;
-        const uint32_t w = quantize_warp(u, a.bits, codes_row, col, Kp);
-        const int kt = (c0 + 256 * warp) / kMxPadK + (lane >> 4);
-        if ((lane & 15) == 0 && kt < nkt) *reinterpret_cast<uint32_t *>(scale_row + (size_t)kt * kMxTileBytes) = w;
+        for (int j = 0; j < 8; ++j) u[j] = u[j] * norm * g[j];
+        if (kVec ? col >= K : col + 8 > K) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col + j >= K) u[j] = 0.f;
+        }
+        return quantize8(u, block_amax(u), a.bits, codes_row, col, Kp);
     };
+    const ByteExchange exchange(lane);
+    const int g4 = (lane >> 2) & 3;  // which group's word this lane writes
     if constexpr (kVals > 0) {
+        uint32_t p = 0;
 #pragma unroll
-        for (int i = 0; i < kVals; ++i)
-            if (i * step < Kp) finish(i * step, v[i]);
+        for (int i = 0; i < kVals; ++i) p |= finish(i * step, v[i]) << (8 * i);
+        const uint32_t w = exchange(p);
+        const int kt = (g4 * step + 256 * warp) / kMxPadK + (lane >> 4);
+        if ((lane & 3) == 0 && g4 < kVals && kt < nkt)
+            *reinterpret_cast<uint32_t *>(scale_row + (size_t)kt * kMxTileBytes) = w;
     } else {
         for (int c0 = 0; c0 < Kp; c0 += step) {
-            load_h(c0 + 8 * threadIdx.x, v[0]);
-            finish(c0, v[0]);
+            load_h(c0, v);
+            const uint32_t w = exchange(finish(c0, v[0]));
+            const int kt = (c0 + 256 * warp) / kMxPadK + (lane >> 4);
+            if ((lane & 15) == 0 && kt < nkt) *reinterpret_cast<uint32_t *>(scale_row + (size_t)kt * kMxTileBytes) = w;
         }
     }
     // Zero scale bytes for the rows past the last one: the CTAs of the last
@@ -268,41 +390,57 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     }
 }
 
-// Codes and scales back to values: a lane takes 8 values.
-template <class T, bool kVec>
+// Codes and scales back to values, with the quantising kernel's division of
+// the work: the scale words of a warp's four rows are one 16-byte load.
+template <class T, bool kVec, int kBits>
 __global__ void __launch_bounds__(256)
     mx_dequantize_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, T *__restrict__ y,
-                         long long y_stride, int K, int bits, long long items) {
-    const int Kp = mx_padded(K), nkt = Kp / kMxPadK, chunks = (Kp + 255) / 256;
-    const long long item = blockIdx.x * 8LL + (threadIdx.x >> 5);
+                         long long y_stride, int K, int rows) {
+    const int Kp = mx_padded(K), nkt = Kp / kMxPadK;
+    const int lane = threadIdx.x & 31;
+    const int c = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int r = blockIdx.x & 31;
+    const unsigned block = blockIdx.x >> 5;
+    const int col = 256 * c + 8 * lane, kt = 2 * c + (lane >> 4);
+    const long long row0 = (long long)block * kMxTileRows + r;
     pdl_wait();
-    if (item >= items) return;
-    const int c = (int)(item % chunks);
-    const long long row = item / chunks;
-    const int col = 256 * c + 8 * (threadIdx.x & 31);
-    if (col >= Kp) return;
-    const float s = mx_scale(scales[((size_t)(row / kMxTileRows) * nkt + col / kMxPadK) * kMxTileBytes +
-                                    16 * (row & 31) + 4 * ((row & 127) >> 5) + ((col >> 5) & 3)]);
-    float v[8];
-    const uint8_t *p = codes + (size_t)row * Kp * bits / 8;
-    if (bits == 4) {
-        const uint32_t q = *reinterpret_cast<const uint32_t *>(p + (col >> 1));
+    if (kt >= nkt || row0 >= rows) return;
+    const uint4 w = *reinterpret_cast<const uint4 *>(scales + ((size_t)block * nkt + kt) * kMxTileBytes + 16 * r);
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    const size_t code_row = (size_t)Kp * kBits / 8;
+    const uint8_t *p = codes + row0 * code_row + (size_t)col * kBits / 8;
+    uint2 q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = mx_from_e2m1x2((q >> (8 * i)) & 0xFFu);
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
-        }
-    } else {
-        const uint2 q = *reinterpret_cast<const uint2 *>(p + col);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = mx_from_e4m3x2(((i < 2 ? q.x : q.y) >> (16 * (i & 1))) & 0xFFFFu);
-            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    for (int i = 0; i < 4; ++i) {
+        q[i] = make_uint2(0u, 0u);
+        if (row0 + 32 * i < rows) {
+            if (kBits == 4)
+                q[i].x = *reinterpret_cast<const uint32_t *>(p + 32 * i * code_row);
+            else
+                q[i] = *reinterpret_cast<const uint2 *>(p + 32 * i * code_row);
         }
     }
+    T *py = y + row0 * y_stride;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= s;
-    store8<kVec>(y + row * y_stride, col, K, v);
+    for (int i = 0; i < 4; ++i) {
+        if (row0 + 32 * i >= rows) break;
+        const float s = mx_scale((word[i] >> (8 * ((lane >> 2) & 3))) & 0xFFu);
+        float2 f[4];
+        if constexpr (kBits == 4) {
+            f[0] = mx_from_e2m1x2<0>(q[i].x), f[1] = mx_from_e2m1x2<1>(q[i].x);
+            f[2] = mx_from_e2m1x2<2>(q[i].x), f[3] = mx_from_e2m1x2<3>(q[i].x);
+        } else {
+            f[0] = mx_from_e4m3x2<0>(q[i].x), f[1] = mx_from_e4m3x2<1>(q[i].x);
+            f[2] = mx_from_e4m3x2<0>(q[i].y), f[3] = mx_from_e4m3x2<1>(q[i].y);
+        }
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 t = __fmul2_rn(f[j], make_float2(s, s));
+            v[2 * j] = t.x, v[2 * j + 1] = t.y;
+        }
+        store8<kVec>(py + 32 * i * y_stride, col, K, v);
+    }
 }
 
 bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -312,25 +450,25 @@ bool rows_aligned(const void *p, long long stride) {
     return aligned16(p) && (stride * (long long)sizeof(T)) % 16 == 0;
 }
 
-// Grids are one-dimensional with 8 warps per CTA: at most 2^31 - 1 CTAs.
-bool grid_of(long long items, unsigned *ctas) {
-    const long long n = (items + 7) / 8;
-    if (n > 0x7FFFFFFFLL) return false;
-    *ctas = (unsigned)n;
-    return true;
+// Warps of 256 columns by groups of four rows: up to 8 column chunks per CTA.
+struct RowGrid {
+    dim3 grid, block;
+};
+RowGrid row_grid(int K, int rows) {
+    const unsigned chunks = (unsigned)(mx_padded(K) + 255) / 256;
+    const unsigned warps = chunks < 8 ? chunks : 8;
+    const unsigned groups = (unsigned)(((long long)rows + kMxTileRows - 1) / kMxTileRows * 32);
+    return RowGrid{dim3(groups, (chunks + warps - 1) / warps), dim3(32 * warps)};
 }
 
 template <class T>
 cudaError_t quantize_t(const LaunchCtx &c, const MxQuantizeArgs &a) {
-    const int chunks = (mx_padded(a.K) + 255) / 256;
-    const long long items = ((long long)a.rows + kMxTileRows - 1) / kMxTileRows * 32 * chunks;
-    unsigned ctas;
-    if (!grid_of(items, &ctas)) return cudaErrorInvalidValue;
+    const RowGrid g = row_grid(a.K, a.rows);
     const bool vec = a.K % 8 == 0 && rows_aligned<T>(a.x, a.x_stride) && (!a.up || rows_aligned<T>(a.up, a.up_stride));
     auto kernel = a.up ? (vec ? mx_quantize_kernel<T, true, true> : mx_quantize_kernel<T, false, true>)
                        : (vec ? mx_quantize_kernel<T, true, false> : mx_quantize_kernel<T, false, false>);
-    return launch_kernel(c, kernel, dim3(ctas), dim3(256), 0, static_cast<const T *>(a.x), a.x_stride,
-                         static_cast<const T *>(a.up), a.up_stride, a.codes, a.scales, a.K, a.rows, a.bits, items);
+    return launch_kernel(c, kernel, g.grid, g.block, 0, static_cast<const T *>(a.x), a.x_stride,
+                         static_cast<const T *>(a.up), a.up_stride, a.codes, a.scales, a.K, a.rows, a.bits);
 }
 
 template <class T>
@@ -341,8 +479,10 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
     const RmsArgs k{a.x, a.residual, a.weight, a.h, a.x_stride, a.residual_stride, a.h_stride, a.codes, a.scales,
                     a.eps, a.K, a.rows, a.bits, a.weight_f32};
     const int Kp = mx_padded(a.K);
-    // Threads: 8 values each up to 8192 wide, then more values per thread.
+    // Values per thread: the fewest that 1024 threads allow while there are
+    // no more rows than SMs, else four groups where they leave four warps.
     int vals = 1;
+    if (a.rows > c.num_sms) vals = Kp >= 4096 ? 4 : Kp >= 2048 ? 2 : 1;
     while (vals < 4 && Kp > 8 * 1024 * vals) vals *= 2;
     const bool kept = Kp <= 8 * 1024 * vals;
     int threads = kept ? (Kp / 8 + vals - 1) / vals : 1024;
@@ -357,12 +497,12 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
 
 template <class T>
 cudaError_t dequantize_t(const LaunchCtx &c, const MxDequantizeArgs &a) {
-    const long long items = (long long)a.rows * ((mx_padded(a.K) + 255) / 256);
-    unsigned ctas;
-    if (!grid_of(items, &ctas)) return cudaErrorInvalidValue;
+    const RowGrid g = row_grid(a.K, a.rows);
     const bool vec = a.K % 8 == 0 && rows_aligned<T>(a.y, a.y_stride);
-    return launch_kernel(c, vec ? mx_dequantize_kernel<T, true> : mx_dequantize_kernel<T, false>, dim3(ctas),
-                         dim3(256), 0, a.codes, a.scales, static_cast<T *>(a.y), a.y_stride, a.K, a.bits, items);
+    auto kernel = a.bits == 4 ? (vec ? mx_dequantize_kernel<T, true, 4> : mx_dequantize_kernel<T, false, 4>)
+                              : (vec ? mx_dequantize_kernel<T, true, 8> : mx_dequantize_kernel<T, false, 8>);
+    return launch_kernel(c, kernel, g.grid, g.block, 0, a.codes, a.scales, static_cast<T *>(a.y), a.y_stride, a.K,
+                         a.rows);
 }
 
 }  // namespace
