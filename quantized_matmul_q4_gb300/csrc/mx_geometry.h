@@ -4,12 +4,23 @@
 
 namespace q4mm {
 
+#if defined(__CUDACC__)
+#define Q4MM_HD __host__ __device__
+#else
+#define Q4MM_HD
+#endif
+
+// A split tile's 128 rows are shared out in fours: rank s of S adds up the
+// rows from first_row(s) to first_row(s + 1).
+constexpr int kMxMaxSplit = 8;  // a portable cluster
+Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
+
 // CTAs that share a tile's K: as many as fill the SMs with two CTAs each, at
-// most 8 (a portable cluster) and two stages of K to each.
+// most 8 and two stages of K to each.
 inline int mx_split(int row_tiles, int tok_tiles, int stages, int num_sms) {
     const long long tiles = (long long)row_tiles * tok_tiles;
     int S = 1;
-    while (S < 8 && tiles * (S + 1) <= 2LL * num_sms && 2 * (S + 1) <= stages) ++S;
+    while (S < kMxMaxSplit && tiles * (S + 1) <= 2LL * num_sms && 2 * (S + 1) <= stages) ++S;
     return S;
 }
 

@@ -136,31 +136,42 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// Four consecutive n of one token, as the type asks; the aligned case is one
-// store.
-__device__ __forceinline__ void store_y4(void *y, MxType type, size_t at, int left, float4 v) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Up to four consecutive n of one token; one store where all four are there
+// and aligned.
+template <class T>
+__device__ __forceinline__ void store_y4(T *p, int left, float4 v) {
     const float e[4] = {v.x, v.y, v.z, v.w};
-    if (type == MxType::kF32) {
-        float *p = static_cast<float *>(y) + at;
-        if (left >= 4 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    if (left >= 4 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0) {
+        if constexpr (sizeof(T) == 4)
             *reinterpret_cast<float4 *>(p) = v;
-        } else {
-            for (int i = 0; i < 4 && i < left; ++i) p[i] = e[i];
-        }
-    } else if (type == MxType::kF16) {
-        __half *p = static_cast<__half *>(y) + at;
-        for (int i = 0; i < 4 && i < left; ++i) p[i] = __float2half_rn(e[i]);
+        else
+            *reinterpret_cast<uint2 *>(p) = make_uint2(mx_pack2<T>(v.x, v.y), mx_pack2<T>(v.z, v.w));
     } else {
-        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(y) + at;
-        for (int i = 0; i < 4 && i < left; ++i) p[i] = __float2bfloat16_rn(e[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) p[i] = mx_from_float<T>(e[i]);
     }
+}
+
+__device__ __forceinline__ void store_y(void *y, MxType type, size_t at, float v) {
+    if (type == MxType::kF32)
+        static_cast<float *>(y)[at] = v;
+    else if (type == MxType::kF16)
+        static_cast<__half *>(y)[at] = __float2half_rn(v);
+    else
+        static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
 }
 
 // Up to 128 tokens per tile, K split over the CTAs of a cluster: rank r of S
 // takes the stages [r·c/S, (r+1)·c/S) and puts its partial sums, [token][row],
-// into its shared memory; rank s then adds the S partial sums of rows
-// 4·(32·s/S) onwards in rank order, read over the cluster, and writes y, so
-// the result does not depend on scheduling.
+// into its shared memory, over the ring; rank s then adds the S partial sums
+// of rows 4·floor(32·s/S) onwards in rank order, read over the cluster eight
+// loads at a time, and writes y, so the result does not depend on scheduling.
+// (Pushed to their owner with st.async instead, the sums of 16 tokens of a
+// 4096 x 4096 product take 0.6 us longer, those of 128 tokens 11.)
 template <bool kX8, int kTok>
 __global__ void __launch_bounds__(kMmThreads, 2)
     mx_mm_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -183,19 +194,50 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     const int row_tile = blockIdx.x / S, row0 = row_tile * kMmRows, tok0 = blockIdx.y * kTok;
     const int all = (Kp + L::kStageK - 1) / L::kStageK;
     const int c_lo = (int)((long long)rank * all / S), chunks = (int)((long long)(rank + 1) * all / S) - c_lo;
+    const int toks = min(kTok, T - tok0);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+    // Four copies per stage, one per lane: a bulk copy holds the thread that
+    // issues it for some 475 cycles (measured), but lanes that issue by one
+    // instruction do so side by side.  Copy j of a stage: weights and tokens
+    // (tensor copies), their scales (plain ones).
+    auto issue = [&](int c, int j, bool here) {
+        const int s = c % L::kStages;
+        const int k0 = (c_lo + c) * L::kStageK, kt = (c_lo + c) * L::kScaleTiles;
+        const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
+        here = here && c != withhold;  // (test only: a stage that never arrives)
+        if (here && j == 0) mbar_arrive_expect_tx(&full[s], L::w_tx + n_mma * 128 + 2 * sbytes);
+        __syncwarp();
+        const int c0 = kX8 ? k0 : k0 / 2;  // 8-bit codes and unpacked 4-bit ones in values, else bytes
+        if (here && j < 2)
+            mm_tma_2d(sbase + s * L::stage + (j ? L::off_x : 0u), j ? &tm_x : &tm_w, c0, j ? tok0 : row0, &full[s]);
+        if (here && j >= 2)
+            bulk_g2s(smem + s * L::stage + (j == 3 ? L::off_sx : L::off_sw),
+                     (j == 3 ? x_scales + (size_t)(tok0 / kMxTileRows) * nkt * kMxTileBytes
+                             : w_scales + (size_t)row_tile * nkt * kMxTileBytes) + (size_t)kt * kMxTileBytes,
+                     sbytes, &full[s]);
+        __syncwarp();
+    };
+    const int lap = min(chunks, L::kStages);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int s = 0; s < L::kStages; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            mbar_init(done, 1);
+            abort_flag = 0;
+            fence_mbar_init();
+            prefetch_map(&tm_w);
+            prefetch_map(&tm_x);
         }
-        mbar_init(done, 1);
-        abort_flag = 0;
-        fence_mbar_init();
-        prefetch_map(&tm_w);
-        prefetch_map(&tm_x);
-    }
-    if (warp == 1) {
+        __syncwarp();
+        // Every operand may come from the previous kernel on the stream, the
+        // weights too (a quantisation is a kernel like any other): copies
+        // start after it.
+        pdl_wait();
+        issue(lane >> 2, lane & 3, (lane >> 2) < lap);
+    } else if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(L::kCols)
                      : "memory");
@@ -206,34 +248,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     mm_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
-    // Every operand may come from the previous kernel on the stream, the
-    // weights too (a quantisation is a kernel like any other).
-    pdl_wait();
 
     if (warp == 0) {
-        // Four copies per stage, one per lane: a bulk copy holds the thread
-        // that issues it for some 475 cycles (measured), but lanes that
-        // issue by one instruction do so side by side.  Copy j of a stage:
-        // weights and tokens (tensor copies), their scales (plain ones).
-        auto issue = [&](int c, int j, bool here) {
-            const int s = c % L::kStages;
-            const int k0 = (c_lo + c) * L::kStageK, kt = (c_lo + c) * L::kScaleTiles;
-            const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
-            here = here && c != withhold;  // (test only: a stage that never arrives)
-            if (here && j == 0) mbar_arrive_expect_tx(&full[s], L::w_tx + n_mma * 128 + 2 * sbytes);
-            __syncwarp();
-            const int c0 = kX8 ? k0 : k0 / 2;  // 8-bit codes and unpacked 4-bit ones in values, else bytes
-            if (here && j < 2)
-                mm_tma_2d(sbase + s * L::stage + (j ? L::off_x : 0u), j ? &tm_x : &tm_w, c0, j ? tok0 : row0, &full[s]);
-            if (here && j >= 2)
-                bulk_g2s(smem + s * L::stage + (j == 3 ? L::off_sx : L::off_sw),
-                         (j == 3 ? x_scales + (size_t)(tok0 / kMxTileRows) * nkt * kMxTileBytes
-                                 : w_scales + (size_t)row_tile * nkt * kMxTileBytes) + (size_t)kt * kMxTileBytes,
-                         sbytes, &full[s]);
-            __syncwarp();
-        };
-        const int lap = min(chunks, L::kStages);
-        issue(lane >> 2, lane & 3, (lane >> 2) < lap);
         int c = lap;
         for (; c < chunks; ++c) {
             const bool ok =
@@ -276,7 +292,7 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                     const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
                     if (j < kts)
                         mx_mma<kX8, 1>(tmem, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(n_mma, sf), tmem + L::kColSw + 4 * j,
-                                    tmem + L::kColSx + 4 * j, (c | m) != 0);
+                                       tmem + L::kColSx + 4 * j, (c | m) != 0);
                 }
                 mm_commit(&empty[s]);
             }
@@ -290,8 +306,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
     // warp; every warp takes part from here on.)
     const bool ok = __syncthreads_and(mbar_wait_bounded(done, 0, wait_limit) ? 1 : 0) != 0 && !abort_flag;
     mm_fence_after();
-    const int toks = min(kTok, T - tok0);
-    float *part = reinterpret_cast<float *>(smem);  // [token][128 rows], over the ring
+    pdl_wait();  // y may still be read by the previous kernel
+    float *part = reinterpret_cast<float *>(smem);  // [token][128 rows]
     if (warp >= 2) {
         const int q = warp & 3;  // tensor-memory lane quarter of this warp
         const int r = 32 * q + lane, n = row0 + r;
@@ -309,42 +325,45 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                     if (t + i < toks) part[(t + i) * kMmRows + r] = v[i];
             } else if (ok && n < N) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (t + i >= toks) break;
-                    const size_t at = (size_t)(tok0 + t + i) * N + n;
-                    if (type == MxType::kF32)
-                        static_cast<float *>(y)[at] = v[i];
-                    else if (type == MxType::kF16)
-                        static_cast<__half *>(y)[at] = __float2half_rn(v[i]);
-                    else
-                        static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v[i]);
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (t + i < toks) store_y(y, type, (size_t)(tok0 + t + i) * N + n, v[i]);
             }
             __syncwarp();
         }
         mm_fence_before();
     }
     if (S > 1) {
-        cluster_sync_all();
-        const int lo = 4 * (32 * rank / S), rows4 = (4 * (32 * (rank + 1) / S) - lo) / 4;
+        cluster_arrive();
+        cluster_wait();
+        const int lo = mx_first_row(rank, S), rows4 = (mx_first_row(rank + 1, S) - lo) / 4;
         for (int i = threadIdx.x; i < rows4 * toks; i += kMmThreads) {
             const int r = lo + 4 * (i % rows4), t = i / rows4;
             const uint32_t at = smem_addr(part + t * kMmRows + r);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int s = 0; s < S; ++s) {
-                const float4 v = ld_cluster_v4(map_to_rank(at, (uint32_t)s));
-                acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-            }
-            if (row0 + r < N) store_y4(y, type, (size_t)(tok0 + t) * N + row0 + r, N - row0 - r, acc);
+            float4 v[kMxMaxSplit];
+#pragma unroll
+            for (int s = 0; s < kMxMaxSplit; ++s)
+                if (s < S) v[s] = ld_cluster_v4(map_to_rank(at, (uint32_t)s));
+            float4 acc = v[0];
+#pragma unroll
+            for (int s = 1; s < kMxMaxSplit; ++s)
+                if (s < S) acc.x += v[s].x, acc.y += v[s].y, acc.z += v[s].z, acc.w += v[s].w;
+            const size_t to = (size_t)(tok0 + t) * N + row0 + r;
+            if (type == MxType::kF32)
+                store_y4(static_cast<float *>(y) + to, N - row0 - r, acc);
+            else if (type == MxType::kF16)
+                store_y4(static_cast<__half *>(y) + to, N - row0 - r, acc);
+            else
+                store_y4(static_cast<__nv_bfloat16 *>(y) + to, N - row0 - r, acc);
         }
-        cluster_sync_all();  // no CTA leaves while another reads its sums
-    } else {
-        __syncthreads();
+        __syncwarp();
+        cluster_arrive();  // this CTA has read its peers' sums
     }
+    __syncthreads();
     if (warp == 1) {
         mm_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
     }
+    if (S > 1) cluster_wait();  // no CTA leaves while another reads its sums
 }
 
 // ---------------------------------------------------------------------------

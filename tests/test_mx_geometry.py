@@ -1,0 +1,50 @@
+"""Launch geometry of the MX products (csrc/mx_geometry.h, the header the
+library compiles): shares of a split tile and the tiles of the CTA-pair
+kernel, over every split and every token count that matters."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def geo(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("mx_geo") / "libmx_geo.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC",
+                    f"-I{os.path.join(ROOT, 'quantized_matmul_q4_gb300', 'csrc')}",
+                    os.path.join(ROOT, "tests", "mx_geometry_shim.cpp"), "-o", out], check=True)
+    return ctypes.CDLL(out)
+
+
+def test_rows_of_a_split_tile(geo):
+    for S in range(1, 9):
+        first = [geo.mx_geo_first_row(s, S) for s in range(S + 1)]
+        assert first[0] == 0 and first[S] == 128
+        assert all(b > a and (b - a) % 4 == 0 for a, b in zip(first, first[1:]))
+
+
+def test_split_gives_every_cta_work(geo):
+    for sms in (1, 132, 148, 152):
+        for tiles in (1, 2, 3, 32, 54, 86, 151, 152, 153, 400, 100000):
+            for stages in (1, 2, 3, 4, 5, 16, 17, 43, 86, 256, 512):
+                S = geo.mx_geo_split(tiles, 1, stages, sms)
+                assert 1 <= S <= 8 and S <= max(1, stages // 2)
+                assert S == 1 or tiles * S <= 2 * sms
+
+
+def test_pair_tiles(geo):
+    for T in list(range(1, 1200)) + [4095, 4096, 4097, 8191, 8192, 100000, 2 ** 31 - 1]:
+        out = (ctypes.c_int * 4)()
+        geo.mx_geo_pairs(T, 11008, out)
+        tok, tok_tiles, row_tiles, x_tiles = out
+        assert tok % 32 == 0 and 32 <= tok <= 256 and row_tiles == 43
+        assert (tok_tiles - 1) * tok < T <= tok_tiles * tok     # every tile has a token, every token a tile
+        starts = {(i * tok) % 128 for i in range(min(tok_tiles, 8))}
+        assert x_tiles == max((s + tok + 127) // 128 for s in starts) <= 3 or tok_tiles < 8
+        assert all((s + tok + 127) // 128 <= x_tiles <= 3 for s in starts)
+        # Blocks of 32 tokens that a tile's scales are shifted by: with a shift
+        # eight columns are taken from three scale tiles, twelve words.
+        assert all(s // 32 + tok // 32 <= 12 for s in starts)
