@@ -370,8 +370,8 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 // Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.
 // ---------------------------------------------------------------------------
 
-constexpr int kPairThreads = 480;  // operand copies, MMA issuer, 4 scale warps, 8 epilogue warps, scale copies
-constexpr int kPairEpiWarp = 6, kPairScaleProducer = 14;
+constexpr int kPairThreads = 608;  // operand copies, MMA issuer, 2 x 4 scale warps, 8 epilogue warps, scale copies
+constexpr int kPairEpiWarp = 10, kPairScaleProducer = 18;
 constexpr int kPairTok = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairXTiles = 3;     // 128-row scale tiles that the tokens of a tile touch at most
@@ -390,7 +390,7 @@ struct PairLayout {
     static constexpr int kScaleCols = kScaleTiles * 12;
     static constexpr int kScaleBufs = 96 / kScaleCols < kPairStages ? 96 / kScaleCols : kPairStages;
     static constexpr uint32_t off_bar = kPairStages * stage;
-    static constexpr int kBars = 3 * kPairStages + kScaleBufs + 5;
+    static constexpr int kBars = 3 * kPairStages + 5;
     static constexpr uint32_t total = off_bar + 8 * kBars + 16 + 1024;
     static_assert(total <= 232448, "shared memory");
     static_assert(kScaleBufs >= 3 && kScaleBufs <= kPairStages, "scale buffers");
@@ -421,24 +421,6 @@ __device__ __forceinline__ void pair_commit(uint64_t *bar) {
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Waits on a barrier that the other CTA of the pair arrives on.
-__device__ __forceinline__ bool mbar_spin_cluster(uint64_t *bar, uint32_t parity, long long limit_cycles,
-                                                  const volatile int *abort) {
-    const long long t0 = clock64();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (*abort || clock64() - t0 > limit_cycles) return false;
-    }
 }
 
 __device__ __forceinline__ void mm_ld32(uint32_t taddr, float (&v)[32]) {
@@ -509,9 +491,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint8_t *smem = mm_smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = smem_addr(smem);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::off_bar), *empty = full + kPairStages;
-    uint64_t *scales_in = empty + kPairStages;               // a stage's scale tiles have landed in this CTA
-    uint64_t *scales_up = scales_in + kPairStages;           // ... and lie in both CTAs' tensor memory
-    uint64_t *acc_full = scales_up + L::kScaleBufs, *acc_free = acc_full + 2;  // one of each per accumulator
+    uint64_t *scales_in = empty + kPairStages;  // a stage's scale tiles have landed in this CTA's shared memory
+    uint64_t *acc_full = scales_in + kPairStages, *acc_free = acc_full + 2;  // one of each per accumulator
     uint64_t *done = acc_free + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
 
@@ -526,11 +507,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 8);  // both CTAs' operands (bytes), 4 scale warps of each
             mbar_init(&empty[s], 1);
             mbar_init(&scales_in[s], 1);
         }
-        for (int b = 0; b < L::kScaleBufs; ++b) mbar_init(&scales_up[b], 8);  // 4 scale warps of both CTAs
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_free[b], 16);  // 8 epilogue warps of both CTAs
@@ -625,38 +605,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
+            // What this thread does between MMAs is time that the tensor pipe
+            // may run dry (it queues little more than one MMA): one barrier
+            // per stage, tested while the stage before is being issued.
             int s = 0, buf = 0, it = 0;
-            uint32_t ph = 0, bph = 0;
-            bool ok = true;
+            uint32_t ph = 0;
+            bool ok = true, ready = false;
+            const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + L::off_x);
             for (long long i = pair; i < tiles && ok; i += pairs, ++it) {
-                const PairTile t = pair_tile(i, row_tiles, tok_tiles, tile_tok);
                 const uint32_t d = tmem + (it & 1) * kPairCol1;
                 // The epilogue frees what this accumulator shares with the
                 // previous tile's first of all; without shared columns the
                 // one two tiles back has to be free.
                 const int before = it - (shared ? 1 : 2);
                 if (before >= 0)
-                    ok = mbar_spin_cluster(&acc_free[before & 1], (before >> 1) & 1, wait_limit, &abort_flag);
+                    ok = mbar_spin_abortable(&acc_free[before & 1], (before >> 1) & 1, wait_limit, &abort_flag);
                 for (int c = 0; c < chunks && ok; ++c) {
-                    ok = mbar_spin_cluster(&scales_up[buf], bph, wait_limit, &abort_flag) &&
-                         mbar_spin_abortable(&full[s], ph, wait_limit, &abort_flag);
+                    if (!ready) ok = mbar_spin_abortable(&full[s], ph, wait_limit, &abort_flag);
                     if (!ok) break;
                     mm_fence_after();
-                    const uint32_t sa = sbase + s * L::stage;
-                    const int kts = min(L::kScaleTiles, nkt - c * L::kScaleTiles);
+                    // (Descriptor addresses count 16 bytes and stay below 256 KB.)
+                    const uint64_t ad = ad0 + (uint32_t)s * (L::stage >> 4), bd = bd0 + (uint32_t)s * (L::stage >> 4);
                     const uint32_t sw = tmem + kPairColScales + buf * L::kScaleCols, sx = sw + 4 * L::kScaleTiles;
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + L::off_x);
+                    const bool second = L::kScaleTiles == 1 || c * L::kScaleTiles + 1 < nkt;
+                    uint64_t *mine = &empty[s];
+                    if (++s == kPairStages) s = 0, ph ^= 1u;
+                    if (++buf == L::kScaleBufs) buf = 0;
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
                         const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
-                        if (j < kts)
+                        if (m < 2 || second)
                             mx_mma<kX8, 2>(d, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows),
-                                           sw + 4 * j, sx + 8 * j,
-                                           (c | m) != 0);
+                                           sw + 4 * j, sx + 8 * j, (c | m) != 0);
+                        if (m == 2) ready = mbar_test_wait(&full[s], ph);
                     }
-                    pair_commit(&empty[s]);
-                    if (++s == kPairStages) s = 0, ph ^= 1u;
-                    if (++buf == L::kScaleBufs) buf = 0, bph ^= 1u;
+                    pair_commit(mine);
                 }
                 pair_commit(&acc_full[it & 1]);
             }
@@ -675,22 +658,25 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // columns.  (tcgen05.cp does the same in one instruction, but for a
         // CTA pair each takes about 128 cycles of the tensor pipe, measured,
         // six per stage against four MMAs of about 128.)
+        // Two groups of four take the stages in turn: an iteration lasts about
+        // as long as a stage's MMAs.
         const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairColScales;
-        const uint32_t up0 = map_to_rank(smem_addr(scales_up), 0);
-        int s = 0, buf = 0;
-        uint32_t ph = 0;
-        long long n = 0;
-        int rs = 0;          // the stage whose MMAs last read this buffer
-        uint32_t rph = 0;
+        const uint32_t full0 = map_to_rank(smem_addr(full), 0);
+        const int group = (warp - 2) >> 2;
+        int n = 0;
         bool ok = true;
         for (long long i = pair; i < tiles && ok; i += pairs) {
             // Blocks of 32 tokens before the tile's first in its scale tile.
             const int skip = pair_tile(i, row_tiles, tok_tiles, tile_tok).tok0 % kMxTileRows / 32;
             for (int c = 0; c < chunks; ++c, ++n) {
-                ok = mbar_wait_abortable(&scales_in[s], ph, wait_limit, &abort_flag);
+                if ((n & 1) != group) continue;
+                const int s = n % kPairStages, buf = n % L::kScaleBufs;
+                ok = mbar_spin_abortable(&scales_in[s], (n / kPairStages) & 1, wait_limit, &abort_flag);
                 if (n >= L::kScaleBufs) {
-                    ok = ok && mbar_wait_abortable(&empty[rs], rph, wait_limit, &abort_flag);
-                    if (++rs == kPairStages) rs = 0, rph ^= 1u;
+                    // The MMAs that last read this buffer.
+                    const int m = n - L::kScaleBufs;
+                    ok = ok && mbar_spin_abortable(&empty[m % kPairStages], (m / kPairStages) & 1, wait_limit,
+                                                   &abort_flag);
                 }
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) {
@@ -730,9 +716,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 mm_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(up0 + 8 * buf);
-                if (++s == kPairStages) s = 0, ph ^= 1u;
-                if (++buf == L::kScaleBufs) buf = 0;
+                if (lane == 0) mbar_arrive_cluster(full0 + 8 * s);
             }
         }
     } else {
