@@ -15,13 +15,46 @@ namespace q4mm {
 constexpr int kMxMaxSplit = 8;  // a portable cluster
 Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 
-// CTAs that share a tile's K: as many as fill the SMs with two CTAs each, at
-// most 8 and two stages of K to each.
-inline int mx_split(int row_tiles, int tok_tiles, int stages, int num_sms) {
-    const long long tiles = (long long)row_tiles * tok_tiles;
-    int S = 1;
-    while (S < kMxMaxSplit && tiles * (S + 1) <= 2LL * num_sms && 2 * (S + 1) <= stages) ++S;
-    return S;
+// Estimates, in microseconds of a call, of the two forms of the product; the
+// form and the split with the lower estimate run.  `stages` are ring stages
+// of K (256 values with 4-bit x, 128 with 8-bit).  The constants are fitted
+// to 185 pairs of measurements on GB300 (chains of calls in a CUDA graph, 17
+// to 2048 tokens, K and N of 256 to 16384), where the choice costs 0.5% on
+// the mean against always the faster form; some of them, single CTAs with K
+// split / CTA pairs:
+//   T    K        N       x     measured       estimated
+//   17   256   -> 4096    4     2.5 /  3.3      2.7 /  3.3
+//   64   4096  -> 4096    8     7.1 / 11.8      7.1 / 11.8
+//   64   2560  -> 6912    4     7.0 /  6.1      6.7 /  6.0
+//   128  1024  -> 4096    8     8.2 /  5.9      6.5 /  5.8
+//   128  4096  -> 4096    4     7.9 /  8.3      7.8 /  8.4
+//   128  4096  -> 11008   8    13.0 / 12.9     12.8 / 12.6
+//   256  8192  -> 8192    4    16.5 / 14.9     16.9 / 15.3
+//   384  4096  -> 11008   8    19.6 / 23.6     16.3 / 22.7
+//   512  11008 -> 4096    8    25.1 / 28.4     24.6 / 30.6
+//   512  4096  -> 11008   8    34.8 / 24.9     30.7 / 23.9
+//   1024 11008 -> 4096    8    38.6 / 29.9     36.3 / 30.6
+
+// Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
+// tile's K: rounds of two CTAs per SM through their stages, then the stores
+// of y or, before them, the sum of the partial sums over the cluster.
+inline double mx_split_us(int row_tiles, int tok_tiles, int tokens, int stages, int S, int x_bits, int num_sms) {
+    const long long ctas = (long long)row_tiles * tok_tiles * S, slots = 2LL * num_sms;
+    const double tok = tokens < 128 ? tokens / 128.0 : 1.0;
+    const double stage = x_bits == 8 ? 0.29 + 0.08 * tok : 0.37 + 0.14 * tok;
+    const double end = S == 1 ? 2.5 * tok : 1.2 + (ctas <= num_sms ? 2.6 : 5.5) * tok;
+    return 2.0 + (double)((ctas + slots - 1) / slots) * (((stages + S - 1) / S) * stage + end);
+}
+
+// The split with the lowest estimate: at most 8 CTAs, two stages to each.
+inline int mx_split(int row_tiles, int tok_tiles, int tokens, int stages, int x_bits, int num_sms) {
+    int best = 1;
+    double us = mx_split_us(row_tiles, tok_tiles, tokens, stages, 1, x_bits, num_sms);
+    for (int S = 2; S <= kMxMaxSplit && 2 * S <= stages; ++S) {
+        const double t = mx_split_us(row_tiles, tok_tiles, tokens, stages, S, x_bits, num_sms);
+        if (t < us) us = t, best = S;
+    }
+    return best;
 }
 
 // Tiles of the CTA-pair kernel: 256 weight rows by tile_tok tokens, a multiple
@@ -46,10 +79,23 @@ inline MxPairTiles mx_pair_tiles(int T, int N) {
     return g;
 }
 
-// Pairs or single CTAs with K split?
-inline bool mx_use_pairs(int T, int N, int num_sms) {
-    const MxPairTiles g = mx_pair_tiles(T, N);
-    return T > 128 && 2LL * g.row_tiles * g.tok_tiles >= num_sms / 2;
+// CTA pairs, tiles of 256 rows x tile_tok tokens, one pair per two SMs.
+inline double mx_pair_us(const MxPairTiles &g, int stages, int x_bits, int num_sms) {
+    const long long tiles = (long long)g.row_tiles * g.tok_tiles, pairs = num_sms / 2;
+    const double n = g.tile_tok / 256.0;
+    const double stage = x_bits == 8 ? 0.255 + 0.05 * n : 0.26 + 0.08 * n;
+    return 2.8 + 1.6 * n + (double)((tiles + pairs - 1) / pairs) * stages * stage;
+}
+
+// Which form runs: CTA pairs never for the smallest calls, whose one tile of
+// 16 tokens they cannot beat.
+inline bool mx_use_pairs(int T, int N, int stages, int x_bits, int num_sms) {
+    if (T <= 16) return false;
+    const int row_tiles = (int)(((long long)N + 127) / 128), tok_tiles = (int)(((long long)T + 127) / 128);
+    if (tok_tiles > 65535) return true;  // the other form's grid has them in y
+    const int S = mx_split(row_tiles, tok_tiles, T, stages, x_bits, num_sms);
+    return mx_pair_us(mx_pair_tiles(T, N), stages, x_bits, num_sms) <
+           mx_split_us(row_tiles, tok_tiles, T, stages, S, x_bits, num_sms);
 }
 
 }  // namespace q4mm

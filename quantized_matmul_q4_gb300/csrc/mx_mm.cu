@@ -824,7 +824,7 @@ cudaError_t launch_split(const LaunchCtx &c, MxType type, const MxMatmulArgs &a)
     if (e != cudaSuccess) return e;
     const int row_tiles = (a.N + kMmRows - 1) / kMmRows, tok_tiles = (a.T + kTok - 1) / kTok;
     const int stages = (Kp + L::kStageK - 1) / L::kStageK;
-    const int S = mx_split(row_tiles, tok_tiles, stages, c.num_sms);
+    const int S = mx_split(row_tiles, tok_tiles, a.T, stages, a.x_bits, c.num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(row_tiles * S, tok_tiles);
     cfg.blockDim = dim3(kMmThreads);
@@ -877,10 +877,12 @@ cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) 
 
 template <bool kX8>
 cudaError_t launch_mm_tokens(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
+    constexpr int kStageK = PairLayout<kX8>::kStageK;
+    if (mx_use_pairs(a.T, a.N, (mx_padded(a.K) + kStageK - 1) / kStageK, a.x_bits, c.num_sms))
+        return launch_pair<kX8>(c, type, a);
     if (a.T <= 16) return launch_split<kX8, 16>(c, type, a);
     if (a.T <= 64) return launch_split<kX8, 64>(c, type, a);
-    if (!mx_use_pairs(a.T, a.N, c.num_sms)) return launch_split<kX8, 128>(c, type, a);
-    return launch_pair<kX8>(c, type, a);
+    return launch_split<kX8, 128>(c, type, a);
 }
 
 }  // namespace

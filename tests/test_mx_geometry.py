@@ -7,6 +7,8 @@ import subprocess
 
 import pytest
 
+from mx_cases import PAIRS, SPLIT
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -30,9 +32,25 @@ def test_split_gives_every_cta_work(geo):
     for sms in (1, 132, 148, 152):
         for tiles in (1, 2, 3, 32, 54, 86, 151, 152, 153, 400, 100000):
             for stages in (1, 2, 3, 4, 5, 16, 17, 43, 86, 256, 512):
-                S = geo.mx_geo_split(tiles, 1, stages, sms)
-                assert 1 <= S <= 8 and S <= max(1, stages // 2)
-                assert S == 1 or tiles * S <= 2 * sms
+                for tokens in (1, 16, 64, 128):
+                    for bits in (4, 8):
+                        S = geo.mx_geo_split(tiles, 1, tokens, stages, bits, sms)
+                        assert 1 <= S <= 8 and S <= max(1, stages // 2)
+    # One token through 4096 x 4096: all eight; many tiles: none.
+    assert geo.mx_geo_split(32, 1, 1, 32, 8, 152) == 8
+    assert geo.mx_geo_split(100000, 1, 128, 32, 8, 152) == 1
+
+
+def test_pairs_take_the_large_products(geo):
+    for bits in (4, 8):
+        stages = 4096 * bits // 1024
+        for T in range(1, 17):
+            assert not geo.mx_geo_use_pairs(T, 11008, stages, bits, 152)
+        assert geo.mx_geo_use_pairs(8192, 11008, stages, bits, 152)
+        # The split form's grid has its token tiles in y: never 65536 of them.
+        for T in (128 * 65535 + 1, 2 ** 31 - 1):
+            for N in (1, 129, 11008):
+                assert geo.mx_geo_use_pairs(T, N, 1, bits, 152)
 
 
 def test_pair_tiles(geo):
@@ -48,3 +66,21 @@ def test_pair_tiles(geo):
         # Blocks of 32 tokens that a tile's scales are shifted by: with a shift
         # eight columns are taken from three scale tiles, twelve words.
         assert all(s // 32 + tok // 32 <= 12 for s in starts)
+
+
+def test_the_product_tests_reach_every_form(geo):
+    def stages(K, bits):
+        return -(-(-(-K // 128) * 128) // (256 if bits == 4 else 128))
+
+    for bits in (4, 8):
+        tiles, splits = set(), set()
+        for T, K, N in PAIRS:
+            assert geo.mx_geo_use_pairs(T, N, stages(K, bits), bits, 152)
+            out = (ctypes.c_int * 4)()
+            geo.mx_geo_pairs(T, N, out)
+            tiles.add(out[0])
+        for T, K, N in SPLIT:
+            assert not geo.mx_geo_use_pairs(T, N, stages(K, bits), bits, 152)
+            splits.add(geo.mx_geo_split(-(-N // 128), -(-T // 128), T, stages(K, bits), bits, 152))
+        assert tiles == {64, 128, 160, 192, 224, 256}
+        assert {1, 3, 4, 5, 8} <= splits
