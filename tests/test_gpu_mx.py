@@ -567,3 +567,27 @@ def test_wait_runs_out_then_next_call_is_right(T, K, N, bits):
     q.device_status()
     _assert_product(q.mx_matmul(x, w), xv, wv, "float32")
     q.device_status()
+
+
+@pytest.mark.parametrize("tokens", [1, 30, 260])
+def test_feed_forward_example(tokens):
+    """The example's block against the same block on the values that its codes
+    stand for: each product is within its own bound of those, and the whole
+    differs from float32 on unquantised values by the formats' error only."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "llama_ffn_mx.py")
+    spec = importlib.util.spec_from_file_location("llama_ffn_mx", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    torch = _torch()
+    weights, x, residual = ex.make(768, 1100, tokens, seed=tokens)
+    block = ex.MxFeedForward(**weights)
+    y, h = block(x, residual)
+    ref = ex.reference(x, residual, **weights)
+    assert torch.equal(h, x + residual)
+    # A 4-bit weight is off by up to a quarter of its value and by about a
+    # ninth on the mean, in three matrices one after the other.
+    off = float((y.float() - ref).norm() / ref.norm())
+    assert 0.02 < off < 0.35
+    _q().device_status()
