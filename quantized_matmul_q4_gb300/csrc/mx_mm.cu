@@ -370,8 +370,9 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 // Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.
 // ---------------------------------------------------------------------------
 
-constexpr int kPairThreads = 608;  // operand copies, MMA issuer, 2 x 4 scale warps, 8 epilogue warps, scale copies
-constexpr int kPairEpiWarp = 10, kPairScaleProducer = 18;
+constexpr int kPairThreads = 736;  // operand copies, MMA issuer, 2 x 4 scale warps, 3 x 4 epilogue warps, scale copies
+constexpr int kPairEpiWarp = 10, kPairScaleProducer = 22;
+constexpr int kPairEpiWarps = 12;  // three for each lane quarter: the accumulators share three blocks of 32 columns
 constexpr int kPairTok = 256;
 constexpr int kPairStages = 6;
 constexpr int kPairXTiles = 3;     // 128-row scale tiles that the tokens of a tile touch at most
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_free[b], 16);  // 8 epilogue warps of both CTAs
+            mbar_init(&acc_free[b], 2 * kPairEpiWarps);  // of both CTAs
         }
         mbar_init(done, 1);
         abort_flag = 0;
@@ -671,11 +672,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int c = 0; c < chunks; ++c, ++n) {
                 if ((n & 1) != group) continue;
                 const int s = n % kPairStages, buf = n % L::kScaleBufs;
-                ok = mbar_spin_abortable(&scales_in[s], (n / kPairStages) & 1, wait_limit, &abort_flag);
+                ok = mbar_wait_abortable(&scales_in[s], (n / kPairStages) & 1, wait_limit, &abort_flag);
                 if (n >= L::kScaleBufs) {
                     // The MMAs that last read this buffer.
                     const int m = n - L::kScaleBufs;
-                    ok = ok && mbar_spin_abortable(&empty[m % kPairStages], (m / kPairStages) & 1, wait_limit,
+                    ok = ok && mbar_wait_abortable(&empty[m % kPairStages], (m / kPairStages) & 1, wait_limit,
                                                    &abort_flag);
                 }
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -720,7 +721,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        const int q = warp & 3, half = (warp - kPairEpiWarp) >> 2;  // lane quarter; even or odd blocks of 32 tokens
+        const int q = warp & 3, third = (warp - kPairEpiWarp) >> 2;  // lane quarter; every third block of 32 tokens
         const uint32_t free_addr = map_to_rank(smem_addr(acc_free), 0);
         int it = 0;
         for (long long i = pair; i < tiles; i += pairs, ++it) {
@@ -736,22 +737,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mm_fence_after();
             const uint32_t col0 = tmem + ((uint32_t)(32 * q) << 16) + (it & 1) * kPairCol1;
             const int n = t.row0 + rank * kMmRows + 32 * q + lane;
+            auto free_accumulator = [&]() {
+                mm_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
+            };
             // The shared columns are the last blocks of the first accumulator
-            // and the first of the second: from there on, away from them.
-            const int first = it & 1 ? 0 : blocks - 1, dir = it & 1 ? 1 : -1;
-            const int gate = shared ? shared : blocks;  // blocks to read before the next tile may be written
-            bool freed = false;
-            for (int b = 0; b < blocks; ++b) {
-                if (b >= gate && !freed) {
-                    mm_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
-                    freed = true;
-                }
-                const int blk = first + dir * b;
-                if ((blk & 1) != half) continue;
+            // and the first of the second, up to three: one for each warp of
+            // a quarter, which reads it before anything else, since the next
+            // tile's MMAs wait for that.
+            const int s0 = it & 1 ? 0 : blocks - shared;
+            const int mine = s0 + (third + 3 - s0 % 3) % 3;  // this warp's first block from s0 on
+            const bool early = mine < s0 + shared;
+            if (shared && !early) free_accumulator();
+            bool first = early;
+            for (int blk = early ? mine : third; blk < blocks;) {
                 float v[32];
                 mm_ld32(col0 + 32 * blk, v);
+                if (first) free_accumulator();
                 const int tok = t.tok0 + 32 * blk, count = min(32, T - tok);
                 if (n < N && count > 0) {
                     const size_t at = (size_t)tok * N + n;
@@ -763,12 +766,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         store_column(static_cast<__nv_bfloat16 *>(y) + at, N, count, v);
                 }
                 __syncwarp();
+                blk = first ? third : blk + 3;
+                first = false;
+                if (early && blk == mine) blk += 3;
             }
-            if (!freed) {
-                mm_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
-            }
+            if (!shared) free_accumulator();
         }
     }
     mm_fence_before();
