@@ -24,13 +24,13 @@ SPLIT = [
     (3, 4224, 257),        # 6, 7
     (16, 2560, 130),       # 5, 7
     (17, 4096, 11008),     # 3, 3
-    (20, 2560, 7000),      # 5, 5
+    (20, 2560, 7000),      # 4, 4
     (24, 8192, 8000),      # 4, 4
     (33, 640, 5000),       # 1, 1
     (64, 8192, 1200),      # 8, 8
     (128, 4096, 600),      # 8, 8
     (200, 8192, 300),      # 8, 8: two tiles of tokens
-    (256, 4224, 520),      # 6, 7
+    (256, 4224, 520),      # 8, 8
     (513, 11008, 129),     # 8, 8: five, the last of one token
 ]
 
