@@ -373,6 +373,9 @@ int ternary_gemv(const float *x, const void *w_packed, float scale, float *y, in
  */
 typedef enum { Q4MM_F32 = 0, Q4MM_F16 = 1, Q4MM_BF16 = 2 } q4mm_dtype;
 
+/* Largest rows, tokens and outputDim of an MX call (indexes stay in an int). */
+#define Q4MM_MX_MAX_ROWS 0x7FFFFE00
+
 #define Q4MM_MX_PADDED(K) (((size_t)(K) + 127) / 128 * 128)
 #define Q4MM_MX_CODE_BYTES(K, rows, bits) ((size_t)(rows) * (Q4MM_MX_PADDED(K) * (bits) / 8))
 #define Q4MM_MX_SCALE_BYTES(K, rows) (((size_t)(rows) + 127) / 128 * (Q4MM_MX_PADDED(K) / 128) * 512)
@@ -380,7 +383,8 @@ typedef enum { Q4MM_F32 = 0, Q4MM_F16 = 1, Q4MM_BF16 = 2 } q4mm_dtype;
 /*
  * mx_quantize — x [rows][K] of type dtype to MX codes and scales.
  * codes: Q4MM_MX_CODE_BYTES(K, rows, bits); scales: Q4MM_MX_SCALE_BYTES(K, rows).
- * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; rows >= 0; bits 4 or 8.
+ * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; 0 <= rows <= Q4MM_MX_MAX_ROWS;
+ *         bits 4 or 8.
  * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
  */
 int mx_quantize(const void *x, long long x_stride, int dtype, void *codes, void *scales, int inputDim, int rows,
@@ -422,7 +426,10 @@ int mx_dequantize(const void *codes, const void *scales, void *y, long long y_st
  * values.  Products of codes and scales are exact; they are added in fp32.
  * y: [tokens][outputDim] of type dtype, contiguous, overwritten, aligned to
  * its element.
- * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; outputDim >= 1; tokens >= 0.
+ * Limits: 1 <= inputDim <= Q4MM_MAX_INPUT_DIM; 1 <= outputDim <=
+ *         Q4MM_MX_MAX_ROWS; 0 <= tokens <= Q4MM_MX_MAX_ROWS.
+ * Precision: |y − y_exact| <= (K/32 + 1)·2^-23·Σ|x·w| before the rounding to
+ *         dtype; the same call gives the same bits again.
  * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
  */
 int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void *w_codes, const void *w_scales,
@@ -444,7 +451,7 @@ int q4mm_device_status(q4mm_stream_t stream, int clear);
  * q4mm_test_fail_next_wait — a test hook for the library's failure
  * detection; the pages have no counterpart.  The calling thread's next call
  * of q4k_matmul (one-token and 3-8 token kernels), q4_0_gemv, q6k_gemv,
- * q4k_ffn_swiglu or q4k_matmul_tc never issues the copy of weight stage
+ * q4k_ffn_swiglu, q4k_matmul_tc or mx_matmul never issues the copy of weight stage
  * `stage` of each CTA (its ring stage, or its 256-row weight tile on the
  * tensor cores) and bounds every in-kernel wait by `limit_cycles` SM cycles
  * (about 2·10^6 per millisecond) instead of about 2·10^9.  The waits on the

@@ -299,7 +299,7 @@ def ternary_gemv(x, w, scale: float = 1.0, N: int | None = None, out=None, strea
 # Microscaled (MX) tensors: layouts and roundings in include/q4mm.h.
 
 MX_BLOCK, MX_TILE_ROWS, MX_TILE_BYTES = 32, 128, 512
-MX_MAX_ROWS = 2 ** 31 - 1   # rows of a call (the C ABI's int)
+MX_MAX_ROWS = 0x7FFFFE00   # rows of a call (Q4MM_MX_MAX_ROWS)
 
 
 class MxTensor(NamedTuple):

@@ -143,6 +143,8 @@ int check_mx_dims(int K, int rows, int bits, const char *rows_name) {
     if (K <= 0 || rows < 0)
         return fail(Q4MM_ERR_DIM, "inputDim (%d) must be positive and %s (%d) not negative", K, rows_name, rows);
     if (K > Q4MM_MAX_INPUT_DIM) return fail(Q4MM_ERR_DIM, "inputDim %d exceeds the limit %d", K, Q4MM_MAX_INPUT_DIM);
+    if (rows > Q4MM_MX_MAX_ROWS)
+        return fail(Q4MM_ERR_DIM, "%s (%d) exceeds the limit %d", rows_name, rows, Q4MM_MX_MAX_ROWS);
     if (bits != 4 && bits != 8) return fail(Q4MM_ERR_DIM, "bits (%d) must be 4 or 8", bits);
     return Q4MM_OK;
 }
@@ -524,7 +526,8 @@ int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void 
     const int K = inputDim, N = outputDim, T = tokens;
     int rc = check_mx_dims(K, T, x_bits, "tokens");
     if (rc || (rc = check_mx_dtype(dtype, "output"))) return rc;
-    if (N <= 0) return fail(Q4MM_ERR_DIM, "outputDim (%d) must be positive", N);
+    if (N <= 0 || N > Q4MM_MX_MAX_ROWS)
+        return fail(Q4MM_ERR_DIM, "outputDim (%d) must be positive and at most %d", N, Q4MM_MX_MAX_ROWS);
     if (T == 0) return Q4MM_OK;
     const Span out{y, (size_t)T * N * mx_size(dtype), "y"};
     const Span ins[4] = {mx_codes(x_codes, K, T, x_bits, "x_codes"), mx_scales(x_scales, K, T, "x_scales"),
@@ -577,6 +580,6 @@ int q4mm_test_fail_next_wait(int stage, long long limit_cycles) {
     return Q4MM_OK;
 }
 
-int q4mm_version(void) { return 200; }
+int q4mm_version(void) { return 300; }
 
 }  // extern "C"

@@ -13,9 +13,30 @@
 // K of packed E2M1, or 128 values with kX8, where the 4-bit weights are
 // unpacked by the tensor copy itself into the 16-bytes-per-16-values form
 // that the mixed MMA reads.  Either way it is four MMAs.  Block scales come
-// as whole 512-byte tiles by plain bulk copies and are put into tensor memory
-// with tcgen05.cp by the thread that issues the MMAs; copies and MMAs of one
-// thread run in order.
+// as whole 512-byte tiles by plain bulk copies and go on to tensor memory,
+// where the MMA takes them from a multiple of four columns on.
+//
+// Two forms, chosen by mx_geometry.h from estimates of both:
+//  * mx_mm_split_kernel, up to 128 tokens a tile, K split over a cluster.  A
+//    call with few tokens reads its weights once and is bound by them and by
+//    the chain of latencies around them: 4096 x 4096 at one token takes 4.5
+//    us (x in 4 bits) and 5.3 (8 bits, whose unpacking copies move 64 bytes
+//    a row) in a chain of calls, of which 1.3 us are the weights' at the
+//    copy rate, 2.9 an empty product's (1024 x 1024).  Large ones reach 5.9
+//    TB/s behind those 3 us (16384 -> 38912: 61 us, 82% of the copy rate).
+//  * mx_mm_pair_kernel, 256 rows x 256 tokens on a pair of CTAs, for the
+//    rest.  8192 tokens 4096 -> 11008: 118 us in 4 bits (6.2 PFLOP/s), 210 in
+//    8 (3.5); 8192 tokens 8192 -> 8192: 156 us (7.1 PFLOP/s).  Bound by the
+//    tensor pipe, which runs 620 cycles for a stage's four MMAs where 512
+//    are nominal and a stage takes 650, and by some 900 cycles between two
+//    tiles; kept busy for seconds, by the board's power limit.
+//
+// Tensor memory: a CTA waits for its columns while another holds them, so two
+// kernels must never wait for each other's.  They do not: every CTA of a grid
+// has its columns before it lets the next grid on the stream start, and grids
+// on different streams share an SM only where both fit, columns included (two
+// CTAs of the split form, at most 256 columns each; a pair's CTA takes all of
+// an SM's shared memory).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -411,7 +432,7 @@ __device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap *map
 }
 
 // Arrives on the barrier at this offset in both CTAs of the pair once the
-// MMAs (and scale copies) issued so far are done.
+// MMAs issued so far are done.
 __device__ __forceinline__ void pair_commit(uint64_t *bar) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
@@ -440,7 +461,10 @@ __device__ __forceinline__ void mm_ld32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// One n of `count` consecutive tokens, N values apart.
+// One n of `count` consecutive tokens, N values apart.  The stores are
+// unrolled; two copies of the loop in the kernel cost a tile a microsecond
+// (instruction cache), and one loop for all types, with an index for every
+// store, more than that.
 template <class T>
 __device__ __forceinline__ void store_column(T *p, int N, int count, const float (&v)[32]) {
     if (count >= 32) {
@@ -477,8 +501,13 @@ __device__ __forceinline__ void mm_st4(uint32_t taddr, uint4 v) {
 // of the tokens, and holds its 128 rows of D.  Half of the operand bytes of
 // two single CTAs, both from L2 and in shared memory.  The pair takes every
 // (number of pairs)-th tile; the epilogue of a tile runs beside the MMAs of
-// the next.  All copies of both CTAs are counted on the leader's barriers,
-// and its one thread issues every MMA; completions are multicast to both.
+// the next, whose accumulator shares three blocks of 32 columns with it (the
+// scales need the rest).  All operand copies of both CTAs are counted on the
+// leader's barriers, and its one thread issues every MMA; completions are
+// multicast to both.  What was measured on the way (8192 tokens 4096 -> 11008
+// in 4 bits): scales by tcgen05.cp 230 us, by scale warps whose arrival
+// releases at cluster scope 326, by the plain arrival 162, copies issued by
+// lanes 142, one barrier a stage 130, shared columns read first 118.
 template <bool kX8>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_mm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,

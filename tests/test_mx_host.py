@@ -78,6 +78,10 @@ def test_sizes_are_checked(q4mm):
     _refused(q4mm, DIM, q4mm.mx_matmul_ptr, A, B, 8, C, D, E, 0, 128, 0, 1, word="outputDim")
     _refused(q4mm, DIM, q4mm.mx_matmul_ptr, A, B, 8, C, D, E, 0, 128, 16, -1, word="tokens")
     _refused(q4mm, DIM, q4mm.mx_quantize_ptr, A, 128, 0, B, C, 128, -1, 8, word="rows")
+    for many in (0x7FFFFE01, 0x7FFFFFFF):      # indexes of the last tiles would not fit
+        _refused(q4mm, DIM, q4mm.mx_quantize_ptr, A, 128, 0, B, C, 128, many, 8, word="rows")
+        _refused(q4mm, DIM, q4mm.mx_matmul_ptr, A, B, 8, C, D, E, 0, 128, many, 1, word="outputDim")
+        _refused(q4mm, DIM, q4mm.mx_matmul_ptr, A, B, 8, C, D, E, 0, 128, 16, many, word="tokens")
     _refused(q4mm, DIM, q4mm.mx_quantize_ptr, A, 127, 0, B, C, 128, 2, 8, word="stride")
     _refused(q4mm, DIM, q4mm.mx_quantize_ptr, A, 1 << 62, 0, B, C, 128, 1 << 30, 8, word="memory")
     _refused(q4mm, DIM, q4mm.mx_rmsnorm_ptr, A, 128, 0, 0, 0, 0, 1, B, 2, 1e-5, C, D, 128, 2, 8, word="weight")
