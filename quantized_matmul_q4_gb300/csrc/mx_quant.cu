@@ -310,6 +310,19 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     const T *res = a.residual ? static_cast<const T *>(a.residual) + row * a.residual_stride : nullptr;
     T *h = a.h ? static_cast<T *>(a.h) + row * a.h_stride : nullptr;
     pdl_wait();
+    if (row >= a.rows) {
+        // The CTAs past the last row write zero scale bytes for the rest of
+        // its 128-row block, a thread per word (one row of 4096: 4.4 -> 2.2
+        // us against leaving it to the row's own CTA).
+        const int first = (a.rows - 1) / kMxTileRows * kMxTileRows, here = a.rows - first;
+        uint8_t *tiles = a.scales + (size_t)(first / kMxTileRows) * nkt * kMxTileBytes;
+        const int words = (kMxTileRows - here) * nkt, all = (int)(gridDim.x - a.rows) * blockDim.x;
+        for (int i = (int)(row - a.rows) * blockDim.x + threadIdx.x; i < words; i += all) {
+            const int p = here + i / nkt, kt = i % nkt;
+            *reinterpret_cast<uint32_t *>(tiles + (size_t)kt * kMxTileBytes + 16 * (p & 31) + 4 * (p >> 5)) = 0u;
+        }
+        return;
+    }
     constexpr int kKept = kVals > 0 ? kVals : 1;
     // Groups are loaded four at a time at most, x and residual together.
     auto load_h = [&](int c0, float (&v)[kKept][8]) {
@@ -342,8 +355,19 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
                 sums = ffma2(f, f, sums);
             }
     };
+    auto load_g = [&](int c0, float (&g)[8]) {
+        if (a.weight_f32) {
+            load8<kVec>(static_cast<const float *>(a.weight), c0 + 8 * threadIdx.x, K, g);
+        } else {
+            load8<kVec>(static_cast<const T *>(a.weight), c0 + 8 * threadIdx.x, K, g);
+        }
+    };
+    float g0[8];
     if constexpr (kVals > 0) {
         load_h(0, v);
+        // With one group a thread, the form for few rows, the chain of
+        // latencies is what counts: the weight is loaded beside x.
+        if constexpr (kVals == 1) load_g(0, g0);
         add_squares();
     } else {
         for (int c0 = 0; c0 < K; c0 += step) {
@@ -367,10 +391,11 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
         const int col = c0 + 8 * threadIdx.x;
         if (h) store8<kVec>(h, col, K, u);
         float g[8];
-        if (a.weight_f32) {
-            load8<kVec>(static_cast<const float *>(a.weight), col, K, g);
+        if constexpr (kVals == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[j] = g0[j];
         } else {
-            load8<kVec>(static_cast<const T *>(a.weight), col, K, g);
+            load_g(c0, g);
         }
         // Past K the values are zeros and so is the weight; an infinite norm
         // or a NaN must not reach the padding.
@@ -399,18 +424,6 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
             const uint32_t w = exchange(finish(c0, v[0]));
             const int kt = (c0 + 256 * warp) / kMxPadK + (lane >> 4);
             if ((lane & 15) == 0 && kt < nkt) *reinterpret_cast<uint32_t *>(scale_row + (size_t)kt * kMxTileBytes) = w;
-        }
-    }
-    // Zero scale bytes for the rows past the last one: the CTAs of the last
-    // 128-row block share them, a thread per word.
-    const long long first = (long long)(a.rows - 1) / kMxTileRows * kMxTileRows;
-    if (row >= first) {
-        const int here = (int)(a.rows - first);
-        uint8_t *tiles = a.scales + (size_t)(first / kMxTileRows) * nkt * kMxTileBytes;
-        const int words = (kMxTileRows - here) * nkt;
-        for (int i = (int)(row - first) * blockDim.x + threadIdx.x; i < words; i += here * blockDim.x) {
-            const int p = here + i / nkt, kt = i % nkt;
-            *reinterpret_cast<uint32_t *>(tiles + (size_t)kt * kMxTileBytes + 16 * (p & 31) + 4 * (p >> 5)) = 0u;
         }
     }
 }
@@ -503,13 +516,14 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
     const RmsArgs k{a.x, a.residual, a.weight, a.h, a.x_stride, a.residual_stride, a.h_stride, a.codes, a.scales,
                     a.eps, a.K, a.rows, a.bits, a.weight_f32};
     const int Kp = mx_padded(a.K);
-    // Values per thread: the fewest that 1024 threads allow while there are
-    // no more rows than SMs (one row of 4096: a group of 8 each); else four
-    // groups of a 16-bit type or two of fp32 (64 bytes a thread) where they
-    // leave four warps.  8192 x 4096 bf16 with a residual: 52.0, 38.1, 37.6
-    // us with one, two, four groups; 4096 x 4096 fp32: 34.1, 33.9, 37.8.
+    // Values per thread: the fewest that 1024 threads allow, a group of 8, for
+    // fp32 and while there are no more rows than SMs (one row of 4096: 2.1
+    // us); for many rows of a 16-bit type four groups, where they leave four
+    // warps.  8192 x 4096 bf16 with a residual: 52.0, 38.1, 37.6 us with one,
+    // two, four groups; 4096 x 4096 fp32: 34.9 with one, 35.9 with two, 37.8
+    // with four.
     int vals = 1;
-    if (a.rows > c.num_sms) vals = Kp >= 4096 && sizeof(T) == 2 ? 4 : Kp >= 2048 ? 2 : 1;
+    if (a.rows > c.num_sms && sizeof(T) == 2) vals = Kp >= 4096 ? 4 : Kp >= 2048 ? 2 : 1;
     while (vals < 4 && Kp > 8 * 1024 * vals) vals *= 2;
     const bool kept = Kp <= 8 * 1024 * vals;
     int threads = kept ? (Kp / 8 + vals - 1) / vals : 1024;
@@ -519,7 +533,10 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
                              mx_rmsnorm_kernel<T, true, 4>, mx_rmsnorm_kernel<T, true, 0>)
                       : pick(mx_rmsnorm_kernel<T, false, 1>, mx_rmsnorm_kernel<T, false, 2>,
                              mx_rmsnorm_kernel<T, false, 4>, mx_rmsnorm_kernel<T, false, 0>);
-    return launch_kernel(c, kernel, dim3(a.rows), dim3(threads), 0, k);
+    // CTAs for the padding's scale bytes, two words a thread.
+    const int words = (kMxTileRows - 1 - (a.rows - 1) % kMxTileRows) * (Kp / kMxPadK);
+    const int padding = (words + 2 * threads - 1) / (2 * threads);
+    return launch_kernel(c, kernel, dim3((unsigned)a.rows + padding), dim3(threads), 0, k);
 }
 
 template <class T>
