@@ -18,22 +18,22 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 // Estimates, in microseconds of a call, of the two forms of the product; the
 // form and the split with the lower estimate run.  `stages` are ring stages
 // of K (256 values with 4-bit x, 128 with 8-bit).  The constants are fitted
-// to 185 pairs of measurements on GB300 (chains of calls in a CUDA graph, 17
-// to 2048 tokens, K and N of 256 to 16384), where the choice costs 0.5% on
-// the mean against always the faster form; some of them, single CTAs with K
-// split / CTA pairs:
+// to some 300 pairs of measurements on GB300 (chains of calls in a CUDA
+// graph, 17 to 2048 tokens, K and N of 256 to 16384), where the choice costs
+// 0.7% on the mean against always the faster form; some of them, single CTAs
+// with K split / CTA pairs:
 //   T    K        N       x     measured       estimated
-//   17   256   -> 4096    4     2.5 /  3.3      2.7 /  3.3
-//   64   4096  -> 4096    8     7.1 / 11.8      7.1 / 11.8
-//   64   2560  -> 6912    4     7.0 /  6.1      6.7 /  6.0
-//   128  1024  -> 4096    8     8.2 /  5.9      6.5 /  5.8
-//   128  4096  -> 4096    4     7.9 /  8.3      7.8 /  8.4
-//   128  4096  -> 11008   8    13.0 / 12.9     12.8 / 12.6
-//   256  8192  -> 8192    4    16.5 / 14.9     16.9 / 15.3
-//   384  4096  -> 11008   8    19.6 / 23.6     16.3 / 22.7
-//   512  11008 -> 4096    8    25.1 / 28.4     24.6 / 30.6
-//   512  4096  -> 11008   8    34.8 / 24.9     30.7 / 23.9
-//   1024 11008 -> 4096    8    38.6 / 29.9     36.3 / 30.6
+//   17   256   -> 4096    4     2.5 /  3.3      2.7 /  3.0
+//   64   4096  -> 4096    8     7.1 / 11.7      7.1 / 11.2
+//   64   2560  -> 6912    4     7.2 /  6.1      6.7 /  5.8
+//   128  1024  -> 4096    8     6.5 /  5.8      6.5 /  5.2
+//   128  4096  -> 4096    4     7.9 /  8.3      7.8 /  7.6
+//   128  4096  -> 11008   8    13.2 / 13.0     12.8 / 12.6
+//   256  1024  -> 1024    8     6.3 /  5.5      6.5 /  5.0
+//   256  8192  -> 8192    4    16.9 / 14.1     16.9 / 13.5
+//   420  11008 -> 4096    8    25.5 / 27.5     24.6 / 27.9
+//   512  4096  -> 11008   8    35.5 / 24.6     32.7 / 24.3
+//   1024 11008 -> 4096    8    39.1 / 29.6     36.3 / 30.9
 
 // Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
 // tile's K: rounds of two CTAs per SM through their stages, then the stores
@@ -69,27 +69,38 @@ inline int mx_split(int row_tiles, int tok_tiles, int tokens, int stages, int x_
 struct MxPairTiles {
     int tile_tok, tok_tiles, row_tiles, x_tiles;
 };
-inline MxPairTiles mx_pair_tiles(int T, int N) {
-    MxPairTiles g;
-    g.tok_tiles = (int)(((long long)T + 255) / 256);
-    const int each = (int)(((long long)T + g.tok_tiles - 1) / g.tok_tiles);
-    g.tile_tok = (each + 31) / 32 * 32;
-    g.row_tiles = (int)(((long long)N + 255) / 256);
-    // The first token's offset in its scale tile is a multiple of
-    // gcd(tile_tok, 128).
-    int step = 128;
-    while (g.tile_tok % step) step /= 2;
-    const int offset = g.tok_tiles > 1 ? 128 - step : 0;
-    g.x_tiles = (offset + g.tile_tok + 127) / 128;
-    return g;
-}
 
-// CTA pairs, tiles of 256 rows x tile_tok tokens, one pair per two SMs.
+// CTA pairs, one per two SMs.
 inline double mx_pair_us(const MxPairTiles &g, int stages, int x_bits, int num_sms) {
-    const long long tiles = (long long)g.row_tiles * g.tok_tiles, pairs = num_sms / 2;
+    const long long tiles = (long long)g.row_tiles * g.tok_tiles, pairs = num_sms > 1 ? num_sms / 2 : 1;
     const double n = g.tile_tok / 256.0;
     const double stage = x_bits == 8 ? 0.255 + 0.05 * n : 0.26 + 0.08 * n;
-    return 2.8 + 1.6 * n + (double)((tiles + pairs - 1) / pairs) * stages * stage;
+    return 2.3 + 1.6 * n + 0.012 * (double)(tiles < pairs ? tiles : pairs) +
+           (double)((tiles + pairs - 1) / pairs) * stages * stage;
+}
+
+// As few tiles of tokens as there can be, or twice or four times as many
+// where the estimate is lower: smaller tiles end sooner while there are pairs
+// to spare.
+inline MxPairTiles mx_pair_tiles(int T, int N, int stages, int x_bits, int num_sms) {
+    MxPairTiles best{};
+    double us = 0.0;
+    for (int more = 1; more <= 4; more *= 2) {
+        MxPairTiles g;
+        const long long parts = ((long long)T + 255) / 256 * more;
+        g.tile_tok = (int)(((T + parts - 1) / parts + 31) / 32 * 32);
+        g.tok_tiles = (int)(((long long)T + g.tile_tok - 1) / g.tile_tok);
+        g.row_tiles = (int)(((long long)N + 255) / 256);
+        // The first token's offset in its scale tile is a multiple of
+        // gcd(tile_tok, 128).
+        int step = 128;
+        while (g.tile_tok % step) step /= 2;
+        const int offset = g.tok_tiles > 1 ? 128 - step : 0;
+        g.x_tiles = (offset + g.tile_tok + 127) / 128;
+        const double t = mx_pair_us(g, stages, x_bits, num_sms);
+        if (more == 1 || t < us) us = t, best = g;
+    }
+    return best;
 }
 
 // Which form runs: CTA pairs never for the smallest calls, whose one tile of
@@ -99,7 +110,7 @@ inline bool mx_use_pairs(int T, int N, int stages, int x_bits, int num_sms) {
     const int row_tiles = (int)(((long long)N + 127) / 128), tok_tiles = (int)(((long long)T + 127) / 128);
     if (tok_tiles > 65535) return true;  // the other form's grid has them in y
     const int S = mx_split(row_tiles, tok_tiles, T, stages, x_bits, num_sms);
-    return mx_pair_us(mx_pair_tiles(T, N), stages, x_bits, num_sms) <
+    return mx_pair_us(mx_pair_tiles(T, N, stages, x_bits, num_sms), stages, x_bits, num_sms) <
            mx_split_us(row_tiles, tok_tiles, T, stages, S, x_bits, num_sms);
 }
 

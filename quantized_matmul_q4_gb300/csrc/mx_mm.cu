@@ -878,7 +878,7 @@ template <bool kX8>
 cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
     using L = PairLayout<kX8>;
     const int Kp = mx_padded(a.K);
-    const MxPairTiles g = mx_pair_tiles(a.T, a.N);
+    const MxPairTiles g = mx_pair_tiles(a.T, a.N, (Kp + L::kStageK - 1) / L::kStageK, a.x_bits, c.num_sms);
     alignas(64) CUtensorMap tm_w, tm_x;
     if (!map_codes(&tm_w, a.w_codes, a.N, Kp, 4, kX8, kMmRows) ||
         !map_codes(&tm_x, a.x_codes, a.T, Kp, a.x_bits, false, g.tile_tok / 2))

@@ -54,18 +54,18 @@ def test_pairs_take_the_large_products(geo):
 
 
 def test_pair_tiles(geo):
-    for T in list(range(1, 1200)) + [4095, 4096, 4097, 8191, 8192, 100000, 2 ** 31 - 1]:
-        out = (ctypes.c_int * 4)()
-        geo.mx_geo_pairs(T, 11008, out)
-        tok, tok_tiles, row_tiles, x_tiles = out
-        assert tok % 32 == 0 and 32 <= tok <= 256 and row_tiles == 43
-        assert (tok_tiles - 1) * tok < T <= tok_tiles * tok     # every tile has a token, every token a tile
-        starts = {(i * tok) % 128 for i in range(min(tok_tiles, 8))}
-        assert x_tiles == max((s + tok + 127) // 128 for s in starts) <= 3 or tok_tiles < 8
-        assert all((s + tok + 127) // 128 <= x_tiles <= 3 for s in starts)
-        # Blocks of 32 tokens that a tile's scales are shifted by: with a shift
-        # eight columns are taken from three scale tiles, twelve words.
-        assert all(s // 32 + tok // 32 <= 12 for s in starts)
+    for N, stages, bits, sms in ((11008, 16, 4, 152), (4096, 32, 8, 152), (129, 1, 4, 152), (1, 512, 8, 1)):
+        for T in list(range(1, 1200)) + [4095, 4096, 4097, 8191, 8192, 100000, 0x7FFFFE00]:
+            out = (ctypes.c_int * 4)()
+            geo.mx_geo_pairs(T, N, stages, bits, sms, out)
+            tok, tok_tiles, row_tiles, x_tiles = out
+            assert tok % 32 == 0 and 32 <= tok <= 256 and row_tiles == -(-N // 256)
+            assert (tok_tiles - 1) * tok < T <= tok_tiles * tok     # every tile has a token, every token a tile
+            starts = {(i * tok) % 128 for i in range(min(tok_tiles, 8))}
+            assert all((s + tok + 127) // 128 <= x_tiles <= 3 for s in starts)
+            # Blocks of 32 tokens that a tile's scales are shifted by: with a
+            # shift eight columns are taken from three scale tiles, twelve words.
+            assert all(s // 32 + tok // 32 <= 12 for s in starts)
 
 
 def test_the_product_tests_reach_every_form(geo):
@@ -77,10 +77,10 @@ def test_the_product_tests_reach_every_form(geo):
         for T, K, N in PAIRS:
             assert geo.mx_geo_use_pairs(T, N, stages(K, bits), bits, 152)
             out = (ctypes.c_int * 4)()
-            geo.mx_geo_pairs(T, N, out)
+            geo.mx_geo_pairs(T, N, stages(K, bits), bits, 152, out)
             tiles.add(out[0])
         for T, K, N in SPLIT:
             assert not geo.mx_geo_use_pairs(T, N, stages(K, bits), bits, 152)
             splits.add(geo.mx_geo_split(-(-N // 128), -(-T // 128), T, stages(K, bits), bits, 152))
-        assert tiles == {64, 128, 160, 192, 224, 256}
+        assert {64, 96, 128, 160, 192, 224, 256} <= tiles
         assert {1, 3, 4, 8} <= splits and splits & {5, 6, 7}
