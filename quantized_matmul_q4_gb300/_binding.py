@@ -324,33 +324,37 @@ def mx_padded(K: int) -> int:
     return -(-K // 128) * 128
 
 
-_MX_DTYPES = {}   # torch type -> q4mm_dtype, filled on first use
+class _Torch:
+    """What the MX calls take from torch, looked up on the first of them (the
+    binding itself imports without torch).  A call costs the host about as
+    much as an elementwise torch operation, mostly its allocations and the
+    launch; what is left is kept short."""
+    dtypes: dict = {}
+    uint8 = float32 = empty = raw_stream = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
+        cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
+        # The current stream's handle alone: a Stream object costs as much as a launch.
+        cls.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _mx_dtype(t, what: str) -> int:
-    code = _MX_DTYPES.get(t)
+    if not _Torch.dtypes:
+        _Torch.load()
+    code = _Torch.dtypes.get(t)
     if code is None:
-        import torch
-        _MX_DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-        code = _MX_DTYPES.get(t)
-        if code is None:
-            raise ValueError(f"{what} must be float32, float16 or bfloat16")
+        raise ValueError(f"{what} must be float32, float16 or bfloat16")
     return code
-
-
-def _mx_stream(stream, device: int) -> int:
-    """The given stream, or torch's current one on the tensors' device (its
-    handle alone: building a Stream object costs as much as a launch)."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
-    return _stream_ptr(stream)
 
 
 def _mx_rows(x, what: str):
     """x as a CUDA matrix of rows with adjacent values, never copied: the
-    matrix, its shape and its row stride."""
-    if not x.is_cuda:
+    matrix, its shape, its row stride and its device."""
+    device = x.get_device()
+    if device < 0:
         raise ValueError(f"{what} must be a CUDA tensor")
     shape = x.shape
     if len(shape) != 2:
@@ -367,30 +371,30 @@ def _mx_rows(x, what: str):
     s0, s1 = x.stride()
     if s1 != 1 and K > 1:
         raise ValueError(f"the values of a row of {what} must be adjacent")
-    return x, rows, K, s0 if rows > 1 else K
+    return x, rows, K, s0 if rows > 1 else K, device
 
 
-def _mx_out(rows: int, K: int, bits: int, x, out) -> MxTensor:
+def _mx_out(rows: int, K: int, bits: int, x, device: int, out) -> MxTensor:
     """`out` checked, or a new MxTensor on x's device."""
     if bits != 4 and bits != 8:
         raise ValueError("bits must be 4 or 8")
     if out is None:
-        import torch
-        kt = -(-K // 128)
-        u8, device = torch.uint8, x.device
-        return MxTensor(torch.empty((rows, kt * 16 * bits), dtype=u8, device=device),
-                        torch.empty((-(-rows // MX_TILE_ROWS), kt, MX_TILE_BYTES), dtype=u8, device=device), K, bits)
-    _mx_check(out, "out", x.get_device())
-    if out.K != K or out.bits != bits or out.codes.shape[0] != rows:
+        kt, where, u8 = -(-K // 128), x.device, _Torch.uint8
+        return MxTensor(_Torch.empty((rows, kt * 16 * bits), dtype=u8, device=where),
+                        _Torch.empty((-(-rows // MX_TILE_ROWS), kt, MX_TILE_BYTES), dtype=u8, device=where), K, bits)
+    if _mx_check(out, "out", device) != rows or out.K != K or out.bits != bits:
         raise ValueError(f"out must hold {rows} rows of {K} values in {bits} bits")
     return out
 
 
 def _mx_check(q: MxTensor, what: str, device: int) -> int:
     """Checks an MxTensor; returns its rows."""
-    import torch
     codes, scales, K, bits = q
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    u8 = _Torch.uint8
+    if codes.dtype != u8 or scales.dtype != u8:
+        if u8 is None:
+            _Torch.load()
+            return _mx_check(q, what, device)
         raise ValueError(f"{what}: codes and scales must be uint8 tensors")
     if codes.get_device() != device or scales.get_device() != device or device < 0:
         raise ValueError("all tensors of a call must be on one CUDA device")
@@ -411,24 +415,30 @@ def _mx_device(device: int, t) -> None:
 
 def mx_quantize(x, bits: int = 8, out: MxTensor | None = None, stream=None) -> MxTensor:
     """x [..., K] (float32, float16 or bfloat16) to an MX tensor of `bits` (4 or 8) bits."""
-    x, rows, K, stride = _mx_rows(x, "x")
-    out = _mx_out(rows, K, bits, x, out)
-    _check(_LIB.mx_quantize(x.data_ptr(), stride, _mx_dtype(x.dtype, "x"), out.codes.data_ptr(),
-                            out.scales.data_ptr(), K, rows, bits, _mx_stream(stream, x.get_device())))
+    x, rows, K, stride, device = _mx_rows(x, "x")
+    dtype = _mx_dtype(x.dtype, "x")
+    out = _mx_out(rows, K, bits, x, device, out)
+    rc = _LIB.mx_quantize(x.data_ptr(), stride, dtype, out[0].data_ptr(), out[1].data_ptr(), K, rows, bits,
+                          _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out
 
 
 def mx_swiglu(gate, up, bits: int = 8, out: MxTensor | None = None, stream=None) -> MxTensor:
     """silu(gate)·up as an MX tensor, in one pass."""
-    gate, rows, K, gs = _mx_rows(gate, "gate")
-    up, urows, uK, us = _mx_rows(up, "up")
-    dtype, device = gate.dtype, gate.get_device()
-    if rows != urows or K != uK or dtype != up.dtype:
+    gate, rows, K, gs, device = _mx_rows(gate, "gate")
+    up, urows, uK, us, udevice = _mx_rows(up, "up")
+    if rows != urows or K != uK or gate.dtype != up.dtype:
         raise ValueError("gate and up must have the same shape and type")
-    _mx_device(device, up)
-    out = _mx_out(rows, K, bits, gate, out)
-    _check(_LIB.mx_swiglu(gate.data_ptr(), gs, up.data_ptr(), us, _mx_dtype(dtype, "gate"), out.codes.data_ptr(),
-                          out.scales.data_ptr(), K, rows, bits, _mx_stream(stream, device)))
+    if device != udevice:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    dtype = _mx_dtype(gate.dtype, "gate")
+    out = _mx_out(rows, K, bits, gate, device, out)
+    rc = _LIB.mx_swiglu(gate.data_ptr(), gs, up.data_ptr(), us, dtype, out[0].data_ptr(), out[1].data_ptr(), K, rows,
+                        bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -440,34 +450,35 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
     where that is given (which may be x or residual itself); without one
     returns the MxTensor alone.
     """
-    shape, dtype = x.shape, x.dtype
-    x, rows, K, xs = _mx_rows(x, "x")
-    device = x.get_device()
+    shape, xtype = x.shape, x.dtype
+    x, rows, K, xs, device = _mx_rows(x, "x")
+    dtype = _mx_dtype(xtype, "x")
     if weight.numel() != K or not weight.is_contiguous():
         raise ValueError("weight must be contiguous and hold one value per column of x")
     _mx_device(device, weight)
     res_ptr, rs, h_ptr, hs = 0, K, 0, K
     if residual is not None:
-        if residual.shape != shape or residual.dtype != dtype:
+        if residual.shape != shape or residual.dtype != xtype:
             raise ValueError("residual must have x's shape and type")
-        r, _, _, rs = _mx_rows(residual, "residual")
-        _mx_device(device, r)
+        _mx_device(device, residual)
+        r, _, _, rs, _ = _mx_rows(residual, "residual")
         res_ptr = r.data_ptr()
         if h_out is None:
-            import torch
-            h = h_out = torch.empty(shape, dtype=dtype, device=x.device)
+            h = h_out = _Torch.empty(shape, dtype=xtype, device=x.device)
         else:
-            if h_out.shape != shape or h_out.dtype != dtype:
+            if h_out.shape != shape or h_out.dtype != xtype:
                 raise ValueError("h_out must have x's shape and type")
-            h, _, _, hs = _mx_rows(h_out, "h_out")
-            _mx_device(device, h)
+            _mx_device(device, h_out)
+            h, _, _, hs, _ = _mx_rows(h_out, "h_out")
         h_ptr = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual: without one h is x")
-    out = _mx_out(rows, K, bits, x, out)
-    _check(_LIB.mx_rmsnorm(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, _mx_dtype(dtype, "x"), weight.data_ptr(),
-                           _mx_dtype(weight.dtype, "weight"), float(eps), out.codes.data_ptr(), out.scales.data_ptr(), K,
-                           rows, bits, _mx_stream(stream, device)))
+    out = _mx_out(rows, K, bits, x, device, out)
+    rc = _LIB.mx_rmsnorm(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, dtype, weight.data_ptr(),
+                         _mx_dtype(weight.dtype, "weight"), float(eps), out[0].data_ptr(), out[1].data_ptr(), K, rows,
+                         bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out if residual is None else (out, h_out)
 
 
@@ -478,15 +489,16 @@ def mx_dequantize(q: MxTensor, dtype=None, out=None, stream=None):
     rows = _mx_check(q, "q", device)
     stride = K
     if out is None:
-        import torch
-        out = torch.empty((rows, K), dtype=dtype or torch.float32, device=codes.device)
+        out = _Torch.empty((rows, K), dtype=dtype or _Torch.float32, device=codes.device)
     else:
         if out.shape != (rows, K) or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be [rows, K] of the given type")
-        _, _, _, stride = _mx_rows(out, "out")
         _mx_device(device, out)
-    _check(_LIB.mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"),
-                              K, rows, bits, _mx_stream(stream, device)))
+        _, _, _, stride, _ = _mx_rows(out, "out")
+    rc = _LIB.mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"), K,
+                            rows, bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -502,12 +514,14 @@ def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
     if K != w_K:
         raise ValueError("x and w must have the same K")
     if out is None:
-        import torch
-        out = torch.empty((T, N), dtype=dtype or torch.float32, device=x_codes.device)
+        out = _Torch.empty((T, N), dtype=dtype or _Torch.float32, device=x_codes.device)
     else:
         if out.shape != (T, N) or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be contiguous, [tokens, outputDim] of the given type")
         _mx_device(device, out)
-    _check(_LIB.mx_matmul(x_codes.data_ptr(), x_scales.data_ptr(), x_bits, w_codes.data_ptr(), w_scales.data_ptr(),
-                          out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T, _mx_stream(stream, device)))
+    rc = _LIB.mx_matmul(x_codes.data_ptr(), x_scales.data_ptr(), x_bits, w_codes.data_ptr(), w_scales.data_ptr(),
+                        out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T,
+                        _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    if rc:
+        _check(rc)
     return out
