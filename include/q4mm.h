@@ -364,8 +364,10 @@ int ternary_gemv(const float *x, const void *w_packed, float scale, float *y, in
  *
  * Element types of the other side are named by a q4mm_dtype.  Rows of those
  * tensors may be strided (in elements, the values of a row adjacent); any
- * base aligned to its element is accepted, and where every row starts on a
- * multiple of eight values in memory and K is a multiple of 8, accesses are wide.
+ * base aligned to its element is accepted.  Accesses are fastest where every
+ * row starts on a multiple of eight values in memory and K is a multiple of 8;
+ * elsewhere up to 15 bytes between two rows of an input may be read with them
+ * (never before the first row or past the last), and are not used.
  *
  * rows = 0 (tokens = 0) is a call with nothing to do and returns Q4MM_OK.
  * Every operand, weights included, may have been written by the previous

@@ -35,52 +35,88 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // Eight consecutive values of a row as they lie in memory, zeros past K.
-// kVec: rows aligned to eight values and K a multiple of 8, so the eight are
-// all inside or all outside.
 template <class T>
 struct Raw8 {
     uint32_t w[4];  // pairs, the lower value in the low half
 };
 template <>
 struct Raw8<float> {
-    float v[8];
+    uint32_t w[8];
 };
 
+// Words m / 32 onwards of c, shifted right by m % 32 bits: kOut words from bit
+// m of the kIn given, m a multiple of 16 below 128, alike in the whole warp.
+template <int kOut, int kIn>
+__device__ __forceinline__ void words_from_bit(const uint32_t (&c)[kIn], int m, uint32_t (&out)[kOut]) {
+    uint32_t u[kIn - 1], t[kIn - 3];
+#pragma unroll
+    for (int i = 0; i < kIn - 1; ++i) u[i] = m & 32 ? c[i + 1] : c[i];
+#pragma unroll
+    for (int i = 0; i < kIn - 3; ++i) t[i] = m & 64 ? u[i + 2] : u[i];
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) out[i] = i + 1 < kIn - 3 ? __funnelshift_r(t[i], t[i + 1], m & 16) : t[i];
+}
+
+// Eight values on their way; several can be before the first is used.
+// kVec: rows aligned to eight values and K a multiple of 8, so the eight are
+// all inside or all outside.  Otherwise load<true> loads the 16-byte granules
+// that hold them, which take() shifts: at the row's ends they reach up to 15
+// bytes over it, so only where another row lies on that side (wide).
+// load<false> loads the values one by one (8192 x 4095 bf16 to 8-bit codes:
+// 26.4 us with that alone, 22.9 so).
 template <bool kVec, class T>
-__device__ __forceinline__ void load8(const T *row, int col, int K, Raw8<T> &r) {
-    if constexpr (sizeof(T) == 4) {
-        if (kVec) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            if (col < K) {
-                a = *reinterpret_cast<const float4 *>(row + col);
-                b = *reinterpret_cast<const float4 *>(row + col + 4);
+struct Fetch8 {
+    static constexpr int kWords = sizeof(T) * 2;
+    uint32_t c[kVec ? kWords : kWords + 4];
+
+    template <bool kWide>
+    __device__ __forceinline__ void load(const T *row, int col, int K) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(row + col);
+        if constexpr (kVec || kWide) {
+            const int skip = kVec ? 0 : (int)(at & 15), have = min(8, K - col) * (int)sizeof(T);  // bytes
+            const uint4 *from = reinterpret_cast<const uint4 *>(at - skip);
+#pragma unroll
+            for (int i = 0; i < (kVec ? kWords : kWords + 4); i += 4) {
+                uint4 a = make_uint4(0u, 0u, 0u, 0u);
+                if (have > 0 && (kVec || 4 * i < skip + have)) a = from[i / 4];
+                c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
             }
-            r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
-            r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r.v[i] = col + i < K ? row[col + i] : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    c[i] = col + i < K ? reinterpret_cast<const uint32_t *>(row)[col + i] : 0u;
+                } else {
+                    const uint32_t b = col + i < K ? reinterpret_cast<const uint16_t *>(row)[col + i] : 0u;
+                    c[i / 2] = i & 1 ? c[i / 2] | b << 16 : b;
+                }
+            }
+#pragma unroll
+            for (int i = kWords; i < kWords + 4; ++i) c[i] = 0u;
         }
-    } else {
-        if (kVec) {
-            uint4 a = make_uint4(0u, 0u, 0u, 0u);
-            if (col < K) a = *reinterpret_cast<const uint4 *>(row + col);
-            r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
-        } else {
-            const unsigned short *p = reinterpret_cast<const unsigned short *>(row);
+    }
+    __device__ __forceinline__ void take(const T *row, int col, int K, bool wide, Raw8<T> &r) const {
+        if constexpr (kVec) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = col + 2 * i < K ? p[col + 2 * i] : 0u;
-                const uint32_t hi = col + 2 * i + 1 < K ? p[col + 2 * i + 1] : 0u;
-                r.w[i] = lo | hi << 16;
+            for (int i = 0; i < kWords; ++i) r.w[i] = c[i];
+        } else {
+            const int skip = wide ? (int)(reinterpret_cast<uintptr_t>(row + col) & 15) : 0;
+            const int have = min(8, K - col) * (int)sizeof(T);
+            words_from_bit(c, 8 * skip, r.w);
+            if (have < 8 * (int)sizeof(T)) {
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) {
+                    if (4 * i >= have) r.w[i] = 0u;
+                    if (sizeof(T) == 2 && 4 * i + 2 == have) r.w[i] &= 0xFFFFu;
+                }
             }
         }
     }
-}
+};
 
 __device__ __forceinline__ void to_float(const Raw8<float> &r, float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = r.v[i];
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
 }
 __device__ __forceinline__ void to_float(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
 #pragma unroll
@@ -99,31 +135,71 @@ __device__ __forceinline__ void to_float(const Raw8<__half> &r, float (&v)[8]) {
 
 template <bool kVec, class T>
 __device__ __forceinline__ void load8(const T *row, int col, int K, float (&v)[8]) {
+    Fetch8<kVec, T> f;
     Raw8<T> r;
-    load8<kVec>(row, col, K, r);
+    f.template load<false>(row, col, K);
+    f.take(row, col, K, false, r);
     to_float(r, v);
 }
 
+// Stores eight values per lane, nothing past K.  Every lane of the warp takes
+// part, with columns eight apart.  Without kVec the row starts anywhere: a
+// lane writes the 16-byte granules that begin among its own values, the last
+// of them with the next lane's first values, and single values only at the
+// warp's and the row's ends.
 template <bool kVec, class T>
 __device__ __forceinline__ void store8(T *row, int col, int K, const float (&v)[8]) {
-    if constexpr (kVec) {
-        if (col < K) {
-            if constexpr (sizeof(T) == 4) {
-                // One 32-byte store: a sector is written at once, not in halves.
-                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + col), "f"(v[0]),
-                             "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                             : "memory");
-            } else {
-                uint32_t w[4];
+    constexpr int kWords = sizeof(T) * 2, kEach = 16 / sizeof(T);  // values of a granule
+    uint32_t d[kWords];
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = mx_pack2<T>(v[2 * i], v[2 * i + 1]);
-                *reinterpret_cast<uint4 *>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+        for (int i = 0; i < 8; ++i) d[i] = __float_as_uint(v[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < K) row[col + i] = mx_from_float<T>(v[i]);
+        for (int i = 0; i < 4; ++i) d[i] = mx_pack2<T>(v[2 * i], v[2 * i + 1]);
+    }
+    if constexpr (kVec) {
+        if (col >= K) return;
+        if constexpr (sizeof(T) == 4) {
+            // One 32-byte store: a sector is written at once, not in halves.
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + col), "r"(d[0]),
+                         "r"(d[1]), "r"(d[2]), "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7])
+                         : "memory");
+        } else {
+            *reinterpret_cast<uint4 *>(row + col) = make_uint4(d[0], d[1], d[2], d[3]);
+        }
+    } else {
+        const int lane = threadIdx.x & 31;
+        const int skip = (int)(reinterpret_cast<uintptr_t>(row + col) & 15) / (int)sizeof(T);
+        const int head = skip ? kEach - skip : 0;  // values before the first granule that begins here
+        uint32_t e[kWords + 4], g[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) e[i] = d[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[kWords + i] = __shfl_down_sync(kFull, d[i], 1);
+        words_from_bit(e, 8 * (int)sizeof(T) * head, g);
+        auto one = [&](int j) {
+            if (col + j < K) row[col + j] = mx_from_float<T>(v[j]);
+        };
+        // The values before the first granule are the previous lane's to
+        // write where it writes that granule whole.
+        const bool mine = lane == 0 || col + head > K;
+#pragma unroll
+        for (int j = 0; j < kEach - 1; ++j)
+            if (j < head && mine) one(j);
+#pragma unroll
+        for (int i = 0; i < 8 / kEach; ++i) {
+            const int first = head + i * kEach;
+            const bool whole = first + kEach <= 8 || lane != 31;
+            if (whole && col + first + kEach <= K) {
+                *reinterpret_cast<uint4 *>(row + col + first) =
+                    make_uint4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j >= first && j < first + kEach) one(j);
+            }
+        }
     }
 }
 
@@ -229,8 +305,11 @@ __device__ __forceinline__ float2 silu2(float2 x) {
 // rows also keep four independent loads in flight per lane).  Rows past the
 // last one get zero scale bytes and no codes.  blockIdx.x: 32 row groups per
 // 128-row block; blockIdx.y and the warp: the column chunk.
+// CTAs per SM that the registers have to allow: SwiGLU 4, and 3 unaligned
+// (4099 x 11008 bf16: 37.5 -> 36.3 us; 8192 x 4095: 51.0, 42.7 with 1, 3);
+// else 4 unaligned (8192 x 4095 bf16 to 8-bit codes: 26.8 -> 22.9).
 template <class T, bool kVec, bool kSwiGLU>
-__global__ void __launch_bounds__(256, kSwiGLU ? 4 : 1)  // (four CTAs: 37.5 -> 36.3 us on 4099 x 11008 bf16)
+__global__ void __launch_bounds__(256, kSwiGLU ? (kVec ? 4 : 3) : (kVec ? 1 : 4))
     mx_quantize_kernel(const T *__restrict__ x, long long x_stride, const T *__restrict__ up, long long up_stride,
                        uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int K, int rows, int bits) {
     const int Kp = mx_padded(K), nkt = Kp / kMxPadK;
@@ -243,22 +322,36 @@ __global__ void __launch_bounds__(256, kSwiGLU ? 4 : 1)  // (four CTAs: 37.5 -> 
     const long long row0 = (long long)block * kMxTileRows + r;
     pdl_wait();
     if (2 * c >= nkt) return;
-    Raw8<T> raw[4];
+    // Neither the first row nor the last one is among the four; K >= 8: a
+    // neighbour is 16 bytes at least.
+    const bool wide = row0 > 0 && K >= 8 && ((rows - 1 - row0) % 32 != 0 || rows - row0 > kMxTileRows);
+    Fetch8<kVec, T> fx[4];
     const T *px = x + row0 * x_stride;
+    auto width = [&](int i) { return row0 + 32 * i < rows ? K : 0; };
+    auto load4 = [&](const T *from, long long stride, Fetch8<kVec, T>(&f)[4]) {
+        if (kVec || wide) {  // (one branch around all of them keeps them side by side)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load8<kVec>(px + 32 * i * x_stride, col, row0 + 32 * i < rows ? K : 0, raw[i]);
+            for (int i = 0; i < 4; ++i) f[i].template load<true>(from + 32 * i * stride, col, width(i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i].template load<false>(from + 32 * i * stride, col, width(i));
+        }
+    };
+    load4(px, x_stride, fx);
     uint32_t p = 0;
     uint8_t *pc = codes + row0 * code_row;
     if constexpr (kSwiGLU) {
-        Raw8<T> rup[4];
+        Fetch8<kVec, T> fu[4];
         const T *pu = up + row0 * up_stride;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load8<kVec>(pu + 32 * i * up_stride, col, row0 + 32 * i < rows ? K : 0, rup[i]);
+        load4(pu, up_stride, fu);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            Raw8<T> rx, ru;
             float v[8], u[8];
-            to_float(raw[i], v);
-            to_float(rup[i], u);
+            fx[i].take(px + 32 * i * x_stride, col, width(i), wide, rx);
+            fu[i].take(pu + 32 * i * up_stride, col, width(i), wide, ru);
+            to_float(rx, v);
+            to_float(ru, u);
 #pragma unroll
             for (int j = 0; j < 8; j += 2) {
                 const float2 f =
@@ -271,9 +364,11 @@ __global__ void __launch_bounds__(256, kSwiGLU ? 4 : 1)  // (four CTAs: 37.5 -> 
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            Raw8<T> rx;
             float v[8];
-            to_float(raw[i], v);
-            p |= quantize8(v, block_amax(raw[i], v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+            fx[i].take(px + 32 * i * x_stride, col, width(i), wide, rx);
+            to_float(rx, v);
+            p |= quantize8(v, block_amax(rx, v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
                  << (8 * i);
         }
     }
@@ -324,21 +419,30 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
         return;
     }
     constexpr int kKept = kVals > 0 ? kVals : 1;
+    const bool wide = row > 0 && row < a.rows - 1 && K >= 8;
     // Groups are loaded four at a time at most, x and residual together.
     auto load_h = [&](int c0, float (&v)[kKept][8]) {
-        Raw8<T> rx[kKept], rr[kKept];
+        Fetch8<kVec, T> fx[kKept], fr[kKept];
+        auto load_all = [&](const T *from, Fetch8<kVec, T>(&f)[kKept]) {
+            if (kVec || wide) {
 #pragma unroll
-        for (int i = 0; i < kKept; ++i) load8<kVec>(x, c0 + i * step + 8 * threadIdx.x, K, rx[i]);
-        if (res) {
+                for (int i = 0; i < kKept; ++i) f[i].template load<true>(from, c0 + i * step + 8 * threadIdx.x, K);
+            } else {
 #pragma unroll
-            for (int i = 0; i < kKept; ++i) load8<kVec>(res, c0 + i * step + 8 * threadIdx.x, K, rr[i]);
-        }
+                for (int i = 0; i < kKept; ++i) f[i].template load<false>(from, c0 + i * step + 8 * threadIdx.x, K);
+            }
+        };
+        load_all(x, fx);
+        if (res) load_all(res, fr);
 #pragma unroll
         for (int i = 0; i < kKept; ++i) {
-            to_float(rx[i], v[i]);
+            Raw8<T> r;
+            fx[i].take(x, c0 + i * step + 8 * threadIdx.x, K, wide, r);
+            to_float(r, v[i]);
             if (res) {
                 float u[8];
-                to_float(rr[i], u);
+                fr[i].take(res, c0 + i * step + 8 * threadIdx.x, K, wide, r);
+                to_float(r, u);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] += u[j];
             }
@@ -442,8 +546,11 @@ __global__ void __launch_bounds__(256)
     const int col = 256 * c + 8 * lane, kt = 2 * c + (lane >> 4);
     const long long row0 = (long long)block * kMxTileRows + r;
     pdl_wait();
-    if (kt >= nkt || row0 >= rows) return;
-    const uint4 w = *reinterpret_cast<const uint4 *>(scales + ((size_t)block * nkt + kt) * kMxTileBytes + 16 * r);
+    if (2 * c >= nkt || row0 >= rows) return;
+    const bool inside = kt < nkt;  // (the warp's second half may lie past the last tile)
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (inside)
+        w = *reinterpret_cast<const uint4 *>(scales + ((size_t)block * nkt + kt) * kMxTileBytes + 16 * r);
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
     const size_t code_row = (size_t)Kp * kBits / 8;
     const uint8_t *p = codes + row0 * code_row + (size_t)col * kBits / 8;
@@ -451,7 +558,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         q[i] = make_uint2(0u, 0u);
-        if (row0 + 32 * i < rows) {
+        if (inside && row0 + 32 * i < rows) {
             if (kBits == 4)
                 q[i].x = *reinterpret_cast<const uint32_t *>(p + 32 * i * code_row);
             else
@@ -521,9 +628,13 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
     // us); for many rows of a 16-bit type four groups, where they leave four
     // warps.  8192 x 4096 bf16 with a residual: 52.0, 38.1, 37.6 us with one,
     // two, four groups; 4096 x 4096 fp32: 34.9 with one, 35.9 with two, 37.8
-    // with four.
+    // with four.  Unaligned rows have more fixed work: two groups where the
+    // aligned ones have one (4096 x 4095 fp32: 59.7, 45.3, 62.5 with one, two,
+    // four; 30000 x 1117 fp16: 86.1, 82.7, 111; 8192 x 4095 bf16: 84.4, 64.1,
+    // 62.1).
     int vals = 1;
     if (a.rows > c.num_sms && sizeof(T) == 2) vals = Kp >= 4096 ? 4 : Kp >= 2048 ? 2 : 1;
+    if (a.rows > c.num_sms && !vec && vals == 1) vals = 2;
     while (vals < 4 && Kp > 8 * 1024 * vals) vals *= 2;
     const bool kept = Kp <= 8 * 1024 * vals;
     int threads = kept ? (Kp / 8 + vals - 1) / vals : 1024;

@@ -307,6 +307,81 @@ def test_swiglu(rows, K, bits, name):
     assert untouched()
 
 
+def _rows_at(a, name, offset, gap):
+    """Rows that start `offset` elements past a 512-byte boundary, `gap` elements between them, NaN all around."""
+    torch = _torch()
+    rows, K = a.shape
+    n = rows * (K + gap) - gap
+    buf = torch.full((GUARD + n + GUARD,), float("nan"), dtype=_dtype(name), device="cuda")
+    view = buf[GUARD + offset:][:n + gap].as_strided((rows, K), (K + gap, 1))
+    view.copy_(torch.from_numpy(a.astype(np.float32)).cuda())
+
+    def surroundings_ok():
+        b = buf.clone()
+        b[GUARD + offset:][:n + gap].as_strided((rows, K), (K + gap, 1)).fill_(float("nan"))
+        return bool(b.isnan().all())
+
+    return view, view.double().cpu().numpy(), surroundings_ok
+
+
+# Rows that end before, on and past a granule of 16 bytes, a scale block, a warp's 256 values; one, two and three rows
+# (no neighbours, one, two) and enough for several 128-row blocks.
+PLACES = [(3, 1, 0), (3, 5, 0), (1, 9, 0), (2, 17, 1), (140, 23, 0), (70, 31, 2), (131, 33, 5), (3, 255, 0), (3, 257, 0),
+          (257, 260, 0), (5, 516, 3), (6, 1119, 0)]
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("offset", range(8))
+@pytest.mark.parametrize("rows,K,gap", PLACES)
+def test_rows_that_start_anywhere(rows, K, gap, offset, name):
+    q, torch = _q(), _torch()
+    g = _rng(rows, K, offset, 5)
+    a, b = _values(g, rows, K), 4 * g.standard_normal((rows, K))
+    x, xv, _ = _rows_at(a, name, offset, gap)
+    r, rv, _ = _rows_at(b, name, (3 * offset + 1) % 8, gap + 1)
+    bits = 4 if offset & 1 else 8
+
+    mx = q.mx_quantize(x, bits=bits)
+    codes, byte = ref.quantize(xv, bits)
+    got, got_byte, _ = _host(mx)
+    assert np.array_equal(got_byte, byte) and np.array_equal(got, codes)
+    _assert_padding(mx)
+
+    y, _, clean = _rows_at(np.zeros((rows, K)), name, offset, gap)
+    q.mx_dequantize(mx, out=y)
+    want = torch.from_numpy(ref.values(codes, byte, bits)[:, :K]).to(torch.float32).to(x.dtype)
+    assert torch.equal(y.cpu(), want) and clean()
+
+    v = ref.swiglu(rv, xv)
+    mx = q.mx_swiglu(r, x, bits=bits)
+    _assert_rounds(mx, v, 1e-6 * np.abs(v) + 1e-36 * np.abs(xv))
+    _assert_padding(mx)
+
+    w, wv, _ = _rows_at(1 + 0.3 * g.standard_normal((1, K)), "float32" if offset & 2 else name, (5 * offset) % 8, 0)
+    h, _, clean = _rows_at(np.zeros((rows, K)), name, (offset + 3) % 8, gap)
+    mx, _ = q.mx_rmsnorm(x, w[0], eps=1e-5, residual=r, bits=bits, h_out=h)
+    v, _ = ref.rmsnorm(xv, wv[0], float(np.float32(1e-5)), rv)
+    _assert_rounds(mx, v, 3e-6 * np.abs(v))
+    _assert_padding(mx)
+    assert torch.equal(h, (x.float() + r.float()).to(x.dtype)) and clean()
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("K", [1001, 4095, 9001, 40001])     # one, two and four groups a thread, and read twice
+def test_rmsnorm_of_many_unaligned_rows(K, name):
+    q, torch = _q(), _torch()
+    g = _rng(K, 6)
+    rows = 180
+    x, xv = _dev(_values(g, rows, K), name)
+    r, rv = _dev(4 * g.standard_normal((rows, K)), name)
+    w, wv = _dev(1 + 0.3 * g.standard_normal(K), name)
+    mx, h = q.mx_rmsnorm(x, w, eps=1e-5, residual=r, h_out=torch.empty_like(x))
+    v, _ = ref.rmsnorm(xv, wv, float(np.float32(1e-5)), rv)
+    _assert_rounds(mx, v, 3e-6 * np.abs(v))
+    _assert_padding(mx)
+    assert torch.equal(h, (x.float() + r.float()).to(x.dtype))
+
+
 # Products.
 
 def _random_mx(g, rows, K, bits, spread=6):
