@@ -391,8 +391,10 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 // Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.
 // ---------------------------------------------------------------------------
 
-constexpr int kPairThreads = 736;  // operand copies, MMA issuer, 2 x 4 scale warps, 3 x 4 epilogue warps, scale copies
-constexpr int kPairEpiWarp = 10, kPairScaleProducer = 22;
+// Operand copies, MMA issuer, 2 x 4 scale warps, 3 x 4 epilogue warps, scale
+// copies, and a second warp for each kind of copy.
+constexpr int kPairThreads = 800;
+constexpr int kPairEpiWarp = 10, kPairCopyWarp = 22;
 constexpr int kPairEpiWarps = 12;  // three for each lane quarter: the accumulators share three blocks of 32 columns
 constexpr int kPairTok = 256;
 constexpr int kPairStages = 6;
@@ -507,7 +509,8 @@ __device__ __forceinline__ void mm_st4(uint32_t taddr, uint4 v) {
 // multicast to both.  What was measured on the way (8192 tokens 4096 -> 11008
 // in 4 bits): scales by tcgen05.cp 230 us, by scale warps whose arrival
 // releases at cluster scope 326, by the plain arrival 162, copies issued by
-// lanes 142, one barrier a stage 130, shared columns read first 118.
+// lanes 142, one barrier a stage 130, shared columns read first 118, the
+// issuing loop unrolled 115.
 template <bool kX8>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_mm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -565,12 +568,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp == 0 || warp == kPairScaleProducer) {
-        // Two warps copy the stages in, one copy per lane and the lanes by
+    if (warp == 0 || warp >= kPairCopyWarp) {
+        // Two warps copy a stage in, one copy per lane and the lanes by
         // one instruction (a copy holds the thread that issues it for some
         // 475 cycles): the first the weights and the tokens, the other the
         // scales of the weights (lane 0) and of the tokens (up to three).
-        const bool operands = warp == 0;
+        // Two such pairs of warps take the stages in turn, since that is
+        // longer than the MMAs of a small tile of tokens (300 tokens 4096 ->
+        // 4096, 8 bits: 12.6 -> 11.8 us).
+        const bool operands = warp == 0 || warp == kPairCopyWarp + 1;
+        const int group = warp > kPairCopyWarp;
         int s = 0;
         uint32_t ph = 1;  // a fresh barrier's previous phase counts as done
         long long n = 0;  // stages issued
@@ -590,6 +597,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                             : x_scales + (size_t)(xt + lane - 1) * nkt * kMxTileBytes;
             const bool mine = operands ? lane < 2 : lane == 0 ? nw != 0 : lane <= nx;
             for (int c = 0; c < chunks; ++c, ++n) {
+                if (((int)n & 1) != group) {
+                    if (++s == kPairStages) s = 0, ph ^= 1u;
+                    continue;
+                }
                 ok = mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) {
@@ -650,6 +661,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int before = it - (shared ? 1 : 2);
                 if (before >= 0)
                     ok = mbar_spin_abortable(&acc_free[before & 1], (before >> 1) & 1, wait_limit, &abort_flag);
+#pragma unroll 2  // (a jump back costs some 200 cycles: 8192 tokens 4096 -> 11008, 4 bits: 118.0 -> 115.4 us)
                 for (int c = 0; c < chunks && ok; ++c) {
                     if (!ready) ok = mbar_spin_abortable(&full[s], ph, wait_limit, &abort_flag);
                     if (!ok) break;
