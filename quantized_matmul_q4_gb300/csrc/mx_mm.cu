@@ -291,6 +291,9 @@ __global__ void __launch_bounds__(kMmThreads, 2)
         __syncwarp();
     } else if (warp == 1) {
         if (lane == 0) {
+            // (A jump back costs some 200 cycles: one token 4096 -> 4096, 8 bits, 5.30
+            // us as a loop, 5.00 unrolled; 4096 -> 22016 13.7, 12.7.)
+#pragma unroll 4
             for (int c = 0; c < chunks; ++c) {
                 const int s = c % L::kStages;
                 if (!mbar_spin_abortable(&full[s], (c / L::kStages) & 1, wait_limit, &abort_flag)) {
