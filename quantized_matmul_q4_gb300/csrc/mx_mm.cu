@@ -399,34 +399,37 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 constexpr int kPairThreads = 800;
 constexpr int kPairEpiWarp = 10, kPairCopyWarp = 22;
 constexpr int kPairEpiWarps = 12;  // three for each lane quarter: the accumulators share three blocks of 32 columns
-constexpr int kPairTok = 256;
-constexpr int kPairStages = 6;
-constexpr int kPairXTiles = 3;     // 128-row scale tiles that the tokens of a tile touch at most
-
-template <bool kX8>
+// kSub: blocks of 128 bytes of K per row and stage.  A stage costs its warps
+// some 400 cycles each besides the MMAs, more than four MMAs of a small tile
+// last: tiles of up to 128 tokens take two blocks a stage.
+template <bool kX8, int kSub>
 struct PairLayout {
-    static constexpr int kStageK = kX8 ? 128 : 256;
+    static constexpr int kTok = 256 / kSub;
+    static constexpr int kStages = kSub == 1 ? 6 : 4;
+    static constexpr int kXTiles = kSub == 1 ? 3 : 2;  // 128-row scale tiles that a tile's tokens touch at most
+    static constexpr int kStageK = kSub * (kX8 ? 128 : 256);
     static constexpr int kScaleTiles = kStageK / 128;
-    static constexpr uint32_t w_tx = kX8 ? kMmWBytes / 2 : kMmWBytes;
-    static constexpr uint32_t off_x = kMmWBytes;
-    static constexpr uint32_t off_sw = off_x + kPairTok / 2 * 128;
+    static constexpr uint32_t w_tx = kX8 ? kMmWBytes / 2 : kMmWBytes;  // of a block
+    static constexpr uint32_t x_block = kTok / 2 * 128;
+    static constexpr uint32_t off_x = kSub * kMmWBytes;
+    static constexpr uint32_t off_sw = off_x + kSub * x_block;
     static constexpr uint32_t off_sx = off_sw + kScaleTiles * kMxTileBytes;
-    static constexpr uint32_t stage = (off_sx + kPairXTiles * kScaleTiles * kMxTileBytes + 1023) / 1024 * 1024;
-    // Tensor memory: per 128 values of K the scales of a stage take 4 columns
-    // for w and 8 for x (256 tokens).
-    static constexpr int kScaleCols = kScaleTiles * 12;
-    static constexpr int kScaleBufs = 96 / kScaleCols < kPairStages ? 96 / kScaleCols : kPairStages;
-    static constexpr uint32_t off_bar = kPairStages * stage;
-    static constexpr int kBars = 3 * kPairStages + 5;
+    static constexpr uint32_t stage = (off_sx + kXTiles * kScaleTiles * kMxTileBytes + 1023) / 1024 * 1024;
+    // Tensor memory: accumulators of up to kTok columns at 0 and at kCol1,
+    // which share what reaches past kCol1, then the scale buffers: per 128
+    // values of K four columns for w and one for 32 tokens.
+    static constexpr int kCol1 = kSub == 1 ? 160 : 128;
+    static constexpr int kColScales = kCol1 + kTok;
+    static constexpr int kXCols = kTok / 32;
+    static constexpr int kScaleCols = kScaleTiles * (4 + kXCols);
+    static constexpr int kScaleRoom = (512 - kColScales) / kScaleCols;
+    static constexpr int kScaleBufs = kScaleRoom < kStages ? kScaleRoom : kStages;
+    static constexpr uint32_t off_bar = kStages * stage;
+    static constexpr int kBars = 3 * kStages + 5;
     static constexpr uint32_t total = off_bar + 8 * kBars + 16 + 1024;
     static_assert(total <= 232448, "shared memory");
-    static_assert(kScaleBufs >= 3 && kScaleBufs <= kPairStages, "scale buffers");
+    static_assert(kScaleBufs >= 3, "scale buffers");
 };
-
-// Tensor memory of a pair's CTA: accumulators of up to 256 columns at 0 and
-// at 160, which share what reaches past 160, then the scale buffers.
-constexpr int kPairCol1 = 160;
-constexpr int kPairColScales = 416;
 
 __device__ __forceinline__ void pair_tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
     asm volatile(
@@ -514,21 +517,21 @@ __device__ __forceinline__ void mm_st4(uint32_t taddr, uint4 v) {
 // releases at cluster scope 326, by the plain arrival 162, copies issued by
 // lanes 142, one barrier a stage 130, shared columns read first 118, the
 // issuing loop unrolled 115.
-template <bool kX8>
+template <bool kX8, int kSub>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_mm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                       const uint8_t *__restrict__ w_scales, const uint8_t *__restrict__ x_scales,
                       void *__restrict__ y, MxType type, int K, int N, int T, int tile_tok, int x_tiles, int row_tiles,
                       int tok_tiles, int *status, long long wait_limit, int withhold) {
-    using L = PairLayout<kX8>;
+    using L = PairLayout<kX8, kSub>;
     extern __shared__ uint8_t mm_smem_raw[];
     __shared__ volatile int abort_flag;
     const uint32_t raw = smem_addr(mm_smem_raw);
     uint8_t *smem = mm_smem_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = smem_addr(smem);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::off_bar), *empty = full + kPairStages;
-    uint64_t *scales_in = empty + kPairStages;  // a stage's scale tiles have landed in this CTA's shared memory
-    uint64_t *acc_full = scales_in + kPairStages, *acc_free = acc_full + 2;  // one of each per accumulator
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::off_bar), *empty = full + L::kStages;
+    uint64_t *scales_in = empty + L::kStages;  // a stage's scale tiles have landed in this CTA's shared memory
+    uint64_t *acc_full = scales_in + L::kStages, *acc_free = acc_full + 2;  // one of each per accumulator
     uint64_t *done = acc_free + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
 
@@ -539,10 +542,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const long long tiles = (long long)row_tiles * tok_tiles;
     const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
     // Blocks of 32 tokens that the two accumulators share.
-    const int blocks = tile_tok / 32, shared = max(0, blocks - kPairCol1 / 32);
+    const int blocks = tile_tok / 32, shared = max(0, blocks - L::kCol1 / 32);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kPairStages; ++s) {
+        for (int s = 0; s < L::kStages; ++s) {
             mbar_init(&full[s], 1 + 8);  // both CTAs' operands (bytes), 4 scale warps of each
             mbar_init(&empty[s], 1);
             mbar_init(&scales_in[s], 1);
@@ -585,23 +588,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t ph = 1;  // a fresh barrier's previous phase counts as done
         long long n = 0;  // stages issued
         bool ok = true;
-        const uint32_t tx = 2 * (L::w_tx + (uint32_t)tile_tok / 2 * 128);
+        const uint32_t tx = 2 * (L::w_tx + (uint32_t)tile_tok / 2 * 128);  // a block of both CTAs
+        const int blocks_k = (Kp + L::kStageK / kSub - 1) / (L::kStageK / kSub);
         const int w_all = (N + kMxTileRows - 1) / kMxTileRows, x_all = (T + kMxTileRows - 1) / kMxTileRows;
         for (long long i = pair; i < tiles && ok; i += pairs) {
             const PairTile t = pair_tile(i, row_tiles, tok_tiles, tile_tok);
             const int wrow = t.row0 + rank * kMmRows, xrow = t.tok0 + rank * (tile_tok / 2);
-            const CUtensorMap *map = lane ? &tm_x : &tm_w;
-            const int crow = lane ? xrow : wrow;
+            // Lanes 0 to kSub - 1: blocks of the weights, then of the tokens.
+            const bool of_x = lane >= kSub;
+            const int sub = of_x ? lane - kSub : lane;
+            const CUtensorMap *map = of_x ? &tm_x : &tm_w;
+            const int crow = of_x ? xrow : wrow;
+            const uint32_t to = of_x ? L::off_x + sub * L::x_block : sub * kMmWBytes;
             // Scale tiles: this CTA's rows (none past the last row) and all
             // of the tile's tokens.
             const int wt = wrow / kMxTileRows, nw = wt < w_all ? 1 : 0;
             const int xt = t.tok0 / kMxTileRows, nx = min(x_tiles, x_all - xt);
             const uint8_t *from = lane == 0 ? w_scales + (size_t)wt * nkt * kMxTileBytes
                                             : x_scales + (size_t)(xt + lane - 1) * nkt * kMxTileBytes;
-            const bool mine = operands ? lane < 2 : lane == 0 ? nw != 0 : lane <= nx;
+            const bool mine = operands ? lane < 2 * kSub : lane == 0 ? nw != 0 : lane <= nx;
             for (int c = 0; c < chunks; ++c, ++n) {
                 if (((int)n & 1) != group) {
-                    if (++s == kPairStages) s = 0, ph ^= 1u;
+                    if (++s == L::kStages) s = 0, ph ^= 1u;
                     continue;
                 }
                 ok = mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag);
@@ -617,10 +625,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const uint32_t off = s * L::stage;
                 if (operands) {
                     const uint32_t bar = map_to_rank(smem_addr(&full[s]), 0);  // the leader's
-                    if (here && lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                    if (here && mine)
-                        pair_tma_2d(sbase + off + (lane ? L::off_x : 0u), map,
-                                    kX8 ? c * L::kStageK : c * (L::kStageK / 2), crow, bar);
+                    const int here_k = min(kSub, blocks_k - c * kSub);
+                    if (here && lane == 0 && rank == 0) mbar_arrive_expect_tx(&full[s], here_k * tx);
+                    // (128 values or, packed, 128 bytes.)
+                    if (here && mine && sub < here_k)
+                        pair_tma_2d(sbase + off + to, map, (c * kSub + sub) * 128, crow, bar);
                 } else {
                     const int kt = c * L::kScaleTiles;
                     const uint32_t sbytes = (uint32_t)min(L::kScaleTiles, nkt - kt) * kMxTileBytes;
@@ -631,16 +640,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                  from + (size_t)kt * kMxTileBytes, sbytes, &scales_in[s]);
                 }
                 __syncwarp();
-                if (++s == kPairStages) s = 0, ph ^= 1u;
+                if (++s == L::kStages) s = 0, ph ^= 1u;
             }
         }
         // No copy may still be writing shared memory at exit: the MMAs wait
         // for every stage, and their completion is awaited here.  After a
         // time-out, which leaves copies that nobody waits for, give them far
         // longer than a copy takes.
-        for (int k = 0; k < kPairStages && ok; ++k) {
+        for (int k = 0; k < L::kStages && ok; ++k) {
             ok = __all_sync(0xffffffffu, mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag) ? 1 : 0) != 0;
-            if (++s == kPairStages) s = 0, ph ^= 1u;
+            if (++s == L::kStages) s = 0, ph ^= 1u;
         }
         if (!ok) {
             if (lane == 0) abort_flag = 1;
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             bool ok = true, ready = false;
             const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + L::off_x);
             for (long long i = pair; i < tiles && ok; i += pairs, ++it) {
-                const uint32_t d = tmem + (it & 1) * kPairCol1;
+                const uint32_t d = tmem + (it & 1) * L::kCol1;
                 // The epilogue frees what this accumulator shares with the
                 // previous tile's first of all; without shared columns the
                 // one two tiles back has to be free.
@@ -671,18 +680,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     mm_fence_after();
                     // (Descriptor addresses count 16 bytes and stay below 256 KB.)
                     const uint64_t ad = ad0 + (uint32_t)s * (L::stage >> 4), bd = bd0 + (uint32_t)s * (L::stage >> 4);
-                    const uint32_t sw = tmem + kPairColScales + buf * L::kScaleCols, sx = sw + 4 * L::kScaleTiles;
-                    const bool second = L::kScaleTiles == 1 || c * L::kScaleTiles + 1 < nkt;
+                    const uint32_t sw = tmem + L::kColScales + buf * L::kScaleCols, sx = sw + 4 * L::kScaleTiles;
+                    const int kts = nkt - c * L::kScaleTiles;
                     uint64_t *mine = &empty[s];
-                    if (++s == kPairStages) s = 0, ph ^= 1u;
+                    if (++s == L::kStages) s = 0, ph ^= 1u;
                     if (++buf == L::kScaleBufs) buf = 0;
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int j = kX8 ? 0 : m / 2, sf = kX8 ? m : 2 * (m % 2);
-                        if (m < 2 || second)
-                            mx_mma<kX8, 2>(d, ad + 2 * m, bd + 2 * m, mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows),
-                                           sw + 4 * j, sx + 8 * j, (c | m) != 0);
-                        if (m == 2) ready = mbar_test_wait(&full[s], ph);
+                    for (int m = 0; m < 4 * kSub; ++m) {
+                        // 32 bytes of each row per MMA: with kX8 32 values and one
+                        // scale byte, else 64 values and two.
+                        const int sub = m / 4, q = m % 4, j = kX8 ? sub : m / 2, sf = kX8 ? q : 2 * (q % 2);
+                        if (j == 0 || j < kts)
+                            mx_mma<kX8, 2>(d, ad + sub * (kMmWBytes >> 4) + 2 * q, bd + sub * (L::x_block >> 4) + 2 * q,
+                                           mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows), sw + 4 * j, sx + L::kXCols * j,
+                                           (c | m) != 0);
+                        if (m == 4 * kSub - 2) ready = mbar_test_wait(&full[s], ph);
                     }
                     pair_commit(mine);
                 }
@@ -705,7 +717,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // six per stage against four MMAs of about 128.)
         // Two groups of four take the stages in turn: an iteration lasts about
         // as long as a stage's MMAs.
-        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPairColScales;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + L::kColScales;
         const uint32_t full0 = map_to_rank(smem_addr(full), 0);
         const int group = (warp - 2) >> 2;
         int n = 0;
@@ -715,12 +727,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int skip = pair_tile(i, row_tiles, tok_tiles, tile_tok).tok0 % kMxTileRows / 32;
             for (int c = 0; c < chunks; ++c, ++n) {
                 if ((n & 1) != group) continue;
-                const int s = n % kPairStages, buf = n % L::kScaleBufs;
-                ok = mbar_wait_abortable(&scales_in[s], (n / kPairStages) & 1, wait_limit, &abort_flag);
+                const int s = n % L::kStages, buf = n % L::kScaleBufs;
+                ok = mbar_wait_abortable(&scales_in[s], (n / L::kStages) & 1, wait_limit, &abort_flag);
                 if (n >= L::kScaleBufs) {
                     // The MMAs that last read this buffer.
                     const int m = n - L::kScaleBufs;
-                    ok = ok && mbar_wait_abortable(&empty[m % kPairStages], (m / kPairStages) & 1, wait_limit,
+                    ok = ok && mbar_wait_abortable(&empty[m % L::kStages], (m / L::kStages) & 1, wait_limit,
                                                    &abort_flag);
                 }
                 if (!__all_sync(0xffffffffu, ok)) {
@@ -746,7 +758,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     // MMA takes scales from a multiple of four columns on.
                     uint4 u = x_words(0), v = x_words(1);
                     if (skip) {
-                        const uint4 w = x_words(2);
+                        const uint4 w = kSub == 1 ? x_words(2) : make_uint4(0u, 0u, 0u, 0u);
                         if (skip == 1) {
                             u = make_uint4(u.y, u.z, u.w, v.x), v = make_uint4(v.y, v.z, v.w, w.x);
                         } else if (skip == 2) {
@@ -755,8 +767,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             u = make_uint4(u.w, v.x, v.y, v.z), v = make_uint4(v.w, w.x, w.y, w.z);
                         }
                     }
-                    mm_st4(col + 4 * L::kScaleTiles + 8 * j, u);
-                    mm_st4(col + 4 * L::kScaleTiles + 8 * j + 4, v);
+                    mm_st4(col + 4 * L::kScaleTiles + L::kXCols * j, u);
+                    if (kSub == 1) mm_st4(col + 4 * L::kScaleTiles + L::kXCols * j + 4, v);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 mm_fence_before();
@@ -779,7 +791,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 break;
             }
             mm_fence_after();
-            const uint32_t col0 = tmem + ((uint32_t)(32 * q) << 16) + (it & 1) * kPairCol1;
+            const uint32_t col0 = tmem + ((uint32_t)(32 * q) << 16) + (it & 1) * L::kCol1;
             const int n = t.row0 + rank * kMmRows + 32 * q + lane;
             auto free_accumulator = [&]() {
                 mm_fence_before();
@@ -889,16 +901,15 @@ cudaError_t launch_split(const LaunchCtx &c, MxType type, const MxMatmulArgs &a)
                               c.status, c.wait_limit, c.withhold);
 }
 
-template <bool kX8>
-cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
-    using L = PairLayout<kX8>;
+template <bool kX8, int kSub>
+cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a, const MxPairTiles &g) {
+    using L = PairLayout<kX8, kSub>;
     const int Kp = mx_padded(a.K);
-    const MxPairTiles g = mx_pair_tiles(a.T, a.N, (Kp + L::kStageK - 1) / L::kStageK, a.x_bits, c.num_sms);
     alignas(64) CUtensorMap tm_w, tm_x;
     if (!map_codes(&tm_w, a.w_codes, a.N, Kp, 4, kX8, kMmRows) ||
         !map_codes(&tm_x, a.x_codes, a.T, Kp, a.x_bits, false, g.tile_tok / 2))
         return cudaErrorInvalidValue;
-    auto kernel = mx_mm_pair_kernel<kX8>;
+    auto kernel = mx_mm_pair_kernel<kX8, kSub>;
     cudaError_t e = ensure_smem(kernel, L::total);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)g.row_tiles * g.tok_tiles;
@@ -923,9 +934,12 @@ cudaError_t launch_pair(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) 
 
 template <bool kX8>
 cudaError_t launch_mm_tokens(const LaunchCtx &c, MxType type, const MxMatmulArgs &a) {
-    constexpr int kStageK = PairLayout<kX8>::kStageK;
-    if (mx_use_pairs(a.T, a.N, (mx_padded(a.K) + kStageK - 1) / kStageK, a.x_bits, c.num_sms))
-        return launch_pair<kX8>(c, type, a);
+    constexpr int kStageK = PairLayout<kX8, 1>::kStageK;
+    const int stages = (mx_padded(a.K) + kStageK - 1) / kStageK;
+    if (mx_use_pairs(a.T, a.N, stages, a.x_bits, c.num_sms)) {
+        const MxPairTiles g = mx_pair_tiles(a.T, a.N, stages, a.x_bits, c.num_sms);
+        return g.tile_tok <= 128 ? launch_pair<kX8, 2>(c, type, a, g) : launch_pair<kX8, 1>(c, type, a, g);
+    }
     if (a.T <= 16) return launch_split<kX8, 16>(c, type, a);
     if (a.T <= 64) return launch_split<kX8, 64>(c, type, a);
     return launch_split<kX8, 128>(c, type, a);
