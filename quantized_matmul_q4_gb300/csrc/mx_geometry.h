@@ -18,22 +18,23 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 // Estimates, in microseconds of a call, of the two forms of the product; the
 // form and the split with the lower estimate run.  `stages` are ring stages
 // of K (256 values with 4-bit x, 128 with 8-bit).  The constants are fitted
-// to some 300 pairs of measurements on GB300 (chains of calls in a CUDA
-// graph, 17 to 2048 tokens, K and N of 256 to 16384), where the choice costs
-// 0.7% on the mean against always the faster form; some of them, single CTAs
-// with K split / CTA pairs:
+// to 1144 measurements of 286 products on GB300 (chains of calls in a CUDA
+// graph, 17 to 2048 tokens, K and N of 256 to 16384, with 1, 2 and 4 times
+// the fewest tiles of tokens), where the choice costs 0.1% on the mean against
+// always the fastest; some of them, single CTAs with K split / CTA pairs:
 //   T    K        N       x     measured       estimated
-//   17   256   -> 4096    4     2.5 /  3.3      2.7 /  3.0
-//   64   4096  -> 4096    8     7.1 / 11.7      7.1 / 11.2
-//   64   2560  -> 6912    4     7.2 /  6.1      6.7 /  5.8
-//   128  1024  -> 4096    8     6.5 /  5.8      6.5 /  5.2
-//   128  4096  -> 4096    4     7.9 /  8.3      7.8 /  7.6
-//   128  4096  -> 11008   8    13.2 / 13.0     12.8 / 12.6
-//   256  1024  -> 1024    8     6.3 /  5.5      6.5 /  5.0
-//   256  8192  -> 8192    4    16.9 / 14.1     16.9 / 13.5
-//   420  11008 -> 4096    8    25.5 / 27.5     24.6 / 27.9
-//   512  4096  -> 11008   8    35.5 / 24.6     32.7 / 24.3
-//   1024 11008 -> 4096    8    39.1 / 29.6     36.3 / 30.9
+//   17   256   -> 4096    4     2.7 /  3.8      2.7 /  3.9
+//   64   4096  -> 4096    8     6.9 /  9.0      7.2 /  9.1
+//   64   2560  -> 6912    4     7.2 /  5.7      6.8 /  5.8
+//   128  1024  -> 4096    8     6.6 /  5.0      6.5 /  5.3
+//   128  4096  -> 4096    4     7.7 /  7.0      7.7 /  7.0
+//   128  4096  -> 11008   8    13.2 / 10.5     13.0 / 10.2
+//   200  4096  -> 4096    8    11.4 /  9.9     11.8 /  9.8
+//   256  1024  -> 1024    8     6.4 /  5.0      6.5 /  5.0
+//   256  8192  -> 8192    4    17.0 / 12.8     16.5 / 11.3
+//   420  11008 -> 4096    8    25.5 / 21.0     25.5 / 20.2
+//   512  4096  -> 11008   8    34.5 / 23.5     36.4 / 22.9
+//   1024 11008 -> 4096    8    39.5 / 30.2     38.8 / 29.2
 
 // Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
 // tile's K: rounds of two CTAs per SM through their stages, then the stores
@@ -42,10 +43,13 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 inline double mx_split_us(int row_tiles, int tok_tiles, int tokens, int stages, int S, int x_bits, int num_sms) {
     const long long ctas = (long long)row_tiles * tok_tiles * S, slots = 2LL * num_sms;
     const double tok = tokens < 128 ? tokens / 128.0 : 1.0;
-    const double stage = x_bits == 8 ? 0.29 + 0.08 * tok : 0.37 + 0.14 * tok;
-    const double end = S == 1 ? 2.5 * tok : 1.2 + (ctas <= num_sms ? 2.6 : 5.5) * tok;
+    const double stage = x_bits == 8 ? 0.34 + 0.05 * tok : 0.49;
+    // CTAs that have an SM to themselves fetch sums twice as fast; clusters of
+    // more than four are packed two to an SM well before the SMs run out.
+    const bool alone = ctas <= (S > 4 ? num_sms / 2 : num_sms);
+    const double end = S == 1 ? 3.55 * tok : 1.18 + (alone ? 2.81 : 5.79) * tok;
     const double rounds = (double)((ctas + slots - 1) / slots);
-    return 2.0 + rounds * (((stages + S - 1) / S) * stage + end) + (rounds - 1.0) * 2.0;
+    return 1.74 + rounds * (((stages + S - 1) / S) * stage + end) + (rounds - 1.0) * 2.57;
 }
 
 // The split with the lowest estimate: at most 8 CTAs, two stages to each.
@@ -70,13 +74,18 @@ struct MxPairTiles {
     int tile_tok, tok_tiles, row_tiles, x_tiles;
 };
 
+// Tiles of up to this many tokens take two of the ring stages that `stages`
+// counts as one.
+constexpr int kMxPairTwoBlocks = 128;
+
 // CTA pairs, one per two SMs.
 inline double mx_pair_us(const MxPairTiles &g, int stages, int x_bits, int num_sms) {
     const long long tiles = (long long)g.row_tiles * g.tok_tiles, pairs = num_sms > 1 ? num_sms / 2 : 1;
-    const double n = g.tile_tok / 256.0;
-    const double stage = x_bits == 8 ? 0.255 + 0.05 * n : 0.26 + 0.08 * n;
-    return 2.3 + 1.6 * n + 0.012 * (double)(tiles < pairs ? tiles : pairs) +
-           (double)((tiles + pairs - 1) / pairs) * stages * stage;
+    const double n = g.tile_tok / 256.0, waves = (double)((tiles + pairs - 1) / pairs);
+    const double in_stages =
+        g.tile_tok <= kMxPairTwoBlocks ? ((stages + 1) / 2) * (x_bits == 8 ? 0.332 + 0.061 * n : 0.381 + 0.066 * n)
+                                       : stages * (x_bits == 8 ? 0.155 + 0.121 * n : 0.231 + 0.059 * n);
+    return 3.07 + 1.52 * n + 0.013 * (double)(tiles < pairs ? tiles : pairs) + waves * in_stages + (waves - 1.0) * 0.36;
 }
 
 // As few tiles of tokens as there can be, or twice or four times as many

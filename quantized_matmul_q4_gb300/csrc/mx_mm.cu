@@ -404,7 +404,7 @@ constexpr int kPairEpiWarps = 12;  // three for each lane quarter: the accumulat
 // last: tiles of up to 128 tokens take two blocks a stage.
 template <bool kX8, int kSub>
 struct PairLayout {
-    static constexpr int kTok = 256 / kSub;
+    static constexpr int kTok = kSub == 1 ? 256 : kMxPairTwoBlocks;
     static constexpr int kStages = kSub == 1 ? 6 : 4;
     static constexpr int kXTiles = kSub == 1 ? 3 : 2;  // 128-row scale tiles that a tile's tokens touch at most
     static constexpr int kStageK = kSub * (kX8 ? 128 : 256);
@@ -938,7 +938,7 @@ cudaError_t launch_mm_tokens(const LaunchCtx &c, MxType type, const MxMatmulArgs
     const int stages = (mx_padded(a.K) + kStageK - 1) / kStageK;
     if (mx_use_pairs(a.T, a.N, stages, a.x_bits, c.num_sms)) {
         const MxPairTiles g = mx_pair_tiles(a.T, a.N, stages, a.x_bits, c.num_sms);
-        return g.tile_tok <= 128 ? launch_pair<kX8, 2>(c, type, a, g) : launch_pair<kX8, 1>(c, type, a, g);
+        return g.tile_tok <= kMxPairTwoBlocks ? launch_pair<kX8, 2>(c, type, a, g) : launch_pair<kX8, 1>(c, type, a, g);
     }
     if (a.T <= 16) return launch_split<kX8, 16>(c, type, a);
     if (a.T <= 64) return launch_split<kX8, 64>(c, type, a);

@@ -66,6 +66,8 @@ def test_pair_tiles(geo):
             # Blocks of 32 tokens that a tile's scales are shifted by: with a
             # shift eight columns are taken from three scale tiles, twelve words.
             assert all(s // 32 + tok // 32 <= 12 for s in starts)
+            # Tiles with two blocks of K a stage have room for two scale tiles.
+            assert tok > 128 or x_tiles <= 2
 
 
 def test_the_product_tests_reach_every_form(geo):
