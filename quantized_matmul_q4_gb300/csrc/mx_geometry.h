@@ -39,7 +39,7 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 // Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
 // tile's K: rounds of two CTAs per SM through their stages, then the stores
 // of y or, before them, the sum of the partial sums over the cluster.  (One
-// token, 4096 -> 22016, 8 bits: 14.4 us unsplit, 17.0 in two rounds of S = 3.)
+// token, 4096 -> 22016, 8 bits: 12.6 us unsplit, 15.8 in two rounds of S = 3.)
 inline double mx_split_us(int row_tiles, int tok_tiles, int tokens, int stages, int S, int x_bits, int num_sms) {
     const long long ctas = (long long)row_tiles * tok_tiles * S, slots = 2LL * num_sms;
     const double tok = tokens < 128 ? tokens / 128.0 : 1.0;
@@ -58,7 +58,7 @@ inline int mx_split(int row_tiles, int tok_tiles, int tokens, int stages, int x_
     double us = mx_split_us(row_tiles, tok_tiles, tokens, stages, 1, x_bits, num_sms);
     for (int S = 2; S <= kMxMaxSplit && 2 * S <= stages; ++S) {
         // Above 16 tokens shares of 16 to 28 rows are summed slowly: 128 tokens
-        // through 4096 x 4096 take 11.2, 13.3 and 11.6 us with S = 4, 6, 8.
+        // through 4096 x 4096 in 8 bits take 8.4, 12.5 and 11.3 us with S = 4, 6, 8.
         if (tokens > 16 && S > 4 && S < 8) continue;
         const double t = mx_split_us(row_tiles, tok_tiles, tokens, stages, S, x_bits, num_sms);
         if (t < us) us = t, best = S;
