@@ -497,11 +497,25 @@ __device__ __forceinline__ PairTile pair_tile(long long i, int row_tiles, int to
     return PairTile{in / width * 2 * kMmRows, (8 * g + in % width) * tile_tok};
 }
 
-// Four columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void mm_st4(uint32_t taddr, uint4 v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
+// 4, 8 or 16 columns of this thread's tensor-memory lane.
+template <int kN>
+__device__ __forceinline__ void mm_st(uint32_t taddr, const uint32_t (&r)[kN]) {
+    static_assert(kN == 4 || kN == 8 || kN == 16, "columns");
+    if constexpr (kN == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3])
+                     : "memory");
+    if constexpr (kN == 8)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                     : "memory");
+    if constexpr (kN == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+            "%15, %16};" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+            "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
 }
 
 // A cluster of two CTAs computes 256 weight rows x tile_tok tokens with
@@ -746,9 +760,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 mm_fence_after();
                 const uint8_t *st = smem + s * L::stage + 16 * lane;
                 const uint32_t col = t_lane + buf * L::kScaleCols;
+                uint32_t ws[4 * L::kScaleTiles], xs[L::kXCols * L::kScaleTiles];
 #pragma unroll
                 for (int j = 0; j < L::kScaleTiles; ++j) {
-                    mm_st4(col + 4 * j, *reinterpret_cast<const uint4 *>(st + L::off_sw + j * kMxTileBytes));
+                    auto put = [](uint32_t *to, uint4 f) { to[0] = f.x, to[1] = f.y, to[2] = f.z, to[3] = f.w; };
+                    put(ws + 4 * j, *reinterpret_cast<const uint4 *>(st + L::off_sw + j * kMxTileBytes));
                     auto x_words = [&](int k) {
                         return k < x_tiles ? *reinterpret_cast<const uint4 *>(
                                                  st + L::off_sx + (k * L::kScaleTiles + j) * kMxTileBytes)
@@ -767,9 +783,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             u = make_uint4(u.w, v.x, v.y, v.z), v = make_uint4(v.w, w.x, w.y, w.z);
                         }
                     }
-                    mm_st4(col + 4 * L::kScaleTiles + L::kXCols * j, u);
-                    if (kSub == 1) mm_st4(col + 4 * L::kScaleTiles + L::kXCols * j + 4, v);
+                    put(xs + L::kXCols * j, u);
+                    if (kSub == 1) put(xs + L::kXCols * j + 4, v);
                 }
+                mm_st(col, ws);
+                mm_st(col + 4 * L::kScaleTiles, xs);
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 mm_fence_before();
                 __syncwarp();
