@@ -153,6 +153,13 @@ __device__ __forceinline__ void mm_ld8(uint32_t taddr, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// True in one lane of the converged warp, the same one each time.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t mine;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(mine));
+    return mine != 0;
+}
+
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
@@ -290,25 +297,30 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                 if (i != withhold) (void)mbar_wait_bounded(&full[i % L::kStages], (i / L::kStages) & 1, wait_limit);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            // (A jump back costs some 200 cycles: one token 4096 -> 4096, 8 bits, 5.30
-            // us as a loop, 5.00 unrolled; 4096 -> 22016 13.7, 12.7.)
-#pragma unroll 4
-            for (int c = 0; c < chunks; ++c) {
-                const int s = c % L::kStages;
-                if (!mbar_spin_abortable(&full[s], (c / L::kStages) & 1, wait_limit, &abort_flag)) {
+        // The whole warp takes the loop and one lane issues, so that addresses
+        // and descriptors stay in uniform registers, where the MMAs want them.
+        const bool leader = elect_lane();
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c % L::kStages;
+            if (!__all_sync(0xffffffffu,
+                            mbar_spin_abortable(&full[s], (c / L::kStages) & 1, wait_limit, &abort_flag))) {
+                if (leader) {
                     abort_flag = 1;
                     flag_timeout(status);
-                    break;
                 }
-                mm_fence_after();
-                const uint32_t sa = sbase + s * L::stage;
-                const int kts = min(L::kScaleTiles, nkt - (c_lo + c) * L::kScaleTiles);
-                for (int j = 0; j < kts; ++j) {
+                break;
+            }
+            mm_fence_after();
+            const uint32_t sa = sbase + s * L::stage;
+            const int kts = min(L::kScaleTiles, nkt - (c_lo + c) * L::kScaleTiles);
+            const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + L::off_x);
+            if (leader) {
+#pragma unroll
+                for (int j = 0; j < L::kScaleTiles; ++j) {
+                    if (j >= kts) break;
                     scale_to_tmem(tmem + L::kColSw + 4 * j, scale_desc(sa + L::off_sw + j * kMxTileBytes));
                     scale_to_tmem(tmem + L::kColSx + 4 * j, scale_desc(sa + L::off_sx + j * kMxTileBytes));
                 }
-                const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + L::off_x);
                 // 32 bytes of each row per MMA: with kX8 32 values and one scale
                 // byte, else 64 values and two.
 #pragma unroll
@@ -320,10 +332,12 @@ __global__ void __launch_bounds__(kMmThreads, 2)
                 }
                 mm_commit(&empty[s]);
             }
-            // Whatever was issued completes before tensor memory is read or freed.
-            mm_commit(done);
-            (void)mbar_wait_bounded(done, 0, wait_limit);
+            __syncwarp();
         }
+        // Whatever was issued completes before tensor memory is read or freed.
+        if (leader) mm_commit(done);
+        __syncwarp();
+        (void)mbar_wait_bounded(done, 0, wait_limit);
         __syncwarp();
     }
     // (The producer and the issuer leave their branches through a reconverged
@@ -671,55 +685,67 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            // What this thread does between MMAs is time that the tensor pipe
+        if (rank == 0) {
+            // What this warp does between MMAs is time that the tensor pipe
             // may run dry (it queues little more than one MMA): one barrier
-            // per stage, tested while the stage before is being issued.
+            // per stage, tested as soon as the stage before is issued.  The
+            // whole warp takes the loop and one lane issues, so that addresses
+            // and descriptors stay in uniform registers, where the MMAs want
+            // them (8192 tokens 4096 -> 11008, 4 bits: 114.4 us with one lane
+            // in the loop, 111 so; 77 tokens 2560 -> 6912: 5.7, 5.25).
+            const bool leader = elect_lane();
             int s = 0, buf = 0, it = 0;
             uint32_t ph = 0;
             bool ok = true, ready = false;
             const uint64_t ad0 = sw128_desc(sbase), bd0 = sw128_desc(sbase + L::off_x);
+            auto spin = [&](uint64_t *bar, uint32_t phase) {
+                return __all_sync(0xffffffffu, mbar_spin_abortable(bar, phase, wait_limit, &abort_flag)) != 0;
+            };
             for (long long i = pair; i < tiles && ok; i += pairs, ++it) {
                 const uint32_t d = tmem + (it & 1) * L::kCol1;
                 // The epilogue frees what this accumulator shares with the
                 // previous tile's first of all; without shared columns the
                 // one two tiles back has to be free.
                 const int before = it - (shared ? 1 : 2);
-                if (before >= 0)
-                    ok = mbar_spin_abortable(&acc_free[before & 1], (before >> 1) & 1, wait_limit, &abort_flag);
-#pragma unroll 2  // (a jump back costs some 200 cycles: 8192 tokens 4096 -> 11008, 4 bits: 118.0 -> 115.4 us)
+                if (before >= 0) ok = spin(&acc_free[before & 1], (before >> 1) & 1);
                 for (int c = 0; c < chunks && ok; ++c) {
-                    if (!ready) ok = mbar_spin_abortable(&full[s], ph, wait_limit, &abort_flag);
+                    if (!ready) ok = spin(&full[s], ph);
                     if (!ok) break;
                     mm_fence_after();
                     // (Descriptor addresses count 16 bytes and stay below 256 KB.)
                     const uint64_t ad = ad0 + (uint32_t)s * (L::stage >> 4), bd = bd0 + (uint32_t)s * (L::stage >> 4);
                     const uint32_t sw = tmem + L::kColScales + buf * L::kScaleCols, sx = sw + 4 * L::kScaleTiles;
                     const int kts = nkt - c * L::kScaleTiles;
-                    uint64_t *mine = &empty[s];
+                    if (leader) {
+#pragma unroll
+                        for (int m = 0; m < 4 * kSub; ++m) {
+                            // 32 bytes of each row per MMA: with kX8 32 values and one
+                            // scale byte, else 64 values and two.
+                            const int sub = m / 4, q = m % 4, j = kX8 ? sub : m / 2, sf = kX8 ? q : 2 * (q % 2);
+                            if (j == 0 || j < kts)
+                                mx_mma<kX8, 2>(d, ad + sub * (kMmWBytes >> 4) + 2 * q,
+                                               bd + sub * (L::x_block >> 4) + 2 * q,
+                                               mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows), sw + 4 * j, sx + L::kXCols * j,
+                                               (c | m) != 0);
+                        }
+                        pair_commit(&empty[s]);
+                    }
                     if (++s == L::kStages) s = 0, ph ^= 1u;
                     if (++buf == L::kScaleBufs) buf = 0;
-#pragma unroll
-                    for (int m = 0; m < 4 * kSub; ++m) {
-                        // 32 bytes of each row per MMA: with kX8 32 values and one
-                        // scale byte, else 64 values and two.
-                        const int sub = m / 4, q = m % 4, j = kX8 ? sub : m / 2, sf = kX8 ? q : 2 * (q % 2);
-                        if (j == 0 || j < kts)
-                            mx_mma<kX8, 2>(d, ad + sub * (kMmWBytes >> 4) + 2 * q, bd + sub * (L::x_block >> 4) + 2 * q,
-                                           mx_idesc<kX8>(tile_tok, sf, 2 * kMmRows), sw + 4 * j, sx + L::kXCols * j,
-                                           (c | m) != 0);
-                        if (m == 4 * kSub - 2) ready = mbar_test_wait(&full[s], ph);
-                    }
-                    pair_commit(mine);
+                    ready = __all_sync(0xffffffffu, mbar_test_wait(&full[s], ph));
                 }
-                pair_commit(&acc_full[it & 1]);
-            }
-            if (!ok) {
-                abort_flag = 1;
-                flag_timeout(status);
+                if (leader) pair_commit(&acc_full[it & 1]);
+                __syncwarp();
             }
             // Whatever was issued completes before tensor memory is freed.
-            pair_commit(done);
+            if (leader) {
+                if (!ok) {
+                    abort_flag = 1;
+                    flag_timeout(status);
+                }
+                pair_commit(done);
+            }
+            __syncwarp();
             (void)mbar_wait_bounded(done, 0, wait_limit);
         }
         __syncwarp();
