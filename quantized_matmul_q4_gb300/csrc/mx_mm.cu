@@ -408,11 +408,12 @@ __global__ void __launch_bounds__(kMmThreads, 2)
 // Many tokens: CTA pairs (cta_group::2), 256 weight rows x up to 256 tokens.
 // ---------------------------------------------------------------------------
 
-// Operand copies, MMA issuer, 2 x 4 scale warps, 3 x 4 epilogue warps, scale
-// copies, and a second warp for each kind of copy.
-constexpr int kPairThreads = 800;
-constexpr int kPairEpiWarp = 10, kPairCopyWarp = 22;
-constexpr int kPairEpiWarps = 12;  // three for each lane quarter: the accumulators share three blocks of 32 columns
+// Warps: operand copies, MMA issuer, 2 x 4 for the scales, the epilogue's (three
+// for each lane quarter: with 256 tokens the accumulators share three blocks
+// of 32 columns), scale copies.
+constexpr int kPairEpiWarp = 10, kPairEpi = 3, kPairCopyWarp = kPairEpiWarp + 4 * kPairEpi;
+constexpr int kPairThreads = 32 * (kPairCopyWarp + 1);
+
 // kSub: blocks of 128 bytes of K per row and stage.  A stage costs its warps
 // some 400 cycles each besides the MMAs, more than four MMAs of a small tile
 // last: tiles of up to 128 tokens take two blocks a stage.
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_free[b], 2 * kPairEpiWarps);  // of both CTAs
+            mbar_init(&acc_free[b], 2 * 4 * kPairEpi);  // of both CTAs
         }
         mbar_init(done, 1);
         abort_flag = 0;
@@ -602,16 +603,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp == 0 || warp >= kPairCopyWarp) {
+    if (warp == 0 || warp == kPairCopyWarp) {
         // Two warps copy a stage in, one copy per lane and the lanes by
         // one instruction (a copy holds the thread that issues it for some
         // 475 cycles): the first the weights and the tokens, the other the
         // scales of the weights (lane 0) and of the tokens (up to three).
-        // Two such pairs of warps take the stages in turn, since that is
-        // longer than the MMAs of a small tile of tokens (300 tokens 4096 ->
-        // 4096, 8 bits: 12.6 -> 11.8 us).
-        const bool operands = warp == 0 || warp == kPairCopyWarp + 1;
-        const int group = warp > kPairCopyWarp;
+        const bool operands = warp == 0;
         int s = 0;
         uint32_t ph = 1;  // a fresh barrier's previous phase counts as done
         long long n = 0;  // stages issued
@@ -636,10 +633,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                             : x_scales + (size_t)(xt + lane - 1) * nkt * kMxTileBytes;
             const bool mine = operands ? lane < 2 * kSub : lane == 0 ? nw != 0 : lane <= nx;
             for (int c = 0; c < chunks; ++c, ++n) {
-                if (((int)n & 1) != group) {
-                    if (++s == L::kStages) s = 0, ph ^= 1u;
-                    continue;
-                }
                 ok = mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) {
@@ -821,7 +814,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        const int q = warp & 3, third = (warp - kPairEpiWarp) >> 2;  // lane quarter; every third block of 32 tokens
+        const int q = warp & 3, part = (warp - kPairEpiWarp) >> 2;  // lane quarter; every kPairEpi-th block of 32 tokens
         const uint32_t free_addr = map_to_rank(smem_addr(acc_free), 0);
         int it = 0;
         for (long long i = pair; i < tiles; i += pairs, ++it) {
@@ -843,15 +836,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(free_addr + 8 * (it & 1));
             };
             // The shared columns are the last blocks of the first accumulator
-            // and the first of the second, up to three: one for each warp of
-            // a quarter, which reads it before anything else, since the next
+            // and the first of the second, up to kPairEpi: one for each warp of a
+            // quarter, which reads it before anything else, since the next
             // tile's MMAs wait for that.
             const int s0 = it & 1 ? 0 : blocks - shared;
-            const int mine = s0 + (third + 3 - s0 % 3) % 3;  // this warp's first block from s0 on
+            const int mine = s0 + (part + kPairEpi - s0 % kPairEpi) % kPairEpi;  // this warp's first block from s0 on
             const bool early = mine < s0 + shared;
             if (shared && !early) free_accumulator();
             bool first = early;
-            for (int blk = early ? mine : third; blk < blocks;) {
+            for (int blk = early ? mine : part; blk < blocks;) {
                 float v[32];
                 mm_ld32(col0 + 32 * blk, v);
                 if (first) free_accumulator();
@@ -866,9 +859,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         store_column(static_cast<__nv_bfloat16 *>(y) + at, N, count, v);
                 }
                 __syncwarp();
-                blk = first ? third : blk + 3;
+                blk = first ? part : blk + kPairEpi;
                 first = false;
-                if (early && blk == mine) blk += 3;
+                if (early && blk == mine) blk += kPairEpi;
             }
             if (!shared) free_accumulator();
         }
