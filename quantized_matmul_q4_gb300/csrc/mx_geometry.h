@@ -20,21 +20,21 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 // of K (256 values with 4-bit x, 128 with 8-bit).  The constants are fitted
 // to 1144 measurements of 286 products on GB300 (chains of calls in a CUDA
 // graph, 17 to 2048 tokens, K and N of 256 to 16384, with 1, 2 and 4 times
-// the fewest tiles of tokens), where the choice costs 0.1% on the mean against
+// the fewest tiles of tokens), where the choice costs 0.3% on the mean against
 // always the fastest; some of them, single CTAs with K split / CTA pairs:
 //   T    K        N       x     measured       estimated
-//   17   256   -> 4096    4     2.7 /  3.8      2.7 /  3.9
-//   64   4096  -> 4096    8     6.9 /  9.0      7.2 /  9.1
-//   64   2560  -> 6912    4     7.2 /  5.7      6.8 /  5.8
-//   128  1024  -> 4096    8     6.6 /  5.0      6.5 /  5.3
-//   128  4096  -> 4096    4     7.7 /  7.0      7.7 /  7.0
-//   128  4096  -> 11008   8    13.2 / 10.5     13.0 / 10.2
-//   200  4096  -> 4096    8    11.4 /  9.9     11.8 /  9.8
-//   256  1024  -> 1024    8     6.4 /  5.0      6.5 /  5.0
-//   256  8192  -> 8192    4    17.0 / 12.8     16.5 / 11.3
-//   420  11008 -> 4096    8    25.5 / 21.0     25.5 / 20.2
-//   512  4096  -> 11008   8    34.5 / 23.5     36.4 / 22.9
-//   1024 11008 -> 4096    8    39.5 / 30.2     38.8 / 29.2
+//   17   256   -> 4096    4     2.5 /  3.5      2.3 /  3.4
+//   64   4096  -> 4096    8     6.6 /  8.0      7.0 /  8.1
+//   64   2560  -> 6912    4     6.2 /  4.8      6.1 /  5.1
+//   128  1024  -> 4096    8     6.5 /  4.5      6.4 /  4.8
+//   128  4096  -> 4096    4     7.3 /  5.9      7.4 /  6.2
+//   128  4096  -> 11008   8    12.9 /  9.7     12.6 /  9.3
+//   200  4096  -> 4096    8    10.7 /  8.9     11.5 /  8.9
+//   256  1024  -> 1024    8     6.3 /  4.5      6.4 /  4.6
+//   256  8192  -> 8192    4    16.0 / 11.7     15.3 / 10.1
+//   420  11008 -> 4096    8    24.4 / 19.7     24.5 / 18.4
+//   512  4096  -> 11008   8    32.5 / 22.2     34.6 / 21.2
+//   1024 11008 -> 4096    8    37.6 / 30.0     37.1 / 29.4
 
 // Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
 // tile's K: rounds of two CTAs per SM through their stages, then the stores
@@ -43,13 +43,13 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 inline double mx_split_us(int row_tiles, int tok_tiles, int tokens, int stages, int S, int x_bits, int num_sms) {
     const long long ctas = (long long)row_tiles * tok_tiles * S, slots = 2LL * num_sms;
     const double tok = tokens < 128 ? tokens / 128.0 : 1.0;
-    const double stage = x_bits == 8 ? 0.34 + 0.05 * tok : 0.49;
+    const double stage = x_bits == 8 ? 0.35 + 0.02 * tok : 0.40 + 0.02 * tok;
     // CTAs that have an SM to themselves fetch sums twice as fast; clusters of
     // more than four are packed two to an SM well before the SMs run out.
     const bool alone = ctas <= (S > 4 ? num_sms / 2 : num_sms);
-    const double end = S == 1 ? 3.55 * tok : 1.18 + (alone ? 2.81 : 5.79) * tok;
+    const double end = S == 1 ? 3.94 * tok : 1.17 + (alone ? 3.19 : 6.07) * tok;
     const double rounds = (double)((ctas + slots - 1) / slots);
-    return 1.74 + rounds * (((stages + S - 1) / S) * stage + end) + (rounds - 1.0) * 2.57;
+    return 1.33 + rounds * (((stages + S - 1) / S) * stage + end) + (rounds - 1.0) * 1.7;
 }
 
 // The split with the lowest estimate: at most 8 CTAs, two stages to each.
@@ -83,9 +83,9 @@ inline double mx_pair_us(const MxPairTiles &g, int stages, int x_bits, int num_s
     const long long tiles = (long long)g.row_tiles * g.tok_tiles, pairs = num_sms > 1 ? num_sms / 2 : 1;
     const double n = g.tile_tok / 256.0, waves = (double)((tiles + pairs - 1) / pairs);
     const double in_stages =
-        g.tile_tok <= kMxPairTwoBlocks ? ((stages + 1) / 2) * (x_bits == 8 ? 0.332 + 0.061 * n : 0.381 + 0.066 * n)
-                                       : stages * (x_bits == 8 ? 0.155 + 0.121 * n : 0.231 + 0.059 * n);
-    return 3.07 + 1.52 * n + 0.013 * (double)(tiles < pairs ? tiles : pairs) + waves * in_stages + (waves - 1.0) * 0.36;
+        g.tile_tok <= kMxPairTwoBlocks ? ((stages + 1) / 2) * (x_bits == 8 ? 0.292 + 0.068 * n : 0.304 + 0.096 * n)
+                                       : stages * (x_bits == 8 ? 0.248 + 0.032 * n : 0.278 + 0.014 * n);
+    return 2.66 + 1.73 * n + 0.014 * (double)(tiles < pairs ? tiles : pairs) + waves * in_stages + (waves - 1.0) * 0.48;
 }
 
 // As few tiles of tokens as there can be, or twice or four times as many

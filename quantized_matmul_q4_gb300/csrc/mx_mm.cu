@@ -19,17 +19,19 @@
 // Two forms, chosen by mx_geometry.h from estimates of both:
 //  * mx_mm_split_kernel, up to 128 tokens a tile, K split over a cluster.  A
 //    call with few tokens reads its weights once and is bound by them and by
-//    the chain of latencies around them: 4096 x 4096 at one token takes 4.5
-//    us (x in 4 bits) and 5.3 (8 bits, whose unpacking copies move 64 bytes
+//    the chain of latencies around them: 4096 x 4096 at one token takes 4.0
+//    us (x in 4 bits) and 4.6 (8 bits, whose unpacking copies move 64 bytes
 //    a row) in a chain of calls, of which 1.3 us are the weights' at the
-//    copy rate, 2.9 an empty product's (1024 x 1024).  Large ones reach 5.9
-//    TB/s behind those 3 us (16384 -> 38912: 61 us, 82% of the copy rate).
+//    copy rate, 2.8 a small product's (1024 x 1024; 128 x 128 unsplit 1.8).
+//    16384 -> 38912 takes 58 us, 5.8 TB/s, 86% of the copy rate.
 //  * mx_mm_pair_kernel, 256 rows x 256 tokens on a pair of CTAs, for the
-//    rest.  8192 tokens 4096 -> 11008: 118 us in 4 bits (6.2 PFLOP/s), 210 in
-//    8 (3.5); 8192 tokens 8192 -> 8192: 156 us (7.1 PFLOP/s).  Bound by the
-//    tensor pipe, which runs 620 cycles for a stage's four MMAs where 512
-//    are nominal and a stage takes 650, and by some 900 cycles between two
-//    tiles; kept busy for seconds, by the board's power limit.
+//    rest.  8192 tokens 4096 -> 11008: 111 us in 4 bits (6.6 PFLOP/s), 205 in
+//    8 (3.6); 8192 tokens 8192 -> 8192: 148 us (7.4 PFLOP/s).  Bound by the
+//    tensor pipe (four MMAs of 256 tokens of a 4-bit stage alone run 620
+//    cycles where 512 are nominal), by some 900 cycles between two tiles and
+//    by the last, partly filled round of tiles; kept busy for seconds, by
+//    the board's power limit.  Small tiles of tokens are bound by the fixed
+//    work of a stage and the launch.
 //
 // Tensor memory: a CTA waits for its columns while another holds them, so two
 // kernels must never wait for each other's.  They do not: every CTA of a grid
@@ -545,7 +547,7 @@ __device__ __forceinline__ void mm_st(uint32_t taddr, const uint32_t (&r)[kN]) {
 // in 4 bits): scales by tcgen05.cp 230 us, by scale warps whose arrival
 // releases at cluster scope 326, by the plain arrival 162, copies issued by
 // lanes 142, one barrier a stage 130, shared columns read first 118, the
-// issuing loop unrolled 115.
+// issuing warp converged 111.
 template <bool kX8, int kSub>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_mm_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
