@@ -133,8 +133,12 @@ __device__ __forceinline__ void to_float(const Raw8<__half> &r, float (&v)[8]) {
     }
 }
 
+// Eight values of one row alone, of which nothing outside may be read.
 template <bool kVec, class T>
 __device__ __forceinline__ void load8(const T *row, int col, int K, float (&v)[8]) {
+    if constexpr (!kVec) {
+        if (reinterpret_cast<uintptr_t>(row) % 16 == 0 && col + 8 <= K) return load8<true>(row, col, K, v);
+    }
     Fetch8<kVec, T> f;
     Raw8<T> r;
     f.template load<false>(row, col, K);
@@ -420,31 +424,38 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
     }
     constexpr int kKept = kVals > 0 ? kVals : 1;
     const bool wide = row > 0 && row < a.rows - 1 && K >= 8;
-    // Groups are loaded four at a time at most, x and residual together.
+    // Groups are loaded four at a time at most, x and residual together; two
+    // unaligned, whose granules would not fit the registers (8192 x 4095 bf16:
+    // 62.1 -> 61.0 us).
     auto load_h = [&](int c0, float (&v)[kKept][8]) {
-        Fetch8<kVec, T> fx[kKept], fr[kKept];
-        auto load_all = [&](const T *from, Fetch8<kVec, T>(&f)[kKept]) {
-            if (kVec || wide) {
+        constexpr int kAhead = kVec || kKept < 2 ? kKept : 2;
 #pragma unroll
-                for (int i = 0; i < kKept; ++i) f[i].template load<true>(from, c0 + i * step + 8 * threadIdx.x, K);
-            } else {
+        for (int i0 = 0; i0 < kKept; i0 += kAhead) {
+            auto col = [&](int i) { return c0 + (i0 + i) * step + 8 * (int)threadIdx.x; };
+            Fetch8<kVec, T> fx[kAhead], fr[kAhead];
+            auto load_all = [&](const T *from, Fetch8<kVec, T>(&f)[kAhead]) {
+                if (kVec || wide) {
 #pragma unroll
-                for (int i = 0; i < kKept; ++i) f[i].template load<false>(from, c0 + i * step + 8 * threadIdx.x, K);
-            }
-        };
-        load_all(x, fx);
-        if (res) load_all(res, fr);
+                    for (int i = 0; i < kAhead; ++i) f[i].template load<true>(from, col(i), K);
+                } else {
 #pragma unroll
-        for (int i = 0; i < kKept; ++i) {
-            Raw8<T> r;
-            fx[i].take(x, c0 + i * step + 8 * threadIdx.x, K, wide, r);
-            to_float(r, v[i]);
-            if (res) {
-                float u[8];
-                fr[i].take(res, c0 + i * step + 8 * threadIdx.x, K, wide, r);
-                to_float(r, u);
+                    for (int i = 0; i < kAhead; ++i) f[i].template load<false>(from, col(i), K);
+                }
+            };
+            load_all(x, fx);
+            if (res) load_all(res, fr);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+            for (int i = 0; i < kAhead; ++i) {
+                Raw8<T> r;
+                fx[i].take(x, col(i), K, wide, r);
+                to_float(r, v[i0 + i]);
+                if (res) {
+                    float u[8];
+                    fr[i].take(res, col(i), K, wide, r);
+                    to_float(r, u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i0 + i][j] += u[j];
+                }
             }
         }
     };
@@ -628,13 +639,13 @@ cudaError_t rmsnorm_t(const LaunchCtx &c, const MxRmsnormArgs &a) {
     // us); for many rows of a 16-bit type four groups, where they leave four
     // warps.  8192 x 4096 bf16 with a residual: 52.0, 38.1, 37.6 us with one,
     // two, four groups; 4096 x 4096 fp32: 34.9 with one, 35.9 with two, 37.8
-    // with four.  Unaligned rows have more fixed work: two groups where the
-    // aligned ones have one (4096 x 4095 fp32: 59.7, 45.3, 62.5 with one, two,
-    // four; 30000 x 1117 fp16: 86.1, 82.7, 111; 8192 x 4095 bf16: 84.4, 64.1,
-    // 62.1).
+    // with four.  Unaligned rows have more fixed work: from 1024 on two groups
+    // where the aligned ones have one (4096 x 4095 fp32: 52.3, 38.7, 42.7 with
+    // one, two, four; 30000 x 1117 fp16: 84.8, 81.3, 110; 20000 x 513 fp32:
+    // 33.9, 38.4, 41.9; 8192 x 4095 bf16: 81.3, 61.3, 58.7).
     int vals = 1;
     if (a.rows > c.num_sms && sizeof(T) == 2) vals = Kp >= 4096 ? 4 : Kp >= 2048 ? 2 : 1;
-    if (a.rows > c.num_sms && !vec && vals == 1) vals = 2;
+    if (a.rows > c.num_sms && !vec && vals == 1 && Kp >= 1024) vals = 2;
     while (vals < 4 && Kp > 8 * 1024 * vals) vals *= 2;
     const bool kept = Kp <= 8 * 1024 * vals;
     int threads = kept ? (Kp / 8 + vals - 1) / vals : 1024;
