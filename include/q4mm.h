@@ -395,7 +395,10 @@ int mx_quantize(const void *x, long long x_stride, int dtype, void *codes, void 
 /*
  * mx_swiglu — silu(gate)·up quantised as by mx_quantize, in one pass:
  * gate / (1 + e^-gate) · up in fp32, rounded once, to codes.  gate and up
- * may be two parts of one tensor's rows.  Limits and returns as mx_quantize.
+ * may be two parts of one tensor's rows.  The value before its rounding is
+ * within 10·2^-24 of the exact one (and 2^-149), also where e^-gate itself is
+ * beyond fp32; gate = -infinity gives NaN, as the formula does.
+ * Limits and returns as mx_quantize.
  */
 int mx_swiglu(const void *gate, long long gate_stride, const void *up, long long up_stride, int dtype, void *codes,
               void *scales, int hiddenDim, int rows, int bits, q4mm_stream_t stream);

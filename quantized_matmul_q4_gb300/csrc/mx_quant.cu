@@ -281,15 +281,15 @@ struct ByteExchange {
     }
 };
 
-// x / (1 + e^-x) of two values, to about 6 units in the last place.  e^-x is
-// 2^t, t = -x·log2 e; the product's rounding, and log2 e's own, would cost
-// |t| units in the last place, so t = hi + lo and 2^t = 2^hi + 2^hi·lo·ln 2
-// (with expf and an exact quotient 4099 x 11008 bf16 takes 42.6 us instead of
-// 36.3, where the bytes alone take 33).
-// Past |x| = 88.7 e^-x is 0 or beyond the range of the approximate quotient,
-// which is then a zero; infinities and NaN pass through the quotient.
+// x / (1 + e^-x) of two values, to 9·2^-24, for x >= kSiluFar.  e^-x is 2^t,
+// t = -x·log2 e; the product's rounding, and log2 e's own, would cost |t|
+// units in the last place, so t = hi + lo and 2^t = 2^hi + 2^hi·lo·ln 2 (with
+// expf and an exact quotient 4099 x 11008 bf16 takes 42.6 us instead of 36.3,
+// where the bytes alone take 33).  Infinities above and NaN pass through the
+// quotient; below kSiluFar its reciprocal would be subnormal, which is flushed.
+constexpr float kSiluFar = -87.f;  // 1 + e^87 < 2^126
 __device__ __forceinline__ float2 silu2(float2 x) {
-    const float2 c = make_float2(fminf(fmaxf(x.x, -88.7f), 100.f), fminf(fmaxf(x.y, -88.7f), 100.f));
+    const float2 c = make_float2(fminf(x.x, 100.f), fminf(x.y, 100.f));
     const float2 l2e = make_float2(-1.44269504f, -1.44269504f);    // -log2 e, and what it lacks
     const float2 rest = make_float2(-1.92596303e-8f, -1.92596303e-8f);
     const float2 ln2 = make_float2(0.693147181f, 0.693147181f);
@@ -302,6 +302,40 @@ __device__ __forceinline__ float2 silu2(float2 x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
     return __fmul2_rn(x, e);
+}
+
+// x / (1 + e^-x) · up for x < kSiluFar, where 1 + e^-x is e^-x to 2^-125: so
+// x·e^x·up.  e^x falls out of fp32's normal range there, while the product
+// with a large up need not: e^x is taken as e^(x + 100)·c·c, c = e^-50, and no
+// product on the way overflows or loses bits that the last one keeps (x + 100
+// is exact).  -inf gives NaN, as the quotient does.
+__device__ __forceinline__ float silu_far(float x, float up) {
+    constexpr float c = 1.92874985e-22f;
+    return (x * expf(x + 100.f)) * (up * c) * c;
+}
+
+__device__ __forceinline__ float min3(float a, float b, float c) {  // of NaN and a number the number
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// silu(v)·u of eight values into v.  least: the least gate so far, which tells
+// whether any is below kSiluFar and its product not to be used (kFar = false),
+// or the products below it are put right (kFar = true).
+template <bool kFar>
+__device__ __forceinline__ void swiglu8(float (&v)[8], const float (&u)[8], float &least) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        float2 f = __fmul2_rn(silu2(make_float2(v[j], v[j + 1])), make_float2(u[j], u[j + 1]));
+        if constexpr (kFar) {
+            if (v[j] < kSiluFar) f.x = silu_far(v[j], u[j]);
+            if (v[j + 1] < kSiluFar) f.y = silu_far(v[j + 1], u[j + 1]);
+        } else {
+            least = min3(least, v[j], v[j + 1]);
+        }
+        v[j] = f.x, v[j + 1] = f.y;
+    }
 }
 
 // One warp per 256 columns of the four rows r, r + 32, r + 64, r + 96 of a
@@ -348,22 +382,37 @@ __global__ void __launch_bounds__(256, kSwiGLU ? (kVec ? 4 : 3) : (kVec ? 1 : 4)
         Fetch8<kVec, T> fu[4];
         const T *pu = up + row0 * up_stride;
         load4(pu, up_stride, fu);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        float least = 0.f;
+        auto row = [&](auto far, int i, const Fetch8<kVec, T> &gx, const Fetch8<kVec, T> &gu) {
             Raw8<T> rx, ru;
             float v[8], u[8];
-            fx[i].take(px + 32 * i * x_stride, col, width(i), wide, rx);
-            fu[i].take(pu + 32 * i * up_stride, col, width(i), wide, ru);
+            gx.take(px + 32 * i * x_stride, col, width(i), wide, rx);
+            gu.take(pu + 32 * i * up_stride, col, width(i), wide, ru);
             to_float(rx, v);
             to_float(ru, u);
+            swiglu8<decltype(far)::value>(v, u, least);
+            return quantize8(v, block_amax(v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+                   << (8 * i);
+        };
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float2 f =
-                    __fmul2_rn(silu2(make_float2(v[j], v[j + 1])), make_float2(u[j], u[j + 1]));
-                v[j] = f.x, v[j + 1] = f.y;
+        for (int i = 0; i < 4; ++i) p |= row(std::false_type{}, i, fx[i], fu[i]);
+        // Gates below kSiluFar are rare: a warp that has met one reads its
+        // four rows again.  (A branch for each row instead: 38 us on 4099 x
+        // 11008 bf16, against 35.7.)
+        if (__any_sync(kFull, least < kSiluFar)) {
+            p = 0;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                Fetch8<kVec, T> gx, gu;
+                if (kVec || wide) {
+                    gx.template load<true>(px + 32 * i * x_stride, col, width(i));
+                    gu.template load<true>(pu + 32 * i * up_stride, col, width(i));
+                } else {
+                    gx.template load<false>(px + 32 * i * x_stride, col, width(i));
+                    gu.template load<false>(pu + 32 * i * up_stride, col, width(i));
+                }
+                p |= row(std::true_type{}, i, gx, gu);
             }
-            p |= quantize8(v, block_amax(v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
-                 << (8 * i);
         }
     } else {
 #pragma unroll

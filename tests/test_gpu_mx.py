@@ -11,9 +11,9 @@ Tolerances, derived:
     addition of eps: below 40 · 2^-24 < 3e-6 in all.  A code must then be one
     that some value within that of the exact one has, under the scale byte
     found, which must be that of some such block maximum.
-  * swiglu: expf (2 ulp), one addition, one division, one multiplication:
-    below 8 · 2^-24 < 1e-6 relative; where e^-gate overflows the result is a
-    zero and the exact value below 1e-36 · |up|.
+  * swiglu: the exponential and its correction (5 · 2^-24), one addition, the
+    reciprocal (2 · 2^-24), two multiplications: 10 · 2^-24 < 1e-6 relative
+    (test_gpu_mx_swiglu_range holds it to that over the whole range of gates).
   * matmul: products are exact; at most Kp / 32 sums are chained per output,
     each within one unit in the last place of a partial sum, 2^-23 of
     sum |x w| (the tensor cores may cut instead of rounding); then the
