@@ -173,8 +173,70 @@ def device_status(stream=None, clear: bool = True) -> None:
 
 
 # Tensor entry points (torch CUDA tensors; y allocated unless `out` is given).
+#
+# stream: a torch stream or a stream's handle; the current stream unless given.
+# On another stream than the current one nothing waits: the tensors have to be
+# ready there, and a user of the results waits for that stream.  Memory is
+# safe, though: results come from the pool of the call's stream, and neither
+# they nor the tensors given are reused before both streams are past them,
+# however early they are dropped.
 
-def _prep(x, w, K, bytes_per_row, out, N):
+class _Torch:
+    """What the calls take from torch, looked up on the first of them (the
+    binding itself imports without torch).  A call costs the host about as
+    much as an elementwise torch operation, mostly its allocations and the
+    launch; what is left is kept short."""
+    dtypes: dict = {}
+    uint8 = float32 = empty = raw_stream = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
+        cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
+        # The current stream's handle alone: a Stream object costs as much as a launch.
+        cls.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call_stream(stream, device: int):
+    """The handle of a call's stream, and the stream where it is not the current one (else None)."""
+    if _Torch.raw_stream is None:
+        _Torch.load()
+    current = _Torch.raw_stream(device)
+    if stream is None:
+        return current, None
+    handle = _stream_ptr(stream)
+    if handle == current:
+        return current, None
+    if not hasattr(stream, "record_event"):
+        import torch
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return handle, stream
+
+
+def _empty_on(side):
+    """torch.empty from the pool of the stream `side`, for a call that runs there (None: the current one)."""
+    if side is None:
+        return _Torch.empty
+
+    def empty(shape, dtype, device):
+        import torch
+        with torch.cuda.stream(side):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream(device))   # whose code has it from now on
+        return t
+
+    return empty
+
+
+def _hold(side, *tensors) -> None:
+    """Memory of the tensors is not reused before `side` is past the call."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(side)
+
+
+def _prep(x, w, K, bytes_per_row, out, N, stream, w2=None):
     import torch
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous float32 CUDA tensor")
@@ -188,32 +250,36 @@ def _prep(x, w, K, bytes_per_row, out, N):
         if bytes_per_row(K_) <= 0 or w.numel() % bytes_per_row(K_):
             raise ValueError("weight size is not a whole number of rows")
         N = w.numel() // bytes_per_row(K_)
-    if out is None:
-        out = torch.empty((T, N), dtype=torch.float32, device=x.device)
-    elif out.dtype != torch.float32 or not out.is_cuda or not out.is_contiguous() or out.numel() != T * N:
+    if out is not None and (out.dtype != torch.float32 or not out.is_cuda or not out.is_contiguous()
+                            or out.numel() != T * N):
         raise ValueError("out must be a contiguous float32 CUDA tensor with tokens·outputDim elements")
-    return x2, T, K_, N, out
+    handle, side = _call_stream(stream, x.get_device())
+    if out is None:
+        out = _empty_on(side)((T, N), dtype=torch.float32, device=x.device)
+    if side is not None:
+        _hold(side, x, w, w2, out)
+    return x2, T, K_, N, out, handle
 
 
 def q4k_matmul(x, w, N: int | None = None, out=None, stream=None):
     """y[T, N] = x[T, K] · dequant(W)ᵀ in FP32 (decode GEMV up to 8 tokens)."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N)
-    q4k_matmul_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N, stream)
+    q4k_matmul_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
 def q4k_matmul_tc(x, w, N: int | None = None, out=None, stream=None):
     """As q4k_matmul on the tensor cores with bf16-rounded operands."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N)
-    q4k_matmul_tc_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N, stream)
+    q4k_matmul_tc_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
 def q4k_matmul_tc_noalloc(x, w, N: int | None = None, out=None, stream=None):
     """As q4k_matmul_tc with its scratch in the library's fixed device array
     (no allocation; calls that overlap on the GPU race on that array)."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N)
-    q4k_matmul_tc_noalloc_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N, stream)
+    q4k_matmul_tc_noalloc_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
@@ -239,11 +305,15 @@ def q4k_relayout_tc(w, K: int, N: int | None = None, out=None, stream=None):
             raise ValueError("weight size is not a whole number of rows")
         N = w.numel() // row
     nbytes = tc_relayout_bytes(K, N)
-    if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
-    elif out.dtype != torch.uint8 or not out.is_cuda or not out.is_contiguous() or out.numel() != nbytes:
+    if out is not None and (out.dtype != torch.uint8 or not out.is_cuda or not out.is_contiguous()
+                            or out.numel() != nbytes):
         raise ValueError("out must be a contiguous uint8 CUDA tensor of tc_relayout_bytes(K, N) bytes")
-    q4k_relayout_tc_ptr(w.data_ptr(), out.data_ptr(), K, N, _stream_ptr(stream))
+    at, side = _call_stream(stream, w.get_device())
+    if out is None:
+        out = _empty_on(side)(nbytes, dtype=torch.uint8, device=w.device)
+    if side is not None:
+        _hold(side, w, out)
+    q4k_relayout_tc_ptr(w.data_ptr(), out.data_ptr(), K, N, at)
     return out
 
 
@@ -252,8 +322,8 @@ def q4k_matmul_tc_relayouted(x, w_tc, N: int, out=None, stream=None):
     required: the padded layout does not give it)."""
     if w_tc.numel() != tc_relayout_bytes(x.shape[-1], N):
         raise ValueError("w_tc size does not match tc_relayout_bytes(K, N)")
-    x2, T, K, N, out = _prep(x, w_tc, None, lambda k: (k // 64) * TC_CHUNK_BYTES, out, N)
-    q4k_matmul_tc_relayouted_ptr(x2.data_ptr(), w_tc.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w_tc, None, lambda k: (k // 64) * TC_CHUNK_BYTES, out, N, stream)
+    q4k_matmul_tc_relayouted_ptr(x2.data_ptr(), w_tc.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
@@ -262,8 +332,8 @@ Q40_VALUES, Q40_BYTES = 32, 18
 
 def q4_0_gemv(x, w, N: int | None = None, out=None, stream=None):
     """y[T, N] = x[T, K] · dequant_q4_0(W)ᵀ in FP32 (up to 8 tokens per weight pass)."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: (k // Q40_VALUES) * Q40_BYTES, out, N)
-    q4_0_gemv_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: (k // Q40_VALUES) * Q40_BYTES, out, N, stream)
+    q4_0_gemv_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
@@ -272,27 +342,27 @@ Q6K_BYTES = 210
 
 def q6k_gemv(x, w, N: int | None = None, out=None, stream=None):
     """y[T, N] = x[T, K] · dequant_q6k(W)ᵀ in FP32 (up to 8 tokens per weight pass)."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q6K_BYTES, out, N)
-    q6k_gemv_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, _stream_ptr(stream))
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: (k // Q4K_VALUES) * Q6K_BYTES, out, N, stream)
+    q6k_gemv_ptr(x2.data_ptr(), w.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
 def q4k_ffn_swiglu(x, w_gate, w_up, N: int | None = None, out=None, stream=None):
     """h[T, N] = silu(x · dequant(W_gate)ᵀ) · (x · dequant(W_up)ᵀ), both Q4_K."""
-    x2, T, K, N, out = _prep(x, w_gate, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N)
     if (w_up.dtype != w_gate.dtype or w_up.numel() != w_gate.numel() or not w_up.is_cuda
             or not w_up.is_contiguous()):
         raise ValueError("w_up must be a contiguous CUDA uint8 tensor of the gate weight's size")
+    x2, T, K, N, out, at = _prep(x, w_gate, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N, stream, w_up)
     q4k_ffn_swiglu_ptr(x2.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
-                       K, N, T, _stream_ptr(stream))
+                       K, N, T, at)
     return out.view(T, N)
 
 
 def ternary_gemv(x, w, scale: float = 1.0, N: int | None = None, out=None, stream=None):
     """y[T, N] = scale · x[T, K] · codes(W)ᵀ, BitNet b1.58 payload, FP32."""
-    x2, T, K, N, out = _prep(x, w, None, lambda k: k // 4, out, N)
+    x2, T, K, N, out, at = _prep(x, w, None, lambda k: k // 4, out, N, stream)
     ternary_gemv_ptr(x2.data_ptr(), w.data_ptr(), float(scale), out.data_ptr(), K, N, T,
-                     _stream_ptr(stream))
+                     at)
     return out.view(T, N)
 
 
@@ -322,23 +392,6 @@ class MxTensor(NamedTuple):
 
 def mx_padded(K: int) -> int:
     return -(-K // 128) * 128
-
-
-class _Torch:
-    """What the MX calls take from torch, looked up on the first of them (the
-    binding itself imports without torch).  A call costs the host about as
-    much as an elementwise torch operation, mostly its allocations and the
-    launch; what is left is kept short."""
-    dtypes: dict = {}
-    uint8 = float32 = empty = raw_stream = None
-
-    @classmethod
-    def load(cls):
-        import torch
-        cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
-        cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
-        # The current stream's handle alone: a Stream object costs as much as a launch.
-        cls.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _mx_dtype(t, what: str) -> int:
@@ -374,14 +427,15 @@ def _mx_rows(x, what: str):
     return x, rows, K, s0 if rows > 1 else K, device
 
 
-def _mx_out(rows: int, K: int, bits: int, x, device: int, out) -> MxTensor:
+def _mx_out(rows: int, K: int, bits: int, x, device: int, out, side) -> MxTensor:
     """`out` checked, or a new MxTensor on x's device."""
     if bits != 4 and bits != 8:
         raise ValueError("bits must be 4 or 8")
     if out is None:
         kt, where, u8 = -(-K // 128), x.device, _Torch.uint8
-        return MxTensor(_Torch.empty((rows, kt * 16 * bits), dtype=u8, device=where),
-                        _Torch.empty((-(-rows // MX_TILE_ROWS), kt, MX_TILE_BYTES), dtype=u8, device=where), K, bits)
+        new = _Torch.empty if side is None else _empty_on(side)
+        return MxTensor(new((rows, kt * 16 * bits), dtype=u8, device=where),
+                        new((-(-rows // MX_TILE_ROWS), kt, MX_TILE_BYTES), dtype=u8, device=where), K, bits)
     if _mx_check(out, "out", device) != rows or out.K != K or out.bits != bits:
         raise ValueError(f"out must hold {rows} rows of {K} values in {bits} bits")
     return out
@@ -417,9 +471,11 @@ def mx_quantize(x, bits: int = 8, out: MxTensor | None = None, stream=None) -> M
     """x [..., K] (float32, float16 or bfloat16) to an MX tensor of `bits` (4 or 8) bits."""
     x, rows, K, stride, device = _mx_rows(x, "x")
     dtype = _mx_dtype(x.dtype, "x")
-    out = _mx_out(rows, K, bits, x, device, out)
-    rc = _LIB.mx_quantize(x.data_ptr(), stride, dtype, out[0].data_ptr(), out[1].data_ptr(), K, rows, bits,
-                          _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    out = _mx_out(rows, K, bits, x, device, out, side)
+    if side is not None:
+        _hold(side, x, out[0], out[1])
+    rc = _LIB.mx_quantize(x.data_ptr(), stride, dtype, out[0].data_ptr(), out[1].data_ptr(), K, rows, bits, at)
     if rc:
         _check(rc)
     return out
@@ -434,9 +490,12 @@ def mx_swiglu(gate, up, bits: int = 8, out: MxTensor | None = None, stream=None)
     if device != udevice:
         raise ValueError("all tensors of a call must be on one CUDA device")
     dtype = _mx_dtype(gate.dtype, "gate")
-    out = _mx_out(rows, K, bits, gate, device, out)
+    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    out = _mx_out(rows, K, bits, gate, device, out, side)
+    if side is not None:
+        _hold(side, gate, up, out[0], out[1])
     rc = _LIB.mx_swiglu(gate.data_ptr(), gs, up.data_ptr(), us, dtype, out[0].data_ptr(), out[1].data_ptr(), K, rows,
-                        bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+                        bits, at)
     if rc:
         _check(rc)
     return out
@@ -456,6 +515,7 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
     if weight.numel() != K or not weight.is_contiguous():
         raise ValueError("weight must be contiguous and hold one value per column of x")
     _mx_device(device, weight)
+    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
     res_ptr, rs, h_ptr, hs = 0, K, 0, K
     if residual is not None:
         if residual.shape != shape or residual.dtype != xtype:
@@ -464,7 +524,8 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
         r, _, _, rs, _ = _mx_rows(residual, "residual")
         res_ptr = r.data_ptr()
         if h_out is None:
-            h = h_out = _Torch.empty(shape, dtype=xtype, device=x.device)
+            new = _Torch.empty if side is None else _empty_on(side)
+            h = h_out = new(shape, dtype=xtype, device=x.device)
         else:
             if h_out.shape != shape or h_out.dtype != xtype:
                 raise ValueError("h_out must have x's shape and type")
@@ -473,10 +534,12 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
         h_ptr = h.data_ptr()
     elif h_out is not None:
         raise ValueError("h_out needs a residual: without one h is x")
-    out = _mx_out(rows, K, bits, x, device, out)
+    out = _mx_out(rows, K, bits, x, device, out, side)
+    if side is not None:
+        _hold(side, x, weight, residual, h_out, out[0], out[1])
     rc = _LIB.mx_rmsnorm(x.data_ptr(), xs, res_ptr, rs, h_ptr, hs, dtype, weight.data_ptr(),
                          _mx_dtype(weight.dtype, "weight"), float(eps), out[0].data_ptr(), out[1].data_ptr(), K, rows,
-                         bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+                         bits, at)
     if rc:
         _check(rc)
     return out if residual is None else (out, h_out)
@@ -487,16 +550,20 @@ def mx_dequantize(q: MxTensor, dtype=None, out=None, stream=None):
     codes, scales, K, bits = q
     device = codes.get_device()
     rows = _mx_check(q, "q", device)
+    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
     stride = K
     if out is None:
-        out = _Torch.empty((rows, K), dtype=dtype or _Torch.float32, device=codes.device)
+        new = _Torch.empty if side is None else _empty_on(side)
+        out = new((rows, K), dtype=dtype or _Torch.float32, device=codes.device)
     else:
         if out.shape != (rows, K) or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be [rows, K] of the given type")
         _mx_device(device, out)
         _, _, _, stride, _ = _mx_rows(out, "out")
+    if side is not None:
+        _hold(side, codes, scales, out)
     rc = _LIB.mx_dequantize(codes.data_ptr(), scales.data_ptr(), out.data_ptr(), stride, _mx_dtype(out.dtype, "out"), K,
-                            rows, bits, _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+                            rows, bits, at)
     if rc:
         _check(rc)
     return out
@@ -513,15 +580,18 @@ def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
         raise ValueError("w must be a 4-bit MX tensor")
     if K != w_K:
         raise ValueError("x and w must have the same K")
+    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
     if out is None:
-        out = _Torch.empty((T, N), dtype=dtype or _Torch.float32, device=x_codes.device)
+        new = _Torch.empty if side is None else _empty_on(side)
+        out = new((T, N), dtype=dtype or _Torch.float32, device=x_codes.device)
     else:
         if out.shape != (T, N) or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be contiguous, [tokens, outputDim] of the given type")
         _mx_device(device, out)
+    if side is not None:
+        _hold(side, x_codes, x_scales, w_codes, w_scales, out)
     rc = _LIB.mx_matmul(x_codes.data_ptr(), x_scales.data_ptr(), x_bits, w_codes.data_ptr(), w_scales.data_ptr(),
-                        out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T,
-                        _Torch.raw_stream(device) if stream is None else _stream_ptr(stream))
+                        out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T, at)
     if rc:
         _check(rc)
     return out
