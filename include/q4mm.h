@@ -28,6 +28,9 @@
  * writes, may be fetched before the previous kernel has finished; x is read
  * and y written only after it has.
  *
+ * Device: a call runs on the current device (cudaGetDevice), whose pointers
+ * and stream it must be given.
+ *
  * Errors: every entry point returns Q4MM_OK (0) or a negative q4mm_status;
  * q4mm_last_error() then returns a message for the calling thread.  No C++
  * exception crosses this boundary.  Asynchronous faults surface through the

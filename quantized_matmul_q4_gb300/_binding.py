@@ -187,7 +187,7 @@ class _Torch:
     much as an elementwise torch operation, mostly its allocations and the
     launch; what is left is kept short."""
     dtypes: dict = {}
-    uint8 = float32 = empty = raw_stream = None
+    uint8 = float32 = empty = raw_stream = current_device = None
 
     @classmethod
     def load(cls):
@@ -195,13 +195,18 @@ class _Torch:
         cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
         cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
         # The current stream's handle alone: a Stream object costs as much as a launch.
-        cls.raw_stream = torch._C._cuda_getCurrentRawStream
+        cls.raw_stream, cls.current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _call_stream(stream, device: int):
-    """The handle of a call's stream, and the stream where it is not the current one (else None)."""
+    """The handle of a call's stream, and the stream where it is not the
+    current one (else None).  The library launches on the current device, so
+    tensors and stream have to be that device's."""
     if _Torch.raw_stream is None:
         _Torch.load()
+    if device != _Torch.current_device():
+        raise ValueError(f"the tensors are on device {device}, the current device is {_Torch.current_device()}: "
+                         "call under torch.cuda.device(...) of the tensors")
     current = _Torch.raw_stream(device)
     if stream is None:
         return current, None
@@ -211,6 +216,8 @@ def _call_stream(stream, device: int):
     if not hasattr(stream, "record_event"):
         import torch
         stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    elif stream.device.index != device:
+        raise ValueError("the stream must be of the tensors' device")
     return handle, stream
 
 
@@ -242,6 +249,9 @@ def _prep(x, w, K, bytes_per_row, out, N, stream, w2=None):
         raise ValueError("x must be a contiguous float32 CUDA tensor")
     if w.dtype != torch.uint8 or not w.is_cuda or not w.is_contiguous():
         raise ValueError("the packed weight must be a contiguous uint8 CUDA tensor")
+    device = x.get_device()
+    if any(t is not None and t.get_device() != device for t in (w, w2, out)):
+        raise ValueError("all tensors of a call must be on one CUDA device")
     x2 = x.reshape(-1, x.shape[-1])
     T, K_ = x2.shape
     if K is not None and K != K_:
@@ -253,7 +263,7 @@ def _prep(x, w, K, bytes_per_row, out, N, stream, w2=None):
     if out is not None and (out.dtype != torch.float32 or not out.is_cuda or not out.is_contiguous()
                             or out.numel() != T * N):
         raise ValueError("out must be a contiguous float32 CUDA tensor with tokens·outputDim elements")
-    handle, side = _call_stream(stream, x.get_device())
+    handle, side = _call_stream(stream, device)
     if out is None:
         out = _empty_on(side)((T, N), dtype=torch.float32, device=x.device)
     if side is not None:
@@ -308,6 +318,8 @@ def q4k_relayout_tc(w, K: int, N: int | None = None, out=None, stream=None):
     if out is not None and (out.dtype != torch.uint8 or not out.is_cuda or not out.is_contiguous()
                             or out.numel() != nbytes):
         raise ValueError("out must be a contiguous uint8 CUDA tensor of tc_relayout_bytes(K, N) bytes")
+    if out is not None and out.get_device() != w.get_device():
+        raise ValueError("all tensors of a call must be on one CUDA device")
     at, side = _call_stream(stream, w.get_device())
     if out is None:
         out = _empty_on(side)(nbytes, dtype=torch.uint8, device=w.device)
@@ -471,7 +483,7 @@ def mx_quantize(x, bits: int = 8, out: MxTensor | None = None, stream=None) -> M
     """x [..., K] (float32, float16 or bfloat16) to an MX tensor of `bits` (4 or 8) bits."""
     x, rows, K, stride, device = _mx_rows(x, "x")
     dtype = _mx_dtype(x.dtype, "x")
-    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    at, side = _call_stream(stream, device)
     out = _mx_out(rows, K, bits, x, device, out, side)
     if side is not None:
         _hold(side, x, out[0], out[1])
@@ -490,7 +502,7 @@ def mx_swiglu(gate, up, bits: int = 8, out: MxTensor | None = None, stream=None)
     if device != udevice:
         raise ValueError("all tensors of a call must be on one CUDA device")
     dtype = _mx_dtype(gate.dtype, "gate")
-    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    at, side = _call_stream(stream, device)
     out = _mx_out(rows, K, bits, gate, device, out, side)
     if side is not None:
         _hold(side, gate, up, out[0], out[1])
@@ -515,7 +527,7 @@ def mx_rmsnorm(x, weight, eps: float = 1e-5, residual=None, bits: int = 8, out: 
     if weight.numel() != K or not weight.is_contiguous():
         raise ValueError("weight must be contiguous and hold one value per column of x")
     _mx_device(device, weight)
-    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    at, side = _call_stream(stream, device)
     res_ptr, rs, h_ptr, hs = 0, K, 0, K
     if residual is not None:
         if residual.shape != shape or residual.dtype != xtype:
@@ -550,7 +562,7 @@ def mx_dequantize(q: MxTensor, dtype=None, out=None, stream=None):
     codes, scales, K, bits = q
     device = codes.get_device()
     rows = _mx_check(q, "q", device)
-    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    at, side = _call_stream(stream, device)
     stride = K
     if out is None:
         new = _Torch.empty if side is None else _empty_on(side)
@@ -580,7 +592,7 @@ def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
         raise ValueError("w must be a 4-bit MX tensor")
     if K != w_K:
         raise ValueError("x and w must have the same K")
-    at, side = (_Torch.raw_stream(device), None) if stream is None else _call_stream(stream, device)
+    at, side = _call_stream(stream, device)
     if out is None:
         new = _Torch.empty if side is None else _empty_on(side)
         out = new((T, N), dtype=dtype or _Torch.float32, device=x_codes.device)

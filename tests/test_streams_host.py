@@ -14,6 +14,7 @@ class _Stream:
 
     def __init__(self, handle):
         self.cuda_stream = handle
+        self.device = types.SimpleNamespace(index=0)
 
     def record_event(self):
         raise AssertionError("nothing is recorded on a stream itself")
@@ -26,7 +27,7 @@ def host(monkeypatch):
     import quantized_matmul_q4_gb300 as q
     from quantized_matmul_q4_gb300 import _binding as b
 
-    h = types.SimpleNamespace(q=q, torch=torch, calls=[], under=CURRENT, pools={}, records=[], keep=[])
+    h = types.SimpleNamespace(q=q, torch=torch, calls=[], device=0, under=CURRENT, pools={}, records=[], keep=[])
 
     class Library:
         def __getattr__(self, name):
@@ -51,6 +52,7 @@ def host(monkeypatch):
     b._Torch.load()
     monkeypatch.setattr(b, "_LIB", Library())
     monkeypatch.setattr(b._Torch, "raw_stream", lambda device: CURRENT)
+    monkeypatch.setattr(b._Torch, "current_device", lambda: h.device)
     monkeypatch.setattr(b._Torch, "empty", empty)
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
@@ -137,3 +139,44 @@ def test_results_written_into_given_tensors_wait_too(host):
     y = torch.zeros(3, 2)
     q.q4k_matmul(torch.zeros(3, 256), torch.zeros(288, dtype=torch.uint8), out=y, stream=OTHER)
     assert (y.data_ptr(), OTHER) in host.records
+
+
+@pytest.mark.parametrize("i", range(COUNT))
+def test_tensors_of_another_device_are_refused(host, i):
+    # The library would launch on the current device with the other one's pointers.
+    host.device = 1
+    for stream in (None, OTHER, _Stream(OTHER)):
+        with pytest.raises(ValueError, match="device"):
+            _calls(host)[i][1](stream)
+    assert not host.calls
+
+
+@pytest.mark.parametrize("i", range(COUNT))
+def test_a_stream_of_another_device_is_refused(host, i):
+    stream = _Stream(OTHER)
+    stream.device.index = 1
+    with pytest.raises(ValueError, match="device"):
+        _calls(host)[i][1](stream)
+    assert not host.calls
+
+
+def test_tensors_of_two_devices_are_refused(host, monkeypatch):
+    q, torch = host.q, host.torch
+    there = []
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: int(any(t is o for o in there)))
+    x, g = torch.zeros(3, 256), torch.zeros(256)
+    wq, up = torch.zeros(2 * 144, dtype=torch.uint8), torch.zeros(2 * 144, dtype=torch.uint8)
+    y, r = torch.zeros(3, 2), torch.zeros(3, 256)
+    codes, scales = torch.zeros(3, 256, dtype=torch.uint8), torch.zeros(1, 2, 512, dtype=torch.uint8)
+    relaid = torch.zeros(q.tc_relayout_bytes(256, 2), dtype=torch.uint8)
+    out = q.MxTensor(codes, scales, 256, 8)
+    for other, call in [(wq, lambda: q.q4k_matmul(x, wq)), (y, lambda: q.q4k_matmul(x, wq, out=y)),
+                        (up, lambda: q.q4k_ffn_swiglu(x, wq, up)),
+                        (relaid, lambda: q.q4k_relayout_tc(wq, 256, out=relaid)),
+                        (r, lambda: q.mx_swiglu(x, r)), (g, lambda: q.mx_rmsnorm(x, g)),
+                        (r, lambda: q.mx_rmsnorm(x, g, residual=r)), (scales, lambda: q.mx_quantize(x, out=out)),
+                        (codes, lambda: q.mx_dequantize(out))]:
+        there[:] = [other]
+        with pytest.raises(ValueError, match="device"):
+            call()
+    assert not host.calls
