@@ -870,6 +870,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     mm_fence_before();
     __syncthreads();
+    // The last commit arrives at both CTAs, and nothing else that the other
+    // one does says that it has: each waits for it itself, or it could land
+    // in the shared memory of the SM's next CTA.
+    if (warp == 1) (void)mbar_wait_bounded(done, 0, wait_limit);
+    __syncwarp();
     cluster_sync_all();  // neither CTA leaves while the other may signal it
     if (warp == 1) {
         mm_fence_after();
