@@ -668,15 +668,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         // No copy may still be writing shared memory at exit: the MMAs wait
         // for every stage, and their completion is awaited here.  After a
-        // time-out, which leaves copies that nobody waits for, give them far
-        // longer than a copy takes.
+        // time-out, which leaves copies that nobody waits for (they count on
+        // the other CTA's barriers), give them far longer than a copy takes.
         for (int k = 0; k < L::kStages && ok; ++k) {
             ok = __all_sync(0xffffffffu, mbar_wait_abortable(&empty[s], ph, wait_limit, &abort_flag) ? 1 : 0) != 0;
             if (++s == L::kStages) s = 0, ph ^= 1u;
         }
         if (!ok) {
             if (lane == 0) abort_flag = 1;
-            __nanosleep(1000000);
+            outlast_copies();
         }
         __syncwarp();
     } else if (warp == 1) {

@@ -144,6 +144,14 @@ __device__ __forceinline__ void fence_async_proxy() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// For about half a millisecond, hundreds of times what a copy takes: the end
+// of a kernel whose wait ran out and which cannot test the barriers of its
+// copies in flight.  (By the clock: a sleep may end at once.)
+__device__ __forceinline__ void outlast_copies() {
+    const long long t0 = clock64();
+    while (clock64() - t0 < 1000000LL) __nanosleep(1000);
+}
+
 // Named barrier over `nthreads` threads (a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
