@@ -18,6 +18,21 @@ struct LaunchCtx {
     int withhold;          // test only: a weight stage never copied (-1: none)
 };
 
+// Tensor memory.  An allocation that finds too few of an SM's 512 columns free
+// waits until another CTA gives its own back, and the scheduler counts no
+// columns: CTAs share an SM wherever threads, registers and shared memory
+// allow.  So that no kernel of this library ever waits there for another (of
+// two clusters, each could hold the SM that the other needs), shared memory
+// keeps apart what does not fit: a kernel that allocates up to half of the
+// columns takes at least kHalfTmemShared of it, so at most two such CTAs share
+// an SM, and one that allocates more leaves less than kHalfTmemShared free.
+// (Sizes with the 1 KB that the system adds to each CTA; asserted where the
+// kernels' layouts are.)
+constexpr uint32_t kSmShared = 228 * 1024;
+constexpr uint32_t kCtaSharedExtra = 1024;
+constexpr uint32_t kHalfTmemShared = 96 * 1024;
+static_assert(3 * kHalfTmemShared > kSmShared, "two CTAs with half of the columns at most");
+
 // Q4_K decode GEMV, 1..8 tokens on the one-token kernel (bulk-copied weight
 // rows, byte planes of x in registers; each compute warp serves one token).
 // Returns cudaErrorNotSupported when the shape is outside its geometry.

@@ -33,12 +33,11 @@
 //    the board's power limit.  Small tiles of tokens are bound by the fixed
 //    work of a stage and the launch.
 //
-// Tensor memory: a CTA waits for its columns while another holds them, so two
-// kernels must never wait for each other's.  They do not: every CTA of a grid
-// has its columns before it lets the next grid on the stream start, and grids
-// on different streams share an SM only where both fit, columns included (two
-// CTAs of the split form, at most 256 columns each; a pair's CTA takes all of
-// an SM's shared memory).
+// Tensor memory: every CTA of a grid has its columns before it lets the next
+// grid on the stream start, and grids of this library on different streams
+// share an SM only where the columns of both fit, which their shared memory
+// sees to (kernels.h): a CTA of the split form takes at most 256 columns and
+// some 100 KB, one of a pair all columns and all shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -81,7 +80,7 @@ struct MmLayout {
     static constexpr int kColsUsed = kColSx + 4 * kScaleTiles;
     static constexpr int kCols = kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128 : 256;
     static_assert(kStages >= 2 && kStages <= 8 && 2 * (total + 1024) <= 233472, "two CTAs per SM");
-    static_assert(2 * kCols <= 512, "tensor memory of two CTAs");
+    static_assert(2 * kCols <= 512 && total + kCtaSharedExtra >= kHalfTmemShared, "tensor memory of two CTAs");
     static_assert(kTok <= kMxTileRows && kTok * kMmRows * 4 <= off_bar, "partial sums fit the ring");
 };
 
@@ -445,6 +444,7 @@ struct PairLayout {
     static constexpr int kBars = 3 * kStages + 5;
     static constexpr uint32_t total = off_bar + 8 * kBars + 16 + 1024;
     static_assert(total <= 232448, "shared memory");
+    static_assert(total + kCtaSharedExtra + kHalfTmemShared > kSmShared, "tensor memory for itself");
     static_assert(kScaleBufs >= 3, "scale buffers");
 };
 

@@ -123,6 +123,7 @@ struct TcLayout {
     static constexpr uint32_t off_misc = off_bar + 8 * n_bars;
     static constexpr uint32_t total = off_misc + 16;
     static_assert(off_w % 1024 == 0, "activation tiles must be 1024-byte aligned");
+    static_assert(total + 1024 + kCtaSharedExtra + kHalfTmemShared > kSmShared, "tensor memory for itself");
     // The epilogue's tiles (own: 256 rows x 72 token slots; receive: S - 1
     // slots of at most 86 rows, S = 3, or 64 rows, S = 4, x 68) reuse the rings.
     static_assert((kTcRows * 72 + 2 * 86 * 68) * 4 <= off_bar && (kTcRows * 72 + 3 * 64 * 68) * 4 <= off_bar,
