@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -426,7 +427,8 @@ def _mx_rows(x, what: str):
         if not shape:
             raise ValueError(f"{what} must have at least one dimension")
         try:
-            x = x.view(-1, shape[-1]) if x.numel() else x.reshape(-1, max(shape[-1], 1))
+            # (No row count can be inferred from nothing: 2 x 0 x 96 is no rows, 2 x 3 x 0 six empty ones.)
+            x = x.view(-1, shape[-1]) if x.numel() else x.reshape(math.prod(shape[:-1]), shape[-1])
         except RuntimeError:
             raise ValueError(f"the leading dimensions of {what} must collapse into evenly spaced rows") from None
         shape = x.shape
