@@ -195,8 +195,10 @@ class _Torch:
         import torch
         cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
         cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
+        cls.current_device = torch._C._cuda_getDevice
         # The current stream's handle alone: a Stream object costs as much as a launch.
-        cls.raw_stream, cls.current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        # Last: who finds it set (every call looks, in _call_stream) finds the others set too.
+        cls.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call_stream(stream, device: int):
