@@ -414,7 +414,8 @@ int mx_swiglu(const void *gate, long long gate_stride, const void *up, long long
  * where h is not NULL (the norm takes it before that rounding).  h may be x
  * or residual itself (same base and stride), and overlaps nothing else.
  * weight: K values of x's type or of Q4MM_F32.  The sum of squares is an
- * fp32 sum in a fixed order; it overflows where h reaches about 1e19.
+ * fp32 sum in a fixed order; it overflows where h reaches about 1e19, and with
+ * eps = 0 a row whose squares all underflow (|h| below about 1e-23) is NaN.
  * Limits and returns as mx_quantize, and eps >= 0.
  */
 int mx_rmsnorm(const void *x, long long x_stride, const void *residual, long long residual_stride, void *h,

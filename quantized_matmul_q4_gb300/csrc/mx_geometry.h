@@ -20,26 +20,27 @@ Q4MM_HD constexpr int mx_first_row(int s, int S) { return 4 * (32 * s / S); }
 // of K (256 values with 4-bit x, 128 with 8-bit).  The constants are fitted
 // to 1144 measurements of 286 products on GB300 (chains of calls in a CUDA
 // graph, 17 to 2048 tokens, K and N of 256 to 16384, with 1, 2 and 4 times
-// the fewest tiles of tokens), where the choice costs 0.3% on the mean against
-// always the fastest; some of them, single CTAs with K split / CTA pairs:
+// the fewest tiles of tokens), where the choice costs 0.4% on the mean against
+// always the fastest, 8% at most; some of them, single CTAs with K split / CTA
+// pairs:
 //   T    K        N       x     measured       estimated
 //   17   256   -> 4096    4     2.5 /  3.5      2.3 /  3.4
-//   64   4096  -> 4096    8     6.6 /  8.0      7.0 /  8.1
+//   64   4096  -> 4096    8     6.6 /  8.1      7.0 /  8.1
 //   64   2560  -> 6912    4     6.2 /  4.8      6.1 /  5.1
-//   128  1024  -> 4096    8     6.5 /  4.5      6.4 /  4.8
-//   128  4096  -> 4096    4     7.3 /  5.9      7.4 /  6.2
-//   128  4096  -> 11008   8    12.9 /  9.7     12.6 /  9.3
-//   200  4096  -> 4096    8    10.7 /  8.9     11.5 /  8.9
-//   256  1024  -> 1024    8     6.3 /  4.5      6.4 /  4.6
-//   256  8192  -> 8192    4    16.0 / 11.7     15.3 / 10.1
-//   420  11008 -> 4096    8    24.4 / 19.7     24.5 / 18.4
-//   512  4096  -> 11008   8    32.5 / 22.2     34.6 / 21.2
-//   1024 11008 -> 4096    8    37.6 / 30.0     37.1 / 29.4
+//   128  1024  -> 4096    8     6.4 /  4.5      6.4 /  4.8
+//   128  4096  -> 4096    4     7.2 /  6.0      7.4 /  6.2
+//   128  4096  -> 11008   8    12.7 /  9.7     12.6 /  9.3
+//   200  4096  -> 4096    8    10.7 /  9.0     11.5 /  8.9
+//   256  1024  -> 1024    8     6.2 /  4.5      6.4 /  4.6
+//   256  8192  -> 8192    4    15.9 / 11.7     15.3 / 10.1
+//   420  11008 -> 4096    8    24.1 / 19.5     24.5 / 18.4
+//   512  4096  -> 11008   8    32.4 / 21.7     34.6 / 21.2
+//   1024 11008 -> 4096    8    37.2 / 29.5     37.1 / 29.4
 
 // Single CTAs, tiles of 128 rows x up to 128 tokens, S of them sharing a
 // tile's K: rounds of two CTAs per SM through their stages, then the stores
 // of y or, before them, the sum of the partial sums over the cluster.  (One
-// token, 4096 -> 22016, 8 bits: 12.6 us unsplit, 15.8 in two rounds of S = 3.)
+// token, 4096 -> 22016, 8 bits: 11.9 us unsplit, 14.8 in two rounds of S = 3.)
 inline double mx_split_us(int row_tiles, int tok_tiles, int tokens, int stages, int S, int x_bits, int num_sms) {
     const long long ctas = (long long)row_tiles * tok_tiles * S, slots = 2LL * num_sms;
     const double tok = tokens < 128 ? tokens / 128.0 : 1.0;
@@ -58,7 +59,7 @@ inline int mx_split(int row_tiles, int tok_tiles, int tokens, int stages, int x_
     double us = mx_split_us(row_tiles, tok_tiles, tokens, stages, 1, x_bits, num_sms);
     for (int S = 2; S <= kMxMaxSplit && 2 * S <= stages; ++S) {
         // Above 16 tokens shares of 16 to 28 rows are summed slowly: 128 tokens
-        // through 4096 x 4096 in 8 bits take 8.4, 12.5 and 11.3 us with S = 4, 6, 8.
+        // through 4096 x 4096 in 8 bits take 8.3, 12.1 and 10.9 us with S = 4, 6, 8.
         if (tokens > 16 && S > 4 && S < 8) continue;
         const double t = mx_split_us(row_tiles, tok_tiles, tokens, stages, S, x_bits, num_sms);
         if (t < us) us = t, best = S;

@@ -19,19 +19,24 @@
 // Two forms, chosen by mx_geometry.h from estimates of both:
 //  * mx_mm_split_kernel, up to 128 tokens a tile, K split over a cluster.  A
 //    call with few tokens reads its weights once and is bound by them and by
-//    the chain of latencies around them: 4096 x 4096 at one token takes 4.0
-//    us (x in 4 bits) and 4.6 (8 bits, whose unpacking copies move 64 bytes
+//    the chain of latencies around them: 4096 x 4096 at one token takes 4.2
+//    us (x in 4 bits) and 4.8 (8 bits, whose unpacking copies move 64 bytes
 //    a row) in a chain of calls, of which 1.3 us are the weights' at the
-//    copy rate, 2.8 a small product's (1024 x 1024; 128 x 128 unsplit 1.8).
-//    16384 -> 38912 takes 58 us, 5.8 TB/s, 86% of the copy rate.
+//    copy rate, 2.9 a small product's (1024 x 1024; 128 x 128 unsplit 1.9).
+//    Tiles are dealt whole, so a width whose tiles do not fill whole rounds
+//    of SMs is bound by the SMs that take one more: 4096 -> 22016, 172 tiles
+//    on 152 SMs, 10.2 and 12.2 us where the bytes take 7.1, against 16384 ->
+//    38912, two tiles to every SM, 52 and 55 us, 6.5 and 6.2 TB/s.
 //  * mx_mm_pair_kernel, 256 rows x 256 tokens on a pair of CTAs, for the
-//    rest.  8192 tokens 4096 -> 11008: 111 us in 4 bits (6.6 PFLOP/s), 205 in
-//    8 (3.6); 8192 tokens 8192 -> 8192: 148 us (7.4 PFLOP/s).  Bound by the
+//    rest.  8192 tokens 4096 -> 11008: 112 us in 4 bits (6.6 PFLOP/s), 206 in
+//    8 (3.6); 8192 tokens 8192 -> 8192: 147 us (7.5 PFLOP/s).  Bound by the
 //    tensor pipe (four MMAs of 256 tokens of a 4-bit stage alone run 620
 //    cycles where 512 are nominal), by some 900 cycles between two tiles and
 //    by the last, partly filled round of tiles; kept busy for seconds, by
 //    the board's power limit.  Small tiles of tokens are bound by the fixed
-//    work of a stage and the launch.
+//    work of a stage and the launch, and, where there are fewer tiles than
+//    pairs, by the stages that each walks one after the other, since pairs
+//    do not split K (300 tokens 11008 -> 4096 in 8 bits: 64 tiles, 19.7 us).
 //
 // Tensor memory: every CTA of a grid has its columns before it lets the next
 // grid on the stream start, and grids of this library on different streams
@@ -717,7 +722,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // whole warp takes the loop and one lane issues, so that addresses
             // and descriptors stay in uniform registers, where the MMAs want
             // them (8192 tokens 4096 -> 11008, 4 bits: 114.4 us with one lane
-            // in the loop, 111 so; 77 tokens 2560 -> 6912: 5.7, 5.25).
+            // in the loop, 111 so).
             const bool leader = elect_lane();
             int s = 0, buf = 0, it = 0;
             uint32_t ph = 0;

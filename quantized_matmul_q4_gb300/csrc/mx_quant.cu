@@ -284,7 +284,7 @@ struct ByteExchange {
 // x / (1 + e^-x) of two values, to 9·2^-24, for x >= kSiluFar.  e^-x is 2^t,
 // t = -x·log2 e; the product's rounding, and log2 e's own, would cost |t|
 // units in the last place, so t = hi + lo and 2^t = 2^hi + 2^hi·lo·ln 2 (with
-// expf and an exact quotient 4099 x 11008 bf16 takes 42.6 us instead of 36.3,
+// expf and an exact quotient 4099 x 11008 bf16 takes 53.6 us instead of 35.7,
 // where the bytes alone take 33).  Infinities above and NaN pass through the
 // quotient; below kSiluFar its reciprocal would be subnormal, which is flushed.
 constexpr float kSiluFar = -87.f;  // 1 + e^87 < 2^126
@@ -362,8 +362,8 @@ struct FarGates {
 // last one get zero scale bytes and no codes.  blockIdx.x: 32 row groups per
 // 128-row block; blockIdx.y and the warp: the column chunk.
 // CTAs per SM that the registers have to allow: SwiGLU 4, and 3 unaligned
-// (4099 x 11008 bf16: 37.5 -> 36.3 us; 8192 x 4095: 51.0, 42.7 with 1, 3);
-// else 4 unaligned (8192 x 4095 bf16 to 8-bit codes: 26.8 -> 22.9).
+// (4099 x 11008 bf16: 46.7 -> 35.7 us; 8192 x 4095: 50.9 -> 43.3);
+// else 4 unaligned (8192 x 4095 bf16 to 8-bit codes: 26.7 -> 22.5).
 template <class T, bool kVec, bool kSwiGLU>
 __global__ void __launch_bounds__(256, kSwiGLU ? (kVec ? 4 : 3) : (kVec ? 1 : 4))
     mx_quantize_kernel(const T *__restrict__ x, long long x_stride, const T *__restrict__ up, long long up_stride,
