@@ -180,7 +180,8 @@ def device_status(stream=None, clear: bool = True) -> None:
 # ready there, and a user of the results waits for that stream.  Memory is
 # safe, though: results come from the pool of the call's stream, and neither
 # they nor the tensors given are reused before both streams are past them,
-# however early they are dropped.
+# however early they are dropped.  (A stream given by its handle has to live
+# as long as that memory.)
 
 class _Torch:
     """What the calls take from torch, looked up on the first of them (the
@@ -368,16 +369,14 @@ def q4k_ffn_swiglu(x, w_gate, w_up, N: int | None = None, out=None, stream=None)
             or not w_up.is_contiguous()):
         raise ValueError("w_up must be a contiguous CUDA uint8 tensor of the gate weight's size")
     x2, T, K, N, out, at = _prep(x, w_gate, None, lambda k: (k // Q4K_VALUES) * Q4K_BYTES, out, N, stream, w_up)
-    q4k_ffn_swiglu_ptr(x2.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(),
-                       K, N, T, at)
+    q4k_ffn_swiglu_ptr(x2.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
 def ternary_gemv(x, w, scale: float = 1.0, N: int | None = None, out=None, stream=None):
     """y[T, N] = scale · x[T, K] · codes(W)ᵀ, BitNet b1.58 payload, FP32."""
     x2, T, K, N, out, at = _prep(x, w, None, lambda k: k // 4, out, N, stream)
-    ternary_gemv_ptr(x2.data_ptr(), w.data_ptr(), float(scale), out.data_ptr(), K, N, T,
-                     at)
+    ternary_gemv_ptr(x2.data_ptr(), w.data_ptr(), float(scale), out.data_ptr(), K, N, T, at)
     return out.view(T, N)
 
 
