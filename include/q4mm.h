@@ -54,7 +54,8 @@ typedef enum {
     Q4MM_ERR_ALIGN = -3,   /* a pointer is not aligned as its entry point requires */
     Q4MM_ERR_CUDA = -4,    /* the CUDA runtime reported an error (launch, device query) */
     Q4MM_ERR_TIMEOUT = -5, /* a bounded in-kernel wait ran out (see q4mm_device_status) */
-    Q4MM_ERR_ALIAS = -6    /* x, W and y overlap */
+    Q4MM_ERR_ALIAS = -6,   /* x, W and y overlap */
+    Q4MM_ERR_INDEX = -7    /* a page number or position outside the cache (see q4mm_device_status) */
 } q4mm_status;
 
 /* Largest inputDim accepted by every entry point. */
@@ -444,6 +445,109 @@ int mx_dequantize(const void *codes, const void *scales, void *y, long long y_st
 int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void *w_codes, const void *w_scales,
               void *y, int dtype, int inputDim, int outputDim, int tokens, q4mm_stream_t stream);
 
+/*
+ * ---- Attention on a paged MX cache ----------------------------------------
+ *
+ * rope_rotate — rotary positions.  x [tokens][heads][headDim] of type dtype,
+ * strides in elements, the values of a head adjacent.  The first `rotated`
+ * values of a head (an even number) are pairs (u, v), (2i, 2i + 1) where
+ * interleaved, else (i, i + rotated / 2); with a = position · frequencies[i]
+ *   u' = magnitude · (u cos a − v sin a),  v' = magnitude · (v cos a + u sin a)
+ * and the values behind them are copied.  out is x itself (same base and
+ * strides) or does not overlap it.
+ * positions: `tokens` values of 32 bits, or of 64 where positions_64; any
+ *            sign.  frequencies: rotated / 2 doubles, radians per position
+ *            (NULL where rotated is 0).  The angle is reduced exactly; the
+ *            frequency is taken to 2^-61 radians (and 2^-60 of itself), so
+ *            an angle is off by that times the position.
+ * Precision: fp32; cos and sin within 2·2^-24, so |u' − exact| <=
+ *            2^-22·magnitude·(|u| + |v|) before the rounding to dtype.
+ * Limits: 1 <= headDim <= Q4MM_ROPE_MAX_HEAD; 0 <= rotated <= headDim, even;
+ *         1 <= heads <= Q4MM_MX_MAX_HEADS; 0 <= tokens <=
+ *         Q4MM_MX_MAX_ROWS; magnitude finite.
+ * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
+ */
+#define Q4MM_ROPE_MAX_HEAD 256
+#define Q4MM_MX_MAX_HEADS 65536
+int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride, int dtype, const void *positions,
+                int positions_64, const double *frequencies, int rotated, int interleaved, float magnitude, void *out,
+                long long out_token_stride, long long out_head_stride, int tokens, int heads, int headDim,
+                q4mm_stream_t stream);
+
+/*
+ * The paged MX cache.  Keys and values of each of kvHeads heads, headDim
+ * values (32, 64, 96 or 128) a token, quantised as by mx_quantize in blocks of
+ * 32 along the head, in `pages` pages of pageTokens tokens (a multiple of 16):
+ *   codes : [pages][kvHeads][pageTokens] rows of headDim·bits/8 bytes
+ *           (16-byte aligned base);
+ *   scales: [pages][kvHeads][pageTokens][4] bytes, block b of the head in byte
+ *           b, bytes past headDim / 32 written as zero and not read (4-byte
+ *           aligned base).
+ * k and v each have codes and scales.
+ *
+ * A batch: sequence i of `sequences` has the rows starts[i] .. starts[i + 1]
+ * of a call's dense tensors (starts has sequences + 1 ascending entries), the
+ * last of the lengths[i] tokens that it has in the cache with them; its
+ * position p lies at place p % pageTokens of page table[i·tableWidth +
+ * p / pageTokens].  The three arrays are device memory, 32-bit; a call reads
+ * them on its stream, so a captured one may be replayed on new contents.  A
+ * page number outside 0 .. pages − 1, or a position beyond the table, is not
+ * accessed: q4mm_device_status then reports Q4MM_ERR_INDEX, and what that call
+ * computes for the sequence is undefined.  Rows before position 0 (more rows
+ * than lengths[i]) take part in nothing; rows behind the last sequence are
+ * left as they were.
+ *
+ * mx_cache_write — k, v [tokens][kvHeads][headDim] of type dtype, strided as
+ * for rope_rotate, to their places: k turned as by rope_rotate at its positions
+ * (rotated = 0: as it is) in fp32 and then quantised, with no rounding between.
+ * Two rows must not have the same place (pages of one table shared with
+ * another sequence hold what neither writes).
+ *
+ * mx_cache_read — the values of the batch's rows, as mx_dequantize gives them.
+ *
+ * Limits: headDim 32, 64, 96 or 128; bits 4 or 8; pages >= 1;
+ *         1 <= kvHeads <= Q4MM_MX_MAX_HEADS; pageTokens a positive multiple of
+ *         16, at most 2^24; 0 <= sequences <= 2^24; tableWidth >= 0; tokens and
+ *         rotated as for rope_rotate.  No tokens or no sequences: nothing to do.
+ * Return Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
+ */
+int mx_cache_write(const void *k, long long k_token_stride, long long k_head_stride, const void *v,
+                   long long v_token_stride, long long v_head_stride, int dtype, const double *frequencies,
+                   int rotated, int interleaved, float magnitude, void *k_codes, void *k_scales, void *v_codes,
+                   void *v_scales, int pages, int kvHeads, int pageTokens, int headDim, int bits, const int *starts,
+                   const int *lengths, const int *table, int sequences, int tableWidth, int tokens,
+                   q4mm_stream_t stream);
+int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales, int pages,
+                  int kvHeads, int pageTokens, int headDim, int bits, const int *starts, const int *lengths,
+                  const int *table, int sequences, int tableWidth, void *k, long long k_token_stride,
+                  long long k_head_stride, void *v, long long v_token_stride, long long v_head_stride, int dtype,
+                  int tokens, q4mm_stream_t stream);
+
+/*
+ * mx_attention — attention of a batch's rows over the cache:
+ *   y[t][h] = Σ_j softmax_j(scale · q[t][h]·k[j][h / G]) v[j][h / G],
+ * G = heads / kvHeads, over the sequence's cached positions j: those up to the
+ * row's own where causal, else all lengths[i].  A row that sees none gives
+ * zeros.  What a row does not see has no part in it, NaN and infinities
+ * included; a block of k that is NaN makes the rows that see it NaN, a block
+ * of v those rows' 32 values.
+ * q, y: [tokens][heads][headDim] of type dtype, strided as for rope_rotate,
+ * aligned to their elements, not overlapping each other or the cache.
+ * Precision: keys and values exact (what lies 2^-31 below the largest scale of
+ *         the 32 tokens around it counts as zero), queries exact to 2^-22 of a
+ *         row's largest value; scores, their maximum, sums and outputs in
+ *         fp32; probabilities rounded to 2^-12 (2^-22 where dtype is
+ *         Q4MM_F32) of their value or 2^-30 of the row's largest.
+ *         The same call gives the same bits again.
+ * Limits: as mx_cache_write; heads a multiple of kvHeads; scale finite, >= 0.
+ * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
+ */
+int mx_attention(const void *q, long long q_token_stride, long long q_head_stride, int dtype, const void *k_codes,
+                 const void *k_scales, const void *v_codes, const void *v_scales, int pages, int kvHeads,
+                 int pageTokens, int headDim, int bits, const int *starts, const int *lengths, const int *table,
+                 int sequences, int tableWidth, float scale, int causal, void *y, long long y_token_stride,
+                 long long y_head_stride, int tokens, int heads, q4mm_stream_t stream);
+
 /* Message for the last error returned on the calling thread ("" if none).
  * The pointer stays valid until the thread's next failing call. */
 const char *q4mm_last_error(void);
@@ -451,7 +555,8 @@ const char *q4mm_last_error(void);
 /*
  * q4mm_device_status — waits for `stream`, then returns Q4MM_OK, or
  * Q4MM_ERR_TIMEOUT if a bounded in-kernel wait of an earlier call on the
- * current device ran out.  clear != 0 resets the status word afterwards.
+ * current device ran out, or Q4MM_ERR_INDEX if one met a page number or a
+ * position outside its cache or table.  clear != 0 resets the status word afterwards.
  * Returns Q4MM_ERR_CUDA if the stream reports an error.
  */
 int q4mm_device_status(q4mm_stream_t stream, int clear);

@@ -13,6 +13,7 @@ Q4K_BYTES = 144
 _SYMBOLS = ("q4k_matmul", "q4k_matmul_tc", "q4k_matmul_tc_noalloc", "q4k_relayout_tc", "q4k_matmul_tc_relayouted",
             "q4_0_gemv", "q6k_gemv", "q4k_ffn_swiglu", "ternary_gemv",
             "mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul",
+            "rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention",
             "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait")
 
 
@@ -53,7 +54,13 @@ def _load() -> ctypes.CDLL:
     lib.mx_rmsnorm.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, f32, vp, vp, i32, i32, i32, vp]
     lib.mx_dequantize.argtypes = [vp, vp, vp, i64, i32, i32, i32, i32, vp]
     lib.mx_matmul.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, i32, vp]
-    for name in ("mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul"):
+    heads, cache, batch = [vp, i64, i64], [vp, vp, vp, vp, i32, i32, i32, i32, i32], [vp, vp, vp, i32, i32]
+    lib.rope_rotate.argtypes = [*heads, i32, vp, i32, vp, i32, i32, f32, *heads, i32, i32, i32, vp]
+    lib.mx_cache_write.argtypes = [*heads, *heads, i32, vp, i32, i32, f32, *cache, *batch, i32, vp]
+    lib.mx_cache_read.argtypes = [*cache, *batch, *heads, *heads, i32, i32, vp]
+    lib.mx_attention.argtypes = [*heads, i32, *cache, *batch, f32, i32, *heads, i32, i32, vp]
+    for name in ("mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul", "rope_rotate",
+                 "mx_cache_write", "mx_cache_read", "mx_attention"):
         getattr(lib, name).restype = i32
     lib.q4mm_last_error.argtypes = []
     lib.q4mm_last_error.restype = ctypes.c_char_p
@@ -162,6 +169,30 @@ def mx_matmul_ptr(x_codes: int, x_scales: int, x_bits: int, w_codes: int, w_scal
     _check(_LIB.mx_matmul(x_codes, x_scales, x_bits, w_codes, w_scales, y, dtype, K, N, T, stream))
 
 
+# (x, k, v, q, out, y: pointer, token stride, head stride; cache: the pointers of k's codes and scales and of v's, then
+# pages, kvHeads, pageTokens, headDim, bits; batch: the pointers starts, lengths, table, then sequences, tableWidth.)
+
+def rope_rotate_ptr(x, dtype: int, positions: int, positions_64: int, frequencies: int, rotated: int, interleaved: int,
+                    magnitude: float, out, tokens: int, heads: int, head_dim: int, stream: int = 0) -> None:
+    _check(_LIB.rope_rotate(*x, dtype, positions, positions_64, frequencies, rotated, interleaved, magnitude, *out,
+                            tokens, heads, head_dim, stream))
+
+
+def mx_cache_write_ptr(k, v, dtype: int, frequencies: int, rotated: int, interleaved: int, magnitude: float, cache,
+                       batch, tokens: int, stream: int = 0) -> None:
+    _check(_LIB.mx_cache_write(*k, *v, dtype, frequencies, rotated, interleaved, magnitude, *cache, *batch, tokens,
+                               stream))
+
+
+def mx_cache_read_ptr(cache, batch, k, v, dtype: int, tokens: int, stream: int = 0) -> None:
+    _check(_LIB.mx_cache_read(*cache, *batch, *k, *v, dtype, tokens, stream))
+
+
+def mx_attention_ptr(q, dtype: int, cache, batch, scale: float, causal: int, y, tokens: int, heads: int,
+                     stream: int = 0) -> None:
+    _check(_LIB.mx_attention(*q, dtype, *cache, *batch, scale, causal, *y, tokens, heads, stream))
+
+
 def arm_wait_failure(stage: int, limit_cycles: int) -> None:
     """Test hook: the calling thread's next call withholds weight stage `stage`
     and bounds its in-kernel waits by `limit_cycles` (see include/q4mm.h)."""
@@ -169,7 +200,8 @@ def arm_wait_failure(stage: int, limit_cycles: int) -> None:
 
 
 def device_status(stream=None, clear: bool = True) -> None:
-    """Raise Q4mmError if a bounded in-kernel wait ran out on this device."""
+    """Raise Q4mmError if a bounded in-kernel wait ran out on this device, or
+    a call met a page number or a position outside its cache or table."""
     _check(_LIB.q4mm_device_status(_stream_ptr(stream), int(clear)))
 
 
@@ -189,11 +221,13 @@ class _Torch:
     much as an elementwise torch operation, mostly its allocations and the
     launch; what is left is kept short."""
     dtypes: dict = {}
-    uint8 = float32 = empty = raw_stream = current_device = None
+    uint8 = float32 = int32 = int64 = float64 = empty = raw_stream = current_device = None
 
     @classmethod
     def load(cls):
         import torch
+        # (Whoever finds the dtypes, or uint8, set finds these set.)
+        cls.int32, cls.int64, cls.float64 = torch.int32, torch.int64, torch.float64
         cls.dtypes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}   # q4mm_dtype
         cls.uint8, cls.float32, cls.empty = torch.uint8, torch.float32, torch.empty
         cls.current_device = torch._C._cuda_getDevice
@@ -607,6 +641,273 @@ def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
         _hold(side, x_codes, x_scales, w_codes, w_scales, out)
     rc = _LIB.mx_matmul(x_codes.data_ptr(), x_scales.data_ptr(), x_bits, w_codes.data_ptr(), w_scales.data_ptr(),
                         out.data_ptr(), _mx_dtype(out.dtype, "out"), K, N, T, at)
+    if rc:
+        _check(rc)
+    return out
+
+
+# Attention on a paged MX cache: layouts, limits and precision in include/q4mm.h.
+
+class Rope(NamedTuple):
+    """Rotary positions of a head's first 2·len(frequencies) values.
+
+    frequencies: float64 CUDA tensor, radians per position of each pair
+    interleaved: pairs (2i, 2i + 1); else (i, i + len(frequencies))
+    magnitude:   factor of the rotated values
+    """
+    frequencies: "torch.Tensor"
+    interleaved: bool = False
+    magnitude: float = 1.0
+
+
+def rope_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original: int | None = None, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Frequencies base^(-2i/dim) of a head's dim / 2 pairs, stretched for a
+    context `factor` times the `original` one by `scaling`:
+      None      not at all
+      "linear"  every frequency divided by factor
+      "ntk"     base multiplied by factor^(dim / (dim - 2)): the slowest pair
+                is divided by factor, the fastest left
+      "parts"   by the turns r that a pair makes in the original context:
+                divided by factor below `slow` of them, left above `fast`, in
+                between mixed linearly (rope_magnitude goes with it)
+    """
+    import torch
+    if dim <= 0 or dim % 2:
+        raise ValueError("dim must be positive and even")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    if scaling not in (None, "linear", "ntk", "parts"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'parts'")
+    if scaling == "ntk":
+        if dim < 4:
+            raise ValueError("'ntk' needs at least two pairs")
+        base *= factor ** (dim / (dim - 2))
+    f = torch.tensor([base ** (-2 * i / dim) for i in range(dim // 2)], dtype=torch.float64)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if original is None or not original > 0 or not fast > slow:
+            raise ValueError("'parts' needs the original context, and fast above slow")
+        kept = ((original * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * kept + f / factor * (1 - kept)
+    return f.to(device)
+
+
+def rope_magnitude(factor: float) -> float:
+    """The magnitude that goes with "parts": 0.1·ln(factor) + 1 for a stretched context."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+class MxCache(NamedTuple):
+    """Keys and values of pages of tokens, quantised in MX blocks along the head.
+
+    k_codes, v_codes:   uint8 [pages, kv heads, page, head_dim·bits/8]
+    k_scales, v_scales: uint8 [pages, kv heads, page, 4]
+
+    A batch of sequences in it is three int32 CUDA tensors that every call
+    takes: starts [sequences + 1], lengths [sequences] and pages [sequences,
+    width].  Rows starts[i] .. starts[i + 1] of a call's tensors are the last of
+    the lengths[i] tokens that sequence i has in the cache; its position p is
+    place p % page of page pages[i, p // page].  Their contents are read on
+    the device: see device_status for those that lie outside the cache.
+    """
+    k_codes: "torch.Tensor"
+    k_scales: "torch.Tensor"
+    v_codes: "torch.Tensor"
+    v_scales: "torch.Tensor"
+    head_dim: int
+    bits: int
+
+
+def mx_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, bits: int = 8, device="cuda") -> MxCache:
+    """An empty cache."""
+    import torch
+    if head_dim not in (32, 64, 96, 128) or bits not in (4, 8) or page <= 0 or page % 16:
+        raise ValueError("head_dim must be 32, 64, 96 or 128, bits 4 or 8, and page a multiple of 16")
+    if pages <= 0 or kv_heads <= 0:
+        raise ValueError("pages and kv_heads must be positive")
+    def side():
+        return (torch.zeros(pages, kv_heads, page, head_dim * bits // 8, dtype=torch.uint8, device=device),
+                torch.zeros(pages, kv_heads, page, 4, dtype=torch.uint8, device=device))
+    return MxCache(*side(), *side(), head_dim, bits)
+
+
+def _heads_arg(x, what: str, shape=None):
+    """A [tokens, heads, head_dim] CUDA tensor: the C ABI's three arguments."""
+    got = x.shape
+    if len(got) != 3 or (shape is not None and got != shape):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim]" + (f" = {list(shape)}" if shape is not None else ""))
+    s0, s1, s2 = x.stride()
+    if s2 != 1 and got[2] > 1:
+        raise ValueError(f"the values of a head of {what} must be adjacent")
+    return x.data_ptr(), s0, s1
+
+
+def _cache_arg(c: MxCache, device: int):
+    kc, ks, vc, vs, D, bits = c
+    if _Torch.uint8 is None:
+        _Torch.load()
+    u8, shape = _Torch.uint8, kc.shape
+    if len(shape) != 4 or bits not in (4, 8) or shape[3] * 8 != D * bits:
+        raise ValueError("cache: codes must be [pages, kv heads, page, head_dim·bits/8]")
+    if vc.shape != shape or ks.shape != (*shape[:3], 4) or vs.shape != ks.shape:
+        raise ValueError("cache: scales must be [pages, kv heads, page, 4], and v's tensors like k's")
+    for t in (kc, ks, vc, vs):
+        if t.dtype != u8 or not t.is_contiguous():
+            raise ValueError("cache: codes and scales must be contiguous uint8 tensors")
+        if t.get_device() != device:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+    return kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], D, bits
+
+
+def _batch_arg(starts, lengths, pages, device: int):
+    i32 = _Torch.int32
+    for t in (starts, lengths, pages):
+        if t.dtype != i32 or not t.is_contiguous():
+            raise ValueError("starts, lengths and pages must be contiguous int32 tensors")
+        if t.get_device() != device:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+    if lengths.dim() != 1 or pages.dim() != 2 or starts.dim() != 1:
+        raise ValueError("starts and lengths must have one dimension, pages two")
+    n = lengths.shape[0]
+    if starts.shape[0] != n + 1 or pages.shape[0] != n:
+        raise ValueError("starts must be [sequences + 1], lengths [sequences] and pages [sequences, width]")
+    return starts.data_ptr(), lengths.data_ptr(), pages.data_ptr(), n, pages.shape[1]
+
+
+_NO_ROPE = (0, 0, 0, 1.0)
+
+
+def _rope_arg(rope: Rope, head_dim: int, device: int):
+    f, interleaved, magnitude = rope
+    if _Torch.float64 is None:
+        _Torch.load()
+    if f.dtype != _Torch.float64 or f.dim() != 1 or not f.is_contiguous():
+        raise ValueError("frequencies must be a contiguous float64 tensor of one dimension")
+    if f.get_device() != device:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    n = 2 * f.shape[0]
+    if n > head_dim:
+        raise ValueError("there are more frequencies than pairs in a head")
+    return f.data_ptr(), n, 1 if interleaved else 0, float(magnitude)
+
+
+def _cuda_device(x, what: str) -> int:
+    device = x.get_device()
+    if device < 0:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return device
+
+
+def rope_rotate(x, positions, rope: Rope, out=None, stream=None):
+    """x [tokens, heads, head_dim] (float32, float16 or bfloat16) with its
+    rotary positions (int32 or int64, one per token); out may be x itself."""
+    device = _cuda_device(x, "x")
+    dtype = _mx_dtype(x.dtype, "x")
+    xa = _heads_arg(x, "x")
+    T, H, D = shape = x.shape
+    if positions.dim() != 1 or positions.shape[0] != T or not positions.is_contiguous() or \
+            positions.dtype not in (_Torch.int32, _Torch.int64):
+        raise ValueError("positions must be a contiguous int32 or int64 tensor with one value per token")
+    _mx_device(device, positions)
+    ra = _rope_arg(rope, D, device)
+    at, side = _call_stream(stream, device)
+    if out is None:
+        new = _Torch.empty if side is None else _empty_on(side)
+        out = new(shape, dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype:
+        raise ValueError("out must have x's type")
+    else:
+        _mx_device(device, out)
+    oa = _heads_arg(out, "out", shape)
+    if side is not None:
+        _hold(side, x, positions, rope.frequencies, out)
+    rc = _LIB.rope_rotate(*xa, dtype, positions.data_ptr(), int(positions.dtype == _Torch.int64), *ra, *oa, T, H, D, at)
+    if rc:
+        _check(rc)
+    return out
+
+
+def mx_cache_write(cache: MxCache, k, v, starts, lengths, pages, rope: Rope | None = None, stream=None) -> MxCache:
+    """k (turned by rope, where it is given, at its positions) and v
+    [tokens, kv heads, head_dim] of a batch's new tokens into the cache."""
+    device = _cuda_device(k, "k")
+    dtype = _mx_dtype(k.dtype, "k")
+    if v.dtype != k.dtype:
+        raise ValueError("k and v must have the same type")
+    _mx_device(device, v)
+    ca = _cache_arg(cache, device)
+    ba = _batch_arg(starts, lengths, pages, device)
+    T = k.shape[0]
+    shape = (T, ca[5], ca[7])
+    ka, va = _heads_arg(k, "k", shape), _heads_arg(v, "v", shape)
+    ra = _NO_ROPE if rope is None else _rope_arg(rope, ca[7], device)
+    at, side = _call_stream(stream, device)
+    if side is not None:
+        _hold(side, k, v, *cache[:4], starts, lengths, pages, rope and rope[0])
+    rc = _LIB.mx_cache_write(*ka, *va, dtype, *ra, *ca, *ba, T, at)
+    if rc:
+        _check(rc)
+    return cache
+
+
+def mx_cache_read(cache: MxCache, starts, lengths, pages, tokens: int | None = None, dtype=None, out=None, stream=None):
+    """The values (k, v), each [tokens, kv heads, head_dim], of a batch's rows
+    (float32 unless dtype or out = (k, v) says otherwise)."""
+    device = _cuda_device(cache[0], "cache")
+    ca = _cache_arg(cache, device)
+    ba = _batch_arg(starts, lengths, pages, device)
+    at, side = _call_stream(stream, device)
+    if out is None:
+        if tokens is None or tokens < 0:
+            raise ValueError("tokens must say how many rows the result has")
+        shape = (tokens, ca[5], ca[7])
+        new = _Torch.empty if side is None else _empty_on(side)
+        dtype = dtype or _Torch.float32
+        k, v = new(shape, dtype=dtype, device=cache[0].device), new(shape, dtype=dtype, device=cache[0].device)
+    else:
+        k, v = out
+        shape = (k.shape[0] if tokens is None else tokens, ca[5], ca[7])
+        if k.dtype != v.dtype or (dtype is not None and k.dtype != dtype):
+            raise ValueError("k and v must have the same, and the given, type")
+        _mx_device(device, k), _mx_device(device, v)
+    ka, va = _heads_arg(k, "k", shape), _heads_arg(v, "v", shape)
+    if side is not None:
+        _hold(side, *cache[:4], starts, lengths, pages, k, v)
+    rc = _LIB.mx_cache_read(*ca, *ba, *ka, *va, _mx_dtype(k.dtype, "out"), shape[0], at)
+    if rc:
+        _check(rc)
+    return k, v
+
+
+def mx_attention(q, cache: MxCache, starts, lengths, pages, scale: float | None = None, causal: bool = True, out=None,
+                 stream=None):
+    """softmax(scale·q·kᵀ)·v of a batch's queries [tokens, heads, head_dim]
+    over their sequences' cached tokens (causal: up to their own), heads a
+    multiple of the cache's; scale is head_dim^-1/2 unless given.  A row that
+    sees nothing gives zeros; rows behind the last sequence are left as they were."""
+    device = _cuda_device(q, "q")
+    dtype = _mx_dtype(q.dtype, "q")
+    ca = _cache_arg(cache, device)
+    ba = _batch_arg(starts, lengths, pages, device)
+    qa = _heads_arg(q, "q")
+    T, H, D = shape = q.shape
+    if D != ca[7] or H == 0 or H % ca[5]:
+        raise ValueError("q must have the cache's head_dim, and a multiple of its heads")
+    at, side = _call_stream(stream, device)
+    if out is None:
+        new = _Torch.empty if side is None else _empty_on(side)
+        out = new(shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype:
+        raise ValueError("out must have q's type")
+    else:
+        _mx_device(device, out)
+    oa = _heads_arg(out, "out", shape)
+    if side is not None:
+        _hold(side, q, *cache[:4], starts, lengths, pages, out)
+    rc = _LIB.mx_attention(*qa, dtype, *ca, *ba, D ** -0.5 if scale is None else float(scale), 1 if causal else 0, *oa,
+                           T, H, at)
     if rc:
         _check(rc)
     return out

@@ -1,0 +1,122 @@
+// What the attention kernels share: the batch's rows in tiles, powers of two
+// as floats, codes to fp16.
+//
+// Numbers.  Codes times scales are exact in fp16 once a power of two is taken
+// out: with `ref` the largest scale exponent of a token (or of a group of
+// tokens), k' = code · 2^(7 + e - ref) is at most 448 · 2^7 < 65504, and what
+// falls below fp16's smallest number is 2^-31 of the group's largest scale.  A
+// query row is scaled by the power of two that puts its largest value into
+// [2^14, 2^15): bf16 and fp16 rows are then exact to 2^-39 of that value, fp32
+// rows are two fp16 numbers (22 bits).  The powers come back in the softmax, whose
+// scores, maxima, sums and probabilities are fp32:
+//
+//   s = scale · log2 e · (q'·k') · 2^(powers of q and k)
+//   u = s + vref                    vref: the power taken out of v
+//   p = 2^(u - M + 6),  M >= max u - 8    (so p <= 2^14 in fp16)
+//   O = Σ p v',  l = Σ p · 2^-vref,  y = O / l
+//
+// M is kept while no u passes it by more than 8, so O is rarely rescaled.
+// Probabilities enter the second product in fp16: one rounding to 2^-12 where
+// y is 16 bits wide, two terms (2^-22) where it is fp32.
+#pragma once
+
+#include <cstdint>
+#include <cuda_fp16.h>
+
+#include "mx_cache.cuh"
+
+namespace q4mm {
+
+constexpr float kLog2e = 1.44269504f;
+constexpr float kPShift = 6.f;      // log2 of p at u = M
+constexpr float kPSlack = 8.f;      // u may pass M by this
+constexpr int kVrefMin = -100;      // lowest power taken out of v (2^-vref stays a normal float)
+constexpr int kNever = 0x7FFFFFFF;  // position of a NaN that there is not
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 2^e, e cut to a normal float's.
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+
+// Two E4M3 codes, or two E2M1 codes, as fp16.
+__device__ __forceinline__ uint32_t half_e4m3x2(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t half_e4m3x2_high(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+template <int k>
+__device__ __forceinline__ uint32_t half_e2m1x2(uint32_t bytes) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b%2;\n\t}"
+        : "=r"(r)
+        : "r"(bytes), "n"(k));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two floats to fp16, the first in the low half.
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The largest scale byte of a word's first `blocks`, NaN bytes left out, and
+// whether there is one of those.
+struct ScaleWord {
+    int b[4];
+    int top;
+    bool nan;
+    __device__ __forceinline__ ScaleWord(uint32_t w, int blocks) {
+        top = 0, nan = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b[i] = i < blocks ? (int)(w >> (8 * i) & 0xFF) : 0;
+            nan |= b[i] == 255;
+            top = max(top, b[i] == 255 ? 0 : b[i]);
+        }
+    }
+};
+
+// A tile of `R` rows of one sequence and kv head.  Row r is token r / group of
+// the sequence's new tokens, query head r % group of the kv head.
+struct RowTile {
+    int seq, first, rows;   // first row, rows (0: no such tile)
+    int start, fresh, len;  // the sequence's first row of q, its new tokens, its cached tokens
+};
+
+// Tiles are numbered so that sequence i has those from starts[i]·group / R + i
+// on: no fewer than its rows need, found by bisection instead of a prefix sum.
+__device__ __forceinline__ RowTile row_tile(const MxBatchView &b, long long tile, int group, int R, int tokens) {
+    auto first_of = [&](int i) { return (long long)b.starts[i] * group / R + i; };
+    RowTile t{};
+    const int i = warp_count_le(first_of, b.seqs, tile) - 1;
+    if (i < 0) return t;
+    const int s0 = b.starts[i], s1 = b.starts[i + 1];
+    if (s0 < 0 || s1 > tokens || s1 <= s0) return t;
+    const long long first = (tile - first_of(i)) * R, all = (long long)(s1 - s0) * group;
+    if (first < 0 || first >= all) return t;
+    t.seq = i, t.first = (int)first, t.rows = (int)min((long long)R, all - first);
+    t.start = s0, t.fresh = s1 - s0, t.len = max(b.lengths[i], 0);
+    return t;
+}
+
+// Keys that row r sees: positions below this (at most the table's).
+__device__ __forceinline__ int keys_of(const RowTile &t, int r, int group, bool causal) {
+    const int seen = causal ? t.len - t.fresh + r / group + 1 : t.len;
+    return max(seen, 0);
+}
+
+}  // namespace q4mm

@@ -1,0 +1,21 @@
+// How attention is split over the GPU: host code, compiled by the kernels'
+// launchers and by the tests.
+#pragma once
+
+namespace q4mm {
+
+constexpr int kFewWarps = 8;      // warps of a CTA for few rows
+constexpr int kFewGroup = 16;     // tokens a warp takes at once
+constexpr int kFewMaxSplit = 16;  // CTAs that share a row tile's keys (a cluster)
+
+// CTAs of a cluster over the keys of one row tile: a power of two that gives
+// the SMs two CTAs each, unless a warp would have less than two groups.
+inline int few_split(long long tiles, int kv_heads, int keys, int num_sms) {
+    const long long ctas = tiles * kv_heads;
+    const int groups = (keys + kFewGroup - 1) / kFewGroup;
+    int s = 1;
+    while (s < kFewMaxSplit && ctas * s < 2LL * num_sms && groups >= 4 * s * kFewWarps) s *= 2;
+    return s;
+}
+
+}  // namespace q4mm

@@ -203,6 +203,79 @@ int check_mx_alias(const Span *outs, int nouts, const Span *ins, int nins) {
     return Q4MM_OK;
 }
 
+// Checks shared by the entry points of attention.
+
+// The bytes that [tokens][heads][D] values with these strides reach over
+// (strides are checked first).
+Span head_span(const void *p, long long token, long long head, int tokens, int heads, int D, size_t size,
+               const char *name) {
+    return Span{p, ((size_t)(tokens - 1) * (size_t)token + (size_t)(heads - 1) * (size_t)head + (size_t)D) * size, name};
+}
+
+// A token's heads, or a head's tokens, may lie inside each other's gaps, but
+// not on each other (`writes`); strides are not negative.
+int check_head_strides(long long token, long long head, int tokens, int heads, int D, bool writes, const char *name) {
+    if ((tokens > 1 && token < 0) || (heads > 1 && head < 0))
+        return fail(Q4MM_ERR_DIM, "the strides of %s (%lld, %lld) must not be negative", name, token, head);
+    if ((tokens > 1 && token > (1LL << 46) / (tokens - 1)) || (heads > 1 && head > (1LL << 46) / (heads - 1)))
+        return fail(Q4MM_ERR_DIM, "%s does not fit in memory with strides %lld and %lld", name, token, head);
+    if (writes) {
+        const bool tokens_outside =
+            (heads == 1 || head >= D) && (tokens == 1 || token >= (heads - 1) * (heads > 1 ? head : 0) + D);
+        const bool heads_outside =
+            (tokens == 1 || token >= D) && (heads == 1 || head >= (tokens - 1) * (tokens > 1 ? token : 0) + D);
+        if (!tokens_outside && !heads_outside)
+            return fail(Q4MM_ERR_ALIAS, "the heads of %s overlap with strides %lld and %lld", name, token, head);
+    }
+    return Q4MM_OK;
+}
+
+int check_rope(const double *frequencies, int rotated, float magnitude, int D) {
+    if (rotated < 0 || rotated > D || rotated % 2)
+        return fail(Q4MM_ERR_DIM, "rotated (%d) must be even and between 0 and headDim (%d)", rotated, D);
+    if (!(magnitude - magnitude == 0.f)) return fail(Q4MM_ERR_DIM, "magnitude must be finite");
+    if (rotated == 0) return Q4MM_OK;
+    return check_mx_ptr(Span{frequencies, (size_t)rotated / 2 * 8, "frequencies"}, 8);
+}
+
+struct CacheCall {
+    q4mm::MxCacheView cache;
+    q4mm::MxBatchView batch;
+    Span spans[7];  // codes and scales of k and v, then starts, lengths, table
+};
+
+// Sizes and pointers of a cache and a batch.
+int check_cache(CacheCall &c, int tokens) {
+    const q4mm::MxCacheView &m = c.cache;
+    const q4mm::MxBatchView &b = c.batch;
+    if (m.D != 32 && m.D != 64 && m.D != 96 && m.D != 128)
+        return fail(Q4MM_ERR_DIM, "headDim (%d) must be 32, 64, 96 or 128", m.D);
+    if (m.bits != 4 && m.bits != 8) return fail(Q4MM_ERR_DIM, "bits (%d) must be 4 or 8", m.bits);
+    if (m.pages <= 0 || m.heads <= 0 || m.heads > Q4MM_MX_MAX_HEADS)
+        return fail(Q4MM_ERR_DIM, "pages (%d) and kvHeads (%d, at most %d) must be positive", m.pages, m.heads,
+                    Q4MM_MX_MAX_HEADS);
+    if (m.page <= 0 || m.page % 16 || m.page > (1 << 24))
+        return fail(Q4MM_ERR_DIM, "pageTokens (%d) must be a positive multiple of 16, at most 2^24", m.page);
+    if (b.seqs < 0 || b.seqs > (1 << 24) || b.width < 0)
+        return fail(Q4MM_ERR_DIM, "sequences (%d, at most 2^24) and tableWidth (%d) must not be negative", b.seqs,
+                    b.width);
+    if (tokens < 0 || tokens > Q4MM_MX_MAX_ROWS)
+        return fail(Q4MM_ERR_DIM, "tokens (%d) must be between 0 and %d", tokens, Q4MM_MX_MAX_ROWS);
+    const size_t slots = (size_t)m.pages * m.heads * m.page;
+    const size_t codes = slots * (m.D * m.bits / 8);
+    c.spans[0] = Span{m.k_codes, codes, "k_codes"}, c.spans[1] = Span{m.k_scales, slots * 4, "k_scales"};
+    c.spans[2] = Span{m.v_codes, codes, "v_codes"}, c.spans[3] = Span{m.v_scales, slots * 4, "v_scales"};
+    c.spans[4] = Span{b.starts, ((size_t)b.seqs + 1) * 4, "starts"}, c.spans[5] = Span{b.lengths, (size_t)b.seqs * 4, "lengths"};
+    c.spans[6] = Span{b.table, (size_t)b.seqs * b.width * 4, "table"};
+    int rc;
+    for (int i = 0; i < 7; ++i) {
+        if (b.seqs == 0 && i >= 4) break;
+        if (b.width == 0 && i == 6) break;
+        if ((rc = check_mx_ptr(c.spans[i], i == 0 || i == 2 ? 16 : 4))) return rc;
+    }
+    return Q4MM_OK;
+}
+
 int mx_quantize_call(const void *x, long long x_stride, const void *up, long long up_stride, bool swiglu, int dtype,
                      void *codes, void *scales, int K, int rows, int bits, q4mm_stream_t stream) {
     int rc = check_mx_dims(K, rows, bits, "rows");
@@ -545,6 +618,142 @@ int mx_matmul(const void *x_codes, const void *x_scales, int x_bits, const void 
     return Q4MM_OK;
 }
 
+int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride, int dtype, const void *positions,
+                int positions_64, const double *frequencies, int rotated, int interleaved, float magnitude, void *out,
+                long long out_token_stride, long long out_head_stride, int tokens, int heads, int headDim,
+                q4mm_stream_t stream) {
+    int rc = check_mx_dtype(dtype, "input");
+    if (rc) return rc;
+    if (headDim <= 0 || headDim > Q4MM_ROPE_MAX_HEAD)
+        return fail(Q4MM_ERR_DIM, "headDim (%d) must be between 1 and %d", headDim, Q4MM_ROPE_MAX_HEAD);
+    if (heads <= 0 || heads > Q4MM_MX_MAX_HEADS)
+        return fail(Q4MM_ERR_DIM, "heads (%d) must be between 1 and %d", heads, Q4MM_MX_MAX_HEADS);
+    if (tokens < 0 || tokens > Q4MM_MX_MAX_ROWS)
+        return fail(Q4MM_ERR_DIM, "tokens (%d) must be between 0 and %d", tokens, Q4MM_MX_MAX_ROWS);
+    if (tokens == 0) return Q4MM_OK;
+    if ((rc = check_rope(frequencies, rotated, magnitude, headDim)) ||
+        (rc = check_head_strides(x_token_stride, x_head_stride, tokens, heads, headDim, false, "x")) ||
+        (rc = check_head_strides(out_token_stride, out_head_stride, tokens, heads, headDim, true, "out")))
+        return rc;
+    const size_t size = mx_size(dtype), psize = positions_64 ? 8 : 4;
+    const Span ins[3] = {head_span(x, x_token_stride, x_head_stride, tokens, heads, headDim, size, "x"),
+                         Span{positions, (size_t)tokens * psize, "positions"},
+                         Span{frequencies, (size_t)rotated / 2 * 8, "frequencies"}};
+    const Span o = head_span(out, out_token_stride, out_head_stride, tokens, heads, headDim, size, "out");
+    if ((rc = check_mx_ptr(ins[0], size)) || (rc = check_mx_ptr(ins[1], psize)) || (rc = check_mx_ptr(o, size)))
+        return rc;
+    const bool same = x == out && (tokens == 1 || x_token_stride == out_token_stride) &&
+                      (heads == 1 || x_head_stride == out_head_stride);
+    if ((rc = check_mx_alias(&o, 1, ins + (same ? 1 : 0), (same ? 1 : 2) + (rotated ? 1 : 0)))) return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::RopeArgs a{x, x_token_stride, x_head_stride, positions, positions_64 != 0,
+                           q4mm::RopeView{frequencies, rotated, interleaved != 0, magnitude}, out, out_token_stride,
+                           out_head_stride, tokens, heads, headDim};
+    const cudaError_t e = q4mm::launch_rope_rotate(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, "rope_rotate launch");
+    return Q4MM_OK;
+}
+
+int mx_cache_write(const void *k, long long k_token_stride, long long k_head_stride, const void *v,
+                   long long v_token_stride, long long v_head_stride, int dtype, const double *frequencies,
+                   int rotated, int interleaved, float magnitude, void *k_codes, void *k_scales, void *v_codes,
+                   void *v_scales, int pages, int kvHeads, int pageTokens, int headDim, int bits, const int *starts,
+                   const int *lengths, const int *table, int sequences, int tableWidth, int tokens,
+                   q4mm_stream_t stream) {
+    CacheCall call{q4mm::MxCacheView{static_cast<uint8_t *>(k_codes), static_cast<uint8_t *>(k_scales),
+                                     static_cast<uint8_t *>(v_codes), static_cast<uint8_t *>(v_scales), pages, kvHeads,
+                                     pageTokens, headDim, bits},
+                   q4mm::MxBatchView{starts, lengths, table, sequences, tableWidth}, {}};
+    int rc = check_mx_dtype(dtype, "input");
+    if (rc || (rc = check_cache(call, tokens)) || (rc = check_rope(frequencies, rotated, magnitude, headDim))) return rc;
+    if (tokens == 0 || sequences == 0) return Q4MM_OK;
+    if ((rc = check_head_strides(k_token_stride, k_head_stride, tokens, kvHeads, headDim, false, "k")) ||
+        (rc = check_head_strides(v_token_stride, v_head_stride, tokens, kvHeads, headDim, false, "v")))
+        return rc;
+    const size_t size = mx_size(dtype);
+    const Span ins[6] = {head_span(k, k_token_stride, k_head_stride, tokens, kvHeads, headDim, size, "k"),
+                         head_span(v, v_token_stride, v_head_stride, tokens, kvHeads, headDim, size, "v"),
+                         Span{frequencies, (size_t)rotated / 2 * 8, "frequencies"}, call.spans[4], call.spans[5],
+                         call.spans[6]};
+    if ((rc = check_mx_ptr(ins[0], size)) || (rc = check_mx_ptr(ins[1], size)) ||
+        (rc = check_mx_alias(call.spans, 4, ins, 6)))
+        return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxCacheIoArgs a{call.cache, call.batch, k, v, k_token_stride, k_head_stride, v_token_stride,
+                                v_head_stride, tokens, ctx.status};
+    const q4mm::RopeView rope{frequencies, rotated, interleaved != 0, magnitude};
+    const cudaError_t e = q4mm::launch_mx_cache_write(ctx, static_cast<q4mm::MxType>(dtype), a, rope);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_cache_write launch");
+    return Q4MM_OK;
+}
+
+int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales, int pages,
+                  int kvHeads, int pageTokens, int headDim, int bits, const int *starts, const int *lengths,
+                  const int *table, int sequences, int tableWidth, void *k, long long k_token_stride,
+                  long long k_head_stride, void *v, long long v_token_stride, long long v_head_stride, int dtype,
+                  int tokens, q4mm_stream_t stream) {
+    auto bytes = [](const void *p) { return const_cast<uint8_t *>(static_cast<const uint8_t *>(p)); };
+    CacheCall call{q4mm::MxCacheView{bytes(k_codes), bytes(k_scales), bytes(v_codes), bytes(v_scales), pages, kvHeads,
+                                     pageTokens, headDim, bits},
+                   q4mm::MxBatchView{starts, lengths, table, sequences, tableWidth}, {}};
+    int rc = check_mx_dtype(dtype, "output");
+    if (rc || (rc = check_cache(call, tokens))) return rc;
+    if (tokens == 0 || sequences == 0) return Q4MM_OK;
+    if ((rc = check_head_strides(k_token_stride, k_head_stride, tokens, kvHeads, headDim, true, "k")) ||
+        (rc = check_head_strides(v_token_stride, v_head_stride, tokens, kvHeads, headDim, true, "v")))
+        return rc;
+    const size_t size = mx_size(dtype);
+    const Span outs[2] = {head_span(k, k_token_stride, k_head_stride, tokens, kvHeads, headDim, size, "k"),
+                          head_span(v, v_token_stride, v_head_stride, tokens, kvHeads, headDim, size, "v")};
+    if ((rc = check_mx_ptr(outs[0], size)) || (rc = check_mx_ptr(outs[1], size)) ||
+        (rc = check_mx_alias(outs, 2, call.spans, 7)))
+        return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxCacheIoArgs a{call.cache, call.batch, k, v, k_token_stride, k_head_stride, v_token_stride,
+                                v_head_stride, tokens, ctx.status};
+    const cudaError_t e = q4mm::launch_mx_cache_read(ctx, static_cast<q4mm::MxType>(dtype), a);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_cache_read launch");
+    return Q4MM_OK;
+}
+
+int mx_attention(const void *q, long long q_token_stride, long long q_head_stride, int dtype, const void *k_codes,
+                 const void *k_scales, const void *v_codes, const void *v_scales, int pages, int kvHeads,
+                 int pageTokens, int headDim, int bits, const int *starts, const int *lengths, const int *table,
+                 int sequences, int tableWidth, float scale, int causal, void *y, long long y_token_stride,
+                 long long y_head_stride, int tokens, int heads, q4mm_stream_t stream) {
+    auto bytes = [](const void *p) { return const_cast<uint8_t *>(static_cast<const uint8_t *>(p)); };
+    CacheCall call{q4mm::MxCacheView{bytes(k_codes), bytes(k_scales), bytes(v_codes), bytes(v_scales), pages, kvHeads,
+                                     pageTokens, headDim, bits},
+                   q4mm::MxBatchView{starts, lengths, table, sequences, tableWidth}, {}};
+    int rc = check_mx_dtype(dtype, "input");
+    if (rc || (rc = check_cache(call, tokens))) return rc;
+    if (heads <= 0 || heads > Q4MM_MX_MAX_HEADS || heads % kvHeads)
+        return fail(Q4MM_ERR_DIM, "heads (%d) must be a positive multiple of kvHeads (%d), at most %d", heads, kvHeads,
+                    Q4MM_MX_MAX_HEADS);
+    if (!(scale >= 0.f && scale - scale == 0.f)) return fail(Q4MM_ERR_DIM, "scale (%g) must be finite and not negative", (double)scale);
+    if (tokens == 0 || sequences == 0) return Q4MM_OK;
+    if ((rc = check_head_strides(q_token_stride, q_head_stride, tokens, heads, headDim, false, "q")) ||
+        (rc = check_head_strides(y_token_stride, y_head_stride, tokens, heads, headDim, true, "y")))
+        return rc;
+    const size_t size = mx_size(dtype);
+    const Span qs = head_span(q, q_token_stride, q_head_stride, tokens, heads, headDim, size, "q");
+    const Span ys = head_span(y, y_token_stride, y_head_stride, tokens, heads, headDim, size, "y");
+    if ((rc = check_mx_ptr(qs, size)) || (rc = check_mx_ptr(ys, size)) || (rc = check_mx_alias(&ys, 1, &qs, 1)) ||
+        (rc = check_mx_alias(&ys, 1, call.spans, 7)))
+        return rc;
+    q4mm::LaunchCtx ctx;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::MxAttentionArgs a{call.cache, call.batch, q, q_token_stride, q_head_stride, y, y_token_stride,
+                                  y_head_stride, scale, causal != 0, tokens, heads, static_cast<q4mm::MxType>(dtype),
+                                  ctx.status};
+    const cudaError_t e = q4mm::launch_mx_attention(ctx, a);
+    if (e != cudaSuccess) return fail_cuda(e, "mx_attention launch");
+    return Q4MM_OK;
+}
+
 const char *q4mm_last_error(void) { return g_err; }
 
 int q4mm_device_status(q4mm_stream_t stream, int clear) {
@@ -562,7 +771,9 @@ int q4mm_device_status(q4mm_stream_t stream, int clear) {
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
         if (e != cudaSuccess) return fail_cuda(e, "clearing the device status word");
     }
-    if (host) return fail(Q4MM_ERR_TIMEOUT, "a bounded in-kernel wait ran out (status word %d)", host);
+    if (host & q4mm::kStatusTimeout)
+        return fail(Q4MM_ERR_TIMEOUT, "a bounded in-kernel wait ran out (status word %d)", host);
+    if (host) return fail(Q4MM_ERR_INDEX, "a call met a page number or a position outside its cache or table");
     return Q4MM_OK;
 }
 
@@ -580,6 +791,6 @@ int q4mm_test_fail_next_wait(int stage, long long limit_cycles) {
     return Q4MM_OK;
 }
 
-int q4mm_version(void) { return 300; }
+int q4mm_version(void) { return 400; }
 
 }  // extern "C"

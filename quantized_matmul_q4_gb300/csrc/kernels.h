@@ -142,6 +142,68 @@ struct MxMatmulArgs {
 };
 cudaError_t launch_mx_matmul(const LaunchCtx &c, MxType type, const MxMatmulArgs &a);
 
+// Bits of the device status word.
+constexpr int kStatusTimeout = 1;  // a bounded wait ran out
+constexpr int kStatusIndex = 2;    // a page number or position outside the cache or its table
+
+// The paged MX cache and a batch of sequences in it; layouts in mx_cache.cuh.
+struct MxCacheView {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int pages, heads, page, D, bits;
+};
+struct MxBatchView {
+    const int *starts, *lengths, *table;
+    int seqs, width;
+};
+
+// Rotation of a head's first `rotated` values (0: none).
+struct RopeView {
+    const double *frequencies;  // rotated / 2, radians per position
+    int rotated;
+    bool interleaved;  // pairs (2i, 2i + 1), else (i, i + rotated / 2)
+    float magnitude;
+};
+
+struct RopeArgs {
+    const void *x;
+    long long x_token, x_head;
+    const void *positions;
+    bool positions_64;
+    RopeView rope;
+    void *out;  // may be x
+    long long out_token, out_head;
+    int tokens, heads, D;
+};
+cudaError_t launch_rope_rotate(const LaunchCtx &c, MxType type, const RopeArgs &a);
+
+// k and v of the batch's rows, written to the cache or read from it.
+struct MxCacheIoArgs {
+    MxCacheView cache;
+    MxBatchView batch;
+    const void *k, *v;
+    long long k_token, k_head, v_token, v_head;
+    int tokens;
+    int *status;
+};
+cudaError_t launch_mx_cache_write(const LaunchCtx &c, MxType type, const MxCacheIoArgs &a, const RopeView &rope);
+cudaError_t launch_mx_cache_read(const LaunchCtx &c, MxType type, const MxCacheIoArgs &a);
+
+// Attention of the batch's rows over the cache.
+struct MxAttentionArgs {
+    MxCacheView cache;
+    MxBatchView batch;
+    const void *q;
+    long long q_token, q_head;
+    void *y;
+    long long y_token, y_head;
+    float scale;
+    bool causal;
+    int tokens, heads;
+    MxType type;
+    int *status;
+};
+cudaError_t launch_mx_attention(const LaunchCtx &c, const MxAttentionArgs &a);
+
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device; the attribute call is made only when the limit grows, so a
 // warmed-up launch (for instance one being captured into a CUDA graph) issues

@@ -74,6 +74,41 @@ __device__ __forceinline__ uint32_t mx_e4m3x4(float v0, float v1, float v2, floa
     return r;
 }
 
+// Float bits of the largest magnitude of eight values, and of the 32 of a
+// block over its four lanes; NaN where one of them is.
+__device__ __forceinline__ uint32_t mx_block_amax(const float (&v)[8]) {
+    const float a = mx_max3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2]));
+    const float b = mx_max3(fabsf(v[3]), fabsf(v[4]), fabsf(v[5]));
+    float m = mx_max3(a, b, fabsf(v[6]));
+    m = mx_max3(m, fabsf(v[7]), __shfl_xor_sync(0xFFFFFFFFu, mx_max3(m, fabsf(v[7]), m), 1));
+    return __float_as_uint(mx_max3(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2), m));
+}
+
+// Quantises the block of `amax` (float bits) that this lane's eight values
+// belong to, stores their codes (nothing where col >= Kp) and returns the
+// block's scale byte.
+__device__ __forceinline__ uint32_t mx_quantize8(const float (&v)[8], uint32_t amax, int bits, uint8_t *codes_row,
+                                                 int col, int Kp) {
+    const uint32_t b = mx_scale_byte(amax, bits == 4 ? 2 : 8);
+    const float2 inv = make_float2(mx_inverse(b), mx_inverse(b));
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), inv);
+        s[2 * i] = f.x, s[2 * i + 1] = f.y;
+    }
+    if (col < Kp) {
+        // The codes under a NaN scale are zeros.
+        if (bits == 4) {
+            *reinterpret_cast<uint32_t *>(codes_row + (col >> 1)) = b == 255 ? 0u : mx_e2m1x8(s);
+        } else {
+            const uint32_t lo = mx_e4m3x4(s[0], s[1], s[2], s[3]), hi = mx_e4m3x4(s[4], s[5], s[6], s[7]);
+            *reinterpret_cast<uint2 *>(codes_row + col) = make_uint2(b == 255 ? 0u : lo, b == 255 ? 0u : hi);
+        }
+    }
+    return b;
+}
+
 // Two codes back to values (exact in fp16, hence in fp32): byte k of four
 // E2M1 pairs, or half k of two E4M3 pairs.
 template <int k>

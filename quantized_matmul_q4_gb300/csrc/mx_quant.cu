@@ -207,20 +207,11 @@ __device__ __forceinline__ void store8(T *row, int col, int K, const float (&v)[
     }
 }
 
-// Float bits of the largest magnitude of eight values, and of the 32 of a
-// block over its four lanes; NaN where one of them is.
-__device__ __forceinline__ uint32_t block_amax(const float (&v)[8]) {
-    const float a = mx_max3(fabsf(v[0]), fabsf(v[1]), fabsf(v[2]));
-    const float b = mx_max3(fabsf(v[3]), fabsf(v[4]), fabsf(v[5]));
-    float m = mx_max3(a, b, fabsf(v[6]));
-    m = mx_max3(m, fabsf(v[7]), __shfl_xor_sync(kFull, mx_max3(m, fabsf(v[7]), m), 1));
-    return __float_as_uint(mx_max3(m, __shfl_xor_sync(kFull, m, 2), m));
-}
-
+// The same from the values as they lie in memory.
 template <class T>
 __device__ __forceinline__ uint32_t block_amax(const Raw8<T> &r, const float (&v)[8]) {
     if constexpr (sizeof(T) == 4) {
-        return block_amax(v);
+        return mx_block_amax(v);
     } else {
         // Two at a time: 16-bit magnitudes as packed numbers of their type.
         using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
@@ -234,32 +225,7 @@ __device__ __forceinline__ uint32_t block_amax(const Raw8<T> &r, const float (&v
         return __float_as_uint(mx_float(__hmax_nan(m.x, m.y)));
     }
 }
-__device__ __forceinline__ uint32_t block_amax(const Raw8<float> &, const float (&v)[8]) { return block_amax(v); }
-
-// Quantises the block of `amax` (float bits) that this lane's eight values
-// belong to, stores their codes (nothing where col >= Kp) and returns the
-// block's scale byte.
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t amax, int bits, uint8_t *codes_row, int col,
-                                              int Kp) {
-    const uint32_t b = mx_scale_byte(amax, bits == 4 ? 2 : 8);
-    const float2 inv = make_float2(mx_inverse(b), mx_inverse(b));
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), inv);
-        s[2 * i] = f.x, s[2 * i + 1] = f.y;
-    }
-    if (col < Kp) {
-        // The codes under a NaN scale are zeros.
-        if (bits == 4) {
-            *reinterpret_cast<uint32_t *>(codes_row + (col >> 1)) = b == 255 ? 0u : mx_e2m1x8(s);
-        } else {
-            const uint32_t lo = mx_e4m3x4(s[0], s[1], s[2], s[3]), hi = mx_e4m3x4(s[4], s[5], s[6], s[7]);
-            *reinterpret_cast<uint2 *>(codes_row + col) = make_uint2(b == 255 ? 0u : lo, b == 255 ? 0u : hi);
-        }
-    }
-    return b;
-}
+__device__ __forceinline__ uint32_t block_amax(const Raw8<float> &, const float (&v)[8]) { return mx_block_amax(v); }
 
 // The exchange of scale bytes.  Four lanes hold a block; the four such groups
 // g = lane / 4 % 4 of a half warp hold, in byte i of `p`, the scale of their
@@ -410,7 +376,7 @@ __global__ void __launch_bounds__(256, kSwiGLU ? (kVec ? 4 : 3) : (kVec ? 1 : 4)
             to_float(ru, u);
             if constexpr (!decltype(far)::value) gates.see(rx, v);
             swiglu8<decltype(far)::value>(v, u);
-            return quantize8(v, block_amax(v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+            return mx_quantize8(v, mx_block_amax(v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
                    << (8 * i);
         };
 #pragma unroll
@@ -440,7 +406,7 @@ __global__ void __launch_bounds__(256, kSwiGLU ? (kVec ? 4 : 3) : (kVec ? 1 : 4)
             float v[8];
             fx[i].take(px + 32 * i * x_stride, col, width(i), wide, rx);
             to_float(rx, v);
-            p |= quantize8(v, block_amax(rx, v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
+            p |= mx_quantize8(v, block_amax(rx, v), bits, pc + 32 * i * code_row, col, row0 + 32 * i < rows ? Kp : 0)
                  << (8 * i);
         }
     }
@@ -589,7 +555,7 @@ __global__ void __launch_bounds__(1024) mx_rmsnorm_kernel(const RmsArgs a) {
             for (int j = 0; j < 8; ++j)
                 if (col + j >= K) u[j] = 0.f;
         }
-        return quantize8(u, block_amax(u), a.bits, codes_row, col, Kp);
+        return mx_quantize8(u, mx_block_amax(u), a.bits, codes_row, col, Kp);
     };
     const ByteExchange exchange(lane);
     const int g4 = (lane >> 2) & 3;  // which group's word this lane writes

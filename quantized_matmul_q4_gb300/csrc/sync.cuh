@@ -7,7 +7,7 @@ namespace q4mm {
 
 // Set when a bounded wait gives up; read by q4mm_device_status().
 __device__ __forceinline__ void flag_timeout(int *status) {
-    if (status) atomicOr(status, 1);
+    if (status) atomicOr(status, 1);  // kStatusTimeout
 }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
