@@ -23,6 +23,7 @@
 #include <cstdint>
 #include <cuda_fp16.h>
 
+#include "mx.cuh"
 #include "mx_cache.cuh"
 
 namespace q4mm {
@@ -117,6 +118,28 @@ __device__ __forceinline__ RowTile row_tile(const MxBatchView &b, long long tile
 __device__ __forceinline__ int keys_of(const RowTile &t, int r, int group, bool causal) {
     const int seen = causal ? t.len - t.fresh + r / group + 1 : t.len;
     return max(seen, 0);
+}
+
+// Four neighbouring outputs.
+__device__ __forceinline__ void store4(void *y, MxType type, long long at, bool vec, float4 v) {
+    if (type == MxType::kF32) {
+        float *p = static_cast<float *>(y) + at;
+        if (vec)
+            *reinterpret_cast<float4 *>(p) = v;
+        else
+            p[0] = v.x, p[1] = v.y, p[2] = v.z, p[3] = v.w;
+        return;
+    }
+    uint32_t lo, hi;
+    if (type == MxType::kF16)
+        lo = mx_pack2<__half>(v.x, v.y), hi = mx_pack2<__half>(v.z, v.w);
+    else
+        lo = mx_pack2<__nv_bfloat16>(v.x, v.y), hi = mx_pack2<__nv_bfloat16>(v.z, v.w);
+    uint16_t *p = static_cast<uint16_t *>(y) + at;
+    if (vec)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(lo, hi);
+    else
+        p[0] = (uint16_t)lo, p[1] = (uint16_t)(lo >> 16), p[2] = (uint16_t)hi, p[3] = (uint16_t)(hi >> 16);
 }
 
 }  // namespace q4mm

@@ -491,7 +491,7 @@ cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a) {
 
 }  // namespace
 
-cudaError_t launch_mx_attention(const LaunchCtx &c, const MxAttentionArgs &a) {
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a) {
     const bool narrow = a.cache.D <= 64;
     if (a.cache.bits == 4) return narrow ? launch_rows<4, 64>(c, a) : launch_rows<4, 128>(c, a);
     return narrow ? launch_rows<8, 64>(c, a) : launch_rows<8, 128>(c, a);

@@ -18,4 +18,21 @@ inline int few_split(long long tiles, int kv_heads, int keys, int num_sms) {
     return s;
 }
 
+constexpr int kManyKeys = 128;   // keys of a tile on tcgen05
+constexpr int kManyMaxSplit = 8;  // CTAs that share a row tile's keys there
+
+// Rows of a sequence and kv head, on average, from which tiles of 128 on the
+// tensor cores are faster.
+inline bool many_rows(long long tokens, int group, int seqs) { return tokens * group > 32LL * (seqs > 0 ? seqs : 1); }
+
+// CTAs of a cluster over the keys: while one CTA per SM is not passed, and
+// each has two tiles of keys.
+inline int many_split(long long rows, int tile_rows, int seqs, int kv_heads, int keys, int num_sms) {
+    const long long whole = rows / tile_rows, tiles = whole > seqs ? whole : seqs;
+    const int key_tiles = (keys + kManyKeys - 1) / kManyKeys;
+    int s = 1;
+    while (s < kManyMaxSplit && tiles * kv_heads * s * 2 <= num_sms && key_tiles >= 4 * s) s *= 2;
+    return s;
+}
+
 }  // namespace q4mm

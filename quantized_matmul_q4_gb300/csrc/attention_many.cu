@@ -1,0 +1,759 @@
+// Attention over a paged MX cache for many rows a key/value head (sm_103a):
+// prompts and chunks of them, tiles of 128 rows on tcgen05.
+//
+//   S[row][key]   = Q Kᵀ     128 x 128, fp16 in, fp32 in tensor memory
+//   P             = 2^(...)  into tensor memory, over S
+//   O[row][value] += P V     fp32 in tensor memory
+//
+// What bounds it is the tensor pipe (two products of 128 x 128 x D a tile and
+// 128 keys) together with the issue slots of the softmax: 256 rows a CTA take
+// 2048 cycles of the pipe per 128 keys, some 3 instructions a score in the
+// softmax 800 issue cycles of each of the SM's four schedulers, the exponentials
+// 1024 cycles of the special functions, and the codes of 256 rows of K and V
+// 400.  So two tiles of 128 rows share every dequantised key and value, and
+// while the softmax of one is computed the pipe works on the other.
+//
+// Warps of a CTA:
+//   softmax  four a tile, a row a thread (a warp reads only its own quarter of
+//            the lanes of tensor memory): maximum, exponentials, P, and,
+//            where the maximum has grown by more than 8, O rescaled.
+//   dequant  four, 32 neighbouring tokens of a tile each: codes from global
+//            memory through registers (the next tile's on their way) to fp16
+//            in shared memory, rows of 128 bytes in the 128-byte swizzle.  V
+//            lies like K, token by token: it is the product's B operand with
+//            the values (N) contiguous.  The power of two taken out (see
+//            attention.cuh) is one for those 32 tokens, and goes to the
+//            softmax beside them.
+//   issue    one warp, one elected lane: S of both tiles, then in turn P V of
+//            one tile and S of its next keys.
+// S of the next keys is written over P by an instruction issued after the one
+// that reads P: instructions of one thread run in order.  A tile's softmax
+// starts when its S is complete, hence also the P V before it, so it may
+// rescale O; P V of these keys waits for its P.
+//
+// fp32 queries take two fp16 terms each for Q and P, and one tile of rows.
+//
+// Keys may be split over a cluster; the parts' sums are joined in rank order.
+#include <cstdint>
+
+#include "attention.cuh"
+#include "attention_geometry.h"
+#include "cluster.cuh"
+#include "common.cuh"
+#include "kernels.h"
+#include "mx.cuh"
+#include "sync.cuh"
+
+namespace q4mm {
+
+namespace {
+
+// kDP: the head's values rounded up to 64 or 128; kTiles x kNP: tiles of 128
+// rows and fp16 terms of a query value, 2 x 1 or 1 x 2.
+template <int kDP, int kTiles, int kNP>
+struct ManyLayout {
+    static constexpr int kSoftmaxWarps = 4 * kTiles, kDequantWarps = 4;
+    static constexpr int kWarps = kSoftmaxWarps + kDequantWarps + 1;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr uint32_t kSlab = kManyKeys * kDP * 2;  // 128 rows of Q, K or V
+    static constexpr int kSlots = kDP == 64 ? 8 : 4;        // of the ring of K and V
+    static constexpr int kMeta = kSlots;                    // tiles whose powers are kept (> kSlots / 2)
+    static constexpr uint32_t off_ring = 2 * kSlab;
+    static constexpr uint32_t off_end = off_ring + kSlots * kSlab;
+    // The sums, where the operands were.
+    static constexpr int kPitch = kDP + 4;
+    static constexpr uint32_t total = off_end + 1024;  // the base is rounded up to 1024 bytes
+    static_assert(2 * kSlab == kTiles * kNP * kSlab && kTiles * 128 * kPitch * 4 <= off_end, "");
+    static_assert(kSmShared - total - kCtaSharedExtra < kHalfTmemShared, "takes all of tensor memory");
+    // Tensor memory: S (and P over it), second terms of P, O.
+    static constexpr uint32_t col_s(int t) { return 128 * t; }
+    static constexpr uint32_t kColLow = 128;  // kNP == 2, kTiles == 1
+    static constexpr uint32_t col_o(int t) { return 256 + kDP * t; }
+};
+
+struct ManyShared {
+    uint64_t ring_full[8], ring_free[8], meta_full[8], s_full[2], p_full[2], q_full, done, dequant_done;
+    int kref[8][4], vref[8][4];  // of a tile's 32-token groups
+    float m[256], l[256];
+    int nan_from[4];
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// Waits for the loads from tensor memory; r, the values of one, are not used before it.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// 32 columns of this thread's lane; the values are there after tc_wait_ld.
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory operands in the 128-byte swizzle: 8 rows of 128 bytes are
+// 1024.  K-major (Q, K: rows are M or N, 64 values of the head a row): groups
+// of 8 rows 1024 bytes apart.  N-major (V: rows are keys, 64 of the N values a
+// row): groups of 8 keys 1024 bytes apart, the next 64 values `next` bytes on.
+__device__ __forceinline__ uint64_t k_major_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+__device__ __forceinline__ uint64_t n_major_desc(uint32_t saddr, uint32_t next) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
+           (uint64_t)1u << 46 | (uint64_t)2u << 61;
+}
+// kind::f16 with fp16 operands and fp32 sums, M = 128; B is N-major or K-major.
+__device__ __forceinline__ constexpr uint32_t f16_idesc(int n, bool b_n_major) {
+    return 1u << 4 | (b_n_major ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t mine;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(mine));
+    return mine != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// kEach values of a row from d on, zeros past D.
+template <int kEach>
+__device__ __forceinline__ void load_row(const void *p, MxType type, long long at, int d, int D, bool vec,
+                                         float (&v)[kEach]) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = 0.f;
+    if (d >= D) return;
+    if (type == MxType::kF32) {
+        const float *q = static_cast<const float *>(p) + at + d;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) v[i] = q[i];
+    } else if (vec) {
+        uint32_t w[kEach / 2];
+        if constexpr (kEach == 4) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at + d);
+            w[0] = u.x, w[1] = u.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + at + d);
+        }
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) {
+            if (type == MxType::kF16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+            } else {
+                v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+        }
+    } else {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + at + d;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            v[i] = type == MxType::kF16 ? __half2float(__ushort_as_half(q[i])) : __uint_as_float((uint32_t)q[i] << 16);
+    }
+}
+
+template <int kBits, int kDP, int kTiles, int kNP>
+__global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
+    mx_attention_many_kernel(const MxAttentionArgs a, const int group, const long long tiles, const bool vec,
+                             const long long wait_limit, const int withhold) {
+    using L = ManyLayout<kDP, kTiles, kNP>;
+    constexpr int kRows = 128 * kTiles;
+    constexpr uint32_t kHalf = kManyKeys * 128;  // bytes of 64 values of 128 rows
+    extern __shared__ uint8_t raw[];
+    __shared__ ManyShared sh;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int S = (int)cluster_size(), rank = (int)cluster_rank();
+    const int D = a.cache.D;
+    volatile int *abort = &sh.abort;
+
+    pdl_wait();
+    const long long item = blockIdx.x / S;
+    const int head = (int)(item % a.cache.heads);
+    // (The last tiles first: with a causal mask they see the most keys.)
+    const RowTile tile = row_tile(a.batch, tiles - 1 - item / a.cache.heads, group, kRows, a.tokens);
+    if (tile.rows == 0) return;  // with the whole cluster
+
+    // Keys that each tile of 128 rows sees, in tiles of 128, and this CTA's share of them.
+    const long long room = (long long)a.batch.width * a.cache.page;
+    int cnt[2] = {0, 0}, keys = 0;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+        const int rows = min(max(tile.rows - 128 * t, 0), 128);
+        int n = rows ? keys_of(tile, tile.first + 128 * t + rows - 1, group, a.causal) : 0;
+        if (n > room) {
+            if (threadIdx.x == 0) atomicOr(a.status, kStatusIndex);
+            n = (int)room;
+        }
+        keys = max(keys, n);
+        cnt[t] = (n + kManyKeys - 1) / kManyKeys;
+    }
+    const int all = max(cnt[0], cnt[1]);
+    const int j0 = (int)((long long)all * rank / S), j1 = (int)((long long)all * (rank + 1) / S);
+    cnt[0] = max(min(cnt[0], j1) - j0, 0), cnt[1] = max(min(cnt[1], j1) - j0, 0);
+    const int steps = max(cnt[0], cnt[1]);
+
+    if (warp == L::kWarps - 1) {
+        if (lane == 0) {
+            for (int i = 0; i < 8; ++i) {
+                mbar_init(&sh.ring_full[i], L::kDequantWarps), mbar_init(&sh.ring_free[i], 1);
+                mbar_init(&sh.meta_full[i], L::kDequantWarps);
+            }
+            for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.q_full, L::kSoftmaxWarps), mbar_init(&sh.done, 1);
+            mbar_init(&sh.dequant_done, L::kDequantWarps);
+            fence_mbar_init();
+            sh.abort = 0;
+            for (int i = 0; i < 4; ++i) sh.nan_from[i] = kNever;
+        }
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    auto give_up = [&]() {
+        if (lane == 0) {
+            *abort = 1;
+            flag_timeout(a.status);
+        }
+    };
+
+    if (warp < L::kSoftmaxWarps) {
+        // ---- softmax ----
+        const int t = warp / 4, quarter = warp % 4;
+        const int mine = 128 * t + 32 * quarter + lane;  // this thread's row of the CTA's
+        int power = 0;
+        {
+            constexpr int kEach = kDP / 32;
+            const uint32_t slab = base + t * kNP * L::kSlab;
+            const int d = lane * kEach;
+            const uint32_t col = (d / 64) * kHalf + (d % 8) * 2;
+#pragma unroll 4
+            for (int i = 0; i < 32; ++i) {
+                const int r = 32 * quarter + i;  // row of the slab
+                const int row = tile.first + 128 * t + r;
+                float v[kEach];
+                if (128 * t + r < tile.rows) {
+                    const long long at = (long long)(tile.start + row / group) * a.q_token +
+                                         (long long)(head * group + row % group) * a.q_head;
+                    load_row<kEach>(a.q, a.type, at, d, D, vec, v);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) v[k] = 0.f;
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                // 2^(141 - e) puts a largest value of biased exponent e at 2^14; not where it is infinite or NaN.
+                const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
+                if (lane == i) power = e - 141;
+                const float mult = __int_as_float((268 - e) << 23);
+                const uint32_t at = slab + col + r * 128 + (((d % 64) / 8) ^ (r & 7)) * 16;
+                uint32_t hi[kEach / 2];
+#pragma unroll
+                for (int k = 0; k < kEach / 2; ++k) hi[k] = half2_of(v[2 * k] * mult, v[2 * k + 1] * mult);
+                if constexpr (kEach == 4)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+                else
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
+                if constexpr (kNP == 2) {
+                    uint32_t lo[kEach / 2];
+#pragma unroll
+                    for (int k = 0; k < kEach / 2; ++k) {
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
+                        lo[k] = half2_of(v[2 * k] * mult - b.x, v[2 * k + 1] * mult - b.y);
+                    }
+                    if constexpr (kEach == 4)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kSlab), "r"(lo[0]), "r"(lo[1])
+                                     : "memory");
+                    else
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kSlab), "r"(lo[0]) : "memory");
+                }
+            }
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full);
+
+        const int sees = mine < tile.rows ? keys_of(tile, tile.first + mine, group, a.causal) : 0;
+        const float c0 = a.scale * kLog2e;
+        const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+        const uint32_t s_at = tmem + lanes + L::col_s(t), o_at = tmem + lanes + L::col_o(t);
+        float M = -INFINITY, l = 0.f;
+        const int n = cnt[t];
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+            const int mi = i % L::kMeta;
+            ok = mbar_wait_abortable(&sh.s_full[t], i & 1, wait_limit, abort) &&
+                 mbar_wait_abortable(&sh.meta_full[mi], (i / L::kMeta) & 1, wait_limit, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const int lim = sees - kManyKeys * (j0 + i);  // this tile's keys below it are seen
+            const bool partial = __any_sync(0xFFFFFFFFu, lim < kManyKeys);
+            float factor[4], vref[4];
+            float top = -INFINITY;
+            uint32_t s[2][32];
+            tc_ld32(s_at, s[0]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                factor[g] = c0 * pow2(power + sh.kref[mi][g]), vref[g] = (float)sh.vref[mi][g];
+                tc_wait_ld(s[g & 1]);
+                if (g < 3) tc_ld32(s_at + 32 * (g + 1), s[(g + 1) & 1]);
+                uint32_t(&x)[32] = s[g & 1];
+                float m = -INFINITY, m2 = -INFINITY;
+                if (partial) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * g + k < lim) m = fmaxf(m, __uint_as_float(x[k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+                        m = max3(m, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                        m2 = max3(m2, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                    }
+                    m = fmaxf(m, m2);
+                }
+                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor[g], vref[g]));
+            }
+            if (__any_sync(0xFFFFFFFFu, top > M + kPSlack)) {
+                const float now = fmaxf(M, top), by = M == -INFINITY ? 0.f : ex2(M - now);
+                M = now, l *= by;
+                if (i > 0) {
+#pragma unroll
+                    for (int k = 0; k < kDP; k += 32) {
+                        uint32_t o[32];
+                        tc_ld32(o_at + k, o);
+                        tc_wait_ld(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+                        tc_st32(o_at + k, o);
+                    }
+                }
+            }
+            const float shift = (M == -INFINITY ? 0.f : M) - kPShift;
+            tc_ld32(s_at, s[0]);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                tc_wait_ld(s[g & 1]);
+                if (g < 3) tc_ld32(s_at + 32 * (g + 1), s[(g + 1) & 1]);
+                uint32_t(&x)[32] = s[g & 1];
+                const float2 f2 = make_float2(factor[g], factor[g]);
+                const float2 b2 = make_float2(vref[g] - shift, vref[g] - shift);
+                float2 sum = make_float2(0.f, 0.f);
+                uint32_t p[16], low[16];
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float2 e = ffma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, b2);
+                    e.x = ex2(e.x), e.y = ex2(e.y);
+                    if (partial) {
+                        e.x = 32 * g + k < lim ? e.x : 0.f;
+                        e.y = 32 * g + k + 1 < lim ? e.y : 0.f;
+                    }
+                    sum = __fadd2_rn(sum, e);
+                    p[k / 2] = half2_of(e.x, e.y);
+                    if constexpr (kNP == 2) {
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&p[k / 2]));
+                        low[k / 2] = half2_of(e.x - b.x, e.y - b.y);
+                    }
+                }
+                l = fmaf(sum.x + sum.y, pow2(-sh.vref[mi][g]), l);
+                tc_st16(s_at + 16 * g, p);
+                if constexpr (kNP == 2) tc_st16(tmem + lanes + L::kColLow + 16 * g, low);
+            }
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+        }
+        if (!ok) give_up();
+        // The sums to shared memory, where the operands were.
+        ok = mbar_wait_abortable(&sh.done, 0, wait_limit, abort) &&
+             mbar_wait_abortable(&sh.dequant_done, 0, wait_limit, abort);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+            give_up();
+        } else {
+            tc_fence_after();
+            sh.m[mine] = M, sh.l[mine] = l;
+            const uint32_t to = base + mine * L::kPitch * 4;
+#pragma unroll
+            for (int k = 0; k < kDP; k += 32) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tc_ld32(o_at + k, o);
+                    tc_wait_ld(o);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = 0u;
+                }
+#pragma unroll
+                for (int x = 0; x < 32; x += 4)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * (k + x)), "r"(o[x]),
+                                 "r"(o[x + 1]), "r"(o[x + 2]), "r"(o[x + 3])
+                                 : "memory");
+            }
+            tc_fence_before();
+        }
+    } else if (warp < L::kSoftmaxWarps + L::kDequantWarps) {
+        // ---- dequant ----
+        constexpr int kLanes = kDP * kBits / 128;   // of 16 bytes a token
+        constexpr int kEach = 32 / kLanes;          // tokens a load
+        constexpr int kVals = 128 / kBits;          // values of a lane: 16 or 32
+        const int w = warp - L::kSoftmaxWarps, c = lane % kLanes;
+        const int half = c * kVals / 64, chunk = c * kVals % 64 / 8, block = c * kVals / kMxBlock;
+        // Lanes of the second 64 values take another token, so that eight
+        // lanes' stores meet in no bank.
+        const int tok0 = (lane / kLanes) ^ (kDP == 64 ? 0 : kBits == 8 ? half : 2 * half);
+        const bool in = c * kVals < D;
+        const int blocks = D / kMxBlock, row_bytes = D * kBits / 8;
+        const int per_page = a.cache.page / 16;
+        // The warp's 32 tokens are two pieces of 16, each in one page.
+        int piece[2], within[2];
+        long long slot[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g16 = 8 * j0 + 2 * w + h;
+            piece[h] = g16 / per_page, within[h] = g16 % per_page;
+        }
+        int left;  // tokens of the 32 that exist
+        bool have[2];
+        uint4 kc[kLanes], vc[kLanes];
+        uint32_t ks, vs;
+        auto find = [&](int j) {
+            left = keys - (kManyKeys * j + 32 * w);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int page = left > 16 * h ? page_of(a.batch, a.cache, tile.seq, piece[h], a.status) : -1;
+                have[h] = page >= 0;
+                slot[h] = first_slot(a.cache, page, head) + 16 * within[h];
+                within[h] += 8 % per_page, piece[h] += 8 / per_page;
+                if (within[h] >= per_page) within[h] -= per_page, ++piece[h];
+            }
+        };
+        auto place = [&](int tok) { return tok < 16 ? slot[0] + tok : slot[1] + tok - 16; };
+        auto exists = [&](int tok) { return tok < left && (tok < 16 ? have[0] : have[1]); };
+        auto fetch = [&](const uint8_t *codes, const uint8_t *scales, uint4(&q)[kLanes], uint32_t &sw) {
+            sw = exists(lane) ? ld_stream_u32(scales + place(lane) * 4) : 0u;
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int tok = kEach * i + tok0;
+                q[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (in && exists(tok)) q[i] = ld_stream_u4(codes + place(tok) * row_bytes + 16 * c);
+            }
+        };
+        // Codes to fp16 in a ring slot.  ref: the power taken out; mults as in attention_few.cu.
+        auto put = [&](const uint4(&q)[kLanes], uint32_t mults, uint32_t to) {
+#pragma unroll
+            for (int i = 0; i < kLanes; ++i) {
+                const int tok = kEach * i + tok0, r = 32 * w + tok;
+                const uint32_t e = __shfl_sync(0xFFFFFFFFu, mults, tok) >> (8 * block) & 0xFF;
+                const float f = __int_as_float((e + 94) << 23);
+                const uint32_t m = half2_of(f, f);
+                const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                const uint32_t at = to + half * kHalf + r * 128;
+                if constexpr (kBits == 8) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((chunk + k) ^ (r & 7)) * 16),
+                                     "r"(half2_mul(half_e4m3x2(word[2 * k]), m)),
+                                     "r"(half2_mul(half_e4m3x2_high(word[2 * k]), m)),
+                                     "r"(half2_mul(half_e4m3x2(word[2 * k + 1]), m)),
+                                     "r"(half2_mul(half_e4m3x2_high(word[2 * k + 1]), m))
+                                     : "memory");
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((chunk + k) ^ (r & 7)) * 16),
+                                     "r"(half2_mul(half_e2m1x2<0>(word[k]), m)),
+                                     "r"(half2_mul(half_e2m1x2<1>(word[k]), m)),
+                                     "r"(half2_mul(half_e2m1x2<2>(word[k]), m)),
+                                     "r"(half2_mul(half_e2m1x2<3>(word[k]), m))
+                                     : "memory");
+                }
+            }
+        };
+        auto mults_of = [&](const ScaleWord &s, int ref, bool is_v) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int e = max(s.b[i] - 127 - ref + 33, 0);
+                if (s.b[i] == 255) e = is_v ? 0 : 161;  // infinite: times a zero code NaN
+                m |= (uint32_t)e << (8 * i);
+            }
+            return m;
+        };
+        bool ok = true;
+        auto wait_free = [&](int use) {  // of the ring, counted through
+            if (use >= L::kSlots)
+                ok = mbar_wait_abortable(&sh.ring_free[use % L::kSlots], (use / L::kSlots - 1) & 1, wait_limit, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            return ok;
+        };
+        if (steps > 0) {
+            find(j0);
+            fetch(a.cache.k_codes, a.cache.k_scales, kc, ks);
+            fetch(a.cache.v_codes, a.cache.v_scales, vc, vs);
+        }
+        for (int i = 0; i < steps; ++i) {
+            const ScaleWord sk(ks, blocks), sv(vs, blocks);
+            const int kref = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sk.top) - 134;
+            const int vref = max((int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sv.top) - 134, kVrefMin);
+            if (sv.nan) {  // NaN in v reaches the rows that see it, and no others
+#pragma unroll
+                for (int b = 0; b < 4; ++b)
+                    if (sv.b[b] == 255) atomicMin(&sh.nan_from[b], kManyKeys * (j0 + i) + 32 * w + lane);
+            }
+            if (!wait_free(2 * i)) break;
+            if (lane == 0) {
+                sh.kref[i % L::kMeta][w] = kref, sh.vref[i % L::kMeta][w] = vref;
+                mbar_arrive(&sh.meta_full[i % L::kMeta]);
+            }
+            put(kc, mults_of(sk, kref, false), base + L::off_ring + (2 * i % L::kSlots) * L::kSlab);
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0 && i != withhold) mbar_arrive(&sh.ring_full[2 * i % L::kSlots]);
+            const uint32_t vmults = mults_of(sv, vref, true);
+            if (i + 1 < steps) {
+                find(j0 + i + 1);
+                fetch(a.cache.k_codes, a.cache.k_scales, kc, ks);
+            }
+            if (!wait_free(2 * i + 1)) break;
+            put(vc, vmults, base + L::off_ring + ((2 * i + 1) % L::kSlots) * L::kSlab);
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.ring_full[(2 * i + 1) % L::kSlots]);
+            if (i + 1 < steps) fetch(a.cache.v_codes, a.cache.v_scales, vc, vs);
+        }
+        if (!ok) give_up();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.dequant_done);
+    } else {
+        // ---- issue ----
+        const bool leader = elect_lane();
+        constexpr uint32_t kIdS = f16_idesc(kManyKeys, false), kIdO = f16_idesc(kDP, true);
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, int parity) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_spin_abortable(bar, parity, wait_limit, abort));
+            tc_fence_after();
+            return ok;
+        };
+        auto scores = [&](int t, int i) {  // S of tile t and the CTA's keys i
+            const uint32_t k_at = base + L::off_ring + (2 * i % L::kSlots) * L::kSlab;
+            if (leader) {
+#pragma unroll
+                for (int p = 0; p < kNP; ++p) {
+                    const uint64_t qd = k_major_desc(base + (t * kNP + p) * L::kSlab), kd = k_major_desc(k_at);
+#pragma unroll
+                    for (int k = 0; k < kDP / 16; ++k) {
+                        const uint32_t at = (k / 4) * (kHalf >> 4) + 2 * (k % 4);
+                        mma_ss(tmem + L::col_s(t), qd + at, kd + at, kIdS, (p | k) != 0);
+                    }
+                }
+                tc_commit(&sh.s_full[t]);
+                if (t == 1 || cnt[1] <= i) tc_commit(&sh.ring_free[2 * i % L::kSlots]);  // no other tile wants K
+            }
+            __syncwarp();
+        };
+        auto outputs = [&](int t, int i) {
+            const uint32_t v_at = base + L::off_ring + ((2 * i + 1) % L::kSlots) * L::kSlab;
+            if (leader) {
+                const uint64_t vd = n_major_desc(v_at, kHalf);
+#pragma unroll
+                for (int p = 0; p < kNP; ++p)
+#pragma unroll
+                    for (int k = 0; k < kManyKeys / 16; ++k)
+                        mma_ts(tmem + L::col_o(t), tmem + (p ? L::kColLow : L::col_s(t)) + 8 * k, vd + (2048 >> 4) * k,
+                               kIdO, (i | p | k) != 0);
+                if (t == 1 || cnt[1] <= i) tc_commit(&sh.ring_free[(2 * i + 1) % L::kSlots]);
+            }
+            __syncwarp();
+        };
+        auto k_ready = [&](int i) { return wait(&sh.ring_full[2 * i % L::kSlots], (2 * i / L::kSlots) & 1); };
+        auto v_ready = [&](int i) { return wait(&sh.ring_full[(2 * i + 1) % L::kSlots], ((2 * i + 1) / L::kSlots) & 1); };
+        if (steps > 0 && wait(&sh.q_full, 0) && k_ready(0)) {
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                if (cnt[t] > 0) scores(t, 0);
+            for (int i = 0; i < steps && ok; ++i) {
+                if (!v_ready(i)) break;
+                bool k_known = false;
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) {
+                    if (i >= cnt[t]) continue;
+                    if (!wait(&sh.p_full[t], i & 1)) break;
+                    outputs(t, i);
+                    if (i + 1 < cnt[t]) {
+                        if (!k_known && !k_ready(i + 1)) break;
+                        k_known = true;
+                        scores(t, i + 1);
+                    }
+                }
+            }
+        }
+        if (!ok) give_up();
+        // Whatever was issued completes before tensor memory is read or freed.
+        if (leader) tc_commit(&sh.done);
+        __syncwarp();
+        if (!mbar_wait_bounded(&sh.done, 0, wait_limit)) outlast_copies();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    const bool failed = *abort != 0;
+    if (S > 1) cluster_sync_all();
+    if (!failed) {
+        const float *o = reinterpret_cast<const float *>(raw + (base - smem_addr(raw)));
+        const uint32_t m_at = smem_addr(sh.m), l_at = smem_addr(sh.l), n_at = smem_addr(sh.nan_from);
+        for (int i = rank * L::kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += S * L::kThreads) {
+            const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
+            if (d >= D) continue;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            float ls = 0.f;
+            int nan_from;
+            if (S == 1) {
+                sum = *reinterpret_cast<const float4 *>(o + r * L::kPitch + d);
+                ls = sh.l[r], nan_from = sh.nan_from[d / kMxBlock];
+            } else {
+                float m = -INFINITY;
+                nan_from = kNever;
+                for (int s = 0; s < S; ++s) {
+                    m = fmaxf(m, ld_cluster_f32(map_to_rank(m_at + 4 * r, s)));
+                    nan_from = min(nan_from, __float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * (d / kMxBlock), s))));
+                }
+                for (int s = 0; s < S; ++s) {
+                    const float mi = ld_cluster_f32(map_to_rank(m_at + 4 * r, s));
+                    const float li = ld_cluster_f32(map_to_rank(l_at + 4 * r, s));
+                    const float4 v = ld_cluster_v4(map_to_rank(base + 4 * (r * L::kPitch + d), s));
+                    const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
+                    ls += mi == -INFINITY ? li : by * li;
+                    sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
+                    sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
+                }
+            }
+            const int row = tile.first + r;
+            if (nan_from < keys_of(tile, row, group, a.causal)) ls = __int_as_float(0x7FC00000);
+            const long long at = (long long)(tile.start + row / group) * a.y_token +
+                                 (long long)(head * group + row % group) * a.y_head + d;
+            // A row that sees nothing has no sum: zeros.
+            const float by = ls == 0.f ? 0.f : 1.f / ls;
+            store4(a.y, a.type, at, vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+        }
+    }
+    if (S > 1)
+        cluster_sync_all();  // no CTA leaves while another reads its sums
+    else
+        __syncthreads();
+    if (warp == L::kWarps - 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int kBits, int kDP, int kTiles, int kNP>
+cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
+    using L = ManyLayout<kDP, kTiles, kNP>;
+    auto kernel = mx_attention_many_kernel<kBits, kDP, kTiles, kNP>;
+    cudaError_t e = ensure_smem(kernel, L::total);
+    if (e != cudaSuccess) return e;
+    const int group = a.heads / a.cache.heads;
+    const long long rows = (long long)a.tokens * group, tiles = rows / (128 * kTiles) + a.batch.seqs;
+    const long long keys = (long long)a.batch.width * a.cache.page;
+    const int S = many_split(rows, 128 * kTiles, a.batch.seqs, a.cache.heads, (int)(keys < 0x7FFFFFFF ? keys : 0x7FFFFFFF),
+                             c.num_sms);
+    const long long ctas = tiles * a.cache.heads * S;
+    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const size_t size = a.type == MxType::kF32 ? 4 : 2;
+    const bool vec = reinterpret_cast<uintptr_t>(a.q) % (4 * size) == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * size) == 0 &&
+                     a.q_token % 4 == 0 && a.q_head % 4 == 0 && a.y_token % 4 == 0 && a.y_head % 4 == 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::total;
+    cfg.stream = c.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, group, tiles, vec, c.wait_limit, c.withhold);
+}
+
+template <int kBits, int kDP>
+cudaError_t launch_type(const LaunchCtx &c, const MxAttentionArgs &a) {
+    return a.type == MxType::kF32 ? launch_many<kBits, kDP, 1, 2>(c, a) : launch_many<kBits, kDP, 2, 1>(c, a);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a) {
+    const bool narrow = a.cache.D <= 64;
+    if (a.cache.bits == 4) return narrow ? launch_type<4, 64>(c, a) : launch_type<4, 128>(c, a);
+    return narrow ? launch_type<8, 64>(c, a) : launch_type<8, 128>(c, a);
+}
+
+}  // namespace q4mm

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "q4mm.h"
+#include "attention_geometry.h"
 #include "dispatch.h"
 #include "kernels.h"
 #include "sync.cuh"
@@ -745,11 +746,12 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
         (rc = check_mx_alias(&ys, 1, call.spans, 7)))
         return rc;
     q4mm::LaunchCtx ctx;
-    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const bool many = q4mm::many_rows(tokens, heads / kvHeads, sequences);
+    if ((rc = device_ctx(stream, &ctx, many))) return rc;
     const q4mm::MxAttentionArgs a{call.cache, call.batch, q, q_token_stride, q_head_stride, y, y_token_stride,
                                   y_head_stride, scale, causal != 0, tokens, heads, static_cast<q4mm::MxType>(dtype),
                                   ctx.status};
-    const cudaError_t e = q4mm::launch_mx_attention(ctx, a);
+    const cudaError_t e = many ? q4mm::launch_mx_attention_many(ctx, a) : q4mm::launch_mx_attention_few(ctx, a);
     if (e != cudaSuccess) return fail_cuda(e, "mx_attention launch");
     return Q4MM_OK;
 }

@@ -202,7 +202,8 @@ struct MxAttentionArgs {
     MxType type;
     int *status;
 };
-cudaError_t launch_mx_attention(const LaunchCtx &c, const MxAttentionArgs &a);
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a);   // few rows a kv head
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a);  // tiles of 128, on tcgen05
 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device; the attribute call is made only when the limit grows, so a

@@ -495,7 +495,8 @@ def test_steps_in_a_graph_and_on_another_stream():
     """Decoding steps captured once and replayed on new tokens, lengths and pages, against plain calls."""
     q, torch = _q(), _torch()
     c = Case(8, [1, 1], [30, 77], 2, 64, 16, 8, spare=4, width=8).fill()
-    c.table[0, 2] = min(set(range(len(c.cache["k_codes"]))) - set(c.table[c.table >= 0].tolist()))   # a free page to grow into
+    for i, n in ((0, 2), (1, 5)):       # free pages to grow into
+        c.table[i, n] = min(set(range(len(c.cache["k_codes"]))) - set(c.table[c.table >= 0].tolist()))
     cache, (starts, lengths, pages) = c.device_cache(), c.device_batch()
     plain = c.device_cache()
     rope = q.Rope(q.rope_frequencies(64))
