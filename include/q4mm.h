@@ -481,7 +481,7 @@ int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride
  *   codes : [pages][kvHeads][pageTokens] rows of headDim·bits/8 bytes
  *           (16-byte aligned base);
  *   scales: [pages][kvHeads][pageTokens][4] bytes, block b of the head in byte
- *           b, bytes past headDim / 32 written as zero and not read (4-byte
+ *           b, bytes past headDim / 32 written as zero and not read (16-byte
  *           aligned base).
  * k and v each have codes and scales.
  *

@@ -14,16 +14,19 @@
 // while the softmax of one is computed the pipe works on the other.
 //
 // Warps of a CTA:
-//   softmax  four a tile, a row a thread (a warp reads only its own quarter of
-//            the lanes of tensor memory): maximum, exponentials, P, and,
-//            where the maximum has grown by more than 8, O rescaled.
-//   dequant  four, 32 neighbouring tokens of a tile each: codes from global
-//            memory through registers (the next tile's on their way) to fp16
-//            in shared memory, rows of 128 bytes in the 128-byte swizzle.  V
-//            lies like K, token by token: it is the product's B operand with
-//            the values (N) contiguous.  The power of two taken out (see
+//   softmax  eight a tile: a thread has half of a row's 128 scores, so that
+//            they stay in its registers (a warp reaches only its own quarter of the lanes
+//            of tensor memory).  Maximum, shared with the other half's thread
+//            through shared memory, exponentials, P, and, where the maximum
+//            has grown by more than 8, O rescaled.
+//   dequant  four, 32 neighbouring tokens of a tile each: codes to fp16 in
+//            shared memory, rows of 128 bytes in the 128-byte swizzle.  V lies
+//            like K, token by token: it is the product's B operand with the
+//            values (N) contiguous.  The power of two taken out (see
 //            attention.cuh) is one for those 32 tokens, and goes to the
 //            softmax beside them.
+//   copy     one: the codes and scales of 16 neighbouring tokens of a head are
+//            one run of a page, hence one bulk copy each, a lane each.
 //   issue    one warp, one elected lane: S of both tiles, then in turn P V of
 //            one tile and S of its next keys.
 // S of the next keys is written over P by an instruction issued after the one
@@ -50,31 +53,44 @@ namespace {
 
 // kDP: the head's values rounded up to 64 or 128; kTiles x kNP: tiles of 128
 // rows and fp16 terms of a query value, 2 x 1 or 1 x 2.
-template <int kDP, int kTiles, int kNP>
+template <int kBits, int kDP, int kTiles, int kNP>
 struct ManyLayout {
-    static constexpr int kSoftmaxWarps = 4 * kTiles, kDequantWarps = 4;
-    static constexpr int kWarps = kSoftmaxWarps + kDequantWarps + 1;
+    static constexpr int kSoftmaxWarps = 8 * kTiles, kDequantWarps = 4;
+    static constexpr int kIssueWarp = kSoftmaxWarps + kDequantWarps, kCopyWarp = kIssueWarp + 1;
+    static constexpr int kWarps = kIssueWarp + 4;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr uint32_t kSlab = kManyKeys * kDP * 2;  // 128 rows of Q, K or V
-    static constexpr int kSlots = kDP == 64 ? 8 : 4;        // of the ring of K and V
-    static constexpr int kMeta = kSlots;                    // tiles whose powers are kept (> kSlots / 2)
+    static constexpr uint32_t kSlab = kManyKeys * kDP * 2;             // 128 rows of Q, K or V
+    static constexpr int kSlots = kDP == 64 ? 6 : 3;                   // of the ring of K and V
+    static constexpr int kMeta = 4;                                    // tiles whose powers are kept
+    static constexpr uint32_t kCodes = kManyKeys * kDP * kBits / 8;    // codes of 128 rows
+    static constexpr int kCodeSlots = kDP == 128 && kBits == 8 ? 3 : 4;
     static constexpr uint32_t off_ring = 2 * kSlab;
-    static constexpr uint32_t off_end = off_ring + kSlots * kSlab;
+    static constexpr uint32_t off_codes = off_ring + kSlots * kSlab;
+    static constexpr uint32_t off_scales = off_codes + kCodeSlots * kCodes;  // of K and V, 512 bytes each, two tiles
+    static constexpr uint32_t off_end = off_scales + 2 * 1024;
     // The sums, where the operands were.
     static constexpr int kPitch = kDP + 4;
     static constexpr uint32_t total = off_end + 1024;  // the base is rounded up to 1024 bytes
-    static_assert(2 * kSlab == kTiles * kNP * kSlab && kTiles * 128 * kPitch * 4 <= off_end, "");
+    static_assert(kTiles * kNP == 2 && kTiles * 128 * kPitch * 4 <= off_codes, "");
     static_assert(kSmShared - total - kCtaSharedExtra < kHalfTmemShared, "takes all of tensor memory");
+    // Powers of tile i + kMeta are written when S of tile i + kMeta - kSlots / 2 is done, after P of tile i.
+    static_assert(kMeta > kSlots / 2, "");
     // Tensor memory: S (and P over it), second terms of P, O.
     static constexpr uint32_t col_s(int t) { return 128 * t; }
+    // P's 16 keys k: over the S of the same half of the keys.
+    static __device__ constexpr uint32_t col_p(int k) { return k / 4 * 64 + 8 * (k % 4); }
     static constexpr uint32_t kColLow = 128;  // kNP == 2, kTiles == 1
     static constexpr uint32_t col_o(int t) { return 256 + kDP * t; }
 };
 
 struct ManyShared {
-    uint64_t ring_full[8], ring_free[8], meta_full[8], s_full[2], p_full[2], q_full, done, dequant_done;
-    int kref[8][4], vref[8][4];  // of a tile's 32-token groups
-    float m[256], l[256];
+    uint64_t ring_full[6], ring_free[6], code_full[4], code_free[4], meta_full[4], s_full[2], p_full[2], q_full, done,
+        dequant_done;
+    int kref[4][4], vref[4][4];  // of a tile's 32-token groups
+    uint32_t valid[4];           // a tile's 16-token groups that were copied
+    float top[2][2][256];        // a tile's maxima, of both halves
+    int power[256];              // of two, taken out of a query row
+    float m[256], l[2][256];
     int nan_from[4];
     uint32_t tmem;
     int abort;
@@ -89,23 +105,12 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                  : "memory");
 }
 
-// Waits for the loads from tensor memory; r, the values of one, are not used before it.
-__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
-
-// 32 columns of this thread's lane; the values are there after tc_wait_ld.
+// Columns of this thread's lane, there when this returns.
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -113,14 +118,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
         : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -158,6 +162,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
                  "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// Bulk copy from global to shared memory (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void *from, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(smem_addr(bar))
                  : "memory");
 }
 __device__ __forceinline__ bool elect_lane() {
@@ -209,16 +219,18 @@ __device__ __forceinline__ void load_row(const void *p, MxType type, long long a
 }
 
 template <int kBits, int kDP, int kTiles, int kNP>
-__global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
+__global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads, 1)
     mx_attention_many_kernel(const MxAttentionArgs a, const int group, const long long tiles, const bool vec,
                              const long long wait_limit, const int withhold) {
-    using L = ManyLayout<kDP, kTiles, kNP>;
+    using L = ManyLayout<kBits, kDP, kTiles, kNP>;
     constexpr int kRows = 128 * kTiles;
     constexpr uint32_t kHalf = kManyKeys * 128;  // bytes of 64 values of 128 rows
     extern __shared__ uint8_t raw[];
     __shared__ ManyShared sh;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    // (By a shuffle, so that the compiler knows it to be one a warp, here and below.)
+    auto uniform = [](int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+    const int lane = threadIdx.x & 31, warp = uniform(threadIdx.x / 32);
     const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int D = a.cache.D;
     volatile int *abort = &sh.abort;
@@ -246,16 +258,16 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
     }
     const int all = max(cnt[0], cnt[1]);
     const int j0 = (int)((long long)all * rank / S), j1 = (int)((long long)all * (rank + 1) / S);
-    cnt[0] = max(min(cnt[0], j1) - j0, 0), cnt[1] = max(min(cnt[1], j1) - j0, 0);
+    cnt[0] = uniform(max(min(cnt[0], j1) - j0, 0)), cnt[1] = uniform(max(min(cnt[1], j1) - j0, 0));
     const int steps = max(cnt[0], cnt[1]);
 
-    if (warp == L::kWarps - 1) {
+    if (warp == L::kIssueWarp) {
         if (lane == 0) {
-            for (int i = 0; i < 8; ++i) {
-                mbar_init(&sh.ring_full[i], L::kDequantWarps), mbar_init(&sh.ring_free[i], 1);
-                mbar_init(&sh.meta_full[i], L::kDequantWarps);
-            }
-            for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+            for (int i = 0; i < L::kSlots; ++i) mbar_init(&sh.ring_full[i], L::kDequantWarps), mbar_init(&sh.ring_free[i], 1);
+            for (int i = 0; i < L::kCodeSlots; ++i)
+                mbar_init(&sh.code_full[i], 1), mbar_init(&sh.code_free[i], L::kDequantWarps);
+            for (int i = 0; i < L::kMeta; ++i) mbar_init(&sh.meta_full[i], L::kDequantWarps);
+            for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 8);
             mbar_init(&sh.q_full, L::kSoftmaxWarps), mbar_init(&sh.done, 1);
             mbar_init(&sh.dequant_done, L::kDequantWarps);
             fence_mbar_init();
@@ -271,6 +283,19 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    // Every warp ends by these, in its own role, so that no role holds registers for what another does afterwards.
+    auto meet = [&]() {  // the CTA's sums, and its cluster's, are in shared memory
+        __syncwarp();
+        named_bar_sync(0, L::kThreads);
+        if (cluster_size() > 1) cluster_sync_all();
+    };
+    auto leave = [&]() {  // no CTA leaves while another reads its sums
+        __syncwarp();
+        if (cluster_size() > 1)
+            cluster_sync_all();
+        else
+            named_bar_sync(0, L::kThreads);
+    };
     auto give_up = [&]() {
         if (lane == 0) {
             *abort = 1;
@@ -280,17 +305,17 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
 
     if (warp < L::kSoftmaxWarps) {
         // ---- softmax ----
-        const int t = warp / 4, quarter = warp % 4;
+        const int t = warp / 8, side = warp / 4 % 2, quarter = warp % 4;
         const int mine = 128 * t + 32 * quarter + lane;  // this thread's row of the CTA's
-        int power = 0;
         {
+            // Query rows to fp16, each by a power of two of its own, 16 a warp.
             constexpr int kEach = kDP / 32;
             const uint32_t slab = base + t * kNP * L::kSlab;
             const int d = lane * kEach;
             const uint32_t col = (d / 64) * kHalf + (d % 8) * 2;
 #pragma unroll 4
-            for (int i = 0; i < 32; ++i) {
-                const int r = 32 * quarter + i;  // row of the slab
+            for (int i = 0; i < 16; ++i) {
+                const int r = 32 * quarter + 16 * side + i;  // row of the slab
                 const int row = tile.first + 128 * t + r;
                 float v[kEach];
                 if (128 * t + r < tile.rows) {
@@ -307,7 +332,7 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
                 top = __reduce_max_sync(0xFFFFFFFFu, top);
                 // 2^(141 - e) puts a largest value of biased exponent e at 2^14; not where it is infinite or NaN.
                 const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
-                if (lane == i) power = e - 141;
+                if (lane == 0) sh.power[128 * t + r] = e - 141;
                 const float mult = __int_as_float((268 - e) << 23);
                 const uint32_t at = slab + col + r * 128 + (((d % 64) / 8) ^ (r & 7)) * 16;
                 uint32_t hi[kEach / 2];
@@ -335,38 +360,39 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
         fence_async_proxy();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.q_full);
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_prompt(&sh.q_full, 0, wait_limit, abort));
 
+        const int power = sh.power[mine];
         const int sees = mine < tile.rows ? keys_of(tile, tile.first + mine, group, a.causal) : 0;
         const float c0 = a.scale * kLog2e;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
-        const uint32_t s_at = tmem + lanes + L::col_s(t), o_at = tmem + lanes + L::col_o(t);
+        const uint32_t s_at = tmem + lanes + L::col_s(t) + 64 * side, o_at = tmem + lanes + L::col_o(t) + kDP / 2 * side;
         float M = -INFINITY, l = 0.f;
         const int n = cnt[t];
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
+        bool go = true;  // the two warps of a quarter leave together, also after a time-out
+        for (int i = 0; i < n && go; ++i) {
             const int mi = i % L::kMeta;
-            ok = mbar_wait_abortable(&sh.s_full[t], i & 1, wait_limit, abort) &&
-                 mbar_wait_abortable(&sh.meta_full[mi], (i / L::kMeta) & 1, wait_limit, abort);
+            ok = ok && mbar_wait_prompt(&sh.s_full[t], i & 1, wait_limit, abort) &&
+                 mbar_wait_prompt(&sh.meta_full[mi], (i / L::kMeta) & 1, wait_limit, abort);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            if (!ok) give_up();
             tc_fence_after();
-            const int lim = sees - kManyKeys * (j0 + i);  // this tile's keys below it are seen
-            const bool partial = __any_sync(0xFFFFFFFFu, lim < kManyKeys);
-            float factor[4], vref[4];
+            const int lim = sees - kManyKeys * (j0 + i) - 64 * side;  // these keys below it are seen
+            const bool partial = __any_sync(0xFFFFFFFFu, lim < 64);
+            // (These loops stay loops, here and in the other warps: what the SM's
+            // warps run between two barriers has to stay in the instruction
+            // caches, or all of them wait for instructions.)
             float top = -INFINITY;
-            uint32_t s[2][32];
-            tc_ld32(s_at, s[0]);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                factor[g] = c0 * pow2(power + sh.kref[mi][g]), vref[g] = (float)sh.vref[mi][g];
-                tc_wait_ld(s[g & 1]);
-                if (g < 3) tc_ld32(s_at + 32 * (g + 1), s[(g + 1) & 1]);
-                uint32_t(&x)[32] = s[g & 1];
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+                uint32_t x[32];
+                tc_ld32(s_at + 32 * g, x);
+                const float factor = c0 * pow2(power + sh.kref[mi][2 * side + g]);
                 float m = -INFINITY, m2 = -INFINITY;
                 if (partial) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (32 * g + k < lim) m = fmaxf(m, __uint_as_float(x[k]));
+                        if (k < lim - 32 * g) m = fmaxf(m, __uint_as_float(x[k]));
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
@@ -375,42 +401,53 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
                     }
                     m = fmaxf(m, m2);
                 }
-                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor[g], vref[g]));
+                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor, (float)sh.vref[mi][2 * side + g]));
             }
+            // The other half's maximum (NaN: it gives up).  Both threads of a row
+            // hold the same M.
+            sh.top[i & 1][side][mine] = ok ? top : __int_as_float(0x7FC00000);
+            named_bar_sync(1 + 4 * t + quarter, 64);
+            const float other = sh.top[i & 1][side ^ 1][mine];
+            go = ok && !isnan(other);
+            top = fmaxf(top, other);
             if (__any_sync(0xFFFFFFFFu, top > M + kPSlack)) {
                 const float now = fmaxf(M, top), by = M == -INFINITY ? 0.f : ex2(M - now);
                 M = now, l *= by;
                 if (i > 0) {
+#pragma unroll 1
+                    for (int k = 0; k < kDP / 2; k += 16) {
+                        uint32_t o[16];
+                        tc_ld16(o_at + k, o);
 #pragma unroll
-                    for (int k = 0; k < kDP; k += 32) {
-                        uint32_t o[32];
-                        tc_ld32(o_at + k, o);
-                        tc_wait_ld(o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-                        tc_st32(o_at + k, o);
+                        for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * by);
+                        tc_st16(o_at + k, o);
                     }
                 }
             }
             const float shift = (M == -INFINITY ? 0.f : M) - kPShift;
-            tc_ld32(s_at, s[0]);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                tc_wait_ld(s[g & 1]);
-                if (g < 3) tc_ld32(s_at + 32 * (g + 1), s[(g + 1) & 1]);
-                uint32_t(&x)[32] = s[g & 1];
-                const float2 f2 = make_float2(factor[g], factor[g]);
-                const float2 b2 = make_float2(vref[g] - shift, vref[g] - shift);
+#pragma unroll 1
+            for (int g = 0; g < 2; ++g) {
+                uint32_t x[32];
+                tc_ld32(s_at + 32 * g, x);
+                const float factor = c0 * pow2(power + sh.kref[mi][2 * side + g]);
+                const int vref = sh.vref[mi][2 * side + g];
+                const float2 f2 = make_float2(factor, factor);
+                const float2 b2 = make_float2((float)vref - shift, (float)vref - shift);
                 float2 sum = make_float2(0.f, 0.f);
                 uint32_t p[16], low[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     float2 e = ffma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, b2);
-                    e.x = ex2(e.x), e.y = ex2(e.y);
-                    if (partial) {
-                        e.x = 32 * g + k < lim ? e.x : 0.f;
-                        e.y = 32 * g + k + 1 < lim ? e.y : 0.f;
-                    }
+                    x[k] = __float_as_uint(ex2(e.x)), x[k + 1] = __float_as_uint(ex2(e.y));
+                }
+                if (partial) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (k >= lim - 32 * g) x[k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    const float2 e = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
                     sum = __fadd2_rn(sum, e);
                     p[k / 2] = half2_of(e.x, e.y);
                     if constexpr (kNP == 2) {
@@ -418,31 +455,30 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
                         low[k / 2] = half2_of(e.x - b.x, e.y - b.y);
                     }
                 }
-                l = fmaf(sum.x + sum.y, pow2(-sh.vref[mi][g]), l);
+                l = fmaf(sum.x + sum.y, pow2(-vref), l);
                 tc_st16(s_at + 16 * g, p);
-                if constexpr (kNP == 2) tc_st16(tmem + lanes + L::kColLow + 16 * g, low);
+                if constexpr (kNP == 2) tc_st16(tmem + lanes + L::kColLow + 32 * side + 16 * g, low);
             }
             tc_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.p_full[t]);
         }
-        if (!ok) give_up();
+        if (!go) give_up();
         // The sums to shared memory, where the operands were.
-        ok = mbar_wait_abortable(&sh.done, 0, wait_limit, abort) &&
-             mbar_wait_abortable(&sh.dequant_done, 0, wait_limit, abort);
+        ok = mbar_wait_prompt(&sh.done, 0, wait_limit, abort) &&
+             mbar_wait_prompt(&sh.dequant_done, 0, wait_limit, abort);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             give_up();
         } else {
             tc_fence_after();
-            sh.m[mine] = M, sh.l[mine] = l;
-            const uint32_t to = base + mine * L::kPitch * 4;
+            sh.m[mine] = M, sh.l[side][mine] = l;
+            const uint32_t to = base + (mine * L::kPitch + kDP / 2 * side) * 4;
 #pragma unroll
-            for (int k = 0; k < kDP; k += 32) {
+            for (int k = 0; k < kDP / 2; k += 32) {
                 uint32_t o[32];
                 if (n > 0) {
                     tc_ld32(o_at + k, o);
-                    tc_wait_ld(o);
                 } else {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) o[x] = 0u;
@@ -455,6 +491,49 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
             }
             tc_fence_before();
         }
+        meet();
+        if (*abort == 0) {
+            const int parts = (int)cluster_size(), part = (int)cluster_rank();
+            constexpr int kThreads = 32 * L::kSoftmaxWarps;
+            const float *o = reinterpret_cast<const float *>(raw + (base - smem_addr(raw)));
+            const uint32_t m_at = smem_addr(sh.m), l_at = smem_addr(sh.l), n_at = smem_addr(sh.nan_from);
+            for (int i = part * kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += parts * kThreads) {
+                const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
+                if (d >= D) continue;
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                float ls = 0.f;
+                int nan_from;
+                if (parts == 1) {
+                    sum = *reinterpret_cast<const float4 *>(o + r * L::kPitch + d);
+                    ls = sh.l[0][r] + sh.l[1][r], nan_from = sh.nan_from[d / kMxBlock];
+                } else {
+                    float m = -INFINITY;
+                    nan_from = kNever;
+                    for (int s = 0; s < parts; ++s) {
+                        m = fmaxf(m, ld_cluster_f32(map_to_rank(m_at + 4 * r, s)));
+                        nan_from = min(nan_from, __float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * (d / kMxBlock), s))));
+                    }
+                    for (int s = 0; s < parts; ++s) {
+                        const float mi = ld_cluster_f32(map_to_rank(m_at + 4 * r, s));
+                        const float li = ld_cluster_f32(map_to_rank(l_at + 4 * r, s)) +
+                                         ld_cluster_f32(map_to_rank(l_at + 4 * (256 + r), s));
+                        const float4 v = ld_cluster_v4(map_to_rank(base + 4 * (r * L::kPitch + d), s));
+                        const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
+                        ls += mi == -INFINITY ? li : by * li;
+                        sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
+                        sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
+                    }
+                }
+                const int row = tile.first + r;
+                if (nan_from < keys_of(tile, row, group, a.causal)) ls = __int_as_float(0x7FC00000);
+                const long long at = (long long)(tile.start + row / group) * a.y_token +
+                                     (long long)(head * group + row % group) * a.y_head + d;
+                // A row that sees nothing has no sum: zeros.
+                const float by = ls == 0.f ? 0.f : 1.f / ls;
+                store4(a.y, a.type, at, vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+            }
+        }
+        leave();
     } else if (warp < L::kSoftmaxWarps + L::kDequantWarps) {
         // ---- dequant ----
         constexpr int kLanes = kDP * kBits / 128;   // of 16 bytes a token
@@ -467,71 +546,59 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
         const int tok0 = (lane / kLanes) ^ (kDP == 64 ? 0 : kBits == 8 ? half : 2 * half);
         const bool in = c * kVals < D;
         const int blocks = D / kMxBlock, row_bytes = D * kBits / 8;
-        const int per_page = a.cache.page / 16;
-        // The warp's 32 tokens are two pieces of 16, each in one page.
-        int piece[2], within[2];
-        long long slot[2];
+        // A unit's codes (K of tile i: 2i, V: 2i + 1) to fp16 in its slot of
+        // the ring.  mults: of each lane's token, four bytes of exponents 33
+        // above those of its blocks' multipliers; exists: a bit a token.
+        auto put = [&](int unit, uint32_t mults, uint32_t exists) {
+            const uint32_t from = base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 32 * w * row_bytes + 16 * c;
+            const uint32_t to = base + L::off_ring + unit % L::kSlots * L::kSlab + half * kHalf;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kLanes; i0 += 2) {
+                uint4 q[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int g16 = 8 * j0 + 2 * w + h;
-            piece[h] = g16 / per_page, within[h] = g16 % per_page;
-        }
-        int left;  // tokens of the 32 that exist
-        bool have[2];
-        uint4 kc[kLanes], vc[kLanes];
-        uint32_t ks, vs;
-        auto find = [&](int j) {
-            left = keys - (kManyKeys * j + 32 * w);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int page = left > 16 * h ? page_of(a.batch, a.cache, tile.seq, piece[h], a.status) : -1;
-                have[h] = page >= 0;
-                slot[h] = first_slot(a.cache, page, head) + 16 * within[h];
-                within[h] += 8 % per_page, piece[h] += 8 / per_page;
-                if (within[h] >= per_page) within[h] -= per_page, ++piece[h];
-            }
-        };
-        auto place = [&](int tok) { return tok < 16 ? slot[0] + tok : slot[1] + tok - 16; };
-        auto exists = [&](int tok) { return tok < left && (tok < 16 ? have[0] : have[1]); };
-        auto fetch = [&](const uint8_t *codes, const uint8_t *scales, uint4(&q)[kLanes], uint32_t &sw) {
-            sw = exists(lane) ? ld_stream_u32(scales + place(lane) * 4) : 0u;
-#pragma unroll
-            for (int i = 0; i < kLanes; ++i) {
-                const int tok = kEach * i + tok0;
-                q[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (in && exists(tok)) q[i] = ld_stream_u4(codes + place(tok) * row_bytes + 16 * c);
-            }
-        };
-        // Codes to fp16 in a ring slot.  ref: the power taken out; mults as in attention_few.cu.
-        auto put = [&](const uint4(&q)[kLanes], uint32_t mults, uint32_t to) {
-#pragma unroll
-            for (int i = 0; i < kLanes; ++i) {
-                const int tok = kEach * i + tok0, r = 32 * w + tok;
-                const uint32_t e = __shfl_sync(0xFFFFFFFFu, mults, tok) >> (8 * block) & 0xFF;
-                const float f = __int_as_float((e + 94) << 23);
-                const uint32_t m = half2_of(f, f);
-                const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-                const uint32_t at = to + half * kHalf + r * 128;
-                if constexpr (kBits == 8) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((chunk + k) ^ (r & 7)) * 16),
-                                     "r"(half2_mul(half_e4m3x2(word[2 * k]), m)),
-                                     "r"(half2_mul(half_e4m3x2_high(word[2 * k]), m)),
-                                     "r"(half2_mul(half_e4m3x2(word[2 * k + 1]), m)),
-                                     "r"(half2_mul(half_e4m3x2_high(word[2 * k + 1]), m))
-                                     : "memory");
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((chunk + k) ^ (r & 7)) * 16),
-                                     "r"(half2_mul(half_e2m1x2<0>(word[k]), m)),
-                                     "r"(half2_mul(half_e2m1x2<1>(word[k]), m)),
-                                     "r"(half2_mul(half_e2m1x2<2>(word[k]), m)),
-                                     "r"(half2_mul(half_e2m1x2<3>(word[k]), m))
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = kEach * (i0 + i) + tok0;
+                    q[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in && (exists >> tok & 1))
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
+                                     : "r"(from + tok * row_bytes)
                                      : "memory");
                 }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = kEach * (i0 + i) + tok0, r = 32 * w + tok;
+                    const uint32_t e = __shfl_sync(0xFFFFFFFFu, mults, tok) >> (8 * block) & 0xFF;
+                    const float f = __int_as_float((e + 94) << 23);
+                    const uint32_t m = half2_of(f, f);
+                    const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+                    const uint32_t at = to + r * 128;
+                    if constexpr (kBits == 8) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             at + ((chunk + k) ^ (r & 7)) * 16),
+                                         "r"(half2_mul(half_e4m3x2(word[2 * k]), m)),
+                                         "r"(half2_mul(half_e4m3x2_high(word[2 * k]), m)),
+                                         "r"(half2_mul(half_e4m3x2(word[2 * k + 1]), m)),
+                                         "r"(half2_mul(half_e4m3x2_high(word[2 * k + 1]), m))
+                                         : "memory");
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             at + ((chunk + k) ^ (r & 7)) * 16),
+                                         "r"(half2_mul(half_e2m1x2<0>(word[k]), m)),
+                                         "r"(half2_mul(half_e2m1x2<1>(word[k]), m)),
+                                         "r"(half2_mul(half_e2m1x2<2>(word[k]), m)),
+                                         "r"(half2_mul(half_e2m1x2<3>(word[k]), m))
+                                         : "memory");
+                    }
+                }
             }
+            fence_async_proxy();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.code_free[unit % L::kCodeSlots]), mbar_arrive(&sh.ring_full[unit % L::kSlots]);
         };
         auto mults_of = [&](const ScaleWord &s, int ref, bool is_v) {
             uint32_t m = 0;
@@ -544,18 +611,25 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
             return m;
         };
         bool ok = true;
-        auto wait_free = [&](int use) {  // of the ring, counted through
-            if (use >= L::kSlots)
-                ok = mbar_wait_abortable(&sh.ring_free[use % L::kSlots], (use / L::kSlots - 1) & 1, wait_limit, abort);
+        auto ready = [&](int unit) {  // its codes are there, and its slot of the ring is free
+            ok = mbar_wait_prompt(&sh.code_full[unit % L::kCodeSlots], (unit / L::kCodeSlots) & 1, wait_limit, abort) &&
+                 (unit < L::kSlots || mbar_wait_prompt(&sh.ring_free[unit % L::kSlots], (unit / L::kSlots - 1) & 1,
+                                                          wait_limit, abort));
             ok = __all_sync(0xFFFFFFFFu, ok);
             return ok;
         };
-        if (steps > 0) {
-            find(j0);
-            fetch(a.cache.k_codes, a.cache.k_scales, kc, ks);
-            fetch(a.cache.v_codes, a.cache.v_scales, vc, vs);
-        }
         for (int i = 0; i < steps; ++i) {
+            if (!ready(2 * i)) break;
+            const int mi = i % L::kMeta, left = keys - (kManyKeys * (j0 + i) + 32 * w);
+            const uint32_t valid = sh.valid[mi] >> (2 * w);
+            uint32_t exists = (valid & 1 ? 0xFFFFu : 0u) | (valid & 2 ? 0xFFFF0000u : 0u);
+            if (left < 32) exists &= left > 0 ? (1u << left) - 1 : 0u;
+            uint32_t ks = 0, vs = 0;
+            if (exists >> lane & 1) {
+                const uint32_t from = base + L::off_scales + i % 2 * 1024 + 4 * (32 * w + lane);
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ks) : "r"(from) : "memory");
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vs) : "r"(from + 512) : "memory");
+            }
             const ScaleWord sk(ks, blocks), sv(vs, blocks);
             const int kref = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sk.top) - 134;
             const int vref = max((int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sv.top) - 134, kVrefMin);
@@ -564,31 +638,25 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
                 for (int b = 0; b < 4; ++b)
                     if (sv.b[b] == 255) atomicMin(&sh.nan_from[b], kManyKeys * (j0 + i) + 32 * w + lane);
             }
-            if (!wait_free(2 * i)) break;
             if (lane == 0) {
-                sh.kref[i % L::kMeta][w] = kref, sh.vref[i % L::kMeta][w] = vref;
-                mbar_arrive(&sh.meta_full[i % L::kMeta]);
+                sh.kref[mi][w] = kref, sh.vref[mi][w] = vref;
+                mbar_arrive(&sh.meta_full[mi]);
             }
-            put(kc, mults_of(sk, kref, false), base + L::off_ring + (2 * i % L::kSlots) * L::kSlab);
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0 && i != withhold) mbar_arrive(&sh.ring_full[2 * i % L::kSlots]);
-            const uint32_t vmults = mults_of(sv, vref, true);
-            if (i + 1 < steps) {
-                find(j0 + i + 1);
-                fetch(a.cache.k_codes, a.cache.k_scales, kc, ks);
+            const uint32_t mults[2] = {mults_of(sk, kref, false), mults_of(sv, vref, true)};
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                if (v && !ready(2 * i + 1)) break;
+                put(2 * i + v, v ? mults[1] : mults[0], exists);
             }
-            if (!wait_free(2 * i + 1)) break;
-            put(vc, vmults, base + L::off_ring + ((2 * i + 1) % L::kSlots) * L::kSlab);
-            fence_async_proxy();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.ring_full[(2 * i + 1) % L::kSlots]);
-            if (i + 1 < steps) fetch(a.cache.v_codes, a.cache.v_scales, vc, vs);
+            if (!ok) break;
         }
         if (!ok) give_up();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.dequant_done);
+        meet();
+        leave();
     } else {
+        if (warp == L::kIssueWarp) {
         // ---- issue ----
         const bool leader = elect_lane();
         constexpr uint32_t kIdS = f16_idesc(kManyKeys, false), kIdO = f16_idesc(kDP, true);
@@ -599,33 +667,34 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
             return ok;
         };
         auto scores = [&](int t, int i) {  // S of tile t and the CTA's keys i
-            const uint32_t k_at = base + L::off_ring + (2 * i % L::kSlots) * L::kSlab;
+            const uint64_t qd = k_major_desc(base + t * kNP * L::kSlab);
+            const uint64_t kd = k_major_desc(base + L::off_ring + 2 * i % L::kSlots * L::kSlab);
+            const bool last = t == 1 || cnt[1] <= i;  // no other tile wants K
+            uint64_t *k_free = &sh.ring_free[2 * i % L::kSlots];
             if (leader) {
 #pragma unroll
-                for (int p = 0; p < kNP; ++p) {
-                    const uint64_t qd = k_major_desc(base + (t * kNP + p) * L::kSlab), kd = k_major_desc(k_at);
-#pragma unroll
-                    for (int k = 0; k < kDP / 16; ++k) {
-                        const uint32_t at = (k / 4) * (kHalf >> 4) + 2 * (k % 4);
-                        mma_ss(tmem + L::col_s(t), qd + at, kd + at, kIdS, (p | k) != 0);
-                    }
+                for (int k = 0; k < kNP * kDP / 16; ++k) {
+                    const int in = k % (kDP / 16);
+                    const uint32_t at = in / 4 * (kHalf >> 4) + 2 * (in % 4);
+                    mma_ss(tmem + L::col_s(t), qd + (k >= kDP / 16 ? L::kSlab >> 4 : 0) + at, kd + at, kIdS, k != 0);
                 }
                 tc_commit(&sh.s_full[t]);
-                if (t == 1 || cnt[1] <= i) tc_commit(&sh.ring_free[2 * i % L::kSlots]);  // no other tile wants K
+                if (last) tc_commit(k_free);
             }
             __syncwarp();
         };
         auto outputs = [&](int t, int i) {
-            const uint32_t v_at = base + L::off_ring + ((2 * i + 1) % L::kSlots) * L::kSlab;
+            const uint64_t vd = n_major_desc(base + L::off_ring + (2 * i + 1) % L::kSlots * L::kSlab, kHalf);
+            const bool last = t == 1 || cnt[1] <= i;
+            uint64_t *v_free = &sh.ring_free[(2 * i + 1) % L::kSlots];
             if (leader) {
-                const uint64_t vd = n_major_desc(v_at, kHalf);
 #pragma unroll
-                for (int p = 0; p < kNP; ++p)
-#pragma unroll
-                    for (int k = 0; k < kManyKeys / 16; ++k)
-                        mma_ts(tmem + L::col_o(t), tmem + (p ? L::kColLow : L::col_s(t)) + 8 * k, vd + (2048 >> 4) * k,
-                               kIdO, (i | p | k) != 0);
-                if (t == 1 || cnt[1] <= i) tc_commit(&sh.ring_free[(2 * i + 1) % L::kSlots]);
+                for (int k = 0; k < kNP * kManyKeys / 16; ++k) {
+                    const int in = k % (kManyKeys / 16);
+                    const uint32_t p_col = k >= kManyKeys / 16 ? L::kColLow + 8 * in : L::col_s(t) + L::col_p(in);
+                    mma_ts(tmem + L::col_o(t), tmem + p_col, vd + (2048 >> 4) * in, kIdO, (i | k) != 0);
+                }
+                if (last) tc_commit(v_free);
             }
             __syncwarp();
         };
@@ -657,62 +726,75 @@ __global__ void __launch_bounds__(ManyLayout<kDP, kTiles, kNP>::kThreads, 1)
         __syncwarp();
         if (!mbar_wait_bounded(&sh.done, 0, wait_limit)) outlast_copies();
         __syncwarp();
-    }
-
-    __syncthreads();
-    const bool failed = *abort != 0;
-    if (S > 1) cluster_sync_all();
-    if (!failed) {
-        const float *o = reinterpret_cast<const float *>(raw + (base - smem_addr(raw)));
-        const uint32_t m_at = smem_addr(sh.m), l_at = smem_addr(sh.l), n_at = smem_addr(sh.nan_from);
-        for (int i = rank * L::kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += S * L::kThreads) {
-            const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
-            if (d >= D) continue;
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float ls = 0.f;
-            int nan_from;
-            if (S == 1) {
-                sum = *reinterpret_cast<const float4 *>(o + r * L::kPitch + d);
-                ls = sh.l[r], nan_from = sh.nan_from[d / kMxBlock];
-            } else {
-                float m = -INFINITY;
-                nan_from = kNever;
-                for (int s = 0; s < S; ++s) {
-                    m = fmaxf(m, ld_cluster_f32(map_to_rank(m_at + 4 * r, s)));
-                    nan_from = min(nan_from, __float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * (d / kMxBlock), s))));
-                }
-                for (int s = 0; s < S; ++s) {
-                    const float mi = ld_cluster_f32(map_to_rank(m_at + 4 * r, s));
-                    const float li = ld_cluster_f32(map_to_rank(l_at + 4 * r, s));
-                    const float4 v = ld_cluster_v4(map_to_rank(base + 4 * (r * L::kPitch + d), s));
-                    const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
-                    ls += mi == -INFINITY ? li : by * li;
-                    sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
-                    sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
-                }
-            }
-            const int row = tile.first + r;
-            if (nan_from < keys_of(tile, row, group, a.causal)) ls = __int_as_float(0x7FC00000);
-            const long long at = (long long)(tile.start + row / group) * a.y_token +
-                                 (long long)(head * group + row % group) * a.y_head + d;
-            // A row that sees nothing has no sum: zeros.
-            const float by = ls == 0.f ? 0.f : 1.f / ls;
-            store4(a.y, a.type, at, vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
-        }
-    }
-    if (S > 1)
-        cluster_sync_all();  // no CTA leaves while another reads its sums
-    else
-        __syncthreads();
-    if (warp == L::kWarps - 1) {
+        meet();
+        leave();
+        if (*abort != 0) outlast_copies();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        return;
+        }
+        if (warp == L::kCopyWarp) {
+        // ---- copy ----
+        // Lane g + 8 · kind has the tile's tokens 16 g ..: kind 0 codes of K,
+        // 1 and 2 scales of K and V, 3 codes of V.
+        const int kind = lane / 8, g16 = lane % 8, row_bytes = D * kBits / 8, per_page = a.cache.page / 16;
+        int piece = (8 * j0 + g16) / per_page, within = (8 * j0 + g16) % per_page;
+        const uint8_t *from = kind == 0 ? a.cache.k_codes : kind == 1 ? a.cache.k_scales : kind == 2 ? a.cache.v_scales
+                                                                                           : a.cache.v_codes;
+        const int token_bytes = kind == 1 || kind == 2 ? 4 : row_bytes;
+        const uint32_t bytes = 16 * token_bytes;
+        auto next_page = [&](int i) {
+            return i < steps && kManyKeys * (j0 + i) + 16 * g16 < keys ? page_of(a.batch, a.cache, tile.seq, piece, a.status)
+                                                                       : -1;
+        };
+        int page = next_page(0), unit = 0;
+        bool ok = true;
+        auto slot_free = [&](int u) {
+            if (u >= L::kCodeSlots)
+                ok = mbar_wait_prompt(&sh.code_free[u % L::kCodeSlots], (u / L::kCodeSlots - 1) & 1, wait_limit, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            return ok;
+        };
+        for (int i = 0; i < steps; ++i) {
+            const uint8_t *at = from + (first_slot(a.cache, page, head) + 16 * within) * token_bytes;
+            const bool mine = page >= 0;
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine) & 0xFF;
+            const int groups = __popc(valid);
+            within += 8 % per_page, piece += 8 / per_page;
+            if (within >= per_page) within -= per_page, ++piece;
+            page = next_page(i + 1);
+            for (int v = 0; v < 2; ++v, ++unit) {
+                if (!slot_free(unit)) break;
+                uint64_t *full = &sh.code_full[unit % L::kCodeSlots];
+                if (lane == 0) {
+                    sh.valid[i % L::kMeta] = valid;
+                    if (i != withhold) mbar_arrive_expect_tx(full, groups * 16 * (row_bytes + (v ? 0 : 8)));
+                }
+                __syncwarp();
+                if (mine && i != withhold && (v ? kind == 3 : kind < 3)) {
+                    const uint32_t to = kind == 1 || kind == 2
+                                            ? base + L::off_scales + i % 2 * 1024 + (kind - 1) * 512 + 64 * g16
+                                            : base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 16 * g16 * row_bytes;
+                    bulk_copy(to, at, bytes, full);
+                }
+            }
+            if (!ok) break;
+        }
+        if (!ok) {
+            give_up();
+            // No copy may still be writing shared memory at exit.
+            outlast_copies();
+        }
+        __syncwarp();
+        }
+        meet();
+        leave();
     }
 }
 
 template <int kBits, int kDP, int kTiles, int kNP>
 cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
-    using L = ManyLayout<kDP, kTiles, kNP>;
+    using L = ManyLayout<kBits, kDP, kTiles, kNP>;
     auto kernel = mx_attention_many_kernel<kBits, kDP, kTiles, kNP>;
     cudaError_t e = ensure_smem(kernel, L::total);
     if (e != cudaSuccess) return e;

@@ -272,7 +272,7 @@ int check_cache(CacheCall &c, int tokens) {
     for (int i = 0; i < 7; ++i) {
         if (b.seqs == 0 && i >= 4) break;
         if (b.width == 0 && i == 6) break;
-        if ((rc = check_mx_ptr(c.spans[i], i == 0 || i == 2 ? 16 : 4))) return rc;
+        if ((rc = check_mx_ptr(c.spans[i], i < 4 ? 16 : 4))) return rc;
     }
     return Q4MM_OK;
 }

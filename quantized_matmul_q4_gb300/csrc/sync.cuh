@@ -93,6 +93,18 @@ __device__ __forceinline__ bool mbar_wait_abortable(uint64_t *bar, uint32_t pari
     }
 }
 
+// As mbar_wait_abortable, but without a suspend-time hint: a thread that is
+// suspended with one may be resumed only when that time is over.
+__device__ __forceinline__ bool mbar_wait_prompt(uint64_t *bar, uint32_t parity, long long limit_cycles,
+                                                 const volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort || clock64() - t0 > limit_cycles) return false;
+    }
+}
+
 // Non-blocking test of phase `parity` of `bar`.
 __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
