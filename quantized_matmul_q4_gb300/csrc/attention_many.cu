@@ -59,6 +59,9 @@ struct ManyLayout {
     static constexpr int kIssueWarp = kSoftmaxWarps + kDequantWarps, kCopyWarp = kIssueWarp + 1;
     static constexpr int kWarps = kIssueWarp + 4;
     static constexpr int kThreads = 32 * kWarps;
+    // 24 warps have 80 registers each; of an SM quarter's 6 x 80 the softmax
+    // takes 4 x 96, dequant 56, issue and copy 40.
+    static constexpr bool kSplitRegs = kTiles == 2;
     static constexpr uint32_t kSlab = kManyKeys * kDP * 2;             // 128 rows of Q, K or V
     static constexpr int kSlots = kDP == 64 ? 6 : 3;                   // of the ring of K and V
     static constexpr int kMeta = 4;                                    // tiles whose powers are kept
@@ -91,6 +94,7 @@ struct ManyShared {
     float top[2][2][256];        // a tile's maxima, of both halves
     int power[256];              // of two, taken out of a query row
     float m[256], l[2][256];
+    uint4 mults[2][128];         // of a tile's tokens of K and V: each block's multiplier as two fp16
     int nan_from[4];
     uint32_t tmem;
     int abort;
@@ -116,6 +120,30 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
+        : "memory");
+}
+// 64 columns, by two loads.
+__device__ __forceinline__ void tc_ld64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31 "
+        "}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, "
+        "%52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63 "
+        "}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]),
+          "=r"(a[15]), "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]),
+          "=r"(a[22]), "=r"(a[23]), "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]),
+          "=r"(a[29]), "=r"(a[30]), "=r"(a[31]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]),
+          "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]),
+          "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]), "=r"(b[18]), "=r"(b[19]),
+          "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]), "=r"(b[26]),
+          "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+        : "r"(taddr), "r"(taddr + 32)
         : "memory");
 }
 __device__ __forceinline__ void tc_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -305,6 +333,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
 
     if (warp < L::kSoftmaxWarps) {
         // ---- softmax ----
+        if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
         const int t = warp / 8, side = warp / 4 % 2, quarter = warp % 4;
         const int mine = 128 * t + 32 * quarter + lane;  // this thread's row of the CTA's
         {
@@ -379,29 +408,26 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             tc_fence_after();
             const int lim = sees - kManyKeys * (j0 + i) - 64 * side;  // these keys below it are seen
             const bool partial = __any_sync(0xFFFFFFFFu, lim < 64);
-            // (These loops stay loops, here and in the other warps: what the SM's
-            // warps run between two barriers has to stay in the instruction
-            // caches, or all of them wait for instructions.)
-            float top = -INFINITY;
-#pragma unroll 1
+            uint32_t x[2][32];
+            tc_ld64(s_at, x[0], x[1]);
+            float factor[2], top = -INFINITY;
+#pragma unroll
             for (int g = 0; g < 2; ++g) {
-                uint32_t x[32];
-                tc_ld32(s_at + 32 * g, x);
-                const float factor = c0 * pow2(power + sh.kref[mi][2 * side + g]);
+                factor[g] = c0 * pow2(power + sh.kref[mi][2 * side + g]);
                 float m = -INFINITY, m2 = -INFINITY;
                 if (partial) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (k < lim - 32 * g) m = fmaxf(m, __uint_as_float(x[k]));
+                        if (k < lim - 32 * g) m = fmaxf(m, __uint_as_float(x[g][k]));
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; k += 4) {
-                        m = max3(m, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                        m2 = max3(m2, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                        m = max3(m, __uint_as_float(x[g][k]), __uint_as_float(x[g][k + 1]));
+                        m2 = max3(m2, __uint_as_float(x[g][k + 2]), __uint_as_float(x[g][k + 3]));
                     }
                     m = fmaxf(m, m2);
                 }
-                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor, (float)sh.vref[mi][2 * side + g]));
+                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor[g], (float)sh.vref[mi][2 * side + g]));
             }
             // The other half's maximum (NaN: it gives up).  Both threads of a row
             // hold the same M.
@@ -425,29 +451,26 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 }
             }
             const float shift = (M == -INFINITY ? 0.f : M) - kPShift;
-#pragma unroll 1
+#pragma unroll
             for (int g = 0; g < 2; ++g) {
-                uint32_t x[32];
-                tc_ld32(s_at + 32 * g, x);
-                const float factor = c0 * pow2(power + sh.kref[mi][2 * side + g]);
                 const int vref = sh.vref[mi][2 * side + g];
-                const float2 f2 = make_float2(factor, factor);
+                const float2 f2 = make_float2(factor[g], factor[g]);
                 const float2 b2 = make_float2((float)vref - shift, (float)vref - shift);
                 float2 sum = make_float2(0.f, 0.f);
                 uint32_t p[16], low[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
-                    float2 e = ffma2(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), f2, b2);
-                    x[k] = __float_as_uint(ex2(e.x)), x[k + 1] = __float_as_uint(ex2(e.y));
+                    float2 e = ffma2(make_float2(__uint_as_float(x[g][k]), __uint_as_float(x[g][k + 1])), f2, b2);
+                    x[g][k] = __float_as_uint(ex2(e.x)), x[g][k + 1] = __float_as_uint(ex2(e.y));
                 }
                 if (partial) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (k >= lim - 32 * g) x[k] = 0u;
+                        if (k >= lim - 32 * g) x[g][k] = 0u;
                 }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
-                    const float2 e = make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    const float2 e = make_float2(__uint_as_float(x[g][k]), __uint_as_float(x[g][k + 1]));
                     sum = __fadd2_rn(sum, e);
                     p[k / 2] = half2_of(e.x, e.y);
                     if constexpr (kNP == 2) {
@@ -536,6 +559,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         leave();
     } else if (warp < L::kSoftmaxWarps + L::kDequantWarps) {
         // ---- dequant ----
+        if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         constexpr int kLanes = kDP * kBits / 128;   // of 16 bytes a token
         constexpr int kEach = 32 / kLanes;          // tokens a load
         constexpr int kVals = 128 / kBits;          // values of a lane: 16 or 32
@@ -546,69 +570,78 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         const int tok0 = (lane / kLanes) ^ (kDP == 64 ? 0 : kBits == 8 ? half : 2 * half);
         const bool in = c * kVals < D;
         const int blocks = D / kMxBlock, row_bytes = D * kBits / 8;
-        // A unit's codes (K of tile i: 2i, V: 2i + 1) to fp16 in its slot of
-        // the ring.  mults: of each lane's token, four bytes of exponents 33
-        // above those of its blocks' multipliers; exists: a bit a token.
-        auto put = [&](int unit, uint32_t mults, uint32_t exists) {
-            const uint32_t from = base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 32 * w * row_bytes + 16 * c;
-            const uint32_t to = base + L::off_ring + unit % L::kSlots * L::kSlab + half * kHalf;
+        // Where a lane's 16 bytes of token tok0 come from and go to; the next
+        // tokens are kEach on.  (The swizzle of a row and the one kEach on
+        // differ in bit 2 of the 16-byte chunk, or not at all.)
+        const int r0 = 32 * w + tok0;
+        const uint32_t from0 = base + L::off_codes + r0 * row_bytes + 16 * c;
+        const uint32_t to0 = base + L::off_ring + half * kHalf + r0 * 128 + ((chunk ^ (r0 & 7)) * 16);
+        const uint32_t mult0 = smem_addr(sh.mults) + r0 * 16 + block * 4;
+        constexpr uint32_t kFlip = kEach == 4 ? 64 : 0;
+        // A unit's codes (K of tile i: 2i, V: 2i + 1) to fp16 in its slot of the ring.
+        auto put = [&](int unit) {
+            uint32_t from = from0 + unit % L::kCodeSlots * L::kCodes, to = to0 + unit % L::kSlots * L::kSlab;
+            uint32_t mult_at = mult0 + unit % 2 * 2048;
 #pragma unroll 1
-            for (int i0 = 0; i0 < kLanes; i0 += 2) {
-                uint4 q[2];
+            for (int i = 0; i < kLanes; i += 2) {
+                uint32_t word[2][4], m[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tok = kEach * (i0 + i) + tok0;
-                    q[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && (exists >> tok & 1))
+                for (int j = 0; j < 2; ++j) {
+                    word[j][0] = word[j][1] = word[j][2] = word[j][3] = 0u;
+                    if (in)
                         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
-                                     : "r"(from + tok * row_bytes)
+                                     : "=r"(word[j][0]), "=r"(word[j][1]), "=r"(word[j][2]), "=r"(word[j][3])
+                                     : "r"(from + j * kEach * row_bytes)
                                      : "memory");
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(m[j]) : "r"(mult_at + j * kEach * 16) : "memory");
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tok = kEach * (i0 + i) + tok0, r = 32 * w + tok;
-                    const uint32_t e = __shfl_sync(0xFFFFFFFFu, mults, tok) >> (8 * block) & 0xFF;
-                    const float f = __int_as_float((e + 94) << 23);
-                    const uint32_t m = half2_of(f, f);
-                    const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-                    const uint32_t at = to + r * 128;
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t at = j ? (to + kEach * 128) ^ kFlip : to;
                     if constexpr (kBits == 8) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             at + ((chunk + k) ^ (r & 7)) * 16),
-                                         "r"(half2_mul(half_e4m3x2(word[2 * k]), m)),
-                                         "r"(half2_mul(half_e4m3x2_high(word[2 * k]), m)),
-                                         "r"(half2_mul(half_e4m3x2(word[2 * k + 1]), m)),
-                                         "r"(half2_mul(half_e4m3x2_high(word[2 * k + 1]), m))
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16 * k)),
+                                         "r"(half2_mul(half_e4m3x2(word[j][2 * k]), m[j])),
+                                         "r"(half2_mul(half_e4m3x2_high(word[j][2 * k]), m[j])),
+                                         "r"(half2_mul(half_e4m3x2(word[j][2 * k + 1]), m[j])),
+                                         "r"(half2_mul(half_e4m3x2_high(word[j][2 * k + 1]), m[j]))
                                          : "memory");
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             at + ((chunk + k) ^ (r & 7)) * 16),
-                                         "r"(half2_mul(half_e2m1x2<0>(word[k]), m)),
-                                         "r"(half2_mul(half_e2m1x2<1>(word[k]), m)),
-                                         "r"(half2_mul(half_e2m1x2<2>(word[k]), m)),
-                                         "r"(half2_mul(half_e2m1x2<3>(word[k]), m))
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (16 * k)),
+                                         "r"(half2_mul(half_e2m1x2<0>(word[j][k]), m[j])),
+                                         "r"(half2_mul(half_e2m1x2<1>(word[j][k]), m[j])),
+                                         "r"(half2_mul(half_e2m1x2<2>(word[j][k]), m[j])),
+                                         "r"(half2_mul(half_e2m1x2<3>(word[j][k]), m[j]))
                                          : "memory");
                     }
                 }
+                from += 2 * kEach * row_bytes, to += 2 * kEach * 128, mult_at += 2 * kEach * 16;
             }
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.code_free[unit % L::kCodeSlots]), mbar_arrive(&sh.ring_full[unit % L::kSlots]);
         };
-        auto mults_of = [&](const ScaleWord &s, int ref, bool is_v) {
-            uint32_t m = 0;
+        // This lane's token's multipliers, 2^(7 + exponent - ref): a NaN scale
+        // infinite for K, whose zero codes make it NaN, and zero for V.
+        auto put_mults = [&](const ScaleWord &s, int ref, bool is_v) {
+            uint32_t m[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                int e = max(s.b[i] - 127 - ref + 33, 0);
-                if (s.b[i] == 255) e = is_v ? 0 : 161;  // infinite: times a zero code NaN
-                m |= (uint32_t)e << (8 * i);
+                const int e = s.b[i] == 255 ? (is_v ? -127 : 128) : max(s.b[i] - 127 - ref, -127);
+                const float f = __int_as_float((e + 127) << 23);
+                m[i] = half2_of(f, f);
             }
-            return m;
+            sh.mults[is_v][32 * w + lane] = make_uint4(m[0], m[1], m[2], m[3]);
+        };
+        // Codes of tokens that do not exist are zeros.
+        auto clear = [&](int unit, uint32_t exists) {
+            if (exists >> lane & 1) return;
+            const uint32_t at = base + L::off_codes + unit % L::kCodeSlots * L::kCodes + (32 * w + lane) * row_bytes;
+            for (int i = 0; i < row_bytes; i += 16)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + i), "r"(0) : "memory");
         };
         bool ok = true;
         auto ready = [&](int unit) {  // its codes are there, and its slot of the ring is free
@@ -642,11 +675,13 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 sh.kref[mi][w] = kref, sh.vref[mi][w] = vref;
                 mbar_arrive(&sh.meta_full[mi]);
             }
-            const uint32_t mults[2] = {mults_of(sk, kref, false), mults_of(sv, vref, true)};
+            put_mults(sk, kref, false), put_mults(sv, vref, true);
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
                 if (v && !ready(2 * i + 1)) break;
-                put(2 * i + v, v ? mults[1] : mults[0], exists);
+                if (exists != 0xFFFFFFFFu) clear(2 * i + v, exists);
+                __syncwarp();
+                put(2 * i + v);
             }
             if (!ok) break;
         }
@@ -656,6 +691,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         meet();
         leave();
     } else {
+        if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == L::kIssueWarp) {
         // ---- issue ----
         const bool leader = elect_lane();
