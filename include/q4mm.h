@@ -39,6 +39,8 @@
 #ifndef Q4MM_H
 #define Q4MM_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -539,6 +541,10 @@ int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes
  *         fp32; probabilities rounded to 2^-12 (2^-22 where dtype is
  *         Q4MM_F32) of their value or 2^-30 of the row's largest.
  *         The same call gives the same bits again.
+ * workspace: device memory (16-byte aligned, overlapping nothing else) for the
+ *         call to write to, workspace_bytes long; NULL with 0 and any length
+ *         are accepted: with less than mx_attention_workspace says the call
+ *         may be slower.  Calls that may overlap in time need one each.
  * Limits: as mx_cache_write; heads a multiple of kvHeads; scale finite, >= 0.
  * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
  */
@@ -546,7 +552,16 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
                  const void *k_scales, const void *v_codes, const void *v_scales, int pages, int kvHeads,
                  int pageTokens, int headDim, int bits, const int *starts, const int *lengths, const int *table,
                  int sequences, int tableWidth, float scale, int causal, void *y, long long y_token_stride,
-                 long long y_head_stride, int tokens, int heads, q4mm_stream_t stream);
+                 long long y_head_stride, int tokens, int heads, void *workspace, size_t workspace_bytes,
+                 q4mm_stream_t stream);
+
+/*
+ * mx_attention_workspace — bytes of workspace with which mx_attention, on the
+ * current device, uses every SM for a call of these sizes: more than none where
+ * few rows meet a long cache.  0 also for sizes that mx_attention refuses.
+ */
+size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequences, int tableWidth, int tokens,
+                              int heads);
 
 /* Message for the last error returned on the calling thread ("" if none).
  * The pointer stays valid until the thread's next failing call. */

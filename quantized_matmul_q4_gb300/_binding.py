@@ -13,7 +13,7 @@ Q4K_BYTES = 144
 _SYMBOLS = ("q4k_matmul", "q4k_matmul_tc", "q4k_matmul_tc_noalloc", "q4k_relayout_tc", "q4k_matmul_tc_relayouted",
             "q4_0_gemv", "q6k_gemv", "q4k_ffn_swiglu", "ternary_gemv",
             "mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul",
-            "rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention",
+            "rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention", "mx_attention_workspace",
             "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait")
 
 
@@ -58,7 +58,9 @@ def _load() -> ctypes.CDLL:
     lib.rope_rotate.argtypes = [*heads, i32, vp, i32, vp, i32, i32, f32, *heads, i32, i32, i32, vp]
     lib.mx_cache_write.argtypes = [*heads, *heads, i32, vp, i32, i32, f32, *cache, *batch, i32, vp]
     lib.mx_cache_read.argtypes = [*cache, *batch, *heads, *heads, i32, i32, vp]
-    lib.mx_attention.argtypes = [*heads, i32, *cache, *batch, f32, i32, *heads, i32, i32, vp]
+    lib.mx_attention.argtypes = [*heads, i32, *cache, *batch, f32, i32, *heads, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.mx_attention_workspace.argtypes = [i32] * 7
+    lib.mx_attention_workspace.restype = ctypes.c_size_t
     for name in ("mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul", "rope_rotate",
                  "mx_cache_write", "mx_cache_read", "mx_attention"):
         getattr(lib, name).restype = i32
@@ -189,8 +191,9 @@ def mx_cache_read_ptr(cache, batch, k, v, dtype: int, tokens: int, stream: int =
 
 
 def mx_attention_ptr(q, dtype: int, cache, batch, scale: float, causal: int, y, tokens: int, heads: int,
-                     stream: int = 0) -> None:
-    _check(_LIB.mx_attention(*q, dtype, *cache, *batch, scale, causal, *y, tokens, heads, stream))
+                     workspace: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(_LIB.mx_attention(*q, dtype, *cache, *batch, scale, causal, *y, tokens, heads, workspace, workspace_bytes,
+                             stream))
 
 
 def arm_wait_failure(stage: int, limit_cycles: int) -> None:
@@ -904,10 +907,18 @@ def mx_attention(q, cache: MxCache, starts, lengths, pages, scale: float | None 
     else:
         _mx_device(device, out)
     oa = _heads_arg(out, "out", shape)
+    # Few rows over a long cache: sums of its parts meet in a workspace.  (The
+    # library has the rule; it is asked only where there may be one.)
+    ws, nbytes, kv = None, 0, ca[5]
+    if (T * (H // kv) // 8 + ba[3]) * kv < 64:
+        nbytes = _LIB.mx_attention_workspace(kv, ca[6], D, ba[3], ba[4], T, H)
+        if nbytes:
+            new = _Torch.empty if side is None else _empty_on(side)
+            ws = new((nbytes,), dtype=_Torch.uint8, device=q.device)
     if side is not None:
-        _hold(side, q, *cache[:4], starts, lengths, pages, out)
+        _hold(side, q, *cache[:4], starts, lengths, pages, out, ws)
     rc = _LIB.mx_attention(*qa, dtype, *ca, *ba, D ** -0.5 if scale is None else float(scale), 1 if causal else 0, *oa,
-                           T, H, at)
+                           T, H, 0 if ws is None else ws.data_ptr(), nbytes, at)
     if rc:
         _check(rc)
     return out

@@ -3,11 +3,10 @@
 //
 // Every byte of the cache is read once by the tile that needs it, so the
 // kernel is meant to be bound by HBM: 8-bit heads of 128 bring an SM some 23
-// values per clock, of which each costs 1.3 instructions here.  Codes go from
-// global memory straight into the fragments of mma.sync (m16n8k16, fp16 in,
-// fp32 out); a tensor instruction with its operands in shared memory would
-// have to pad 8 rows to 128.  With the tokens or head values on M and the rows
-// on N:
+// values per clock, of which each costs 0.8 instructions here.  A tensor-core
+// tile of 128 rows would be empty but for 8, so the products are mma.sync's
+// (m16n8k16, fp16 in, fp32 out), with the tokens or head values on M and the
+// rows on N:
 //
 //   Sᵀ[token][row] = K Qᵀ      16 tokens x 8 rows, 16 values of the head a step
 //   Oᵀ[value][row] = Vᵀ Pᵀ     16 values x 8 rows, 16 tokens a step
@@ -19,10 +18,13 @@
 // tokens at a time are interleaved by a byte permute and converted together.
 // Pᵀ's fragment is Sᵀ's transposed in 8 x 8 pieces by movmatrix.
 //
-// Warps take groups of 16 tokens in turn, the next group's codes on their way
-// while one is computed; each keeps a maximum, sum and accumulator of its own.
-// They are joined in shared memory, and the CTAs of a cluster, which share a
-// tile's keys, through distributed shared memory, in a fixed order.
+// Warps take groups of 16 tokens in turn (they lie in one page, a run each of
+// K and V), by asynchronous copies into stages of their own, some 150 KB an SM
+// under way; each keeps a maximum, sum and accumulator of its own.  They are
+// joined in shared memory, and the CTAs of a cluster, which share a tile's
+// keys, through distributed shared memory, in a fixed order.  Where even 16
+// CTAs a tile leave SMs idle, several clusters share it, and a second kernel
+// joins what they leave in the caller's workspace.
 #include <cstdint>
 
 #include "attention.cuh"
@@ -38,6 +40,7 @@ namespace q4mm {
 namespace {
 
 constexpr int kThreads = 32 * kFewWarps;
+constexpr int kJoinThreads = 128;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -54,23 +57,38 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return r;
 }
 
-// kWords words from p (kWords·4 bytes aligned, 16 at most).
+// 16 bytes (4) to shared memory, zeros where not `ok`, complete after cp_wait.
+__device__ __forceinline__ void cp_async16(uint32_t to, const uint8_t *from, bool ok) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t to, const uint8_t *from, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 template <int kWords>
-__device__ __forceinline__ void load_words(const uint8_t *p, bool ok, uint32_t (&w)[kWords]) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0;
-    if (!ok) return;
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[kWords]) {
     if constexpr (kWords >= 4) {
 #pragma unroll
-        for (int i = 0; i < kWords; i += 4) {
-            const uint4 v = ld_stream_u4(p + 4 * i);
-            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-        }
+        for (int i = 0; i < kWords; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + 4 * i)
+                         : "memory");
     } else if constexpr (kWords == 2) {
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
     } else {
-        w[0] = ld_stream_u32(p);
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
     }
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ float value_at(const void *p, MxType type, long long i) {
@@ -78,61 +96,139 @@ __device__ __forceinline__ float value_at(const void *p, MxType type, long long 
            : type == MxType::kF16 ? __half2float(static_cast<const __half *>(p)[i])
                                   : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
-__device__ __forceinline__ void store_at(void *p, MxType type, long long i, float v) {
-    if (type == MxType::kF32)
-        static_cast<float *>(p)[i] = v;
-    else if (type == MxType::kF16)
-        static_cast<__half *>(p)[i] = __float2half_rn(v);
-    else
-        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-}
+
+// Sums over parts of the keys, each under a maximum of its own.
+struct Joined {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    __device__ __forceinline__ void add(float mi, float m, float li, float4 v) {
+        // (A part without a maximum has zeros, or NaN where its scores are.)
+        const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
+        l += mi == -INFINITY ? li : by * li;
+        o.x = fmaf(by, v.x, o.x), o.y = fmaf(by, v.y, o.y), o.z = fmaf(by, v.z, o.z), o.w = fmaf(by, v.w, o.w);
+    }
+    // Four outputs from value d on; a row that sees nothing has no sum: zeros.
+    __device__ __forceinline__ void store(const MxAttentionArgs &a, const RowTile &tile, int row, int head, int group,
+                                          int d, bool nan) const {
+        const long long at = (long long)(tile.start + row / group) * a.y_token +
+                             (long long)(head * group + row % group) * a.y_head + d;
+        const float by = nan ? __int_as_float(0x7FC00000) : l == 0.f ? 0.f : 1.f / l;
+        store4(a.y, a.type, at, a.vec, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+    }
+};
 
 // kDP: the head's values rounded up to 64 or 128; kNR: row tiles of 8; kNP:
 // fp16 terms of a query value and a probability.
-template <int kDP, int kNR, int kNP>
+template <int kBits, int kDP, int kNR, int kNP>
 struct FewShared {
     static constexpr int kR = 8 * kNR;
-    static constexpr int kPitch = kDP + 8;  // halves of a staged query row
+    static constexpr int kPitch = kDP + 8;                   // halves of a staged query row
+    static constexpr int kRow = kDP * kBits / 8;             // bytes of a staged token
+    static constexpr int kStage = 32 * kRow + 128;           // K, V, and a scale word each
+    static constexpr int kStages = kRow == 128 ? 3 : kRow == 64 ? 5 : 8;
     union {
-        __half q[kNP][kR][kPitch];
+        uint8_t stage[kFewWarps][kStages][kStage];
         float o[kFewWarps][kR][kDP];  // each warp's sums; the CTA's in [0]
     };
+    __half q[kNP][kR][kPitch];
+    uint2 mults[kFewWarps][32];  // of a token's blocks, K's of 16 tokens and V's
     float m[kFewWarps][kR], l[kFewWarps][kR];
     float m_all[kR], l_all[kR];
-    int power[kR];   // of two, taken out of a query row
-    int nan_from[4]; // first position whose v has NaN in a block
+    int power[kR];    // of two, taken out of a query row
+    int nan_from[4];  // first position whose v has NaN in a block
 };
+
+// Sums of one part of a tile's keys in the workspace: `parts` of these a tile,
+// for each of its rows kDP outputs, then the maximum and the sum, and at the end nan_from.
+__host__ __device__ constexpr size_t few_part_floats(int rows, int dp) { return (size_t)rows * (dp + 2) + 4; }
 
 template <int kBits, int kDP, int kNR, int kNP>
 __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
-    mx_attention_few_kernel(const MxAttentionArgs a, const int group) {
-    using Shared = FewShared<kDP, kNR, kNP>;
-    constexpr int kR = Shared::kR;
-    constexpr int kSteps = kDP / 16;             // of 16 head values
+    mx_attention_few_kernel(const MxAttentionArgs a, const int group, const int parts) {
+    using Shared = FewShared<kBits, kDP, kNR, kNP>;
+    constexpr int kR = Shared::kR, kRow = Shared::kRow, kStages = Shared::kStages;
+    constexpr int kSteps = kDP / 16;                 // of 16 head values
     constexpr int kKRun = kDP / 4, kVRun = kDP / 8;  // neighbouring values of a lane
     constexpr int kKW = kKRun * kBits / 32, kVW = kVRun * kBits / 32;
+    constexpr int kLanes = kRow / 16, kEach = 32 / kLanes;  // 16-byte pieces of a token, tokens a copy
     extern __shared__ __align__(16) uint8_t raw[];
     Shared &sh = *reinterpret_cast<Shared *>(raw);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), g = lane >> 2, t = lane & 3;
     const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int D = a.cache.D, blocks = D / kMxBlock;
 
     pdl_wait();
-    const long long item = blockIdx.x / S;
+    long long item = blockIdx.x / S;
+    const int part = (int)(item % parts);
+    item /= parts;
     const int head = (int)(item % a.cache.heads);
     const RowTile tile = row_tile(a.batch, item / a.cache.heads, group, kR, a.tokens);
     if (tile.rows == 0) return;  // with the whole cluster
 
+    // Keys that any row sees, in groups, and this CTA's share of them.
+    int keys = keys_of(tile, tile.first + tile.rows - 1, group, a.causal);
+    const long long room = (long long)a.batch.width * a.cache.page;
+    if (keys > room) {
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusIndex);
+        keys = (int)room;
+    }
+    const int groups = (keys + kFewGroup - 1) / kFewGroup;
+    const int share = part * S + rank, shares = parts * S;
+    const int g0 = (int)((long long)groups * share / shares), g1 = (int)((long long)groups * (share + 1) / shares);
+
+    // The warp's groups, every kFewWarps-th: copies of the next ones under way.
+    const int per_page = a.cache.page / kFewGroup, row_bytes = D * kBits / 8;
+    int piece = (g0 + warp) / per_page, within = (g0 + warp) % per_page;  // page and group within it
+    int ahead = g0 + warp;                                                // the next group to copy
+    auto next_page = [&]() { return ahead < g1 ? page_of(a.batch, a.cache, tile.seq, piece, a.status) : -1; };
+    int page = next_page();
+    uint32_t bad = 0;  // a bit a stage: its group is in no page
+    // A token's 16-byte pieces are staged in an order that depends on the
+    // token, so that the fragments' loads meet in no bank (8 bits) or in two.
+    const int c = lane % kLanes, tok0 = lane / kLanes;
+    auto swizzle = [](int tok, int piece16) { return kRow == 128 ? piece16 ^ (tok & 7) : piece16 ^ (tok >> 1 & (kLanes - 1)); };
+    const uint32_t stages = smem_addr(sh.stage[warp]);
+    auto copy = [&](int at_stage) {
+        const uint32_t to = stages + at_stage * Shared::kStage;
+        const int left = page < 0 ? 0 : keys - kFewGroup * ahead;
+        const long long slot = page < 0 ? 0 : first_slot(a.cache, page, head) + kFewGroup * within;
+        const uint8_t *k = a.cache.k_codes + (slot + tok0) * row_bytes + 16 * c;
+        const uint8_t *v = a.cache.v_codes + (slot + tok0) * row_bytes + 16 * c;
+        const bool in = 16 * c < row_bytes;
+        if (ahead < g1) {
+#pragma unroll
+            for (int i = 0; i < 16; i += kEach) {
+                const int tok = tok0 + i;
+                if (kEach <= 16 || tok < 16) {
+                    const bool ok = in && tok < left;
+                    const uint32_t at = to + tok * kRow + 16 * swizzle(tok, c);
+                    cp_async16(at, ok ? k + i * row_bytes : a.cache.k_codes, ok);
+                    cp_async16(at + 16 * kRow, ok ? v + i * row_bytes : a.cache.v_codes, ok);
+                }
+            }
+            const bool ok = (lane & 15) < left;
+            const uint8_t *scales = lane < 16 ? a.cache.k_scales : a.cache.v_scales;
+            cp_async4(to + 32 * kRow + 4 * lane, ok ? scales + (slot + (lane & 15)) * 4 : scales, ok);
+            bad = (bad & ~(1u << at_stage)) | (page < 0 ? 1u << at_stage : 0u);
+        }
+        cp_commit();
+        ahead += kFewWarps, within += kFewWarps % per_page, piece += kFewWarps / per_page;
+        if (within >= per_page) within -= per_page, ++piece;
+        page = next_page();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) copy(i);
+
     // Query rows to fp16, each by a power of two of its own.
     for (int r = warp; r < kR; r += kFewWarps) {
-        constexpr int kEach = kDP / 32;
-        float v[kEach];
+        constexpr int kEachLane = kDP / 32;
+        float v[kEachLane];
         uint32_t top = 0;
         const int row = tile.first + r;
         const long long at = (long long)(tile.start + row / group) * a.q_token +
                              (long long)(head * group + row % group) * a.q_head;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < kEachLane; ++i) {
             const int d = lane + 32 * i;
             v[i] = r < tile.rows && d < D ? value_at(a.q, a.type, at + d) : 0.f;
             top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
@@ -142,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
         const float mult = __int_as_float((268 - e) << 23);
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
+        for (int i = 0; i < kEachLane; ++i) {
             const float x = v[i] * mult;
             const __half hi = __float2half_rn(x);
             sh.q[0][r][lane + 32 * i] = hi;
@@ -155,7 +251,6 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
 
     uint32_t qf[kNP][kNR][kSteps][2];
     int power[kNR][2], sees[kNR][2];  // of this lane's rows 2t and 2t + 1
-    int keys = 0;                     // that any row sees
 #pragma unroll
     for (int n = 0; n < kNR; ++n) {
 #pragma unroll
@@ -169,19 +264,9 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         for (int j = 0; j < 2; ++j) {
             const int r = 8 * n + 2 * t + j;
             power[n][j] = sh.power[r];
-            sees[n][j] = r < tile.rows ? keys_of(tile, tile.first + r, group, a.causal) : 0;
+            sees[n][j] = r < tile.rows ? min(keys_of(tile, tile.first + r, group, a.causal), keys) : 0;
         }
     }
-    keys = keys_of(tile, tile.first + tile.rows - 1, group, a.causal);
-    const long long room = (long long)a.batch.width * a.cache.page;
-    if (keys > room) {
-        if (threadIdx.x == 0) atomicOr(a.status, kStatusIndex);
-        keys = (int)room;
-    }
-    __syncthreads();  // the staged rows have been read: their memory is the sums'
-
-    const int groups = (keys + kFewGroup - 1) / kFewGroup;
-    const int g0 = (int)((long long)groups * rank / S), g1 = (int)((long long)groups * (rank + 1) / S);
     const float c0 = a.scale * kLog2e;
 
     float o[kNR][kSteps][4];
@@ -195,125 +280,121 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         M[n][0] = M[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
     }
 
-    // The warp's groups: codes of one on their way while another is used.
-    uint32_t kw[2][kKW], vw[4][kVW], sw = 0;
-    const int per_page = a.cache.page / kFewGroup, row_bytes = D * kBits / 8;
-    int piece = (g0 + warp) / per_page, within = (g0 + warp) % per_page;  // page and group within it
-    const bool k_in = t * kKRun < D, v_in = g * kVRun < D;
-    auto next_page = [&](int gi) { return gi < g1 ? page_of(a.batch, a.cache, tile.seq, piece, a.status) : -1; };
-    auto advance = [&]() {
-        within += kFewWarps % per_page, piece += kFewWarps / per_page;
-        if (within >= per_page) within -= per_page, ++piece;
-    };
-    int gi = g0 + warp;
-    int page = next_page(gi);
-    long long slot = first_slot(a.cache, page, head) + kFewGroup * within;
-    auto load_k = [&](int left) {  // tokens of the group that exist
+    // This lane's pieces of a stage.
+    uint32_t k_at[2], v_at[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            load_words<kKW>(a.cache.k_codes + (slot + g + 8 * i) * row_bytes + t * kKRun * kBits / 8,
-                            k_in && g + 8 * i < left, kw[i]);
-    };
-    auto load_v = [&](int left) {
+    for (int i = 0; i < 2; ++i) k_at[i] = (g + 8 * i) * kRow;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tok = 2 * t + (i & 1) + 8 * (i >> 1);
-            load_words<kVW>(a.cache.v_codes + (slot + tok) * row_bytes + g * kVRun * kBits / 8, v_in && tok < left,
-                            vw[i]);
-        }
-    };
-    // Scales: lane i < 16 has token i's word for k, lane 16 + i for v.
-    auto load_s = [&](int left) {
-        sw = 0;
-        if ((lane & 15) < left)
-            sw = ld_stream_u32((lane < 16 ? a.cache.k_scales : a.cache.v_scales) + (slot + (lane & 15)) * 4);
-    };
-    auto tokens_left = [&](int gi_, int page_) { return page_ < 0 || gi_ >= g1 ? 0 : keys - kFewGroup * gi_; };
-    int left = tokens_left(gi, page);
-    load_k(left), load_s(left), load_v(left);
+    for (int i = 0; i < 4; ++i) {
+        const int tok = 2 * t + (i & 1) + 8 * (i >> 1), byte = g * kVRun * kBits / 8;
+        v_at[i] = (16 + tok) * kRow + 16 * swizzle(tok, byte / 16) + byte % 16;
+    }
+    const uint32_t mults = smem_addr(sh.mults[warp]);
+    int at_stage = 0;
+    for (int gi = g0 + warp; gi < g1; gi += kFewWarps) {
+        cp_wait<kStages - 2>();
+        __syncwarp();
+        copy(at_stage == 0 ? kStages - 1 : at_stage - 1);  // into the stage used last
+        const uint32_t stage = stages + at_stage * Shared::kStage;
+        const int base = kFewGroup * gi, here = bad >> at_stage & 1 ? 0 : keys - base;
+        at_stage = at_stage == kStages - 1 ? 0 : at_stage + 1;
 
-    for (; gi < g1; gi += kFewWarps) {
-        const int here = left, base = kFewGroup * gi;
-        // This group's scales: of each token the power taken out, and four
-        // bytes of exponents 33 above those of its blocks' multipliers.
+        // The group's scales: the power taken out of K and V, and each token's
+        // multipliers 2^(7 + exponent - power).
+        uint32_t sw;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(stage + 32 * kRow + 4 * lane) : "memory");
         const ScaleWord s(sw, blocks);
         const bool is_v = lane >= 16;
-        int ref = s.top - 134;
-        if (is_v) ref = max(ref, kVrefMin);
-        uint32_t mults = 0;
+        const int ktop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? 0u : (unsigned)s.top);
+        const int vtop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? (unsigned)s.top : 0u);
+        const int kref = ktop - 134, vref = max(vtop - 134, kVrefMin);
+        {
+            const int ref = is_v ? vref : kref;
+            float f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            int e = max(s.b[i] - 127 - ref + 33, 0);
-            if (s.b[i] == 255) e = is_v ? 0 : 161;  // infinite: times a zero code NaN
-            mults |= (uint32_t)e << (8 * i);
-        }
-        if (__any_sync(0xFFFFFFFFu, is_v && s.nan)) {  // NaN in v reaches the rows that see it, and no others
+            for (int i = 0; i < 4; ++i) f[i] = __int_as_float(max(s.b[i] - ref, 0) << 23);
+            if (__any_sync(0xFFFFFFFFu, s.nan)) {
+                // NaN in v reaches the rows that see it, and no others; an
+                // infinite multiplier makes the zero codes of k NaN.
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (is_v && s.b[i] == 255) atomicMin(&sh.nan_from[i], base + (lane & 15));
+                for (int i = 0; i < 4; ++i)
+                    if (s.b[i] == 255) {
+                        f[i] = is_v ? 0.f : INFINITY;
+                        if (is_v) atomicMin(&sh.nan_from[i], base + (lane & 15));
+                    }
+            }
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(mults + 8 * lane), "r"(half2_of(f[0], f[1])),
+                         "r"(half2_of(f[2], f[3]))
+                         : "memory");
+            __syncwarp();
         }
-        auto mult_of = [&](int from, int block) {  // a multiplier in both halves
-            const uint32_t w = __shfl_sync(0xFFFFFFFFu, mults, from);
-            const float f = __int_as_float(((w >> (8 * block) & 0xFF) + 94) << 23);
-            return half2_of(f, f);
-        };
-        int kref[2], vref[2];
-        uint32_t km[2];
+        uint32_t km[2], vm[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            kref[i] = __shfl_sync(0xFFFFFFFFu, ref, g + 8 * i), vref[i] = __shfl_sync(0xFFFFFFFFu, ref, 16 + g + 8 * i);
-            km[i] = mult_of(g + 8 * i, t * kKRun / kMxBlock);
-        }
-        uint32_t vm[2];  // of tokens 2t and 2t + 1, and of those 8 on
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = mult_of(16 + 2 * t + 8 * i, g * kVRun / kMxBlock);
-            const uint32_t hi = mult_of(17 + 2 * t + 8 * i, g * kVRun / kMxBlock);
-            vm[i] = __byte_perm(lo, hi, 0x5410);
+            km[i] = lds_u16(mults + 8 * (g + 8 * i) + 2 * (t * kKRun / kMxBlock)) * 0x10001u;
+            const uint32_t lo = lds_u16(mults + 8 * (16 + 2 * t + 8 * i) + 2 * (g * kVRun / kMxBlock));
+            const uint32_t hi = lds_u16(mults + 8 * (17 + 2 * t + 8 * i) + 2 * (g * kVRun / kMxBlock));
+            vm[i] = lo | hi << 16;
         }
 
         float sc[kNR][4];
 #pragma unroll
         for (int n = 0; n < kNR; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-            uint32_t f[2][2];
+        {
+            uint32_t kw[2][kKW];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if constexpr (kBits == 8) {
-                    f[i][0] = half_e4m3x2(kw[i][k]), f[i][1] = half_e4m3x2_high(kw[i][k]);
-                } else if (k % 2 == 0) {
-                    f[i][0] = half_e2m1x2<0>(kw[i][k / 2]), f[i][1] = half_e2m1x2<1>(kw[i][k / 2]);
-                } else {
-                    f[i][0] = half_e2m1x2<2>(kw[i][k / 2]), f[i][1] = half_e2m1x2<3>(kw[i][k / 2]);
+                constexpr int kPieces = kKW >= 4 ? kKW / 4 : 1;
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    const int byte = t * kKRun * kBits / 8 + 16 * j;
+                    const uint32_t at = stage + k_at[i] + 16 * swizzle(g + 8 * i, byte / 16) + byte % 16;
+                    if constexpr (kKW >= 4) {
+                        uint32_t four[4];
+                        lds_words<4>(at, four);
+                        kw[i][4 * j] = four[0], kw[i][4 * j + 1] = four[1], kw[i][4 * j + 2] = four[2],
+                                  kw[i][4 * j + 3] = four[3];
+                    } else {
+                        lds_words<kKW>(at, kw[i]);
+                    }
                 }
-                f[i][0] = half2_mul(f[i][0], km[i]), f[i][1] = half2_mul(f[i][1], km[i]);
             }
 #pragma unroll
-            for (int n = 0; n < kNR; ++n)
+            for (int k = 0; k < kSteps; ++k) {
+                uint32_t f[2][2];
 #pragma unroll
-                for (int p = 0; p < kNP; ++p)
-                    mma_16816(sc[n], f[0][0], f[1][0], f[0][1], f[1][1], qf[p][n][k][0], qf[p][n][k][1]);
+                for (int i = 0; i < 2; ++i) {
+                    if constexpr (kBits == 8) {
+                        f[i][0] = half_e4m3x2(kw[i][k]), f[i][1] = half_e4m3x2_high(kw[i][k]);
+                    } else if (k % 2 == 0) {
+                        f[i][0] = half_e2m1x2<0>(kw[i][k / 2]), f[i][1] = half_e2m1x2<1>(kw[i][k / 2]);
+                    } else {
+                        f[i][0] = half_e2m1x2<2>(kw[i][k / 2]), f[i][1] = half_e2m1x2<3>(kw[i][k / 2]);
+                    }
+                    f[i][0] = half2_mul(f[i][0], km[i]), f[i][1] = half2_mul(f[i][1], km[i]);
+                }
+#pragma unroll
+                for (int n = 0; n < kNR; ++n)
+#pragma unroll
+                    for (int p = 0; p < kNP; ++p)
+                        mma_16816(sc[n], f[0][0], f[1][0], f[0][1], f[1][1], qf[p][n][k][0], qf[p][n][k][1]);
+            }
         }
-
-        // The next group: its page, then K and the scales; V once this one's is used.
-        advance();
-        page = next_page(gi + kFewWarps);
-        slot = first_slot(a.cache, page, head) + kFewGroup * within;
-        left = tokens_left(gi + kFewWarps, page);
-        load_k(left), load_s(left);
 
         float u[kNR][4];
         bool more = false;
+        const bool whole = here >= kFewGroup;
 #pragma unroll
-        for (int n = 0; n < kNR; ++n)
+        for (int n = 0; n < kNR; ++n) {
+            const float f0 = c0 * pow2(power[n][0] + kref), f1 = c0 * pow2(power[n][1] + kref);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int i = j >> 1, tok = g + 8 * i;
-                const float s2 = sc[n][j] * c0 * pow2(power[n][j & 1] + kref[i]) + (float)vref[i];
-                u[n][j] = tok < here && base + tok < sees[n][j & 1] ? s2 : -INFINITY;
+                const int tok = g + 8 * (j >> 1);
+                const float s2 = fmaf(sc[n][j], j & 1 ? f1 : f0, (float)vref);
+                u[n][j] = (whole || tok < here) && base + tok < sees[n][j & 1] ? s2 : -INFINITY;
                 more |= u[n][j] > M[n][j & 1] + kPSlack;
             }
+        }
         if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
             for (int n = 0; n < kNR; ++n)
@@ -330,15 +411,13 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
                 }
         }
         uint32_t pf[kNP][kNR][2];
+        const float unit = pow2(-vref);
 #pragma unroll
         for (int n = 0; n < kNR; ++n) {
             float p[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float m = M[n][j & 1];
-                p[j] = ex2(u[n][j] - ((m == -INFINITY ? 0.f : m) - kPShift));
-                l[n][j & 1] = fmaf(p[j], pow2(-vref[j >> 1]), l[n][j & 1]);
-            }
+            for (int j = 0; j < 4; ++j) p[j] = ex2(u[n][j] - ((M[n][j & 1] == -INFINITY ? 0.f : M[n][j & 1]) - kPShift));
+            l[n][0] = fmaf(p[0] + p[2], unit, l[n][0]), l[n][1] = fmaf(p[1] + p[3], unit, l[n][1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t hi = half2_of(p[2 * i], p[2 * i + 1]);
@@ -349,6 +428,9 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
                 }
             }
         }
+        uint32_t vw[4][kVW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_words<kVW>(stage + v_at[i], vw[i]);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
             uint32_t f[2][2];  // tokens' pair, value 2k or 2k + 1 of the lane's
@@ -374,8 +456,9 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
                 for (int p = 0; p < kNP; ++p)
                     mma_16816(o[n][k], f[0][0], f[0][1], f[1][0], f[1][1], pf[p][n][0], pf[p][n][1]);
         }
-        load_v(left);
     }
+    cp_wait<0>();
+    __syncthreads();  // the stages have been read: their memory is the sums'
 
     // Sums over a warp's tokens, then over the warps, then over the cluster.
 #pragma unroll
@@ -397,19 +480,12 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kFewWarps; ++w) m = fmaxf(m, sh.m[w][r]);
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float ls = 0.f;
+        Joined sum;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) {
-            const float by = sh.m[w][r] == -INFINITY ? 0.f : ex2(sh.m[w][r] - m);
-            const float4 v = *reinterpret_cast<const float4 *>(&sh.o[w][r][d]);
-            // (A warp without a maximum has zeros, or NaN where its scores are.)
-            ls += sh.m[w][r] == -INFINITY ? sh.l[w][r] : by * sh.l[w][r];
-            sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
-            sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
-        }
-        *reinterpret_cast<float4 *>(&sh.o[0][r][d]) = sum;
-        if (d == 0) sh.m_all[r] = m, sh.l_all[r] = ls;
+        for (int w = 0; w < kFewWarps; ++w)
+            sum.add(sh.m[w][r], m, sh.l[w][r], *reinterpret_cast<const float4 *>(&sh.o[w][r][d]));
+        *reinterpret_cast<float4 *>(&sh.o[0][r][d]) = sum.o;
+        if (d == 0) sh.m_all[r] = m, sh.l_all[r] = sum.l;
     }
     if (S > 1)
         cluster_sync_all();
@@ -417,6 +493,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         __syncthreads();
     const uint32_t o_at = smem_addr(sh.o), m_at = smem_addr(sh.m_all), l_at = smem_addr(sh.l_all),
                    n_at = smem_addr(sh.nan_from);
+    float *ws = parts > 1 ? a.workspace + (size_t)(blockIdx.x / S) * few_part_floats(kR, kDP) : nullptr;
     for (int i = rank * kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += S * kThreads) {
         const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
         if (d >= D) continue;
@@ -426,42 +503,68 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
             m = fmaxf(m, ld_cluster_f32(map_to_rank(m_at + 4 * r, s)));
             nan_from = min(nan_from, __float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * (d / kMxBlock), s))));
         }
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        float ls = 0.f;
-        for (int s = 0; s < S; ++s) {
-            const float mi = ld_cluster_f32(map_to_rank(m_at + 4 * r, s)), li = ld_cluster_f32(map_to_rank(l_at + 4 * r, s));
-            const float4 v = ld_cluster_v4(map_to_rank(o_at + 4 * (r * kDP + d), s));
-            const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
-            ls += mi == -INFINITY ? li : by * li;
-            sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
-            sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
+        Joined sum;
+        for (int s = 0; s < S; ++s)
+            sum.add(ld_cluster_f32(map_to_rank(m_at + 4 * r, s)), m, ld_cluster_f32(map_to_rank(l_at + 4 * r, s)),
+                    ld_cluster_v4(map_to_rank(o_at + 4 * (r * kDP + d), s)));
+        if (parts > 1) {
+            *reinterpret_cast<float4 *>(ws + r * kDP + d) = sum.o;
+            if (d == 0) ws[kR * kDP + r] = m, ws[kR * (kDP + 1) + r] = sum.l;
+            if (r == 0 && d % kMxBlock == 0) ws[kR * (kDP + 2) + d / kMxBlock] = __int_as_float(nan_from);
+        } else {
+            const int row = tile.first + r;
+            sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
         }
-        const int row = tile.first + r;
-        if (nan_from < keys_of(tile, row, group, a.causal)) ls = __int_as_float(0x7FC00000);
-        const long long at = (long long)(tile.start + row / group) * a.y_token +
-                             (long long)(head * group + row % group) * a.y_head + d;
-        // A row that sees nothing has no sum: zeros.
-        const float by = ls == 0.f ? 0.f : 1.f / ls;
-        store_at(a.y, a.type, at, sum.x * by), store_at(a.y, a.type, at + 1, sum.y * by);
-        store_at(a.y, a.type, at + 2, sum.z * by), store_at(a.y, a.type, at + 3, sum.w * by);
     }
     if (S > 1) cluster_sync_all();  // no CTA leaves while another reads its sums
+}
+
+// Joins the parts of a tile's keys that the clusters left in the workspace.
+template <int kDP, int kNR>
+__global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const MxAttentionArgs a, const int group,
+                                                                         const int parts) {
+    constexpr int kR = 8 * kNR;
+    pdl_wait();
+    const int head = (int)(blockIdx.x % a.cache.heads);
+    const RowTile tile = row_tile(a.batch, blockIdx.x / a.cache.heads, group, kR, a.tokens);
+    const float *ws = a.workspace + (size_t)blockIdx.x * parts * few_part_floats(kR, kDP);
+    for (int i = threadIdx.x; i < tile.rows * (kDP / 4); i += kJoinThreads) {
+        const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
+        if (d >= a.cache.D) continue;
+        float m = -INFINITY;
+        int nan_from = kNever;
+        for (int s = 0; s < parts; ++s) {
+            const float *w = ws + s * few_part_floats(kR, kDP);
+            m = fmaxf(m, w[kR * kDP + r]);
+            nan_from = min(nan_from, __float_as_int(w[kR * (kDP + 2) + d / kMxBlock]));
+        }
+        Joined sum;
+        for (int s = 0; s < parts; ++s) {
+            const float *w = ws + s * few_part_floats(kR, kDP);
+            sum.add(w[kR * kDP + r], m, w[kR * (kDP + 1) + r], *reinterpret_cast<const float4 *>(w + r * kDP + d));
+        }
+        const int row = tile.first + r;
+        sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
+    }
 }
 
 template <int kBits, int kDP, int kNR, int kNP>
 cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a) {
     auto kernel = mx_attention_few_kernel<kBits, kDP, kNR, kNP>;
-    constexpr size_t bytes = sizeof(FewShared<kDP, kNR, kNP>);
+    constexpr size_t bytes = sizeof(FewShared<kBits, kDP, kNR, kNP>);
     cudaError_t e = ensure_smem(kernel, bytes);
     if (e != cudaSuccess) return e;
     const int group = a.heads / a.cache.heads;
-    const long long tiles = (long long)a.tokens * group / (8 * kNR) + a.batch.seqs;
-    // (A table's width bounds the keys; their number is the device's to know.)
-    const long long keys = (long long)a.batch.width * a.cache.page;
-    const int S = few_split(tiles, a.cache.heads, (int)(keys < 0x7FFFFFFF ? keys : 0x7FFFFFFF), c.num_sms);
-    const long long ctas = tiles * a.cache.heads * S;
+    const long long tiles = few_tiles(a.tokens, group, kNR, a.batch.seqs);
+    FewSplit f = few_split(tiles, a.cache.heads, few_keys(a.batch.width, a.cache.page), c.num_sms);
+    // As many parts as the workspace holds.
+    const size_t part_bytes = tiles * a.cache.heads * few_part_floats(8 * kNR, kDP) * sizeof(float);
+    if ((size_t)f.parts > a.workspace_bytes / part_bytes) f.parts = (int)(a.workspace_bytes / part_bytes);
+    if (f.parts < 1 || !a.workspace) f.parts = 1;
+    const long long ctas = tiles * a.cache.heads * f.parts * f.cluster;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    if (S > 8 && (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    if (f.cluster > 8 &&
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -470,26 +573,35 @@ cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a) {
     cfg.stream = c.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.x = f.cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, group);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, group, f.parts);
+    if (e != cudaSuccess || f.parts == 1) return e;
+    return launch_kernel(c, mx_attention_join_kernel<kDP, kNR>, dim3((unsigned)(tiles * a.cache.heads)), dim3(kJoinThreads),
+                         0, a, group, f.parts);
 }
 
 template <int kBits, int kDP>
 cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a) {
-    const long long rows = (long long)a.tokens * (a.heads / a.cache.heads);
-    const bool wide = rows > 8LL * a.batch.seqs;  // more than 8 rows a sequence and kv head
+    const bool wide = few_row_tiles(a.tokens, a.heads / a.cache.heads, a.batch.seqs) == 2;
     if (a.type == MxType::kF32)
         return wide ? launch_few<kBits, kDP, 2, 2>(c, a) : launch_few<kBits, kDP, 1, 2>(c, a);
     return wide ? launch_few<kBits, kDP, 2, 1>(c, a) : launch_few<kBits, kDP, 1, 1>(c, a);
 }
 
 }  // namespace
+
+size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, int width, int page, int num_sms) {
+    const int nr = few_row_tiles(tokens, heads / kv_heads, seqs);
+    const long long tiles = few_tiles(tokens, heads / kv_heads, nr, seqs);
+    const FewSplit f = few_split(tiles, kv_heads, few_keys(width, page), num_sms);
+    return f.parts == 1 ? 0 : tiles * kv_heads * f.parts * few_part_floats(8 * nr, D <= 64 ? 64 : 128) * sizeof(float);
+}
 
 cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a) {
     const bool narrow = a.cache.D <= 64;

@@ -8,14 +8,35 @@ constexpr int kFewWarps = 8;      // warps of a CTA for few rows
 constexpr int kFewGroup = 16;     // tokens a warp takes at once
 constexpr int kFewMaxSplit = 16;  // CTAs that share a row tile's keys (a cluster)
 
-// CTAs of a cluster over the keys of one row tile: a power of two that gives
-// the SMs two CTAs each, unless a warp would have less than two groups.
-inline int few_split(long long tiles, int kv_heads, int keys, int num_sms) {
-    const long long ctas = tiles * kv_heads;
-    const int groups = (keys + kFewGroup - 1) / kFewGroup;
+// Row tiles of 8 that a CTA takes: two where a sequence and kv head have more than 8 rows on average.
+inline int few_row_tiles(long long tokens, int group, int seqs) { return tokens * group > 8LL * seqs ? 2 : 1; }
+
+// Tiles of 8 · nr rows, at most (see row_tile).
+inline long long few_tiles(long long tokens, int group, int nr, int seqs) { return tokens * group / (8 * nr) + seqs; }
+
+// Keys of a sequence, at most: what its table has room for (their number is the device's to know).
+inline int few_keys(int width, int page) {
+    const long long keys = (long long)width * page;
+    return keys < 0x7FFFFFFF ? (int)keys : 0x7FFFFFFF;
+}
+
+// How a tile's keys are shared: `parts` clusters of `cluster` CTAs.
+struct FewSplit {
+    int cluster, parts;
+};
+
+// Enough to give the SMs two CTAs each, unless a warp would have less than
+// kFewLeast groups; beyond a cluster's 16, parts joined by a second kernel.
+constexpr int kFewLeast = 2;
+inline FewSplit few_split(long long tiles, int kv_heads, int keys, int num_sms) {
+    const long long ctas = tiles * kv_heads, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
+    long long want = 2LL * num_sms / (ctas > 0 ? ctas : 1);
+    const long long most = groups / (kFewLeast * kFewWarps);
+    if (want > most) want = most;
     int s = 1;
-    while (s < kFewMaxSplit && ctas * s < 2LL * num_sms && groups >= 4 * s * kFewWarps) s *= 2;
-    return s;
+    while (s < kFewMaxSplit && 2 * s <= want) s *= 2;
+    const int parts = s == kFewMaxSplit ? (int)(want / s) : 1;
+    return FewSplit{s, parts > 1 ? parts : 1};
 }
 
 constexpr int kManyKeys = 128;   // keys of a tile on tcgen05

@@ -248,8 +248,7 @@ __device__ __forceinline__ void load_row(const void *p, MxType type, long long a
 
 template <int kBits, int kDP, int kTiles, int kNP>
 __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads, 1)
-    mx_attention_many_kernel(const MxAttentionArgs a, const int group, const long long tiles, const bool vec,
-                             const long long wait_limit, const int withhold) {
+    mx_attention_many_kernel(const MxAttentionArgs a, const int group, const long long tiles, const long long wait_limit, const int withhold) {
     using L = ManyLayout<kBits, kDP, kTiles, kNP>;
     constexpr int kRows = 128 * kTiles;
     constexpr uint32_t kHalf = kManyKeys * 128;  // bytes of 64 values of 128 rows
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 if (128 * t + r < tile.rows) {
                     const long long at = (long long)(tile.start + row / group) * a.q_token +
                                          (long long)(head * group + row % group) * a.q_head;
-                    load_row<kEach>(a.q, a.type, at, d, D, vec, v);
+                    load_row<kEach>(a.q, a.type, at, d, D, a.vec, v);
                 } else {
 #pragma unroll
                     for (int k = 0; k < kEach; ++k) v[k] = 0.f;
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                                      (long long)(head * group + row % group) * a.y_head + d;
                 // A row that sees nothing has no sum: zeros.
                 const float by = ls == 0.f ? 0.f : 1.f / ls;
-                store4(a.y, a.type, at, vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+                store4(a.y, a.type, at, a.vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
             }
         }
         leave();
@@ -841,9 +840,6 @@ cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
                              c.num_sms);
     const long long ctas = tiles * a.cache.heads * S;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    const size_t size = a.type == MxType::kF32 ? 4 : 2;
-    const bool vec = reinterpret_cast<uintptr_t>(a.q) % (4 * size) == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * size) == 0 &&
-                     a.q_token % 4 == 0 && a.q_head % 4 == 0 && a.y_token % 4 == 0 && a.y_head % 4 == 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(L::kThreads);
@@ -858,7 +854,7 @@ cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = c.pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, group, tiles, vec, c.wait_limit, c.withhold);
+    return cudaLaunchKernelEx(&cfg, kernel, a, group, tiles, c.wait_limit, c.withhold);
 }
 
 template <int kBits, int kDP>

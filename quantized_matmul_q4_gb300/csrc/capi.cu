@@ -724,7 +724,8 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
                  const void *k_scales, const void *v_codes, const void *v_scales, int pages, int kvHeads,
                  int pageTokens, int headDim, int bits, const int *starts, const int *lengths, const int *table,
                  int sequences, int tableWidth, float scale, int causal, void *y, long long y_token_stride,
-                 long long y_head_stride, int tokens, int heads, q4mm_stream_t stream) {
+                 long long y_head_stride, int tokens, int heads, void *workspace, size_t workspace_bytes,
+                 q4mm_stream_t stream) {
     auto bytes = [](const void *p) { return const_cast<uint8_t *>(static_cast<const uint8_t *>(p)); };
     CacheCall call{q4mm::MxCacheView{bytes(k_codes), bytes(k_scales), bytes(v_codes), bytes(v_scales), pages, kvHeads,
                                      pageTokens, headDim, bits},
@@ -745,15 +746,35 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
     if ((rc = check_mx_ptr(qs, size)) || (rc = check_mx_ptr(ys, size)) || (rc = check_mx_alias(&ys, 1, &qs, 1)) ||
         (rc = check_mx_alias(&ys, 1, call.spans, 7)))
         return rc;
+    if (workspace_bytes) {
+        const Span ws{workspace, workspace_bytes, "workspace"};
+        if ((rc = check_mx_ptr(ws, 16)) || (rc = check_mx_alias(&ws, 1, call.spans, 7)) ||
+            (rc = check_mx_alias(&ws, 1, &qs, 1)) || (rc = check_mx_alias(&ws, 1, &ys, 1)))
+            return rc;
+    }
     q4mm::LaunchCtx ctx;
     const bool many = q4mm::many_rows(tokens, heads / kvHeads, sequences);
+    const bool vec = reinterpret_cast<uintptr_t>(q) % (4 * size) == 0 && reinterpret_cast<uintptr_t>(y) % (4 * size) == 0 &&
+                     q_token_stride % 4 == 0 && q_head_stride % 4 == 0 && y_token_stride % 4 == 0 &&
+                     y_head_stride % 4 == 0;
     if ((rc = device_ctx(stream, &ctx, many))) return rc;
     const q4mm::MxAttentionArgs a{call.cache, call.batch, q, q_token_stride, q_head_stride, y, y_token_stride,
                                   y_head_stride, scale, causal != 0, tokens, heads, static_cast<q4mm::MxType>(dtype),
-                                  ctx.status};
+                                  vec, static_cast<float *>(workspace), workspace_bytes, ctx.status};
     const cudaError_t e = many ? q4mm::launch_mx_attention_many(ctx, a) : q4mm::launch_mx_attention_few(ctx, a);
     if (e != cudaSuccess) return fail_cuda(e, "mx_attention launch");
     return Q4MM_OK;
+}
+
+size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequences, int tableWidth, int tokens,
+                              int heads) {
+    if (kvHeads <= 0 || heads <= 0 || heads % kvHeads || pageTokens <= 0 || sequences <= 0 || tableWidth < 0 || tokens <= 0)
+        return 0;
+    if (q4mm::many_rows(tokens, heads / kvHeads, sequences)) return 0;
+    q4mm::LaunchCtx ctx;
+    if (device_ctx(nullptr, &ctx, false)) return 0;
+    return q4mm::mx_attention_few_workspace(tokens, heads, kvHeads, headDim, sequences, tableWidth, pageTokens,
+                                            ctx.num_sms);
 }
 
 const char *q4mm_last_error(void) { return g_err; }

@@ -200,8 +200,13 @@ struct MxAttentionArgs {
     bool causal;
     int tokens, heads;
     MxType type;
+    bool vec;  // every four neighbouring values of q and y are aligned
+    float *workspace;
+    size_t workspace_bytes;
     int *status;
 };
+// Bytes of workspace with which the kernel for few rows uses every SM.
+size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, int width, int page, int num_sms);
 cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a);   // few rows a kv head
 cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a);  // tiles of 128, on tcgen05
 
