@@ -535,10 +535,10 @@ int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes
  * of v those rows' 32 values.
  * q, y: [tokens][heads][headDim] of type dtype, strided as for rope_rotate,
  * aligned to their elements, not overlapping each other or the cache.
- * Precision: keys and values exact (what lies 2^-31 below the largest scale of
- *         the 32 tokens around it counts as zero), queries exact to 2^-22 of a
+ * Precision: keys and values exact (a block whose scale is 2^-17 of its
+ *         token's and head's largest counts as zero), queries exact to 2^-22 of a
  *         row's largest value; scores, their maximum, sums and outputs in
- *         fp32; probabilities rounded to 2^-12 (2^-22 where dtype is
+ *         fp32; probabilities rounded to 2^-11 (2^-22 where dtype is
  *         Q4MM_F32) of their value or 2^-30 of the row's largest.
  *         The same call gives the same bits again.
  * workspace: device memory (16-byte aligned, overlapping nothing else) for the

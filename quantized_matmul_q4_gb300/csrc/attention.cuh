@@ -2,10 +2,11 @@
 // as floats, codes to fp16.
 //
 // Numbers.  Codes times scales are exact in fp16 once a power of two is taken
-// out: with `ref` the largest scale exponent of a token (or of a group of
-// tokens), k' = code · 2^(7 + e - ref) is at most 448 · 2^7 < 65504, and what
-// falls below fp16's smallest number is 2^-31 of the group's largest scale.  A
-// query row is scaled by the power of two that puts its largest value into
+// out: with `ref` the largest scale exponent of a group of tokens,
+// k' = code · 2^(7 + e - ref) is at most 448 · 2^7 < 65504.  Where the tokens
+// of a group differ by more than 2^kWide, each has a power of its own, so that
+// no token, seen or not, costs another its bits; blocks 2^-17 below the
+// largest of their token count as zero.  A query row is scaled by the power of two that puts its largest value into
 // [2^14, 2^15): bf16 and fp16 rows are then exact to 2^-39 of that value, fp32
 // rows are two fp16 numbers (22 bits).  The powers come back in the softmax, whose
 // scores, maxima, sums and probabilities are fp32:
@@ -16,7 +17,7 @@
 //   O = Σ p v',  l = Σ p · 2^-vref,  y = O / l
 //
 // M is kept while no u passes it by more than 8, so O is rarely rescaled.
-// Probabilities enter the second product in fp16: one rounding to 2^-12 where
+// Probabilities enter the second product in fp16: one rounding to 2^-11 where
 // y is 16 bits wide, two terms (2^-22) where it is fp32.
 #pragma once
 
@@ -32,6 +33,7 @@ constexpr float kLog2e = 1.44269504f;
 constexpr float kPShift = 6.f;      // log2 of p at u = M
 constexpr float kPSlack = 8.f;      // u may pass M by this
 constexpr int kVrefMin = -100;      // lowest power taken out of v (2^-vref stays a normal float)
+constexpr int kWide = 4;            // a group's tokens share a power while their largest scales are within 2^this
 constexpr int kNever = 0x7FFFFFFF;  // position of a NaN that there is not
 
 __device__ __forceinline__ float ex2(float x) {

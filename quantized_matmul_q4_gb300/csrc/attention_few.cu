@@ -57,11 +57,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     return r;
 }
 
-// 16 bytes (4) to shared memory, zeros where not `ok`, complete after cp_wait.
-__device__ __forceinline__ void cp_async16(uint32_t to, const uint8_t *from, bool ok) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+// 16 bytes (4) to shared memory, there after cp_wait; with _if zeros where not `ok`.
+__device__ __forceinline__ void cp_async16(uint32_t to, const uint8_t *from) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t to, const uint8_t *from, bool ok) {
+__device__ __forceinline__ void cp_async4(uint32_t to, const uint8_t *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async16_if(uint32_t to, const uint8_t *from, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_if(uint32_t to, const uint8_t *from, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(ok ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -194,21 +200,29 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         const long long slot = page < 0 ? 0 : first_slot(a.cache, page, head) + kFewGroup * within;
         const uint8_t *k = a.cache.k_codes + (slot + tok0) * row_bytes + 16 * c;
         const uint8_t *v = a.cache.v_codes + (slot + tok0) * row_bytes + 16 * c;
-        const bool in = 16 * c < row_bytes;
-        if (ahead < g1) {
+        if (left >= kFewGroup && row_bytes == kRow) {  // whole: nothing to leave out, offsets known
+            const uint32_t at = to + tok0 * kRow;
+#pragma unroll
+            for (int i = 0; i < 16; i += kEach) {
+                const uint32_t to_i = at + i * kRow + 16 * swizzle(tok0 + i, c);
+                cp_async16(to_i, k + i * kRow);
+                cp_async16(to_i + 16 * kRow, v + i * kRow);
+            }
+            cp_async4(to + 32 * kRow + 4 * lane, (lane < 16 ? a.cache.k_scales : a.cache.v_scales) + (slot + (lane & 15)) * 4);
+            bad &= ~(1u << at_stage);
+        } else if (ahead < g1) {
+            const bool in = 16 * c < row_bytes;
 #pragma unroll
             for (int i = 0; i < 16; i += kEach) {
                 const int tok = tok0 + i;
-                if (kEach <= 16 || tok < 16) {
-                    const bool ok = in && tok < left;
-                    const uint32_t at = to + tok * kRow + 16 * swizzle(tok, c);
-                    cp_async16(at, ok ? k + i * row_bytes : a.cache.k_codes, ok);
-                    cp_async16(at + 16 * kRow, ok ? v + i * row_bytes : a.cache.v_codes, ok);
-                }
+                const bool ok = in && tok < left;
+                const uint32_t at = to + tok * kRow + 16 * swizzle(tok, c);
+                cp_async16_if(at, ok ? k + i * row_bytes : a.cache.k_codes, ok);
+                cp_async16_if(at + 16 * kRow, ok ? v + i * row_bytes : a.cache.v_codes, ok);
             }
             const bool ok = (lane & 15) < left;
             const uint8_t *scales = lane < 16 ? a.cache.k_scales : a.cache.v_scales;
-            cp_async4(to + 32 * kRow + 4 * lane, ok ? scales + (slot + (lane & 15)) * 4 : scales, ok);
+            cp_async4_if(to + 32 * kRow + 4 * lane, ok ? scales + (slot + (lane & 15)) * 4 : scales, ok);
             bad = (bad & ~(1u << at_stage)) | (page < 0 ? 1u << at_stage : 0u);
         }
         cp_commit();
@@ -268,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         }
     }
     const float c0 = a.scale * kLog2e;
+    // Keys that every row of the tile sees; rows that do not exist do not matter.
+    const int all_see = min(keys_of(tile, tile.first, group, a.causal), keys);
 
     float o[kNR][kSteps][4];
     float M[kNR][2], l[kNR][2];
@@ -290,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         v_at[i] = (16 + tok) * kRow + 16 * swizzle(tok, byte / 16) + byte % 16;
     }
     const uint32_t mults = smem_addr(sh.mults[warp]);
+    const uint32_t block_mask = blocks == 4 ? 0xFFFFFFFFu : (1u << (8 * blocks)) - 1;
     int at_stage = 0;
     for (int gi = g0 + warp; gi < g1; gi += kFewWarps) {
         cp_wait<kStages - 2>();
@@ -303,29 +320,43 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         // multipliers 2^(7 + exponent - power).
         uint32_t sw;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(stage + 32 * kRow + 4 * lane) : "memory");
-        const ScaleWord s(sw, blocks);
+        sw &= block_mask;
+        const uint32_t pair = __vmaxu2(sw & 0x00FF00FFu, sw >> 8 & 0x00FF00FFu);
+        uint32_t top = max(pair & 0xFFFFu, pair >> 16);
         const bool is_v = lane >= 16;
-        const int ktop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? 0u : (unsigned)s.top);
-        const int vtop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? (unsigned)s.top : 0u);
-        const int kref = ktop - 134, vref = max(vtop - 134, kVrefMin);
-        {
-            const int ref = is_v ? vref : kref;
-            float f[4];
+        uint32_t any_nan = 0;  // a bit a block
+        if (__any_sync(0xFFFFFFFFu, top == 255)) {
+            // NaN in v reaches the rows that see it, and no others.
+            top = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __int_as_float(max(s.b[i] - ref, 0) << 23);
-            if (__any_sync(0xFFFFFFFFu, s.nan)) {
-                // NaN in v reaches the rows that see it, and no others; an
-                // infinite multiplier makes the zero codes of k NaN.
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = sw >> (8 * i) & 0xFF;
+                any_nan |= (e == 255) << i;
+                top = max(top, e == 255 ? 0u : e);
+                if (e == 255 && is_v) atomicMin(&sh.nan_from[i], base + (lane & 15));
+                if (e == 255) sw &= ~(0xFFu << (8 * i));
+            }
+        }
+        const int ktop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? 0u : top);
+        const int vtop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? top : 0u);
+        const int kref = ktop - 134, vref = max(vtop - 134, kVrefMin);
+        int ref = is_v ? vref : kref;
+        const bool wide = __any_sync(0xFFFFFFFFu, top != 0 && (int)top + kWide < (is_v ? vtop : ktop));
+        if (wide && top != 0) ref = is_v ? max((int)top - 134, kVrefMin) : (int)top - 134;
+        {
+            // fp16 exponent fields of two blocks at once: exponent - ref - 112,
+            // 22 for the largest, at least 0 (then the multiplier is zero).
+            const uint32_t up = (uint32_t)(512 - 112 - ref) * 0x10001u;
+            uint32_t m[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                m[i] = (__vmaxu2(__byte_perm(sw, 0, i ? 0x4342 : 0x4140) + up, 0x02000200u) - 0x02000200u) << 10;
+            if (any_nan) {  // zero for v; infinite for k, whose zero codes make it NaN
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (s.b[i] == 255) {
-                        f[i] = is_v ? 0.f : INFINITY;
-                        if (is_v) atomicMin(&sh.nan_from[i], base + (lane & 15));
-                    }
+                    if ((any_nan >> i & 1) && !is_v) m[i / 2] |= i % 2 ? 0x7C000000u : 0x7C00u;
             }
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(mults + 8 * lane), "r"(half2_of(f[0], f[1])),
-                         "r"(half2_of(f[2], f[3]))
-                         : "memory");
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(mults + 8 * lane), "r"(m[0]), "r"(m[1]) : "memory");
             __syncwarp();
         }
         uint32_t km[2], vm[2];
@@ -383,18 +414,40 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
 
         float u[kNR][4];
         bool more = false;
-        const bool whole = here >= kFewGroup;
+        float unit[2];  // 2^-vref of tokens g and g + 8
+        if (!wide) {
+            unit[0] = unit[1] = pow2(-vref);
 #pragma unroll
-        for (int n = 0; n < kNR; ++n) {
-            const float f0 = c0 * pow2(power[n][0] + kref), f1 = c0 * pow2(power[n][1] + kref);
+            for (int n = 0; n < kNR; ++n) {
+                const float f0 = c0 * pow2(power[n][0] + kref), f1 = c0 * pow2(power[n][1] + kref);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tok = g + 8 * (j >> 1);
-                const float s2 = fmaf(sc[n][j], j & 1 ? f1 : f0, (float)vref);
-                u[n][j] = (whole || tok < here) && base + tok < sees[n][j & 1] ? s2 : -INFINITY;
-                more |= u[n][j] > M[n][j & 1] + kPSlack;
+                for (int j = 0; j < 4; ++j) u[n][j] = fmaf(sc[n][j], j & 1 ? f1 : f0, (float)vref);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int kr = __shfl_sync(0xFFFFFFFFu, ref, g + 8 * i), vr = __shfl_sync(0xFFFFFFFFu, ref, 16 + g + 8 * i);
+                unit[i] = pow2(-vr);
+#pragma unroll
+                for (int n = 0; n < kNR; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        u[n][2 * i + j] = fmaf(sc[n][2 * i + j], c0 * pow2(power[n][j] + kr), (float)vr);
             }
         }
+        if (base + kFewGroup > all_see || here <= 0) {
+#pragma unroll
+            for (int n = 0; n < kNR; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = g + 8 * (j >> 1);
+                    if (tok >= here || base + tok >= sees[n][j & 1]) u[n][j] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < kNR; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) more |= u[n][j] > M[n][j & 1] + kPSlack;
         if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
             for (int n = 0; n < kNR; ++n)
@@ -411,13 +464,13 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
                 }
         }
         uint32_t pf[kNP][kNR][2];
-        const float unit = pow2(-vref);
 #pragma unroll
         for (int n = 0; n < kNR; ++n) {
             float p[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) p[j] = ex2(u[n][j] - ((M[n][j & 1] == -INFINITY ? 0.f : M[n][j & 1]) - kPShift));
-            l[n][0] = fmaf(p[0] + p[2], unit, l[n][0]), l[n][1] = fmaf(p[1] + p[3], unit, l[n][1]);
+            l[n][0] = fmaf(p[0], unit[0], fmaf(p[2], unit[1], l[n][0]));
+            l[n][1] = fmaf(p[1], unit[0], fmaf(p[3], unit[1], l[n][1]));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t hi = half2_of(p[2 * i], p[2 * i + 1]);

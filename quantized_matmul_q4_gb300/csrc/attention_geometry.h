@@ -6,7 +6,13 @@ namespace q4mm {
 
 constexpr int kFewWarps = 8;      // warps of a CTA for few rows
 constexpr int kFewGroup = 16;     // tokens a warp takes at once
-constexpr int kFewMaxSplit = 16;  // CTAs that share a row tile's keys (a cluster)
+#ifndef PROBE_MAX
+#define PROBE_MAX 8
+#define PROBE_PART 4
+#define PROBE_LEAST 2
+#endif
+constexpr int kFewMaxSplit = PROBE_MAX;  // CTAs of a cluster that share a row tile's keys
+constexpr int kFewPartSplit = PROBE_PART;  // and of each, where there are several clusters
 
 // Row tiles of 8 that a CTA takes: two where a sequence and kv head have more than 8 rows on average.
 inline int few_row_tiles(long long tokens, int group, int seqs) { return tokens * group > 8LL * seqs ? 2 : 1; }
@@ -27,15 +33,16 @@ struct FewSplit {
 
 // Enough to give the SMs two CTAs each, unless a warp would have less than
 // kFewLeast groups; beyond a cluster's 16, parts joined by a second kernel.
-constexpr int kFewLeast = 2;
+constexpr int kFewLeast = PROBE_LEAST;
 inline FewSplit few_split(long long tiles, int kv_heads, int keys, int num_sms) {
     const long long ctas = tiles * kv_heads, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
     long long want = 2LL * num_sms / (ctas > 0 ? ctas : 1);
     const long long most = groups / (kFewLeast * kFewWarps);
     if (want > most) want = most;
+    const int most_cta = want > kFewMaxSplit ? kFewPartSplit : kFewMaxSplit;
     int s = 1;
-    while (s < kFewMaxSplit && 2 * s <= want) s *= 2;
-    const int parts = s == kFewMaxSplit ? (int)(want / s) : 1;
+    while (s < most_cta && 2 * s <= want) s *= 2;
+    const int parts = want > kFewMaxSplit ? (int)(want / s) : 1;
     return FewSplit{s, parts > 1 ? parts : 1};
 }
 

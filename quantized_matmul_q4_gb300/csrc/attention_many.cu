@@ -74,6 +74,7 @@ struct ManyLayout {
     // The sums, where the operands were.
     static constexpr int kPitch = kDP + 4;
     static constexpr uint32_t total = off_end + 1024;  // the base is rounded up to 1024 bytes
+    static_assert(total + 15 * 1024 <= kSmShared - kCtaSharedExtra, "room for ManyShared");
     static_assert(kTiles * kNP == 2 && kTiles * 128 * kPitch * 4 <= off_codes, "");
     static_assert(kSmShared - total - kCtaSharedExtra < kHalfTmemShared, "takes all of tensor memory");
     // Powers of tile i + kMeta are written when S of tile i + kMeta - kSlots / 2 is done, after P of tile i.
@@ -89,7 +90,9 @@ struct ManyLayout {
 struct ManyShared {
     uint64_t ring_full[6], ring_free[6], code_full[4], code_free[4], meta_full[4], s_full[2], p_full[2], q_full, done,
         dequant_done;
-    int kref[4][4], vref[4][4];  // of a tile's 32-token groups
+    int kref[4][4], vref[4][4];  // powers of a tile's 32-token groups,
+    int wide[4][4];              // or whether each token has its own:
+    short krefs[4][128], vrefs[4][128];
     uint32_t valid[4];           // a tile's 16-token groups that were copied
     float top[2][2][256];        // a tile's maxima, of both halves
     int power[256];              // of two, taken out of a query row
@@ -99,6 +102,8 @@ struct ManyShared {
     uint32_t tmem;
     int abort;
 };
+
+static_assert(sizeof(ManyShared) <= 15 * 1024, "");
 
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -409,10 +414,17 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             const bool partial = __any_sync(0xFFFFFFFFu, lim < 64);
             uint32_t x[2][32];
             tc_ld64(s_at, x[0], x[1]);
-            float factor[2], top = -INFINITY;
+            float factor[2], vref[2], top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                factor[g] = c0 * pow2(power + sh.kref[mi][2 * side + g]);
+                factor[g] = c0 * pow2(power + sh.kref[mi][2 * side + g]), vref[g] = (float)sh.vref[mi][2 * side + g];
+                if (sh.wide[mi][2 * side + g]) {
+                    const short *kr = &sh.krefs[mi][64 * side + 32 * g], *vr = &sh.vrefs[mi][64 * side + 32 * g];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        x[g][k] = __float_as_uint(fmaf(__uint_as_float(x[g][k]), c0 * pow2(power + kr[k]), (float)vr[k]));
+                    factor[g] = 1.f, vref[g] = 0.f;
+                }
                 float m = -INFINITY, m2 = -INFINITY;
                 if (partial) {
 #pragma unroll
@@ -426,7 +438,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                     }
                     m = fmaxf(m, m2);
                 }
-                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor[g], (float)sh.vref[mi][2 * side + g]));
+                top = fmaxf(top, m == -INFINITY ? -INFINITY : fmaf(m, factor[g], vref[g]));
             }
             // The other half's maximum (NaN: it gives up).  Both threads of a row
             // hold the same M.
@@ -452,9 +464,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             const float shift = (M == -INFINITY ? 0.f : M) - kPShift;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int vref = sh.vref[mi][2 * side + g];
                 const float2 f2 = make_float2(factor[g], factor[g]);
-                const float2 b2 = make_float2((float)vref - shift, (float)vref - shift);
+                const float2 b2 = make_float2(vref[g] - shift, vref[g] - shift);
                 float2 sum = make_float2(0.f, 0.f);
                 uint32_t p[16], low[16];
 #pragma unroll
@@ -477,7 +488,13 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                         low[k / 2] = half2_of(e.x - b.x, e.y - b.y);
                     }
                 }
-                l = fmaf(sum.x + sum.y, pow2(-vref), l);
+                if (sh.wide[mi][2 * side + g]) {
+                    const short *vr = &sh.vrefs[mi][64 * side + 32 * g];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) l = fmaf(__uint_as_float(x[g][k]), pow2(-vr[k]), l);
+                } else {
+                    l = fmaf(sum.x + sum.y, pow2(-(int)vref[g]), l);
+                }
                 tc_st16(s_at + 16 * g, p);
                 if constexpr (kNP == 2) tc_st16(tmem + lanes + L::kColLow + 32 * side + 16 * g, low);
             }
@@ -670,11 +687,20 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 for (int b = 0; b < 4; ++b)
                     if (sv.b[b] == 255) atomicMin(&sh.nan_from[b], kManyKeys * (j0 + i) + 32 * w + lane);
             }
+            int rk = kref, rv = vref;
+            const bool wide = __any_sync(0xFFFFFFFFu, (sk.top != 0 && sk.top - 134 + kWide < kref) ||
+                                                          (sv.top != 0 && sv.top - 134 + kWide < vref));
+            if (wide) {
+                if (sk.top != 0) rk = sk.top - 134;
+                if (sv.top != 0) rv = max(sv.top - 134, kVrefMin);
+                sh.krefs[mi][32 * w + lane] = (short)rk, sh.vrefs[mi][32 * w + lane] = (short)rv;
+                __syncwarp();
+            }
             if (lane == 0) {
-                sh.kref[mi][w] = kref, sh.vref[mi][w] = vref;
+                sh.kref[mi][w] = kref, sh.vref[mi][w] = vref, sh.wide[mi][w] = wide;
                 mbar_arrive(&sh.meta_full[mi]);
             }
-            put_mults(sk, kref, false), put_mults(sv, vref, true);
+            put_mults(sk, rk, false), put_mults(sv, rv, true);
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
                 if (v && !ready(2 * i + 1)) break;

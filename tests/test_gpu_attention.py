@@ -391,6 +391,25 @@ def test_attention_of_wide_ranges(spread, n, dtype):
     _check(c, x, y, xv, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [7, 150])
+def test_attention_hidden_keys_have_no_part(n, dtype):
+    """Huge, tiny and infinite-scale keys and values at positions that a row does not see, in the same group of tokens
+    as those that it sees, leave its output as it is, to the rounding of other powers of two."""
+    q, torch = _q(), _torch()
+    c = Case(7, [n], [n + 20], 1, 128, 16, 8).fill()
+    x, xv = _dev(c.rng.normal(size=(n, 2, 128)), dtype)
+    for w in "kv":
+        for p in range(22, n + 20):         # all but the first rows' last keys
+            s = c.cache[w + "_scales"][c.table[0, p // 16], 0, p % 16]
+            s[:] = np.clip(s.astype(int) + int(c.rng.choice([-60, 0, 40, 100])), 0, 254)
+    y = q.mx_attention(x, c.device_cache(), *c.device_batch())
+    d = Case(7, [2], [22], 1, 128, 16, 8)
+    d.cache, d.table = c.cache, c.table
+    few, _ = _dev(xv[:2], dtype)
+    _check(d, few, y[:2], xv[:2], dtype)
+
+
 @pytest.mark.parametrize("n", [1, 3, 140])
 def test_attention_nan_stays_where_it_is_seen(n):
     """NaN blocks of k and v behind a row's last key, in other sequences' pages and in free ones do not reach it; seen
