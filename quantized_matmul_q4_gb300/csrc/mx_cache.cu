@@ -22,6 +22,7 @@
 // cosine (their next terms, x^11 / 11! and x^12 / 12!, are below 2^-29), so c
 // and s are within 2·2^-24.
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -55,14 +56,19 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
 __device__ __forceinline__ float2 cos_sin(uint64_t turn, float m) {
     const int32_t a = (int32_t)(turn >> 32);
     const int32_t q = (a >> 29) + 1 >> 1;                                        // nearest quarter
-    const float x = (float)(int32_t)((uint32_t)a - ((uint32_t)q << 30)) * 1.46291807926715968e-9f;  // 2π / 2^32
+    // The rest in radians as x + xl, both roundings on the way kept.
+    const int32_t r = (int32_t)((uint32_t)a - ((uint32_t)q << 30));
+    constexpr float kRad = 1.46291807926715968e-9f;                        // 2π / 2^32,
+    constexpr float kRadRest = (float)(1.46291807926715968105e-9 - (double)kRad);  // and what it lacks
+    const float hi = (float)r, lo = (float)(r - (int32_t)hi);
+    const float x = hi * kRad, xl = fmaf(hi, kRad, -x) + fmaf(hi, kRadRest, lo * kRad);
     const float z = x * x;
     float s = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
     s = fmaf(s, z, 8.33333333e-3f), s = fmaf(s, z, -1.66666667e-1f);
-    s = fmaf(x * z, s, x);
+    s = x + fmaf(x * z, s, xl);                                            // (xl's factor, cos x, is 0.7 at least)
     float c = fmaf(z, -2.75573192e-7f, 2.48015873e-5f);
     c = fmaf(c, z, -1.38888889e-3f), c = fmaf(c, z, 4.16666667e-2f), c = fmaf(c, z, -0.5f);
-    c = fmaf(c, z, 1.f);
+    c = 1.f + fmaf(c, z, -x * xl);
     float co = q & 1 ? s : c, si = q & 1 ? c : s;     // a quarter on: (c, s) -> (-s, c)
     if ((q & 3) == 1 || (q & 3) == 2) co = -co;
     if (q & 2) si = -si;
@@ -200,17 +206,53 @@ struct Turned8 {
     }
 };
 
-// How a warp's lanes share the heads of a CTA's tokens: item r is token
-// r % tokens (a power of two) of vector r / tokens, lanes of 8 values each.
+// How the lanes of a CTA's warps share the heads of its tokens (a power of
+// two): each lane stays with one token and takes every step-th vector, so
+// that its addresses advance by constants.
 struct Items {
-    int sub, subs, d;  // which of the warp's items this lane serves, how many it has, the lane's first value
-    __device__ __forceinline__ explicit Items(int lanes_log) {
-        const int lane = threadIdx.x & 31;
-        sub = lane >> lanes_log, subs = 32 >> lanes_log, d = 8 * (lane & ((1 << lanes_log) - 1));
+    int d;          // the lane's first value
+    int token;      // of the CTA's
+    int first, step;
+    __device__ __forceinline__ Items(int lanes_log, int tokens_log) {
+        const int lane = threadIdx.x & 31, subs = 32 >> lanes_log;
+        const int q = (blockIdx.y * kWarps + threadIdx.x / 32) * subs + (lane >> lanes_log);
+        d = 8 * (lane & ((1 << lanes_log) - 1));
+        token = q & ((1 << tokens_log) - 1), first = q >> tokens_log;
+        step = (gridDim.y * kWarps * subs) >> tokens_log;
     }
 };
 
-template <class T, bool kVec>
+// A lane's values d .. d + 7 of a head and, half a head on, its partners in
+// the rotation of split halves: both are turned by the same angles.
+template <class T>
+struct TurnedPairs {
+    Eight<T> u, v;
+    __device__ __forceinline__ void load(const T *head, int d, int half) {
+        u = fetch8(head + d), v = fetch8(head + d + half);
+    }
+    __device__ __forceinline__ void turn(const float *cos, const float *sin, int d, float (&a)[8], float (&b)[8]) const {
+        float x[8], y[8];
+        floats8(u, x), floats8(v, y);
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(cos + d + i);
+            const float4 s = *reinterpret_cast<const float4 *>(sin + d + i);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const float2 c2 = j ? make_float2(c.z, c.w) : make_float2(c.x, c.y);
+                const float2 s2 = j ? make_float2(s.z, s.w) : make_float2(s.x, s.y);
+                const float2 x2 = make_float2(x[i + j], x[i + j + 1]), y2 = make_float2(y[i + j], y[i + j + 1]);
+                const float2 ys = __fmul2_rn(y2, s2), xs = __fmul2_rn(x2, s2);
+                const float2 p = ffma2(x2, c2, make_float2(-ys.x, -ys.y)), q = ffma2(y2, c2, xs);
+                a[i + j] = p.x, a[i + j + 1] = p.y, b[i + j] = q.x, b[i + j + 1] = q.y;
+            }
+        }
+    }
+};
+
+// kForm: 2 for split halves of whole heads, a lane with both partners (lanes
+// for half a head); 1 for aligned heads; 0 for any.
+template <class T, int kForm>
 __global__ void __launch_bounds__(kThreads) rope_rotate_kernel(const RopeArgs a, const int lanes_log,
                                                                const int tokens_log) {
     constexpr int kU = 2;
@@ -223,31 +265,45 @@ __global__ void __launch_bounds__(kThreads) rope_rotate_kernel(const RopeArgs a,
                               : (long long)static_cast<const int *>(a.positions)[t0 + s];
     });
     __syncthreads();
-    const Items it(lanes_log);
-    const long long rows = (long long)a.heads << tokens_log;
-    const T *x = static_cast<const T *>(a.x);
-    T *out = static_cast<T *>(a.out);
-    const long long each = (long long)gridDim.y * kWarps * it.subs * kU;
-    for (long long r0 = ((long long)blockIdx.y * kWarps + threadIdx.x / 32) * it.subs * kU; r0 < rows; r0 += each) {
-        Turned8<kVec, T> v[kU];
+    const Items it(lanes_log, tokens_log);
+    const int s = it.token, span = kForm == 2 ? a.D / 2 : a.D;
+    const bool mine = s < tokens && it.d < span;
+    const T *x = static_cast<const T *>(a.x) + (t0 + s) * a.x_token + it.first * a.x_head;
+    T *out = static_cast<T *>(a.out) + (t0 + s) * a.out_token + it.first * a.out_head;
+    // (Out may be x: a head is read whole, by lanes of one warp, before any of it is written.)
+    for (int h = it.first; __any_sync(0xFFFFFFFFu, h < a.heads); h += kU * it.step) {
         bool ok[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long r = r0 + u * it.subs + it.sub, h = r >> tokens_log;
-            const int s = (int)(r & ((1 << tokens_log) - 1));
-            ok[u] = r < rows && s < tokens && it.d < a.D;
-            if (ok[u]) v[u].load(x + (t0 + s) * a.x_token + h * a.x_head, it.d, a.D, a.rope);
-        }
-        __syncwarp();  // out may be x: a head is read whole before any of it is written
+        for (int u = 0; u < kU; ++u) ok[u] = mine && h + u * it.step < a.heads;
+        if constexpr (kForm == 2) {
+            TurnedPairs<T> v[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (!ok[u]) continue;
-            const long long r = r0 + u * it.subs + it.sub, h = r >> tokens_log;
-            const int s = (int)(r & ((1 << tokens_log) - 1));
-            float f[8];
-            v[u].turn(table.cos[s], table.sin[s], it.d, a.rope, f);
-            put8<kVec>(out + (t0 + s) * a.out_token + h * a.out_head + it.d, a.D - it.d, f);
+            for (int u = 0; u < kU; ++u)
+                if (ok[u]) v[u].load(x + u * it.step * a.x_head, it.d, span);
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (!ok[u]) continue;
+                float f[8], g[8];
+                v[u].turn(table.cos[s], table.sin[s], it.d, f, g);
+                put8<true>(out + u * it.step * a.out_head + it.d, 8, f);
+                put8<true>(out + u * it.step * a.out_head + it.d + span, 8, g);
+            }
+        } else {
+            Turned8<kForm == 1, T> v[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (ok[u]) v[u].load(x + u * it.step * a.x_head, it.d, a.D, a.rope);
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (!ok[u]) continue;
+                float f[8];
+                v[u].turn(table.cos[s], table.sin[s], it.d, a.rope, f);
+                put8<kForm == 1>(out + u * it.step * a.out_head + it.d, a.D - it.d, f);
+            }
         }
+        x += kU * it.step * a.x_head, out += kU * it.step * a.out_head;
     }
 }
 
@@ -275,7 +331,21 @@ __device__ __forceinline__ void find_places(Places &p, const MxBatchView &b, con
     __syncthreads();
 }
 
-template <class T, bool kVec, int kBits>
+// Quantises eight values of a block of four lanes into a slot: codes at
+// `codes`, the block's scale byte (and the padding's zeros) at `scales`.
+template <int kBits>
+__device__ __forceinline__ void put_codes(const float (&f)[8], uint8_t *codes, uint8_t *scales, int d, int D, bool ok) {
+    const uint32_t amax = mx_block_amax(f);
+    const uint32_t b = mx_quantize8(f, amax, kBits, codes, d, ok ? D : 0);
+    if (ok && (d & 31) == 0) {
+        const int block = d / kMxBlock, blocks = D / kMxBlock;
+        scales[block] = (uint8_t)b;
+        for (int pad = block + blocks; pad < 4; pad += blocks) scales[pad] = 0;
+    }
+}
+
+// kForm as for rope_rotate, for the keys.
+template <class T, int kForm, int kBits>
 __global__ void __launch_bounds__(kThreads) mx_cache_write_kernel(const MxCacheIoArgs a, const RopeView rope,
                                                                   const int lanes_log, const int tokens_log) {
     constexpr int kU = 2;
@@ -289,49 +359,58 @@ __global__ void __launch_bounds__(kThreads) mx_cache_write_kernel(const MxCacheI
         fill_angles(table, rope, tokens, [&](int s) { return (long long)at.position[s]; });
         __syncthreads();
     }
-    const Items it(lanes_log);
-    const int D = a.cache.D, blocks = D / kMxBlock, H = a.cache.heads;
-    const long long rows = (long long)2 * H << tokens_log;
-    const long long each = (long long)gridDim.y * kWarps * it.subs * kU;
+    const int D = a.cache.D, H = a.cache.heads, row_bytes = D * kBits / 8;
+    auto heads = [&](const Items &it, const void *from, long long token, long long head, uint8_t *codes, uint8_t *scales,
+                     auto pairs, const RopeView &r) {
+        constexpr bool kPairs = decltype(pairs)::value;
+        const int s = it.token, span = kPairs ? D / 2 : D;
+        const bool mine = s < tokens && it.d < span && at.slot[s < tokens ? s : 0] >= 0;
+        const T *x = static_cast<const T *>(from) + (t0 + s) * token + it.first * head;
+        const long long slot = mine ? at.slot[s] + (long long)it.first * a.cache.page : 0;
+        const long long apart = (long long)it.step * a.cache.page;  // slots between the lane's heads
+        codes += slot * row_bytes, scales += slot * 4;
+        for (int h = it.first; __any_sync(0xFFFFFFFFu, h < H); h += kU * it.step) {
+            bool ok[kU];
+            std::conditional_t<kPairs, TurnedPairs<T>, Turned8<kForm != 0, T>> v[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                ok[u] = mine && h + u * it.step < H;
+                if (!ok[u]) continue;
+                if constexpr (kPairs)
+                    v[u].load(x + u * it.step * head, it.d, span);
+                else
+                    v[u].load(x + u * it.step * head, it.d, D, r);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = 0.f;
+                uint8_t *c = codes + u * apart * row_bytes, *b = scales + u * apart * 4;
+                if constexpr (kPairs) {
+                    float g[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = 0.f;
+                    if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, f, g);
+                    put_codes<kBits>(f, c, b, it.d, D, ok[u]);
+                    put_codes<kBits>(g, c, b, it.d + span, D, ok[u]);
+                } else {
+                    if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, r, f);
+                    put_codes<kBits>(f, c, b, it.d, D, ok[u]);
+                }
+            }
+            x += kU * it.step * head, codes += kU * apart * row_bytes, scales += kU * apart * 4;
+        }
+    };
     const RopeView still{nullptr, 0, false, 1.f};
-    for (long long r0 = ((long long)blockIdx.y * kWarps + threadIdx.x / 32) * it.subs * kU; r0 < rows; r0 += each) {
-        Turned8<kVec, T> v[kU];
-        bool ok[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long r = r0 + u * it.subs + it.sub;
-            const int s = (int)(r & ((1 << tokens_log) - 1)), hv = (int)(r >> tokens_log);
-            const bool is_v = hv >= H;
-            const int h = is_v ? hv - H : hv;
-            ok[u] = r < rows && s < tokens && it.d < D && at.slot[s < tokens ? s : 0] >= 0;
-            if (ok[u]) {
-                const T *head = static_cast<const T *>(is_v ? a.v : a.k) + (t0 + s) * (is_v ? a.v_token : a.k_token) +
-                                h * (is_v ? a.v_head : a.k_head);
-                v[u].load(head, it.d, D, is_v ? still : rope);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long r = r0 + u * it.subs + it.sub;
-            const int s = (int)(r & ((1 << tokens_log) - 1)), hv = (int)(r >> tokens_log);
-            const bool is_v = hv >= H;
-            const int h = is_v ? hv - H : hv;
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = 0.f;
-            if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, is_v ? still : rope, f);
-            const uint32_t amax = mx_block_amax(f);
-            const long long slot = ok[u] ? at.slot[s] + (long long)h * a.cache.page : 0;
-            uint8_t *codes = (is_v ? a.cache.v_codes : a.cache.k_codes) + slot * (D * kBits / 8);
-            const uint32_t b = mx_quantize8(f, amax, kBits, codes, it.d, ok[u] ? D : 0);
-            if (ok[u] && (it.d & 31) == 0) {
-                uint8_t *scales = (is_v ? a.cache.v_scales : a.cache.k_scales) + slot * 4;
-                const int block = it.d / kMxBlock;
-                scales[block] = (uint8_t)b;
-                for (int pad = block + blocks; pad < 4; pad += blocks) scales[pad] = 0;
-            }
-        }
-    }
+    if constexpr (kForm == 2)
+        heads(Items(lanes_log - 1, tokens_log), a.k, a.k_token, a.k_head, a.cache.k_codes, a.cache.k_scales,
+              std::true_type{}, rope);
+    else
+        heads(Items(lanes_log, tokens_log), a.k, a.k_token, a.k_head, a.cache.k_codes, a.cache.k_scales,
+              std::false_type{}, rope);
+    heads(Items(lanes_log, tokens_log), a.v, a.v_token, a.v_head, a.cache.v_codes, a.cache.v_scales, std::false_type{},
+          still);
 }
 
 template <class T, bool kVec, int kBits>
@@ -343,55 +422,51 @@ __global__ void __launch_bounds__(kThreads) mx_cache_read_kernel(const MxCacheIo
     const long long t0 = (long long)blockIdx.x << tokens_log;
     const int tokens = (int)min((long long)1 << tokens_log, a.tokens - t0);
     find_places(at, a.batch, a.cache, t0, tokens, a.status);
-    const Items it(lanes_log);
-    const int D = a.cache.D, H = a.cache.heads;
-    const long long rows = (long long)2 * H << tokens_log;
-    const long long each = (long long)gridDim.y * kWarps * it.subs * kU;
-    for (long long r0 = ((long long)blockIdx.y * kWarps + threadIdx.x / 32) * it.subs * kU; r0 < rows; r0 += each) {
-        uint2 q[kU];
-        uint32_t b[kU];
-        bool ok[kU];
+    const Items it(lanes_log, tokens_log);
+    const int D = a.cache.D, H = a.cache.heads, s = it.token, row_bytes = D * kBits / 8;
+    if (s >= tokens || it.d >= D || at.slot[s] < 0) return;
+    const long long slot = at.slot[s] + (long long)it.first * a.cache.page, apart = (long long)it.step * a.cache.page;
+    auto heads = [&](const uint8_t *codes, const uint8_t *scales, const void *to, long long token, long long head) {
+        codes += slot * row_bytes + it.d * kBits / 8, scales += slot * 4 + it.d / kMxBlock;
+        T *y = static_cast<T *>(const_cast<void *>(to)) + (t0 + s) * token + it.first * head + it.d;
+        for (int h = it.first; h < H; h += kU * it.step) {
+            uint2 q[kU];
+            uint32_t b[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const long long r = r0 + u * it.subs + it.sub;
-            const int s = (int)(r & ((1 << tokens_log) - 1)), hv = (int)(r >> tokens_log);
-            const bool is_v = hv >= H;
-            ok[u] = r < rows && s < tokens && it.d < D && at.slot[s < tokens ? s : 0] >= 0;
-            q[u] = make_uint2(0u, 0u), b[u] = 0;
-            if (ok[u]) {
-                const long long slot = at.slot[s] + (long long)(is_v ? hv - H : hv) * a.cache.page;
-                const uint8_t *p = (is_v ? a.cache.v_codes : a.cache.k_codes) + (slot * D + it.d) * kBits / 8;
+            for (int u = 0; u < kU; ++u) {
+                if (h + u * it.step >= H) continue;
+                const uint8_t *p = codes + u * apart * row_bytes;
                 if constexpr (kBits == 8)
                     q[u] = __ldg(reinterpret_cast<const uint2 *>(p));
                 else
                     q[u].x = __ldg(reinterpret_cast<const uint32_t *>(p));
-                b[u] = __ldg((is_v ? a.cache.v_scales : a.cache.k_scales) + slot * 4 + it.d / kMxBlock);
+                b[u] = __ldg(scales + u * apart * 4);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            if (!ok[u]) continue;
-            const long long r = r0 + u * it.subs + it.sub;
-            const int s = (int)(r & ((1 << tokens_log) - 1)), hv = (int)(r >> tokens_log);
-            const bool is_v = hv >= H;
-            const int h = is_v ? hv - H : hv;
-            float2 g[4];
-            if constexpr (kBits == 4) {
-                g[0] = mx_from_e2m1x2<0>(q[u].x), g[1] = mx_from_e2m1x2<1>(q[u].x);
-                g[2] = mx_from_e2m1x2<2>(q[u].x), g[3] = mx_from_e2m1x2<3>(q[u].x);
-            } else {
-                g[0] = mx_from_e4m3x2<0>(q[u].x), g[1] = mx_from_e4m3x2<1>(q[u].x);
-                g[2] = mx_from_e4m3x2<0>(q[u].y), g[3] = mx_from_e4m3x2<1>(q[u].y);
+            for (int u = 0; u < kU; ++u) {
+                if (h + u * it.step >= H) continue;
+                float2 g[4];
+                if constexpr (kBits == 4) {
+                    g[0] = mx_from_e2m1x2<0>(q[u].x), g[1] = mx_from_e2m1x2<1>(q[u].x);
+                    g[2] = mx_from_e2m1x2<2>(q[u].x), g[3] = mx_from_e2m1x2<3>(q[u].x);
+                } else {
+                    g[0] = mx_from_e4m3x2<0>(q[u].x), g[1] = mx_from_e4m3x2<1>(q[u].x);
+                    g[2] = mx_from_e4m3x2<0>(q[u].y), g[3] = mx_from_e4m3x2<1>(q[u].y);
+                }
+                const float scale = mx_scale(b[u]);
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 z = __fmul2_rn(g[i], make_float2(scale, scale));
+                    f[2 * i] = z.x, f[2 * i + 1] = z.y;
+                }
+                put8<kVec>(y + u * it.step * head, D - it.d, f);
             }
-            const float scale = mx_scale(b[u]);
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[2 * i] = g[i].x * scale, f[2 * i + 1] = g[i].y * scale;
-            T *head = static_cast<T *>(const_cast<void *>(is_v ? a.v : a.k)) +
-                      (t0 + s) * (is_v ? a.v_token : a.k_token) + h * (is_v ? a.v_head : a.k_head);
-            put8<kVec>(head + it.d, D - it.d, f);
+            codes += kU * apart * row_bytes, scales += kU * apart * 4, y += kU * it.step * head;
         }
-    }
+    };
+    heads(a.cache.k_codes, a.cache.k_scales, a.k, a.k_token, a.k_head);
+    heads(a.cache.v_codes, a.cache.v_scales, a.v, a.v_token, a.v_head);
 }
 
 // Every head of every token starts on 16 bytes.
@@ -419,13 +494,17 @@ Shape shape_of(const LaunchCtx &c, int tokens, int vectors, int D, int unroll) {
     return s;
 }
 
+// Split halves of whole aligned heads of 8 · 2^n values each.
+bool whole_halves(const RopeView &r, int D) { return !r.interleaved && r.rotated == D && D >= 16 && (D & (D - 1)) == 0; }
+
 template <class T>
 cudaError_t rope_t(const LaunchCtx &c, const RopeArgs &a) {
     const bool vec = a.D % 8 == 0 && heads_aligned(a.x, a.x_token, a.x_head, sizeof(T)) &&
                      heads_aligned(a.out, a.out_token, a.out_head, sizeof(T)) &&
                      (a.rope.interleaved || a.rope.rotated % 16 == 0);
-    const Shape s = shape_of(c, a.tokens, a.heads, a.D, 2);
-    auto kernel = vec ? rope_rotate_kernel<T, true> : rope_rotate_kernel<T, false>;
+    const bool pairs = vec && whole_halves(a.rope, a.D);
+    const Shape s = shape_of(c, a.tokens, a.heads, pairs ? a.D / 2 : a.D, 2);
+    auto kernel = pairs ? rope_rotate_kernel<T, 2> : vec ? rope_rotate_kernel<T, 1> : rope_rotate_kernel<T, 0>;
     return launch_kernel(c, kernel, s.grid, dim3(kThreads), 0, a, s.lanes_log, s.tokens_log);
 }
 
@@ -434,9 +513,13 @@ cudaError_t write_t(const LaunchCtx &c, const MxCacheIoArgs &a, const RopeView &
     const bool vec = heads_aligned(a.k, a.k_token, a.k_head, sizeof(T)) &&
                      heads_aligned(a.v, a.v_token, a.v_head, sizeof(T)) &&
                      (rope.interleaved || rope.rotated % 16 == 0);
-    const Shape s = shape_of(c, a.tokens, 2 * a.cache.heads, a.cache.D, 2);
-    auto kernel = a.cache.bits == 4 ? (vec ? mx_cache_write_kernel<T, true, 4> : mx_cache_write_kernel<T, false, 4>)
-                                    : (vec ? mx_cache_write_kernel<T, true, 8> : mx_cache_write_kernel<T, false, 8>);
+    // (A block is four lanes, so half a head is one block at least.)
+    const bool pairs = vec && whole_halves(rope, a.cache.D) && a.cache.D >= 64;
+    const Shape s = shape_of(c, a.tokens, a.cache.heads, a.cache.D, 2);
+    auto pick = [&](auto f2, auto f1, auto f0) { return pairs ? f2 : vec ? f1 : f0; };
+    auto kernel = a.cache.bits == 4
+                      ? pick(mx_cache_write_kernel<T, 2, 4>, mx_cache_write_kernel<T, 1, 4>, mx_cache_write_kernel<T, 0, 4>)
+                      : pick(mx_cache_write_kernel<T, 2, 8>, mx_cache_write_kernel<T, 1, 8>, mx_cache_write_kernel<T, 0, 8>);
     return launch_kernel(c, kernel, s.grid, dim3(kThreads), 0, a, rope, s.lanes_log, s.tokens_log);
 }
 
@@ -444,7 +527,7 @@ template <class T>
 cudaError_t read_t(const LaunchCtx &c, const MxCacheIoArgs &a) {
     const bool vec = heads_aligned(a.k, a.k_token, a.k_head, sizeof(T)) &&
                      heads_aligned(a.v, a.v_token, a.v_head, sizeof(T));
-    const Shape s = shape_of(c, a.tokens, 2 * a.cache.heads, a.cache.D, 4);
+    const Shape s = shape_of(c, a.tokens, a.cache.heads, a.cache.D, 4);
     auto kernel = a.cache.bits == 4 ? (vec ? mx_cache_read_kernel<T, true, 4> : mx_cache_read_kernel<T, false, 4>)
                                     : (vec ? mx_cache_read_kernel<T, true, 8> : mx_cache_read_kernel<T, false, 8>);
     return launch_kernel(c, kernel, s.grid, dim3(kThreads), 0, a, s.lanes_log, s.tokens_log);
