@@ -22,7 +22,7 @@
 // K and V), by asynchronous copies into stages of their own, some 150 KB an SM
 // under way; each keeps a maximum, sum and accumulator of its own.  They are
 // joined in shared memory, and the CTAs of a cluster, which share a tile's
-// keys, through distributed shared memory, in a fixed order.  Where even 16
+// keys, through distributed shared memory, in a fixed order.  Where even 8
 // CTAs a tile leave SMs idle, several clusters share it, and a second kernel
 // joins what they leave in the caller's workspace.
 #include <cstdint>
@@ -40,7 +40,7 @@ namespace q4mm {
 namespace {
 
 constexpr int kThreads = 32 * kFewWarps;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -586,12 +586,14 @@ __global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const M
         if (d >= a.cache.D) continue;
         float m = -INFINITY;
         int nan_from = kNever;
+#pragma unroll 8
         for (int s = 0; s < parts; ++s) {
             const float *w = ws + s * few_part_floats(kR, kDP);
             m = fmaxf(m, w[kR * kDP + r]);
             nan_from = min(nan_from, __float_as_int(w[kR * (kDP + 2) + d / kMxBlock]));
         }
         Joined sum;
+#pragma unroll 8
         for (int s = 0; s < parts; ++s) {
             const float *w = ws + s * few_part_floats(kR, kDP);
             sum.add(w[kR * kDP + r], m, w[kR * (kDP + 1) + r], *reinterpret_cast<const float4 *>(w + r * kDP + d));
@@ -616,9 +618,6 @@ cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a) {
     if (f.parts < 1 || !a.workspace) f.parts = 1;
     const long long ctas = tiles * a.cache.heads * f.parts * f.cluster;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-    if (f.cluster > 8 &&
-        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-        return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kThreads);

@@ -6,13 +6,7 @@ namespace q4mm {
 
 constexpr int kFewWarps = 8;      // warps of a CTA for few rows
 constexpr int kFewGroup = 16;     // tokens a warp takes at once
-#ifndef PROBE_MAX
-#define PROBE_MAX 8
-#define PROBE_PART 4
-#define PROBE_LEAST 2
-#endif
-constexpr int kFewMaxSplit = PROBE_MAX;  // CTAs of a cluster that share a row tile's keys
-constexpr int kFewPartSplit = PROBE_PART;  // and of each, where there are several clusters
+constexpr int kFewMaxSplit = 8;   // CTAs of a cluster that share a row tile's keys
 
 // Row tiles of 8 that a CTA takes: two where a sequence and kv head have more than 8 rows on average.
 inline int few_row_tiles(long long tokens, int group, int seqs) { return tokens * group > 8LL * seqs ? 2 : 1; }
@@ -31,19 +25,20 @@ struct FewSplit {
     int cluster, parts;
 };
 
-// Enough to give the SMs two CTAs each, unless a warp would have less than
-// kFewLeast groups; beyond a cluster's 16, parts joined by a second kernel.
-constexpr int kFewLeast = PROBE_LEAST;
+// Enough to give the SMs two CTAs each, while each warp has a group: up to a
+// cluster, and with two groups a warp several of them, joined by a second kernel.
+// One row over 1000 tokens, 32 heads: 8.1 us with a group a warp, 10.0 with two.
+// Over 131072, one key head: 29.7 us in 37 clusters of 8 (in 75 of 4 37.0, the join is longer; of
+// clusters of 16 only 14 are resident at once).
 inline FewSplit few_split(long long tiles, int kv_heads, int keys, int num_sms) {
     const long long ctas = tiles * kv_heads, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
-    long long want = 2LL * num_sms / (ctas > 0 ? ctas : 1);
-    const long long most = groups / (kFewLeast * kFewWarps);
-    if (want > most) want = most;
-    const int most_cta = want > kFewMaxSplit ? kFewPartSplit : kFewMaxSplit;
+    const long long fill = 2LL * num_sms / (ctas > 0 ? ctas : 1);
+    const long long each = groups / kFewWarps < fill ? groups / kFewWarps : fill;
     int s = 1;
-    while (s < most_cta && 2 * s <= want) s *= 2;
-    const int parts = want > kFewMaxSplit ? (int)(want / s) : 1;
-    return FewSplit{s, parts > 1 ? parts : 1};
+    while (s < kFewMaxSplit && 2 * s <= each) s *= 2;
+    const long long both = groups / (2 * kFewWarps) < fill ? groups / (2 * kFewWarps) : fill;
+    const int parts = (int)(both / s);
+    return FewSplit{s, s == kFewMaxSplit && parts > 1 ? parts : 1};
 }
 
 constexpr int kManyKeys = 128;   // keys of a tile on tcgen05

@@ -346,9 +346,8 @@ __device__ __forceinline__ void put_codes(const float (&f)[8], uint8_t *codes, u
 
 // kForm as for rope_rotate, for the keys.
 template <class T, int kForm, int kBits>
-__global__ void __launch_bounds__(kThreads) mx_cache_write_kernel(const MxCacheIoArgs a, const RopeView rope,
+__global__ void __launch_bounds__(kThreads, kForm == 0 ? 1 : 4) mx_cache_write_kernel(const MxCacheIoArgs a, const RopeView rope,
                                                                   const int lanes_log, const int tokens_log) {
-    constexpr int kU = 2;
     __shared__ __align__(16) Angles table;
     __shared__ Places at;
     pdl_wait();
@@ -363,6 +362,7 @@ __global__ void __launch_bounds__(kThreads) mx_cache_write_kernel(const MxCacheI
     auto heads = [&](const Items &it, const void *from, long long token, long long head, uint8_t *codes, uint8_t *scales,
                      auto pairs, const RopeView &r) {
         constexpr bool kPairs = decltype(pairs)::value;
+        constexpr int kU = kPairs ? 2 : 4;
         const int s = it.token, span = kPairs ? D / 2 : D;
         const bool mine = s < tokens && it.d < span && at.slot[s < tokens ? s : 0] >= 0;
         const T *x = static_cast<const T *>(from) + (t0 + s) * token + it.first * head;
