@@ -85,6 +85,13 @@ struct ManyLayout {
     static __device__ constexpr uint32_t col_p(int k) { return k / 4 * 64 + 8 * (k % 4); }
     static constexpr uint32_t kColLow = 128;  // kNP == 2, kTiles == 1
     static constexpr uint32_t col_o(int t) { return 256 + kDP * t; }
+    // Tensor-core sums drop what falls below their last bit, so that long ones
+    // fall short (one of 7500 keys by 1.6e-5 of its value, 940 steps of 16).
+    // With fp32 outputs they are therefore taken every two tiles of keys, 32
+    // steps, and added up by fp32 additions in other columns.  (16-bit outputs:
+    // half an fp16 step is 2.4e-4, and that many rows over that many keys are split.)
+    static constexpr int kDrain = kNP == 2 ? 2 : 0;
+    static constexpr uint32_t kColSum = 384;
 };
 
 struct ManyShared {
@@ -400,6 +407,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         const float c0 = a.scale * kLog2e;
         const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
         const uint32_t s_at = tmem + lanes + L::col_s(t) + 64 * side, o_at = tmem + lanes + L::col_o(t) + kDP / 2 * side;
+        constexpr int kDrain = L::kDrain;
+        const uint32_t sum_at = tmem + lanes + L::kColSum + kDP / 2 * side;
         float M = -INFINITY, l = 0.f;
         const int n = cnt[t];
         bool go = true;  // the two warps of a quarter leave together, also after a time-out
@@ -447,10 +456,12 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             const float other = sh.top[i & 1][side ^ 1][mine];
             go = ok && !isnan(other);
             top = fmaxf(top, other);
+            float grown = 1.f;
             if (__any_sync(0xFFFFFFFFu, top > M + kPSlack)) {
                 const float now = fmaxf(M, top), by = M == -INFINITY ? 0.f : ex2(M - now);
                 M = now, l *= by;
-                if (i > 0) {
+                if (kDrain > 0) grown = by;
+                if (kDrain == 0 && i > 0) {
 #pragma unroll 1
                     for (int k = 0; k < kDP / 2; k += 16) {
                         uint32_t o[16];
@@ -458,6 +469,29 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
 #pragma unroll
                         for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__uint_as_float(o[z]) * by);
                         tc_st16(o_at + k, o);
+                    }
+                }
+            }
+            if constexpr (kDrain > 0) {
+                const bool drain = i > 0 && i % kDrain == 0;
+                if (i > 0 && (drain || __any_sync(0xFFFFFFFFu, grown != 1.f))) {
+#pragma unroll 1
+                    for (int k = 0; k < kDP / 2; k += 16) {
+                        uint32_t o[16], sums[16];
+                        tc_ld16(o_at + k, o);
+                        if (i > kDrain) {
+                            tc_ld16(sum_at + k, sums);
+                        } else {
+#pragma unroll
+                            for (int z = 0; z < 16; ++z) sums[z] = 0u;
+                        }
+#pragma unroll
+                        for (int z = 0; z < 16; ++z) {
+                            const float x = __uint_as_float(o[z]), y = __uint_as_float(sums[z]);
+                            sums[z] = __float_as_uint((drain ? x + y : y) * grown), o[z] = __float_as_uint(x * grown);
+                        }
+                        if (!drain) tc_st16(o_at + k, o);
+                        if (drain || i > kDrain) tc_st16(sum_at + k, sums);
                     }
                 }
             }
@@ -518,6 +552,13 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 uint32_t o[32];
                 if (n > 0) {
                     tc_ld32(o_at + k, o);
+                    if (kDrain > 0 && n > kDrain) {
+                        uint32_t sums[32];
+                        tc_ld32(sum_at + k, sums);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(sums[x]));
+                    }
                 } else {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) o[x] = 0u;
@@ -737,7 +778,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 for (int k = 0; k < kNP * kDP / 16; ++k) {
                     const int in = k % (kDP / 16);
                     const uint32_t at = in / 4 * (kHalf >> 4) + 2 * (in % 4);
-                    mma_ss(tmem + L::col_s(t), qd + (k >= kDP / 16 ? L::kSlab >> 4 : 0) + at, kd + at, kIdS, k != 0);
+                    // (Second terms first, while there is little to cut off.)
+                    mma_ss(tmem + L::col_s(t), qd + (k < (kNP - 1) * kDP / 16 ? L::kSlab >> 4 : 0) + at, kd + at, kIdS, k != 0);
                 }
                 tc_commit(&sh.s_full[t]);
                 if (last) tc_commit(k_free);
@@ -752,8 +794,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
 #pragma unroll
                 for (int k = 0; k < kNP * kManyKeys / 16; ++k) {
                     const int in = k % (kManyKeys / 16);
-                    const uint32_t p_col = k >= kManyKeys / 16 ? L::kColLow + 8 * in : L::col_s(t) + L::col_p(in);
-                    mma_ts(tmem + L::col_o(t), tmem + p_col, vd + (2048 >> 4) * in, kIdO, (i | k) != 0);
+                    const uint32_t p_col = k < (kNP - 1) * kManyKeys / 16 ? L::kColLow + 8 * in : L::col_s(t) + L::col_p(in);
+                    mma_ts(tmem + L::col_o(t), tmem + p_col, vd + (2048 >> 4) * in, kIdO, (L::kDrain > 0 ? i % L::kDrain : i) != 0 || k != 0);
                 }
                 if (last) tc_commit(v_free);
             }
