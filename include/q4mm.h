@@ -563,6 +563,15 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
 size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequences, int tableWidth, int tokens,
                               int heads);
 
+/*
+ * q4mm_call — one of the calls named below with its arguments, in their order,
+ * in 8-byte words: pointers, strides and sizes as they are, integers sign-
+ * extended, a float as a double.  For bindings that pay for every argument of
+ * a foreign call.  Returns what the call returns.
+ */
+enum { Q4MM_CALL_ROPE_ROTATE = 0, Q4MM_CALL_MX_CACHE_WRITE = 1, Q4MM_CALL_MX_CACHE_READ = 2, Q4MM_CALL_MX_ATTENTION = 3 };
+int q4mm_call(int which, const long long *words);
+
 /* Message for the last error returned on the calling thread ("" if none).
  * The pointer stays valid until the thread's next failing call. */
 const char *q4mm_last_error(void);

@@ -4,6 +4,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -14,6 +15,7 @@ _SYMBOLS = ("q4k_matmul", "q4k_matmul_tc", "q4k_matmul_tc_noalloc", "q4k_relayou
             "q4_0_gemv", "q6k_gemv", "q4k_ffn_swiglu", "ternary_gemv",
             "mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul",
             "rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention", "mx_attention_workspace",
+            "q4mm_call",
             "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait")
 
 
@@ -61,6 +63,8 @@ def _load() -> ctypes.CDLL:
     lib.mx_attention.argtypes = [*heads, i32, *cache, *batch, f32, i32, *heads, i32, i32, vp, ctypes.c_size_t, vp]
     lib.mx_attention_workspace.argtypes = [i32] * 7
     lib.mx_attention_workspace.restype = ctypes.c_size_t
+    lib.q4mm_call.argtypes = [i32, ctypes.c_char_p]
+    lib.q4mm_call.restype = i32
     for name in ("mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul", "rope_rotate",
                  "mx_cache_write", "mx_cache_read", "mx_attention"):
         getattr(lib, name).restype = i32
@@ -651,6 +655,15 @@ def mx_matmul(x: MxTensor, w: MxTensor, dtype=None, out=None, stream=None):
 
 # Attention on a paged MX cache: layouts, limits and precision in include/q4mm.h.
 
+# The words of q4mm_call, which takes its arguments in a buffer: one by one they
+# cost ctypes 2.5 us, more than the launch.
+_ROPE_WORDS = struct.Struct("=9qd7q").pack
+_WRITE_WORDS = struct.Struct("=10qd16q").pack
+_READ_WORDS = struct.Struct("=23q").pack
+_ATTENTION_WORDS = struct.Struct("=18qd9q").pack
+_ROPE, _WRITE, _READ, _ATTENTION = range(4)     # Q4MM_CALL_...
+
+
 class Rope(NamedTuple):
     """Rotary positions of a head's first 2·len(frequencies) values.
 
@@ -749,19 +762,22 @@ def _heads_arg(x, what: str, shape=None):
 
 def _cache_arg(c: MxCache, device: int):
     kc, ks, vc, vs, D, bits = c
-    if _Torch.uint8 is None:
+    u8 = _Torch.uint8
+    if u8 is None:
         _Torch.load()
-    u8, shape = _Torch.uint8, kc.shape
-    if len(shape) != 4 or bits not in (4, 8) or shape[3] * 8 != D * bits:
+        u8 = _Torch.uint8
+    shape = kc.shape
+    if len(shape) != 4 or (bits != 8 and bits != 4) or shape[3] * 8 != D * bits:
         raise ValueError("cache: codes must be [pages, kv heads, page, head_dim·bits/8]")
-    if vc.shape != shape or ks.shape != (*shape[:3], 4) or vs.shape != ks.shape:
+    pages, heads, page, _ = shape
+    if vc.shape != shape or ks.shape != (pages, heads, page, 4) or vs.shape != ks.shape:
         raise ValueError("cache: scales must be [pages, kv heads, page, 4], and v's tensors like k's")
     for t in (kc, ks, vc, vs):
         if t.dtype != u8 or not t.is_contiguous():
             raise ValueError("cache: codes and scales must be contiguous uint8 tensors")
         if t.get_device() != device:
             raise ValueError("all tensors of a call must be on one CUDA device")
-    return kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), shape[0], shape[1], shape[2], D, bits
+    return kc.data_ptr(), ks.data_ptr(), vc.data_ptr(), vs.data_ptr(), pages, heads, page, D, bits
 
 
 def _batch_arg(starts, lengths, pages, device: int):
@@ -826,7 +842,8 @@ def rope_rotate(x, positions, rope: Rope, out=None, stream=None):
     oa = _heads_arg(out, "out", shape)
     if side is not None:
         _hold(side, x, positions, rope.frequencies, out)
-    rc = _LIB.rope_rotate(*xa, dtype, positions.data_ptr(), int(positions.dtype == _Torch.int64), *ra, *oa, T, H, D, at)
+    rc = _LIB.q4mm_call(_ROPE, _ROPE_WORDS(*xa, dtype, positions.data_ptr(), positions.dtype == _Torch.int64, *ra, *oa, T, H,
+                                           D, at))
     if rc:
         _check(rc)
     return out
@@ -849,7 +866,7 @@ def mx_cache_write(cache: MxCache, k, v, starts, lengths, pages, rope: Rope | No
     at, side = _call_stream(stream, device)
     if side is not None:
         _hold(side, k, v, *cache[:4], starts, lengths, pages, rope and rope[0])
-    rc = _LIB.mx_cache_write(*ka, *va, dtype, *ra, *ca, *ba, T, at)
+    rc = _LIB.q4mm_call(_WRITE, _WRITE_WORDS(*ka, *va, dtype, *ra, *ca, *ba, T, at))
     if rc:
         _check(rc)
     return cache
@@ -878,7 +895,7 @@ def mx_cache_read(cache: MxCache, starts, lengths, pages, tokens: int | None = N
     ka, va = _heads_arg(k, "k", shape), _heads_arg(v, "v", shape)
     if side is not None:
         _hold(side, *cache[:4], starts, lengths, pages, k, v)
-    rc = _LIB.mx_cache_read(*ca, *ba, *ka, *va, _mx_dtype(k.dtype, "out"), shape[0], at)
+    rc = _LIB.q4mm_call(_READ, _READ_WORDS(*ca, *ba, *ka, *va, _mx_dtype(k.dtype, "out"), shape[0], at))
     if rc:
         _check(rc)
     return k, v
@@ -917,8 +934,9 @@ def mx_attention(q, cache: MxCache, starts, lengths, pages, scale: float | None 
             ws = new((nbytes,), dtype=_Torch.uint8, device=q.device)
     if side is not None:
         _hold(side, q, *cache[:4], starts, lengths, pages, out, ws)
-    rc = _LIB.mx_attention(*qa, dtype, *ca, *ba, D ** -0.5 if scale is None else float(scale), 1 if causal else 0, *oa,
-                           T, H, 0 if ws is None else ws.data_ptr(), nbytes, at)
+    rc = _LIB.q4mm_call(_ATTENTION, _ATTENTION_WORDS(*qa, dtype, *ca, *ba, D ** -0.5 if scale is None else float(scale),
+                                                     1 if causal else 0, *oa, T, H, 0 if ws is None else ws.data_ptr(),
+                                                     nbytes, at))
     if rc:
         _check(rc)
     return out

@@ -777,6 +777,36 @@ size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequ
                                             ctx.num_sms);
 }
 
+int q4mm_call(int which, const long long *w) {
+    auto p = [&](int i) { return reinterpret_cast<void *>(w[i]); };
+    auto ints = [&](int i) { return reinterpret_cast<const int *>(w[i]); };
+    auto real = [&](int i) {
+        double d;
+        memcpy(&d, w + i, sizeof(d));
+        return (float)d;
+    };
+    auto i32 = [&](int i) { return (int)(w[i] > 0x7FFFFFFF ? 0x7FFFFFFF : w[i] < -1 ? -1 : w[i]); };
+    auto stream = [&](int i) { return reinterpret_cast<q4mm_stream_t>(w[i]); };
+    if (!w) return fail(Q4MM_ERR_NULL, "the words of a call must be non-NULL");
+    switch (which) {
+        case Q4MM_CALL_ROPE_ROTATE:
+            return rope_rotate(p(0), w[1], w[2], i32(3), p(4), i32(5), static_cast<const double *>(p(6)), i32(7), i32(8),
+                               real(9), p(10), w[11], w[12], i32(13), i32(14), i32(15), stream(16));
+        case Q4MM_CALL_MX_CACHE_WRITE:
+            return mx_cache_write(p(0), w[1], w[2], p(3), w[4], w[5], i32(6), static_cast<const double *>(p(7)), i32(8),
+                                  i32(9), real(10), p(11), p(12), p(13), p(14), i32(15), i32(16), i32(17), i32(18), i32(19),
+                                  ints(20), ints(21), ints(22), i32(23), i32(24), i32(25), stream(26));
+        case Q4MM_CALL_MX_CACHE_READ:
+            return mx_cache_read(p(0), p(1), p(2), p(3), i32(4), i32(5), i32(6), i32(7), i32(8), ints(9), ints(10), ints(11),
+                                 i32(12), i32(13), p(14), w[15], w[16], p(17), w[18], w[19], i32(20), i32(21), stream(22));
+        case Q4MM_CALL_MX_ATTENTION:
+            return mx_attention(p(0), w[1], w[2], i32(3), p(4), p(5), p(6), p(7), i32(8), i32(9), i32(10), i32(11), i32(12),
+                                ints(13), ints(14), ints(15), i32(16), i32(17), real(18), i32(19), p(20), w[21], w[22],
+                                i32(23), i32(24), p(25), (size_t)w[26], stream(27));
+    }
+    return fail(Q4MM_ERR_DIM, "there is no call %d", which);
+}
+
 const char *q4mm_last_error(void) { return g_err; }
 
 int q4mm_device_status(q4mm_stream_t stream, int clear) {

@@ -231,6 +231,36 @@ def test_symbols_take_the_declared_arguments(q4mm):
         assert len(fn.argtypes) == n and fn.restype is ctypes.c_int
 
 
+def test_packed_calls_check_the_same(q4mm):
+    """The calls with their arguments in words: each bad one is refused as it is by the call itself."""
+    import struct
+    lib = q4mm.library()
+    def pack(fmt, *a):
+        return struct.pack(fmt, *a)
+    rope = ["=9qd7q", H, 128, 64, 0, A, 0, B, 64, 0, 1.0, I, 128, 64, 3, 2, 64, 0]
+    write = ["=10qd16q", H, 128, 64, I, 128, 64, 0, 0, 0, 0, 1.0, A, B, C, D, 4, 2, 16, 64, 8, E, F, G, 1, 4, 3, 0]
+    read = ["=23q", A, B, C, D, 4, 2, 16, 64, 8, E, F, G, 1, 4, H, 128, 64, I, 128, 64, 0, 3, 0]
+    att = ["=18qd9q", H, 128, 64, 0, A, B, C, D, 4, 2, 16, 64, 8, E, F, G, 1, 4, 0.125, 1, I, 128, 64, 3, 2, 0, 0, 0]
+    for which, words, bad in (
+            (0, rope, ((0, 0, NULL, "x"), (1, -1, DIM, "strides"), (3, 7, DIM, "type"), (4, A + 2, ALIGN, "positions"), (6, 0, NULL, "frequencies"),
+                       (7, 66, DIM, "rotated"), (9, float("inf"), DIM, "magnitude"), (10, 0, NULL, "out"), (12, 32, ALIAS, "out"),
+                       (13, -5, DIM, "tokens"), (14, 0, DIM, "heads"), (15, 500, DIM, "headDim"), (13, 2 ** 40, DIM, "tokens"))),
+            (1, write, ((0, 0, NULL, "k"), (3, 0, NULL, "v"), (6, 9, DIM, "type"), (8, 3, DIM, "rotated"), (10, float("nan"), DIM, "magnitude"),
+                        (11, 0, NULL, "k_codes"), (14, D + 4, ALIGN, "v_scales"), (15, 0, DIM, "pages"), (16, 0, DIM, "kvHeads"), (17, 20, DIM, "pageTokens"),
+                        (18, 65, DIM, "headDim"), (19, 5, DIM, "bits"), (20, 0, NULL, "starts"), (21, 0, NULL, "lengths"), (22, 0, NULL, "table"),
+                        (23, -1, DIM, "sequences"), (24, -1, DIM, "tableWidth"), (25, -1, DIM, "tokens"))),
+            (2, read, ((3, 0, NULL, "v_scales"), (8, 7, DIM, "bits"), (9, E + 1, ALIGN, "starts"), (12, -1, DIM, "sequences"), (14, 0, NULL, "k"), (17, H, ALIAS, "overlap"),
+                       (20, 5, DIM, "type"), (21, -1, DIM, "tokens"))),
+            (3, att, ((0, 0, NULL, "q"), (3, 3, DIM, "type"), (4, 0, NULL, "k_codes"), (12, 3, DIM, "bits"), (15, 0, NULL, "table"), (17, -2, DIM, "tableWidth"),
+                      (18, -0.5, DIM, "scale"), (20, 0, NULL, "y"), (22, 32, ALIAS, "y"), (23, -1, DIM, "tokens"), (24, 5, DIM, "heads"), (26, 64, NULL, "workspace")))):
+        for at, value, code, word in bad:
+            w = words.copy()
+            w[1 + at] = value
+            assert lib.q4mm_call(which, pack(*w)) == code, (which, at, q4mm.last_error())
+            assert word in q4mm.last_error(), (which, at, q4mm.last_error())
+    assert lib.q4mm_call(9, b"") == DIM and lib.q4mm_call(0, None) == NULL
+
+
 # Refusals of the Python calls.
 
 @pytest.fixture

@@ -1,5 +1,7 @@
 """Streams, memory and devices of the attention calls, on the host: what
 test_streams_host asks of every other tensor call."""
+import struct
+
 import pytest
 
 from test_streams_host import CURRENT, OTHER, _Stream, _tensors, host  # noqa: F401
@@ -22,8 +24,16 @@ def _calls(h):
     ]
 
 
+NAMES = ("rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention")
+
+
+def _words(args):
+    """The 8-byte words of a packed call; the last is its stream."""
+    return struct.unpack(f"={len(args[1]) // 8}q", args[1])
+
+
 def _launches(h):
-    return [(n, a[-1]) for n, a in h.calls if n != "mx_attention_workspace"]
+    return [(NAMES[a[0]], _words(a)[-1]) for n, a in h.calls if n != "mx_attention_workspace" and n == "q4mm_call"]
 
 
 @pytest.mark.parametrize("i", range(4))
@@ -87,6 +97,6 @@ def test_a_workspace_waits_like_a_result(host):  # noqa: F811
         call(OTHER)
     finally:
         b._LIB = lib
-    (args,) = [a for n, a in host.calls if n == name]
+    (args,) = [_words(a) for n, a in host.calls if n == "q4mm_call"]
     assert args[-2] == 4096 and host.pools[args[-3]] == OTHER
     assert {(args[-3], OTHER), (args[-3], CURRENT)} <= set(host.records)
