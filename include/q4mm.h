@@ -589,9 +589,9 @@ int q4mm_device_status(q4mm_stream_t stream, int clear);
  * q4mm_test_fail_next_wait — a test hook for the library's failure
  * detection; the pages have no counterpart.  The calling thread's next call
  * of q4k_matmul (one-token and 3-8 token kernels), q4_0_gemv, q6k_gemv,
- * q4k_ffn_swiglu, q4k_matmul_tc or mx_matmul never issues the copy of weight stage
- * `stage` of each CTA (its ring stage, or its 256-row weight tile on the
- * tensor cores) and bounds every in-kernel wait by `limit_cycles` SM cycles
+ * q4k_ffn_swiglu, q4k_matmul_tc, mx_matmul or mx_attention (many rows) never issues
+ * the copy of weight stage `stage` of each CTA (its ring stage, its 256-row weight
+ * tile on the tensor cores, or its keys' tile of 128, the last if it has fewer) and bounds every in-kernel wait by `limit_cycles` SM cycles
  * (about 2·10^6 per millisecond) instead of about 2·10^9.  The waits on the
  * missing stage then run out: the kernel sets the device status word, lets
  * every copy it did issue land, and exits; that call's y is undefined and
@@ -601,6 +601,14 @@ int q4mm_device_status(q4mm_stream_t stream, int clear);
  * disarms it; otherwise stage >= 0 and limit_cycles > 0, else Q4MM_ERR_DIM.
  */
 int q4mm_test_fail_next_wait(int stage, long long limit_cycles);
+
+/*
+ * q4mm_test_attention_kernel — a test hook: the calling thread's mx_attention
+ * (and mx_attention_workspace) take the kernel for few rows (1) or the one for
+ * many (2) whatever the sizes, until 0 leaves the choice to the library again.
+ * Else Q4MM_ERR_DIM.
+ */
+int q4mm_test_attention_kernel(int which);
 
 /* Library version, major·10000 + minor·100 + patch. */
 int q4mm_version(void);

@@ -16,7 +16,8 @@ _SYMBOLS = ("q4k_matmul", "q4k_matmul_tc", "q4k_matmul_tc_noalloc", "q4k_relayou
             "mx_quantize", "mx_swiglu", "mx_rmsnorm", "mx_dequantize", "mx_matmul",
             "rope_rotate", "mx_cache_write", "mx_cache_read", "mx_attention", "mx_attention_workspace",
             "q4mm_call",
-            "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait")
+            "q4mm_last_error", "q4mm_device_status", "q4mm_version", "q4mm_test_fail_next_wait",
+            "q4mm_test_attention_kernel")
 
 
 class Q4mmError(RuntimeError):
@@ -76,6 +77,8 @@ def _load() -> ctypes.CDLL:
     lib.q4mm_version.restype = i32
     lib.q4mm_test_fail_next_wait.argtypes = [i32, ctypes.c_longlong]
     lib.q4mm_test_fail_next_wait.restype = i32
+    lib.q4mm_test_attention_kernel.argtypes = [i32]
+    lib.q4mm_test_attention_kernel.restype = i32
     return lib
 
 
@@ -204,6 +207,12 @@ def arm_wait_failure(stage: int, limit_cycles: int) -> None:
     """Test hook: the calling thread's next call withholds weight stage `stage`
     and bounds its in-kernel waits by `limit_cycles` (see include/q4mm.h)."""
     _check(_LIB.q4mm_test_fail_next_wait(int(stage), int(limit_cycles)))
+
+
+def force_attention_kernel(which: str | None) -> None:
+    """Test hook: the calling thread's mx_attention takes the kernel for "few"
+    rows, or for "many", until None leaves the choice to the library."""
+    _check(_LIB.q4mm_test_attention_kernel((None, "few", "many").index(which)))
 
 
 def device_status(stream=None, clear: bool = True) -> None:

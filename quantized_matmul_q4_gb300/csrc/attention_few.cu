@@ -614,14 +614,13 @@ __global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const M
 }
 
 template <int kBits, int kDP, int kNR, int kNP>
-cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a) {
+cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a, FewSplit f) {
     auto kernel = mx_attention_few_kernel<kBits, kDP, kNR, kNP>;
     constexpr size_t bytes = sizeof(FewShared<kBits, kDP, kNR, kNP>);
     cudaError_t e = ensure_smem(kernel, bytes);
     if (e != cudaSuccess) return e;
     const int group = a.heads / a.cache.heads;
     const long long tiles = few_tiles(a.tokens, group, kNR, a.batch.seqs);
-    FewSplit f = few_split(tiles, a.cache.heads, few_keys(a.batch.width, a.cache.page), c.num_sms);
     // As many parts as the workspace holds.
     const size_t part_bytes = tiles * a.cache.heads * few_part_floats(8 * kNR, kDP) * sizeof(float);
     if ((size_t)f.parts > a.workspace_bytes / part_bytes) f.parts = (int)(a.workspace_bytes / part_bytes);
@@ -649,26 +648,24 @@ cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a) {
 }
 
 template <int kBits, int kDP>
-cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a) {
-    const bool wide = few_row_tiles(a.tokens, a.heads / a.cache.heads, a.batch.seqs) == 2;
-    if (a.type == MxType::kF32)
-        return wide ? launch_few<kBits, kDP, 2, 2>(c, a) : launch_few<kBits, kDP, 1, 2>(c, a);
-    return wide ? launch_few<kBits, kDP, 2, 1>(c, a) : launch_few<kBits, kDP, 1, 1>(c, a);
+cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f) {
+    const bool f32 = a.type == MxType::kF32;
+    if (f32) return f.rows_8 == 2 ? launch_few<kBits, kDP, 2, 2>(c, a, f) : launch_few<kBits, kDP, 1, 2>(c, a, f);
+    return f.rows_8 == 2 ? launch_few<kBits, kDP, 2, 1>(c, a, f) : launch_few<kBits, kDP, 1, 1>(c, a, f);
 }
 
 }  // namespace
 
-size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, int width, int page, int num_sms) {
-    const int nr = few_row_tiles(tokens, heads / kv_heads, seqs);
-    const long long tiles = few_tiles(tokens, heads / kv_heads, nr, seqs);
-    const FewSplit f = few_split(tiles, kv_heads, few_keys(width, page), num_sms);
-    return f.parts == 1 ? 0 : tiles * kv_heads * f.parts * few_part_floats(8 * nr, D <= 64 ? 64 : 128) * sizeof(float);
+size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, const FewSplit &f) {
+    if (f.parts == 1) return 0;
+    const size_t tiles = few_tiles(tokens, heads / kv_heads, f.rows_8, seqs);
+    return tiles * kv_heads * f.parts * few_part_floats(8 * f.rows_8, D <= 64 ? 64 : 128) * sizeof(float);
 }
 
-cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a) {
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f) {
     const bool narrow = a.cache.D <= 64;
-    if (a.cache.bits == 4) return narrow ? launch_rows<4, 64>(c, a) : launch_rows<4, 128>(c, a);
-    return narrow ? launch_rows<8, 64>(c, a) : launch_rows<8, 128>(c, a);
+    if (a.cache.bits == 4) return narrow ? launch_rows<4, 64>(c, a, f) : launch_rows<4, 128>(c, a, f);
+    return narrow ? launch_rows<8, 64>(c, a, f) : launch_rows<8, 128>(c, a, f);
 }
 
 }  // namespace q4mm

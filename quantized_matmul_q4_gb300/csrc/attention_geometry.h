@@ -4,58 +4,130 @@
 
 namespace q4mm {
 
+constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a row tile's keys (of 16 only 14 are resident)
+
+// Clusters of s CTAs that are resident at once with one CTA an SM, and with
+// two, on 152 SMs: the GPU's processing clusters have 16 to 20 SMs, so that larger
+// clusters leave some over, most of all those of 7, which are not used.
+constexpr int kResident[2][kMaxSplit + 1] = {{0, 152, 76, 46, 36, 28, 23, 15, 15}, {0, 304, 152, 97, 74, 58, 46, 38, 36}};
+inline long long resident(int cluster, bool two, int num_sms) {
+    const long long n = (long long)kResident[two][cluster] * num_sms / 152;
+    return n > 0 ? n : 1;
+}
+
+// Row tiles of a sequence's share of the rows, over all sequences.
+inline long long even_tiles(long long rows, int tile_rows, int seqs) {
+    return seqs * ((rows + (long long)tile_rows * seqs - 1) / ((long long)tile_rows * seqs));
+}
+
 constexpr int kFewWarps = 8;      // warps of a CTA for few rows
 constexpr int kFewGroup = 16;     // tokens a warp takes at once
-constexpr int kFewMaxSplit = 8;   // CTAs of a cluster that share a row tile's keys
-
-// Row tiles of 8 that a CTA takes: two where a sequence and kv head have more than 8 rows on average.
-inline int few_row_tiles(long long tokens, int group, int seqs) { return tokens * group > 8LL * seqs ? 2 : 1; }
 
 // Tiles of 8 · nr rows, at most (see row_tile).
 inline long long few_tiles(long long tokens, int group, int nr, int seqs) { return tokens * group / (8 * nr) + seqs; }
 
 // Keys of a sequence, at most: what its table has room for (their number is the device's to know).
-inline int few_keys(int width, int page) {
+inline int table_keys(int width, int page) {
     const long long keys = (long long)width * page;
     return keys < 0x7FFFFFFF ? (int)keys : 0x7FFFFFFF;
 }
 
-// How a tile's keys are shared: `parts` clusters of `cluster` CTAs.
+// How few rows are split: tiles of 8 · rows_8 rows, the keys of each shared by
+// `parts` clusters of `cluster` CTAs, whose sums a second kernel joins.
 struct FewSplit {
-    int cluster, parts;
+    int rows_8, cluster, parts;
 };
 
-// Enough to give the SMs two CTAs each, while each warp has a group: up to a
-// cluster, and with two groups a warp several of them, joined by a second kernel.
-// One row over 1000 tokens, 32 heads: 8.1 us with a group a warp, 10.0 with two.
-// Over 131072, one key head: 29.7 us in 37 clusters of 8 (in 75 of 4 37.0, the join is longer; of
-// clusters of 16 only 14 are resident at once).
-inline FewSplit few_split(long long tiles, int kv_heads, int keys, int num_sms) {
-    const long long ctas = tiles * kv_heads, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
-    const long long fill = 2LL * num_sms / (ctas > 0 ? ctas : 1);
-    const long long each = groups / kFewWarps < fill ? groups / kFewWarps : fill;
-    int s = 1;
-    while (s < kFewMaxSplit && 2 * s <= each) s *= 2;
-    const long long both = groups / (2 * kFewWarps) < fill ? groups / (2 * kFewWarps) : fill;
-    const int parts = (int)(both / s);
-    return FewSplit{s, s == kFewMaxSplit && parts > 1 ? parts : 1};
+// Microseconds of a split. A CTA is paid for by the rounds of 8 groups that
+// its warps take: 5 and 1.06 a round alone on its SM, 6.25 and 1.36 for two there, where
+// the registers leave room for two (8 rows, 16-bit), and 7 and 1.1 with 16
+// rows; fp32 takes 5.5 and 1.26, 7 and 1.5.  A cluster costs 1.4, the second
+// kernel 2.7 and 0.3 a part.  These were fitted to 9500 measurements, of 1 to
+// 64 sequences, 60 to 40000 keys, 8 to 32 rows: the split of least cost takes
+// 1.3% longer than the best of those measured on average, 21% at most (one that
+// fills the SMs' places twice with clusters of 1, 2, 4 or 8 14% and 129%: of 8
+// sequences with 8 heads over 8000 keys 51.9 us in clusters of 2, 32.2 in clusters of 4;
+// of 20 with 5 over 1000, 19.4 whole, 15.3 in clusters of 2).
+inline double few_cost(long long tiles, int kv_heads, long long groups, const FewSplit &f, bool f32, int num_sms) {
+    const long long clusters = tiles * kv_heads * f.parts, shares = (long long)kFewWarps * f.cluster * f.parts;
+    const double rounds = (double)((groups + shares - 1) / shares);
+    const double more = (f.cluster > 1 ? 1.4 : 0) + (f.parts > 1 ? 2.7 + 0.3 * f.parts : 0);
+    const long long one = resident(f.cluster, false, num_sms);
+    if (f.rows_8 == 1 && !f32) {
+        const long long two = resident(f.cluster, true, num_sms), rest = clusters % two;
+        const double alone = 5 + 1.06 * rounds, pair = 6.25 + 1.36 * rounds;
+        return more + (double)(clusters / two) * pair + (rest == 0 ? 0 : rest <= one ? alone : pair);
+    }
+    const double each = !f32 ? 7 + 1.1 * rounds : f.rows_8 == 1 ? 5.5 + 1.26 * rounds : 7 + 1.5 * rounds;
+    return more + (double)((clusters + one - 1) / one) * each;
 }
 
-constexpr int kManyKeys = 128;   // keys of a tile on tcgen05
-constexpr int kManyMaxSplit = 8;  // CTAs that share a row tile's keys there
+// The split of least cost, as if the rows were spread evenly over the sequences and all of the table were keys.
+inline FewSplit few_split(long long tokens, int group, int seqs, int kv_heads, int keys, bool f32, int num_sms,
+                          double &least) {
+    const long long rows = tokens * group, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
+    FewSplit best = {1, 1, 1};
+    least = -1;
+    const auto consider = [&](long long tiles, const FewSplit &f) {
+        const double c = few_cost(tiles, kv_heads, groups, f, f32, num_sms);
+        if (least < 0 || c < least) best = f, least = c;
+    };
+    for (int nr = 1; nr <= (rows > 8LL * seqs ? 2 : 1); ++nr) {
+        const long long tiles = even_tiles(rows, 8 * nr, seqs);
+        for (int s = 1; s <= kMaxSplit; ++s)
+            if (s != 7) consider(tiles, {nr, s, 1});
+        for (int two = 0; two < 2; ++two) {  // as many parts as are resident, alone on an SM or by twos
+            const long long parts = resident(kMaxSplit, two, num_sms) / (tiles * kv_heads);
+            if (parts > 1 && parts * kMaxSplit * kFewWarps <= groups) consider(tiles, {nr, kMaxSplit, (int)parts});
+        }
+    }
+    return best;
+}
 
-// Rows of a sequence and kv head, on average, from which tiles of 128 on the
-// tensor cores are faster.
-inline bool many_rows(long long tokens, int group, int seqs) { return tokens * group > 32LL * (seqs > 0 ? seqs : 1); }
+constexpr int kManyKeys = 128;  // keys of a tile on tcgen05
 
-// CTAs of a cluster over the keys: while one CTA per SM is not passed, and
-// each has two tiles of keys.
-inline int many_split(long long rows, int tile_rows, int seqs, int kv_heads, int keys, int num_sms) {
-    const long long whole = rows / tile_rows, tiles = whole > seqs ? whole : seqs;
-    const int key_tiles = (keys + kManyKeys - 1) / kManyKeys;
-    int s = 1;
-    while (s < kManyMaxSplit && tiles * kv_heads * s * 2 <= num_sms && key_tiles >= 4 * s) s *= 2;
-    return s;
+// CTAs of a cluster that share a tile's keys there, by the same kind of cost:
+// 17 us and 2.25 a tile of keys and pair of row tiles, 16.6 and 3.1 for fp32's
+// tile.  Fitted to 2600 measurements (1 and 4 sequences, 34 to 3000 rows, 400 to
+// 30000 keys); it takes 1.0% longer than their best on average.
+inline int many_split(long long rows, int tile_rows, int seqs, int kv_heads, int keys, bool f32, int num_sms,
+                      double &least) {
+    const long long clusters = even_tiles(rows, tile_rows, seqs) * kv_heads;
+    const int tiles = (int)(((long long)keys + kManyKeys - 1) / kManyKeys);
+    int best = 1;
+    least = -1;
+    for (int s = 1; s <= kMaxSplit; ++s) {
+        if (s == 7) continue;
+        const long long n = resident(s, false, num_sms);
+        const double waves = clusters <= 3 * n ? (double)((clusters + n - 1) / n) : (double)clusters / n + 0.5;
+        const int each = (tiles + s - 1) / s;
+        const double c = 3 + waves * ((f32 ? 13.6 + 3.1 * each : 14 + 2.25 * each) + (s > 1 ? 0.9 : 0));
+        if (least < 0 || c < least) best = s, least = c;
+    }
+    return best;
+}
+
+// How a call is made: by tiles of 128 rows on the tensor cores (`many`, with
+// clusters of `split`) or by the kernel for few rows, whichever costs less.
+// (Of 375 calls measured both ways it takes 0.5% longer than the faster on average, 78%
+// at most; by rows alone, more than 32 a sequence and head, it took up to 3.5 times as
+// long: one sequence with 2 heads, 400 rows each over 500 keys, is 29 us on tcgen05
+// and 9 here; 8 with 8 heads over 4000 keys 55 there with 32 rows and 56
+// with 48, here 44 and 83.)
+struct AttentionPlan {
+    bool many;
+    int split;
+    FewSplit few;
+};
+
+inline AttentionPlan attention_plan(long long tokens, int group, int seqs, int kv_heads, int keys, bool f32,
+                                    int num_sms) {
+    double few = 0, many = 0;
+    AttentionPlan p;
+    p.few = few_split(tokens, group, seqs, kv_heads, keys, f32, num_sms, few);
+    p.split = many_split(tokens * group, f32 ? 128 : 256, seqs, kv_heads, keys, f32, num_sms, many);
+    p.many = many < few;
+    return p;
 }
 
 }  // namespace q4mm

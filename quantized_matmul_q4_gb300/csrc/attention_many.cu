@@ -40,7 +40,6 @@
 #include <cstdint>
 
 #include "attention.cuh"
-#include "attention_geometry.h"
 #include "cluster.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -858,6 +857,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             ok = __all_sync(0xFFFFFFFFu, ok);
             return ok;
         };
+        const int held = withhold < 0 ? -1 : min(withhold, steps - 1);
         for (int i = 0; i < steps; ++i) {
             const uint8_t *at = from + (first_slot(a.cache, page, head) + 16 * within) * token_bytes;
             const bool mine = page >= 0;
@@ -871,10 +871,10 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 uint64_t *full = &sh.code_full[unit % L::kCodeSlots];
                 if (lane == 0) {
                     sh.valid[i % L::kMeta] = valid;
-                    if (i != withhold) mbar_arrive_expect_tx(full, groups * 16 * (row_bytes + (v ? 0 : 8)));
+                    if (i != held) mbar_arrive_expect_tx(full, groups * 16 * (row_bytes + (v ? 0 : 8)));
                 }
                 __syncwarp();
-                if (mine && i != withhold && (v ? kind == 3 : kind < 3)) {
+                if (mine && i != held && (v ? kind == 3 : kind < 3)) {
                     const uint32_t to = kind == 1 || kind == 2
                                             ? base + L::off_scales + i % 2 * 1024 + (kind - 1) * 512 + 64 * g16
                                             : base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 16 * g16 * row_bytes;
@@ -896,16 +896,13 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
 }
 
 template <int kBits, int kDP, int kTiles, int kNP>
-cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
+cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a, int S) {
     using L = ManyLayout<kBits, kDP, kTiles, kNP>;
     auto kernel = mx_attention_many_kernel<kBits, kDP, kTiles, kNP>;
     cudaError_t e = ensure_smem(kernel, L::total);
     if (e != cudaSuccess) return e;
     const int group = a.heads / a.cache.heads;
     const long long rows = (long long)a.tokens * group, tiles = rows / (128 * kTiles) + a.batch.seqs;
-    const long long keys = (long long)a.batch.width * a.cache.page;
-    const int S = many_split(rows, 128 * kTiles, a.batch.seqs, a.cache.heads, (int)(keys < 0x7FFFFFFF ? keys : 0x7FFFFFFF),
-                             c.num_sms);
     const long long ctas = tiles * a.cache.heads * S;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -926,16 +923,16 @@ cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a) {
 }
 
 template <int kBits, int kDP>
-cudaError_t launch_type(const LaunchCtx &c, const MxAttentionArgs &a) {
-    return a.type == MxType::kF32 ? launch_many<kBits, kDP, 1, 2>(c, a) : launch_many<kBits, kDP, 2, 1>(c, a);
+cudaError_t launch_type(const LaunchCtx &c, const MxAttentionArgs &a, int split) {
+    return a.type == MxType::kF32 ? launch_many<kBits, kDP, 1, 2>(c, a, split) : launch_many<kBits, kDP, 2, 1>(c, a, split);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a) {
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split) {
     const bool narrow = a.cache.D <= 64;
-    if (a.cache.bits == 4) return narrow ? launch_type<4, 64>(c, a) : launch_type<4, 128>(c, a);
-    return narrow ? launch_type<8, 64>(c, a) : launch_type<8, 128>(c, a);
+    if (a.cache.bits == 4) return narrow ? launch_type<4, 64>(c, a, split) : launch_type<4, 128>(c, a, split);
+    return narrow ? launch_type<8, 64>(c, a, split) : launch_type<8, 128>(c, a, split);
 }
 
 }  // namespace q4mm

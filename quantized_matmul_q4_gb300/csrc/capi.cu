@@ -56,6 +56,25 @@ struct TestFault {
 };
 thread_local TestFault g_test_fault;
 
+void take_fault(q4mm::LaunchCtx *ctx) {
+    if (!g_test_fault.armed) return;
+    ctx->wait_limit = g_test_fault.limit;
+    ctx->withhold = g_test_fault.stage;
+    g_test_fault.armed = false;
+}
+
+// The kernel that the calling thread's attention calls take, set by
+// q4mm_test_attention_kernel: 0 as planned, 1 few rows, 2 many.
+thread_local int g_test_attention = 0;
+
+q4mm::AttentionPlan plan_attention(int tokens, int heads, int kv_heads, int seqs, int width, int page, bool f32,
+                                   int num_sms) {
+    q4mm::AttentionPlan p = q4mm::attention_plan(tokens, heads / kv_heads, seqs, kv_heads, q4mm::table_keys(width, page),
+                                                 f32, num_sms);
+    if (g_test_attention) p.many = g_test_attention == 2;
+    return p;
+}
+
 // take_test_fault: a compute call (it consumes an armed test fault).
 int device_ctx(q4mm_stream_t stream, q4mm::LaunchCtx *ctx, bool take_test_fault = true) {
     int dev = 0;
@@ -84,11 +103,7 @@ int device_ctx(q4mm_stream_t stream, q4mm::LaunchCtx *ctx, bool take_test_fault 
     ctx->pdl = true;
     ctx->wait_limit = q4mm::kWaitLimitCycles;
     ctx->withhold = -1;
-    if (take_test_fault && g_test_fault.armed) {
-        ctx->wait_limit = g_test_fault.limit;
-        ctx->withhold = g_test_fault.stage;
-        g_test_fault.armed = false;
-    }
+    if (take_test_fault) take_fault(ctx);
     return Q4MM_OK;
 }
 
@@ -753,15 +768,18 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
             return rc;
     }
     q4mm::LaunchCtx ctx;
-    const bool many = q4mm::many_rows(tokens, heads / kvHeads, sequences);
     const bool vec = reinterpret_cast<uintptr_t>(q) % (4 * size) == 0 && reinterpret_cast<uintptr_t>(y) % (4 * size) == 0 &&
                      q_token_stride % 4 == 0 && q_head_stride % 4 == 0 && y_token_stride % 4 == 0 &&
                      y_head_stride % 4 == 0;
-    if ((rc = device_ctx(stream, &ctx, many))) return rc;
+    if ((rc = device_ctx(stream, &ctx, false))) return rc;
+    const q4mm::AttentionPlan plan = plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens,
+                                                    dtype == Q4MM_F32, ctx.num_sms);
+    if (plan.many) take_fault(&ctx);
     const q4mm::MxAttentionArgs a{call.cache, call.batch, q, q_token_stride, q_head_stride, y, y_token_stride,
                                   y_head_stride, scale, causal != 0, tokens, heads, static_cast<q4mm::MxType>(dtype),
                                   vec, static_cast<float *>(workspace), workspace_bytes, ctx.status};
-    const cudaError_t e = many ? q4mm::launch_mx_attention_many(ctx, a) : q4mm::launch_mx_attention_few(ctx, a);
+    const cudaError_t e =
+        plan.many ? q4mm::launch_mx_attention_many(ctx, a, plan.split) : q4mm::launch_mx_attention_few(ctx, a, plan.few);
     if (e != cudaSuccess) return fail_cuda(e, "mx_attention launch");
     return Q4MM_OK;
 }
@@ -770,11 +788,17 @@ size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequ
                               int heads) {
     if (kvHeads <= 0 || heads <= 0 || heads % kvHeads || pageTokens <= 0 || sequences <= 0 || tableWidth < 0 || tokens <= 0)
         return 0;
-    if (q4mm::many_rows(tokens, heads / kvHeads, sequences)) return 0;
     q4mm::LaunchCtx ctx;
     if (device_ctx(nullptr, &ctx, false)) return 0;
-    return q4mm::mx_attention_few_workspace(tokens, heads, kvHeads, headDim, sequences, tableWidth, pageTokens,
-                                            ctx.num_sms);
+    size_t most = 0;
+    for (int f32 = 0; f32 < 2; ++f32) {
+        const q4mm::AttentionPlan plan =
+            plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens, f32, ctx.num_sms);
+        const size_t bytes =
+            plan.many ? 0 : q4mm::mx_attention_few_workspace(tokens, heads, kvHeads, headDim, sequences, plan.few);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 int q4mm_call(int which, const long long *w) {
@@ -841,6 +865,12 @@ int q4mm_test_fail_next_wait(int stage, long long limit_cycles) {
     g_test_fault.armed = true;
     g_test_fault.stage = stage;
     g_test_fault.limit = limit_cycles;
+    return Q4MM_OK;
+}
+
+int q4mm_test_attention_kernel(int which) {
+    if (which < 0 || which > 2) return fail(Q4MM_ERR_DIM, "q4mm_test_attention_kernel: %d must be 0, 1 or 2", which);
+    g_test_attention = which;
     return Q4MM_OK;
 }
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <utility>
 
+#include "attention_geometry.h"
+
 namespace q4mm {
 
 struct LaunchCtx {
@@ -205,10 +207,10 @@ struct MxAttentionArgs {
     size_t workspace_bytes;
     int *status;
 };
-// Bytes of workspace with which the kernel for few rows uses every SM.
-size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, int width, int page, int num_sms);
-cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a);   // few rows a kv head
-cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a);  // tiles of 128, on tcgen05
+// Bytes of workspace that a split of few rows takes.
+size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, const FewSplit &f);
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f);  // few rows a kv head
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split);  // tiles of 128, on tcgen05
 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device; the attribute call is made only when the limit grows, so a

@@ -28,9 +28,7 @@ def geo(tmp_path_factory):
                     f"-I{os.path.join(ROOT, 'quantized_matmul_q4_gb300', 'csrc')}",
                     os.path.join(ROOT, "tests", "attention_geometry_shim.cpp"), "-o", out], check=True)
     lib = ctypes.CDLL(out)
-    lib.att_geo_few.argtypes = [ctypes.c_longlong] + [ctypes.c_int] * 6 + [ctypes.POINTER(ctypes.c_int)]
-    lib.att_geo_many.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int]
-    lib.att_geo_many_split.argtypes = [ctypes.c_longlong] + [ctypes.c_int] * 5
+    lib.att_geo.argtypes = [ctypes.c_longlong] + [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_int)]
     return lib
 
 
@@ -75,31 +73,35 @@ def test_frequencies_refuse_what_they_cannot_be(q4mm):
 # How the work is split.
 
 def test_few_rows_split(geo):
-    out = (ctypes.c_int * 4)()
-    for sms in (1, 132, 152):
+    out = (ctypes.c_int * 6)()
+    for sms, f32 in ((1, 0), (132, 1), (152, 0), (152, 1)):
         for tokens, seqs in ((1, 1), (1, 3), (64, 64), (300, 7), (5, 5), (8192, 1000)):
             for group in (1, 4, 7, 16):
                 for kv in (1, 5, 8, 32):
                     for width, page in ((1, 16), (63, 16), (40, 48), (8192, 16), (2 ** 21, 4096), (0, 16)):
-                        geo.att_geo_few(tokens, group, seqs, kv, width, page, sms, out)
-                        nr, tiles, cluster, parts = out
+                        geo.att_geo(tokens, group, seqs, kv, width, page, f32, sms, out)
+                        nr, tiles, cluster, parts, _, split = out
+                        assert split in (1, 2, 3, 4, 5, 6, 8) and split <= max(1, -(-min(width * page, 0x7FFFFFFF) // 128))
                         assert nr in (1, 2) and tiles == tokens * group // (8 * nr) + seqs
-                        assert cluster in (1, 2, 4, 8) and parts >= 1 and (parts == 1 or cluster == 8)
+                        assert nr == 1 or tokens * group > 8 * seqs
+                        assert cluster in (1, 2, 3, 4, 5, 6, 8) and parts >= 1 and (parts == 1 or cluster == 8)
                         groups = min(width * page, 0x7FFFFFFF) // 16
-                        if cluster * parts > 1:
-                            assert cluster * parts * 8 <= groups and tiles * kv * cluster * parts <= 2 * sms
+                        if parts > 1:   # a group a warp, and all of them resident; what is shared in vain costs
+                            even = seqs * -(-tokens * group // (8 * nr * seqs))
+                            assert cluster * parts * 8 <= groups and even * kv * cluster * parts <= 2 * sms
+                            assert (tokens * group // 8 + seqs) * kv < 64   # where the Python call asks for a workspace
+                        if groups <= 8:
+                            assert cluster == 1
 
 
-def test_many_rows_split(geo):
-    assert not geo.att_geo_many(64, 1, 64) and not geo.att_geo_many(8, 4, 1) and geo.att_geo_many(9, 4, 1)
-    for rows in (33, 128, 2048, 262144):
-        for seqs in (1, 4):
-            for kv in (1, 8, 32):
-                for keys in (0, 16, 1000, 8192, 2 ** 20):
-                    s = geo.att_geo_many_split(rows, 256, seqs, kv, keys, 152)
-                    assert s in (1, 2, 4, 8)
-                    if s > 1:
-                        assert max(rows // 256, seqs) * kv * s <= 152 and (keys + 127) // 128 >= 2 * s
+def test_which_kernel(geo):
+    out = (ctypes.c_int * 6)()
+    for tokens, group, seqs, kv, keys, f32, many, split in (
+            (1, 1, 1, 32, 1000, 0, 0, None), (64, 1, 64, 32, 4096, 0, 0, None), (1, 8, 1, 1, 2 ** 20, 0, 0, None),
+            (8192, 1, 1, 32, 8192, 0, 1, 1), (512, 8, 1, 4, 8192, 0, 1, 2), (2000, 4, 1, 8, 2000, 0, 1, None), (200, 4, 1, 1, 500, 0, 0, None),
+            (64, 4, 8, 8, 30000, 0, 0, None), (96, 4, 8, 8, 30000, 0, 1, 2), (2000, 4, 1, 8, 2000, 1, 1, None)):
+        geo.att_geo(tokens, group, seqs, kv, -(-keys // 16), 16, f32, 152, out)
+        assert out[4] == many and (split is None or out[5] == split), (tokens, group, seqs, kv, keys, list(out))
 
 
 def test_numbers_of_row_tiles():

@@ -34,6 +34,20 @@ def _torch():
     return torch
 
 
+@pytest.fixture(autouse=True)
+def kernel(request):
+    """The attention kernel that a test's calls take: as planned, or the one that `KERNELS` says."""
+    which = getattr(request, "param", None)
+    if which:
+        _q().force_attention_kernel(which)
+    yield which
+    if which:
+        _q().force_attention_kernel(None)
+
+
+KERNELS = pytest.mark.parametrize("kernel", ["few", "many"], indirect=True)
+
+
 def _q():
     import quantized_matmul_q4_gb300 as q
     return q
@@ -320,6 +334,7 @@ ATT = [  # new tokens, lengths, kv heads, group, D, page, bits
     ([300], [300], 1, 1, 128, 16, 4), ([129], [700], 1, 4, 128, 64, 8)]
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("news,lengths,heads,group,D,page,bits", ATT)
 def test_attention(news, lengths, heads, group, D, page, bits, dtype):
@@ -331,6 +346,7 @@ def test_attention(news, lengths, heads, group, D, page, bits, dtype):
     _check(c, x, y, xv, dtype)
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("news,lengths", [([1, 1], [70, 33]), ([20, 7], [100, 7]), ([140], [200])])
 def test_attention_without_causal_mask(news, lengths, dtype):
@@ -341,6 +357,7 @@ def test_attention_without_causal_mask(news, lengths, dtype):
     _check(c, x, y, xv, dtype, causal=False, scale=0.3)
 
 
+@KERNELS
 @pytest.mark.parametrize("news", [[3, 2], [60, 150]])
 def test_attention_rows_that_see_nothing(news):
     """More new rows than tokens, and sequences of no tokens: zeros; rows of no sequence stay."""
@@ -356,6 +373,7 @@ def test_attention_rows_that_see_nothing(news):
     assert (y[2 + news[0]:c.T] == 0).all()
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("n", [4, 100])
 def test_attention_strided(n, dtype):
@@ -371,6 +389,7 @@ def test_attention_strided(n, dtype):
     assert (buf[:, :, :3] == 9).all() and (buf[:, :, 99:] == 9).all()
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 150])
 @pytest.mark.parametrize("spread", ["tokens", "blocks", "queries"])
@@ -391,6 +410,7 @@ def test_attention_of_wide_ranges(spread, n, dtype):
     _check(c, x, y, xv, dtype)
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("n", [7, 150])
 def test_attention_hidden_keys_have_no_part(n, dtype):
@@ -410,6 +430,7 @@ def test_attention_hidden_keys_have_no_part(n, dtype):
     _check(d, few, y[:2], xv[:2], dtype)
 
 
+@KERNELS
 @pytest.mark.parametrize("n", [1, 3, 140])
 def test_attention_nan_stays_where_it_is_seen(n):
     """NaN blocks of k and v behind a row's last key, in other sequences' pages and in free ones do not reach it; seen
@@ -443,6 +464,7 @@ def test_attention_nan_stays_where_it_is_seen(n):
         assert bad[0, 0].all() and not bad[0, 1].any() and bad[1, 1].all() and not bad[1, 0].any()
 
 
+@KERNELS
 def test_attention_repeats_bit_by_bit():
     q, torch = _q(), _torch()
     for news, lengths, heads in (([1, 1], [3000, 777], 2), ([200], [1500], 1)):
@@ -464,6 +486,7 @@ def _bad_batches():
     yield "positions beyond the table", 5, lambda c: c.lengths.__setitem__(0, 10 ** 6)
 
 
+@KERNELS
 @pytest.mark.parametrize("n", [5, 150])
 @pytest.mark.parametrize("what", range(3))
 def test_bad_pages_are_reported_and_not_accessed(what, n):
@@ -552,6 +575,7 @@ def test_steps_in_a_graph_and_on_another_stream():
     q.device_status()
 
 
+@KERNELS
 def test_long_cache_offsets_pass_32_bits():
     """Pages whose bytes lie beyond 2^32 of the base."""
     q, torch = _q(), _torch()

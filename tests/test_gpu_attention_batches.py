@@ -20,6 +20,21 @@ def _torch():
     return torch
 
 
+@pytest.fixture(autouse=True)
+def kernel(request):
+    """The attention kernel that a test's calls take: as planned, or the one that `KERNELS` says."""
+    which = getattr(request, "param", None)
+    if which:
+        _q().force_attention_kernel(which)
+    yield which
+    if which:
+        _q().force_attention_kernel(None)
+
+
+KERNELS = pytest.mark.parametrize("kernel", ["few", "many"], indirect=True)
+MANY = pytest.mark.parametrize("kernel", ["many"], indirect=True)
+
+
 def _q():
     import quantized_matmul_q4_gb300 as q
     return q
@@ -90,6 +105,7 @@ LARGE = [  # new tokens, lengths, kv heads, group, D, page, bits
     ([2049], [2049], 1, 1, 128, 64, 8), ([700], [1500], 2, 3, 96, 16, 4), ([257], [5000], 1, 1, 128, 128, 8)]
 
 
+@KERNELS
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 @pytest.mark.parametrize("news,lengths,kv,group,D,page,bits", LARGE)
 def test_large(news, lengths, kv, group, D, page, bits, dtype):
@@ -122,6 +138,24 @@ def test_workspace_of_any_size(dtype):
     q.device_status()
 
 
+@KERNELS
+def test_long_fp32_sums_do_not_drift(kernel):
+    """Values of one over 60000 keys that no other CTA shares: outputs are one, and not always short of it.  A tensor-core
+    sum drops at most a step, 2^-23, each of the 33 times that it is added to, and fp32 additions round by
+    chance: over 16 rows and 60000 / 128 additions by sqrt(470) 2^-24 / 4 = 3.2e-7 on average."""
+    q, torch = _q(), _torch()
+    b = Batch([60000], [60000], 2, 64, 16, 8)
+    ones = torch.ones(60000, 2, 64, device="cuda")
+    q.mx_cache_write(b.cache, b.k, ones, *b.whole)
+    x = torch.randn(200, 8, 64, generator=b.g, device="cuda")
+    y = q.mx_attention(x, b.cache, torch.arange(201, dtype=torch.int32, device="cuda"), b.batch[1].expand(200).contiguous(),
+                       b.batch[2].expand(200, -1).contiguous())
+    q.device_status()
+    assert abs(float((y.double() - 1).mean())) < 33 * 2.0 ** -23 + 3.2e-7
+    assert float((y.double() - 1).abs().max()) < 2 * (33 + 60000 / 128) * 2.0 ** -23
+
+
+@KERNELS
 def test_a_sequence_alone_and_among_others():
     """A row's bits do not depend on the sequences beside it, as long as the keys are shared alike."""
     q, torch = _q(), _torch()
@@ -137,6 +171,7 @@ def test_a_sequence_alone_and_among_others():
         b.check(x, together)
 
 
+@KERNELS
 def test_new_tokens_in_any_chunks():
     """A prompt written and attended to in chunks gives, to the tolerance of both, what it gives at once."""
     q, torch = _q(), _torch()
@@ -156,6 +191,7 @@ def test_new_tokens_in_any_chunks():
         assert torch.equal(s, t)
 
 
+@KERNELS
 def test_streams_at_once():
     """Calls on four streams at once, parted ones with a workspace each among them, one on top of the next."""
     q, torch = _q(), _torch()
@@ -197,6 +233,7 @@ def test_two_graphs_of_parted_calls():
         assert torch.equal(want, y)
 
 
+@MANY
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("news,lengths,bits", [([300], [900], 8), ([200, 100], [200, 4000], 4)])
 def test_wait_runs_out_then_next_call_is_right(news, lengths, bits, dtype):
