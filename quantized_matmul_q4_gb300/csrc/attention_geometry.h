@@ -15,9 +15,10 @@ inline long long resident(int cluster, bool two, int num_sms) {
     return n > 0 ? n : 1;
 }
 
-// Row tiles of a sequence's share of the rows, over all sequences.
-inline long long even_tiles(long long rows, int tile_rows, int seqs) {
-    return seqs * ((rows + (long long)tile_rows * seqs - 1) / ((long long)tile_rows * seqs));
+// Row tiles where the rows are spread evenly over the sequences that can have any.
+inline long long even_tiles(long long tokens, int group, int tile_rows, int seqs) {
+    const long long some = tokens < seqs ? tokens : seqs, each = (long long)tile_rows * some;
+    return some * ((tokens * group + each - 1) / each);
 }
 
 constexpr int kFewWarps = 8;      // warps of a CTA for few rows
@@ -31,6 +32,8 @@ inline int table_keys(int width, int page) {
     const long long keys = (long long)width * page;
     return keys < 0x7FFFFFFF ? (int)keys : 0x7FFFFFFF;
 }
+
+constexpr int kPartedTiles = 64;  // tiles of 8 rows and key heads, at most, that are shared by several clusters
 
 // How few rows are split: tiles of 8 · rows_8 rows, the keys of each shared by
 // `parts` clusters of `cluster` CTAs, whose sums a second kernel joins.
@@ -65,18 +68,19 @@ inline double few_cost(long long tiles, int kv_heads, long long groups, const Fe
 // The split of least cost, as if the rows were spread evenly over the sequences and all of the table were keys.
 inline FewSplit few_split(long long tokens, int group, int seqs, int kv_heads, int keys, bool f32, int num_sms,
                           double &least) {
-    const long long rows = tokens * group, groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
+    const long long groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
     FewSplit best = {1, 1, 1};
     least = -1;
     const auto consider = [&](long long tiles, const FewSplit &f) {
         const double c = few_cost(tiles, kv_heads, groups, f, f32, num_sms);
         if (least < 0 || c < least) best = f, least = c;
     };
-    for (int nr = 1; nr <= (rows > 8LL * seqs ? 2 : 1); ++nr) {
-        const long long tiles = even_tiles(rows, 8 * nr, seqs);
+    for (int nr = 1; nr <= (tokens * group > 8LL * seqs ? 2 : 1); ++nr) {
+        const long long tiles = even_tiles(tokens, group, 8 * nr, seqs);
         for (int s = 1; s <= kMaxSplit; ++s)
             if (s != 7) consider(tiles, {nr, s, 1});
-        for (int two = 0; two < 2; ++two) {  // as many parts as are resident, alone on an SM or by twos
+        // As many parts as are resident, alone on an SM or by twos; a workspace has room for all tiles there may be.
+        for (int two = 0; two < 2 && few_tiles(tokens, group, 1, seqs) * kv_heads < kPartedTiles; ++two) {
             const long long parts = resident(kMaxSplit, two, num_sms) / (tiles * kv_heads);
             if (parts > 1 && parts * kMaxSplit * kFewWarps <= groups) consider(tiles, {nr, kMaxSplit, (int)parts});
         }
@@ -90,9 +94,9 @@ constexpr int kManyKeys = 128;  // keys of a tile on tcgen05
 // 17 us and 2.25 a tile of keys and pair of row tiles, 16.6 and 3.1 for fp32's
 // tile.  Fitted to 2600 measurements (1 and 4 sequences, 34 to 3000 rows, 400 to
 // 30000 keys); it takes 1.0% longer than their best on average.
-inline int many_split(long long rows, int tile_rows, int seqs, int kv_heads, int keys, bool f32, int num_sms,
+inline int many_split(long long tokens, int group, int tile_rows, int seqs, int kv_heads, int keys, bool f32, int num_sms,
                       double &least) {
-    const long long clusters = even_tiles(rows, tile_rows, seqs) * kv_heads;
+    const long long clusters = even_tiles(tokens, group, tile_rows, seqs) * kv_heads;
     const int tiles = (int)(((long long)keys + kManyKeys - 1) / kManyKeys);
     int best = 1;
     least = -1;
@@ -125,7 +129,7 @@ inline AttentionPlan attention_plan(long long tokens, int group, int seqs, int k
     double few = 0, many = 0;
     AttentionPlan p;
     p.few = few_split(tokens, group, seqs, kv_heads, keys, f32, num_sms, few);
-    p.split = many_split(tokens * group, f32 ? 128 : 256, seqs, kv_heads, keys, f32, num_sms, many);
+    p.split = many_split(tokens, group, f32 ? 128 : 256, seqs, kv_heads, keys, f32, num_sms, many);
     p.many = many < few;
     return p;
 }

@@ -75,7 +75,7 @@ def test_frequencies_refuse_what_they_cannot_be(q4mm):
 def test_few_rows_split(geo):
     out = (ctypes.c_int * 6)()
     for sms, f32 in ((1, 0), (132, 1), (152, 0), (152, 1)):
-        for tokens, seqs in ((1, 1), (1, 3), (64, 64), (300, 7), (5, 5), (8192, 1000)):
+        for tokens, seqs in ((1, 1), (1, 3), (2, 50), (64, 64), (300, 7), (5, 5), (8192, 1000), (1, 2 ** 24)):
             for group in (1, 4, 7, 16):
                 for kv in (1, 5, 8, 32):
                     for width, page in ((1, 16), (63, 16), (40, 48), (8192, 16), (2 ** 21, 4096), (0, 16)):
@@ -87,7 +87,8 @@ def test_few_rows_split(geo):
                         assert cluster in (1, 2, 3, 4, 5, 6, 8) and parts >= 1 and (parts == 1 or cluster == 8)
                         groups = min(width * page, 0x7FFFFFFF) // 16
                         if parts > 1:   # a group a warp, and all of them resident; what is shared in vain costs
-                            even = seqs * -(-tokens * group // (8 * nr * seqs))
+                            some = min(tokens, seqs)
+                            even = some * -(-tokens * group // (8 * nr * some))
                             assert cluster * parts * 8 <= groups and even * kv * cluster * parts <= 2 * sms
                             assert (tokens * group // 8 + seqs) * kv < 64   # where the Python call asks for a workspace
                         if groups <= 8:

@@ -575,6 +575,63 @@ def test_steps_in_a_graph_and_on_another_stream():
     q.device_status()
 
 
+def test_captured_without_a_call_before():
+    """A process whose first calls are captured: nothing of them needs a call outside a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, quantized_matmul_q4_gb300 as q
+cache = q.mx_cache(64, 1, 64, page=16)
+rope = q.Rope(q.rope_frequencies(64))
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+x, v = torch.randn(2, 200, 1, 64, device="cuda")
+many = (i32(0, 200), i32(200), torch.arange(64, dtype=torch.int32, device="cuda")[None])
+few = (i32(0, 1), i32(200), many[2])
+pos = torch.arange(200, device="cuda")
+def calls():
+    q.mx_cache_write(cache, x, v, *many, rope=rope)
+    out = [q.rope_rotate(x, pos, rope), *q.mx_cache_read(cache, *many, tokens=200)]
+    for which in ("few", "many"):
+        q.force_attention_kernel(which)
+        out.append(q.mx_attention(x, cache, *many))
+    q.force_attention_kernel(None)
+    return out + [q.mx_attention(x[:1], cache, *few)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+q.device_status()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@KERNELS
+def test_broadcast_inputs():
+    """Rows, heads, keys and values of stride zero."""
+    q, torch = _q(), _torch()
+    c = Case(12, [40], [50], 2, 64, 16, 8).fill()
+    one, _ = _dev(c.rng.normal(size=(1, 1, 64)), "float32")
+    row, _ = _dev(c.rng.normal(size=(1, 6, 64)), "float32")
+    for x in (one.expand(40, 6, 64), row.expand(40, 6, 64)):
+        y = q.mx_attention(x, c.device_cache(), *c.device_batch())
+        assert torch.equal(y, q.mx_attention(x.contiguous(), c.device_cache(), *c.device_batch()))
+    got, want = c.device_cache(), c.device_cache()
+    rope = q.Rope(q.rope_frequencies(64))
+    k = one.expand(40, 2, 64)
+    q.mx_cache_write(got, k, k, *c.device_batch(), rope=rope)
+    q.mx_cache_write(want, k.contiguous(), k.contiguous(), *c.device_batch(), rope=rope)
+    assert all(torch.equal(a, b) for a, b in zip(got[:4], want[:4]))
+    pos = torch.arange(40, device="cuda")
+    assert torch.equal(q.rope_rotate(k, pos, rope, out=torch.empty(40, 2, 64, device="cuda")), q.rope_rotate(k.contiguous(), pos, rope))
+
+
 @KERNELS
 def test_long_cache_offsets_pass_32_bits():
     """Pages whose bytes lie beyond 2^32 of the base."""
