@@ -77,7 +77,7 @@ def _i32(a):
 
 ROPE = [(1, 1, 32, 32, False), (1, 32, 128, 128, False), (5, 3, 96, 48, False), (3, 2, 64, 64, True),
         (7, 5, 128, 2, True), (9, 1, 80, 24, False), (4, 3, 33, 10, True), (6, 2, 250, 250, False), (2, 1, 1, 0, False),
-        (2500, 2, 64, 32, True), (2500, 3, 128, 128, False), (40, 7, 256, 256, True), (1, 700, 128, 128, False)]
+        (2500, 2, 64, 32, True), (2500, 3, 128, 128, False), (700, 3, 128, 128, False), (1301, 2, 96, 96, False), (40, 7, 256, 256, True), (1, 700, 128, 128, False)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -215,7 +215,8 @@ class Case:
 
 
 CACHE = [([1], [1], 1, 32, 16), ([1, 1, 1], [5, 17, 64], 3, 128, 16), ([3, 0, 40], [3, 9, 100], 2, 64, 48),
-         ([70], [200], 5, 96, 32), ([2, 5], [1, 33], 1, 128, 64), ([2600, 31], [2700, 31], 2, 64, 128)]
+         ([70], [200], 5, 96, 32), ([2, 5], [1, 33], 1, 128, 64), ([2600, 31], [2700, 31], 2, 64, 128),
+         ([800], [850], 3, 128, 16), ([1400, 9], [1500, 40], 2, 64, 32)]
 
 
 @pytest.mark.parametrize("bits", [4, 8])
@@ -293,6 +294,29 @@ def test_cache_write_turns_keys(R, interleaved, D, dtype, bits):
             above = mx.code_values(bits)[mx.nearest_code((w + o) / unit, bits)]
             assert ((below <= got) & (got <= above)).all()
     q.device_status()
+
+
+@pytest.mark.parametrize("T", [700, 1301, 2600])
+def test_rows_in_pieces_and_at_once(T):
+    """Rotated and written rows have the same bits whatever the number of rows that a call has."""
+    q, torch = _q(), _torch()
+    c = Case(T, [T], [T + 11], 3, 128, 16, 8)
+    k, _ = _dev(c.rng.normal(size=(T, 3, 128)), "bfloat16")
+    rope = q.Rope(q.rope_frequencies(128))
+    _, lengths, pages = c.device_batch()
+    at_once, pieces = c.device_cache(), c.device_cache()
+    q.mx_cache_write(at_once, k, k, *c.device_batch(), rope=rope)
+    turned = q.rope_rotate(k, torch.arange(11, T + 11, device="cuda"), rope)
+    for i in range(0, T, 100):
+        n = min(100, T - i)
+        q.mx_cache_write(pieces, k[i:i + n], k[i:i + n], _i32([0, n]), _i32([11 + i + n]), pages, rope=rope)
+        assert torch.equal(turned[i:i + n], q.rope_rotate(k[i:i + n], torch.arange(11 + i, 11 + i + n, device="cuda"), rope))
+    assert all(torch.equal(a, b) for a, b in zip(at_once[:4], pieces[:4]))
+    back = q.mx_cache_read(at_once, *c.device_batch(), tokens=T)
+    for i in range(0, T, 100):
+        n = min(100, T - i)
+        some = q.mx_cache_read(at_once, _i32([0, n]), _i32([11 + i + n]), pages, tokens=n)
+        assert torch.equal(back[0][i:i + n], some[0]) and torch.equal(back[1][i:i + n], some[1])
 
 
 def test_cache_write_specials():
