@@ -103,16 +103,29 @@ struct RowTile {
 // Tiles are numbered so that sequence i has those from starts[i]·group / R + i
 // on: no fewer than its rows need, found by bisection instead of a prefix sum.
 __device__ __forceinline__ RowTile row_tile(const MxBatchView &b, long long tile, int group, int R, int tokens) {
-    auto first_of = [&](int i) { return (long long)b.starts[i] * group / R + i; };
     RowTile t{};
-    const int i = warp_count_le(first_of, b.seqs, tile) - 1;
-    if (i < 0) return t;
-    const int s0 = b.starts[i], s1 = b.starts[i + 1];
+    int i, s0, s1, len;
+    long long from;
+    if (b.seqs < 32) {  // starts and lengths by one load each, a lane each
+        const int lane = threadIdx.x & 31;
+        const int mine = lane <= b.seqs ? b.starts[lane] : 0, mine_len = lane < b.seqs ? b.lengths[lane] : 0;
+        const long long mine_from = (long long)mine * group / R + lane;
+        i = __popc(__ballot_sync(0xFFFFFFFFu, lane < b.seqs && mine_from <= tile)) - 1;
+        if (i < 0) return t;
+        s0 = __shfl_sync(0xFFFFFFFFu, mine, i), s1 = __shfl_sync(0xFFFFFFFFu, mine, i + 1);
+        len = __shfl_sync(0xFFFFFFFFu, mine_len, i);
+        from = (long long)s0 * group / R + i;
+    } else {
+        auto first_of = [&](int j) { return (long long)b.starts[j] * group / R + j; };
+        i = warp_count_le(first_of, b.seqs, tile) - 1;
+        if (i < 0) return t;
+        s0 = b.starts[i], s1 = b.starts[i + 1], len = b.lengths[i], from = first_of(i);
+    }
     if (s0 < 0 || s1 > tokens || s1 <= s0) return t;
-    const long long first = (tile - first_of(i)) * R, all = (long long)(s1 - s0) * group;
+    const long long first = (tile - from) * R, all = (long long)(s1 - s0) * group;
     if (first < 0 || first >= all) return t;
     t.seq = i, t.first = (int)first, t.rows = (int)min((long long)R, all - first);
-    t.start = s0, t.fresh = s1 - s0, t.len = max(b.lengths[i], 0);
+    t.start = s0, t.fresh = s1 - s0, t.len = max(len, 0);
     return t;
 }
 

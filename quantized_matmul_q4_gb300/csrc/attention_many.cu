@@ -74,6 +74,7 @@ struct ManyLayout {
     static constexpr int kPitch = kDP + 4;
     static constexpr uint32_t total = off_end + 1024;  // the base is rounded up to 1024 bytes
     static_assert(total + 15 * 1024 <= kSmShared - kCtaSharedExtra, "room for ManyShared");
+    static_assert(256 * 48 <= kCodeSlots * kCodes, "room for a RowOut a row");
     static_assert(kTiles * kNP == 2 && kTiles * 128 * kPitch * 4 <= off_codes, "");
     static_assert(kSmShared - total - kCtaSharedExtra < kHalfTmemShared, "takes all of tensor memory");
     // Powers of tile i + kMeta are written when S of tile i + kMeta - kSlots / 2 is done, after P of tile i.
@@ -110,6 +111,15 @@ struct ManyShared {
 };
 
 static_assert(sizeof(ManyShared) <= 15 * 1024, "");
+
+// What a row's output is made of: how much each CTA's sums count, the
+// reciprocal of the sum, blocks that are NaN, its place in y.
+struct RowOut {
+    float by[kMaxSplit];
+    float scale;
+    int nan;
+    long long at;
+};
 
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -221,41 +231,51 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// kEach values of a row from d on, zeros past D.
-template <int kEach>
-__device__ __forceinline__ void load_row(const void *p, MxType type, long long at, int d, int D, bool vec,
-                                         float (&v)[kEach]) {
+// kEach neighbouring values as they lie in memory: floats (kNP == 2), or pairs of 16 bits.
+template <int kEach, int kNP>
+struct RawRow {
+    uint32_t w[kEach * kNP / 2];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) v[i] = 0.f;
-    if (d >= D) return;
-    if (type == MxType::kF32) {
-        const float *q = static_cast<const float *>(p) + at + d;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) v[i] = q[i];
-    } else if (vec) {
-        uint32_t w[kEach / 2];
-        if constexpr (kEach == 4) {
-            const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + at + d);
-            w[0] = u.x, w[1] = u.y;
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + at + d);
-        }
-#pragma unroll
-        for (int i = 0; i < kEach / 2; ++i) {
-            if (type == MxType::kF16) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        for (uint32_t &x : w) x = 0u;
+    }
+    __device__ __forceinline__ void load(const void *p, long long at, bool vec) {
+        constexpr int kWords = kEach * kNP / 2;
+        if (vec) {
+            const char *q = static_cast<const char *>(p) + at * (2 * kNP);
+            if constexpr (kWords == 4) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(q);
+                w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+            } else if constexpr (kWords == 2) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(q);
+                w[0] = u.x, w[1] = u.y;
             } else {
-                v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                w[0] = *reinterpret_cast<const uint32_t *>(q);
+            }
+        } else if constexpr (kNP == 2) {
+            const uint32_t *q = static_cast<const uint32_t *>(p) + at;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = q[i];
+        } else {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+        }
+    }
+    __device__ __forceinline__ void values(MxType type, float (&v)[kEach]) const {
+        if constexpr (kNP == 2) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach / 2; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+                v[2 * i] = type == MxType::kF16 ? f.x : __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = type == MxType::kF16 ? f.y : __uint_as_float(w[i] & 0xFFFF0000u);
             }
         }
-    } else {
-        const uint16_t *q = static_cast<const uint16_t *>(p) + at + d;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            v[i] = type == MxType::kF16 ? __half2float(__ushort_as_half(q[i])) : __uint_as_float((uint32_t)q[i] << 16);
     }
-}
+};
 
 template <int kBits, int kDP, int kTiles, int kNP>
 __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads, 1)
@@ -347,24 +367,30 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         const int t = warp / 8, side = warp / 4 % 2, quarter = warp % 4;
         const int mine = 128 * t + 32 * quarter + lane;  // this thread's row of the CTA's
         {
-            // Query rows to fp16, each by a power of two of its own, 16 a warp.
-            constexpr int kEach = kDP / 32;
+            // Query rows to fp16, each by a power of two of its own, 16 a warp,
+            // the loads of 8 under way at once (one after the other they took 6 us).
+            constexpr int kEach = kDP / 32, kAtOnce = 8;
             const uint32_t slab = base + t * kNP * L::kSlab;
             const int d = lane * kEach;
             const uint32_t col = (d / 64) * kHalf + (d % 8) * 2;
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const int r = 32 * quarter + 16 * side + i;  // row of the slab
-                const int row = tile.first + 128 * t + r;
-                float v[kEach];
-                if (128 * t + r < tile.rows) {
-                    const long long at = (long long)(tile.start + row / group) * a.q_token +
-                                         (long long)(head * group + row % group) * a.q_head;
-                    load_row<kEach>(a.q, a.type, at, d, D, a.vec, v);
-                } else {
+            const int first = 128 * t + 32 * quarter + 16 * side;  // of the tile's
+            int tok = (tile.first + first) / group, row_head = (tile.first + first) % group;
+#pragma unroll 1
+            for (int b = 0; b < 16; b += kAtOnce) {
+            RawRow<kEach, kNP> rows[kAtOnce];
 #pragma unroll
-                    for (int k = 0; k < kEach; ++k) v[k] = 0.f;
-                }
+            for (int i = 0; i < kAtOnce; ++i) {
+                rows[i].zero();
+                if (first + b + i < tile.rows && d < D)
+                    rows[i].load(a.q, (long long)(tile.start + tok) * a.q_token + (long long)(head * group + row_head) * a.q_head + d,
+                                 a.vec);
+                if (++row_head == group) row_head = 0, ++tok;
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int r = 32 * quarter + 16 * side + b + i;  // row of the slab
+                float v[kEach];
+                rows[i].values(a.type, v);
                 uint32_t top = 0;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
@@ -394,6 +420,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                     else
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kSlab), "r"(lo[0]) : "memory");
                 }
+            }
             }
         }
         fence_async_proxy();
@@ -571,45 +598,59 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             tc_fence_before();
         }
         meet();
-        if (*abort == 0) {
+        {
+            // Each CTA of the cluster joins and writes its share of the rows:
+            // first a thread a row, by how much each CTA's sums count.
             const int parts = (int)cluster_size(), part = (int)cluster_rank();
-            constexpr int kThreads = 32 * L::kSoftmaxWarps;
-            const float *o = reinterpret_cast<const float *>(raw + (base - smem_addr(raw)));
+            constexpr int kThreads = 32 * L::kSoftmaxWarps, kQuads = kDP / 4;
+            const int r0 = tile.rows * part / parts, here = tile.rows * (part + 1) / parts - r0;
+            RowOut *out = reinterpret_cast<RowOut *>(raw + (base - smem_addr(raw)) + L::off_codes);
             const uint32_t m_at = smem_addr(sh.m), l_at = smem_addr(sh.l), n_at = smem_addr(sh.nan_from);
-            for (int i = part * kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += parts * kThreads) {
-                const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
-                if (d >= D) continue;
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                float ls = 0.f;
-                int nan_from;
-                if (parts == 1) {
-                    sum = *reinterpret_cast<const float4 *>(o + r * L::kPitch + d);
-                    ls = sh.l[0][r] + sh.l[1][r], nan_from = sh.nan_from[d / kMxBlock];
-                } else {
-                    float m = -INFINITY;
-                    nan_from = kNever;
-                    for (int s = 0; s < parts; ++s) {
-                        m = fmaxf(m, ld_cluster_f32(map_to_rank(m_at + 4 * r, s)));
-                        nan_from = min(nan_from, __float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * (d / kMxBlock), s))));
-                    }
-                    for (int s = 0; s < parts; ++s) {
-                        const float mi = ld_cluster_f32(map_to_rank(m_at + 4 * r, s));
-                        const float li = ld_cluster_f32(map_to_rank(l_at + 4 * r, s)) +
-                                         ld_cluster_f32(map_to_rank(l_at + 4 * (256 + r), s));
-                        const float4 v = ld_cluster_v4(map_to_rank(base + 4 * (r * L::kPitch + d), s));
-                        const float by = mi == -INFINITY ? 0.f : ex2(mi - m);
-                        ls += mi == -INFINITY ? li : by * li;
-                        sum.x = fmaf(by, v.x, sum.x), sum.y = fmaf(by, v.y, sum.y);
-                        sum.z = fmaf(by, v.z, sum.z), sum.w = fmaf(by, v.w, sum.w);
-                    }
+            if ((int)threadIdx.x < here) {
+                const int r = r0 + threadIdx.x, row = tile.first + r, tok = row / group, sees = keys_of(tile, row, group, a.causal);
+                float m[kMaxSplit], l[kMaxSplit], top = -INFINITY, ls = 0.f;
+                RowOut o;
+                o.nan = 0;
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s) {
+                    m[s] = -INFINITY, l[s] = 0.f;
+                    if (s >= parts) continue;
+                    m[s] = ld_cluster_f32(map_to_rank(m_at + 4 * r, s));
+                    l[s] = ld_cluster_f32(map_to_rank(l_at + 4 * r, s)) + ld_cluster_f32(map_to_rank(l_at + 4 * (256 + r), s));
+#pragma unroll
+                    for (int b = 0; b < kDP / kMxBlock; ++b)
+                        o.nan |= (__float_as_int(ld_cluster_f32(map_to_rank(n_at + 4 * b, s))) < sees) << b;
+                    top = fmaxf(top, m[s]);
                 }
-                const int row = tile.first + r;
-                if (nan_from < keys_of(tile, row, group, a.causal)) ls = __int_as_float(0x7FC00000);
-                const long long at = (long long)(tile.start + row / group) * a.y_token +
-                                     (long long)(head * group + row % group) * a.y_head + d;
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s) {
+                    o.by[s] = m[s] == -INFINITY ? 0.f : ex2(m[s] - top);
+                    ls += m[s] == -INFINITY ? l[s] : o.by[s] * l[s];
+                }
                 // A row that sees nothing has no sum: zeros.
-                const float by = ls == 0.f ? 0.f : 1.f / ls;
-                store4(a.y, a.type, at, a.vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
+                o.scale = ls == 0.f ? 0.f : 1.f / ls;
+                o.at = (long long)(tile.start + tok) * a.y_token + (long long)(head * group + row - tok * group) * a.y_head;
+                out[threadIdx.x] = o;
+            }
+            named_bar_sync(9, kThreads);  // (1 to 8 are the halves' of a quarter)
+            for (int i = *abort ? here * kQuads : (int)threadIdx.x; i < here * kQuads; i += kThreads) {
+                const int r = i / kQuads, d = 4 * (i % kQuads);
+                if (d >= D) continue;
+                const RowOut &o = out[r];
+                const uint32_t from = base + 4 * ((r0 + r) * L::kPitch + d);
+                float4 v[kMaxSplit];
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s)
+                    if (s < parts) v[s] = ld_cluster_v4(map_to_rank(from, s));
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int s = 0; s < kMaxSplit; ++s) {
+                    if (s >= parts) continue;
+                    sum.x = fmaf(o.by[s], v[s].x, sum.x), sum.y = fmaf(o.by[s], v[s].y, sum.y);
+                    sum.z = fmaf(o.by[s], v[s].z, sum.z), sum.w = fmaf(o.by[s], v[s].w, sum.w);
+                }
+                const float by = o.nan >> (d / kMxBlock) & 1 ? __int_as_float(0x7FC00000) : o.scale;
+                store4(a.y, a.type, o.at + d, a.vec, make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by));
             }
         }
         leave();
