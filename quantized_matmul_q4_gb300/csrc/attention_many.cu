@@ -633,7 +633,28 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 out[threadIdx.x] = o;
             }
             named_bar_sync(9, kThreads);  // (1 to 8 are the halves' of a quarter)
-            for (int i = *abort ? here * kQuads : (int)threadIdx.x; i < here * kQuads; i += kThreads) {
+            const int all_quads = *abort ? 0 : here * kQuads;
+            if (parts == 1) {  // the sums lie here: four at a time
+                const float *sums = reinterpret_cast<const float *>(raw + (base - smem_addr(raw)));
+                for (int i = threadIdx.x; i < all_quads; i += 4 * kThreads) {
+                    float4 v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = i + k * kThreads;
+                        if (at < all_quads)
+                            v[k] = *reinterpret_cast<const float4 *>(sums + at / kQuads * L::kPitch + 4 * (at % kQuads));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = i + k * kThreads, d = 4 * (at % kQuads);
+                        if (at >= all_quads || d >= D) continue;
+                        const RowOut &o = out[at / kQuads];
+                        const float by = o.by[0] * (o.nan >> (d / kMxBlock) & 1 ? __int_as_float(0x7FC00000) : o.scale);
+                        store4(a.y, a.type, o.at + d, a.vec, make_float4(v[k].x * by, v[k].y * by, v[k].z * by, v[k].w * by));
+                    }
+                }
+            }
+            for (int i = parts == 1 ? all_quads : (int)threadIdx.x; i < all_quads; i += kThreads) {
                 const int r = i / kQuads, d = 4 * (i % kQuads);
                 if (d >= D) continue;
                 const RowOut &o = out[r];
