@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     const int D = a.cache.D, blocks = D / kMxBlock;
 
     pdl_wait();
-    long long item = blockIdx.x / S;
-    const int part = (int)(item % parts);
-    item /= parts;
-    const int head = (int)(item % a.cache.heads);
-    const RowTile tile = row_tile(a.batch, item / a.cache.heads, group, kR, a.tokens);
+    // (Divisions of 32 bits here and below: ones of 64 take a hundred instructions each.)
+    unsigned item = blockIdx.x / (unsigned)S;
+    const int part = (int)(item % (unsigned)parts);
+    item /= (unsigned)parts;
+    const int head = (int)(item % (unsigned)a.cache.heads);
+    const RowTile tile = row_tile(a.batch, item / (unsigned)a.cache.heads, group, kR, a.tokens);
     if (tile.rows == 0) return;  // with the whole cluster
 
     // Keys that any row sees, in groups, and this CTA's share of them.
@@ -180,7 +181,11 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     }
     const int groups = (keys + kFewGroup - 1) / kFewGroup;
     const int share = part * S + rank, shares = parts * S;
-    const int g0 = (int)((long long)groups * share / shares), g1 = (int)((long long)groups * (share + 1) / shares);
+    auto first_group = [&](int i) {
+        return shares < 1024 && groups < 1 << 21 ? (int)((unsigned)groups * (unsigned)i / (unsigned)shares)
+                                                 : (int)((long long)groups * i / shares);
+    };
+    const int g0 = first_group(share), g1 = first_group(share + 1);
 
     // The warp's groups, every kFewWarps-th: copies of the next ones under way.
     const int per_page = a.cache.page / kFewGroup, row_bytes = D * kBits / 8;

@@ -294,10 +294,11 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
     volatile int *abort = &sh.abort;
 
     pdl_wait();
-    const long long item = blockIdx.x / S;
-    const int head = (int)(item % a.cache.heads);
+    // (Divisions of 32 bits here: ones of 64 take a hundred instructions each.)
+    const unsigned item = blockIdx.x / (unsigned)S;
+    const int head = (int)(item % (unsigned)a.cache.heads);
     // (The last tiles first: with a causal mask they see the most keys.)
-    const RowTile tile = row_tile(a.batch, tiles - 1 - item / a.cache.heads, group, kRows, a.tokens);
+    const RowTile tile = row_tile(a.batch, tiles - 1 - item / (unsigned)a.cache.heads, group, kRows, a.tokens);
     if (tile.rows == 0) return;  // with the whole cluster
 
     // Keys that each tile of 128 rows sees, in tiles of 128, and this CTA's share of them.
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         cnt[t] = (n + kManyKeys - 1) / kManyKeys;
     }
     const int all = max(cnt[0], cnt[1]);
-    const int j0 = (int)((long long)all * rank / S), j1 = (int)((long long)all * (rank + 1) / S);
+    // (A tile is 128 keys: all · S is below 2^28.)
+    const int j0 = (int)((unsigned)all * (unsigned)rank / (unsigned)S), j1 = (int)((unsigned)all * (unsigned)(rank + 1) / (unsigned)S);
     cnt[0] = uniform(max(min(cnt[0], j1) - j0, 0)), cnt[1] = uniform(max(min(cnt[1], j1) - j0, 0));
     const int steps = max(cnt[0], cnt[1]);
 
