@@ -26,6 +26,7 @@
 // CTAs a tile leave SMs idle, several clusters share it, and a second kernel
 // joins what they leave in the caller's workspace.
 #include <cstdint>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "attention_geometry.h"
@@ -95,12 +96,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
     return v;
-}
-
-__device__ __forceinline__ float value_at(const void *p, MxType type, long long i) {
-    return type == MxType::kF32   ? static_cast<const float *>(p)[i]
-           : type == MxType::kF16 ? __half2float(static_cast<const __half *>(p)[i])
-                                  : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
 // Sums over parts of the keys, each under a maximum of its own.
@@ -187,6 +182,22 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     };
     const int g0 = first_group(share), g1 = first_group(share + 1);
 
+    // The warp's query rows, on their way while the first page is looked up.
+    constexpr int kEachLane = kDP / 32;
+    std::conditional_t<kNP == 2, float, uint16_t> query[kNR][kEachLane];
+#pragma unroll
+    for (int n = 0; n < kNR; ++n) {
+        const int r = warp + kFewWarps * n, row = tile.first + r;
+        const auto *x = static_cast<const std::remove_reference_t<decltype(query[0][0])> *>(a.q) +
+                        ((long long)(tile.start + row / group) * a.q_token +
+                         (long long)(head * group + row % group) * a.q_head + lane);
+#pragma unroll
+        for (int i = 0; i < kEachLane; ++i) {
+            query[n][i] = 0;
+            if (r < tile.rows && lane + 32 * i < D) query[n][i] = x[32 * i];
+        }
+    }
+
     // The warp's groups, every kFewWarps-th: copies of the next ones under way.
     const int per_page = a.cache.page / kFewGroup, row_bytes = D * kBits / 8;
     int piece = (g0 + warp) / per_page, within = (g0 + warp) % per_page;  // page and group within it
@@ -239,19 +250,21 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     for (int i = 0; i < kStages - 1; ++i) copy(i);
 
     // Query rows to fp16, each by a power of two of its own.
-    for (int r = warp; r < kR; r += kFewWarps) {
-        constexpr int kEachLane = kDP / 32;
+#pragma unroll
+    for (int n = 0; n < kNR; ++n) {
+        const int r = warp + kFewWarps * n;
         float v[kEachLane];
-        uint32_t top = 0;
-        const int row = tile.first + r;
-        const long long at = (long long)(tile.start + row / group) * a.q_token +
-                             (long long)(head * group + row % group) * a.q_head;
 #pragma unroll
         for (int i = 0; i < kEachLane; ++i) {
-            const int d = lane + 32 * i;
-            v[i] = r < tile.rows && d < D ? value_at(a.q, a.type, at + d) : 0.f;
-            top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            if constexpr (kNP == 2)
+                v[i] = query[n][i];
+            else
+                v[i] = a.type == MxType::kF16 ? __half2float(__ushort_as_half(query[n][i]))
+                                              : __uint_as_float((uint32_t)query[n][i] << 16);
         }
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kEachLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         // 2^(141 - e) puts a largest value of biased exponent e at 2^14; not where it is infinite or NaN.
         const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
