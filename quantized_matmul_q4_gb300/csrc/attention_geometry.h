@@ -42,26 +42,27 @@ struct FewSplit {
 };
 
 // Microseconds of a split. A CTA is paid for by the rounds of 8 groups that
-// its warps take: 5 and 1.06 a round alone on its SM, 6.25 and 1.36 for two there, where
-// the registers leave room for two (8 rows, 16-bit), and 7 and 1.1 with 16
-// rows; fp32 takes 5.5 and 1.26, 7 and 1.5.  A cluster costs 1.4, the second
-// kernel 2.7 and 0.3 a part.  These were fitted to 9500 measurements, of 1 to
-// 64 sequences, 60 to 40000 keys, 8 to 32 rows: the split of least cost takes
-// 1.3% longer than the best of those measured on average, 21% at most (one that
-// fills the SMs' places twice with clusters of 1, 2, 4 or 8 14% and 129%: of 8
-// sequences with 8 heads over 8000 keys 51.9 us in clusters of 2, 32.2 in clusters of 4;
-// of 20 with 5 over 1000, 19.4 whole, 15.3 in clusters of 2).
+// its warps take: 4 and 1.04 a round alone on its SM, 4.9 and 1.34 for two there, where
+// the registers leave room for two (8 rows, 16-bit), and 5 and 1.08 with 16
+// rows; fp32 takes 4.3 and 1.2, 5.4 and 1.48.  A cluster costs 1.5, the second
+// kernel 2.4 and 0.3 a part.  These were fitted to 9000 measurements, of 1 to
+// 64 sequences, 60 to 40000 keys, 8 to 24 rows: the split of least cost takes
+// 1.1% longer than the best of those measured on average, 16% at most (one that
+// fills the SMs' places twice with clusters of 1, 2, 4 or 8 14% and 129%).  8 sequences
+// with 8 heads over 8000 keys, whole, in clusters of 2, 4 and 8: 71.6, 49.5, 30.6, 38.1 us;
+// 20 with 5 over 1000, 7 rows, by tiles of 8 and of 16: whole 17.4 and 15.9, in
+// clusters of 2 13.7 and 21.8.
 inline double few_cost(long long tiles, int kv_heads, long long groups, const FewSplit &f, bool f32, int num_sms) {
     const long long clusters = tiles * kv_heads * f.parts, shares = (long long)kFewWarps * f.cluster * f.parts;
     const double rounds = (double)((groups + shares - 1) / shares);
-    const double more = (f.cluster > 1 ? 1.4 : 0) + (f.parts > 1 ? 2.7 + 0.3 * f.parts : 0);
+    const double more = (f.cluster > 1 ? 1.5 : 0) + (f.parts > 1 ? 2.4 + 0.3 * f.parts : 0);
     const long long one = resident(f.cluster, false, num_sms);
     if (f.rows_8 == 1 && !f32) {
         const long long two = resident(f.cluster, true, num_sms), rest = clusters % two;
-        const double alone = 5 + 1.06 * rounds, pair = 6.25 + 1.36 * rounds;
+        const double alone = 4 + 1.04 * rounds, pair = 4.9 + 1.34 * rounds;
         return more + (double)(clusters / two) * pair + (rest == 0 ? 0 : rest <= one ? alone : pair);
     }
-    const double each = !f32 ? 7 + 1.1 * rounds : f.rows_8 == 1 ? 5.5 + 1.26 * rounds : 7 + 1.5 * rounds;
+    const double each = !f32 ? 5 + 1.08 * rounds : f.rows_8 == 1 ? 4.3 + 1.2 * rounds : 5.4 + 1.48 * rounds;
     return more + (double)((clusters + one - 1) / one) * each;
 }
 
@@ -91,9 +92,9 @@ inline FewSplit few_split(long long tokens, int group, int seqs, int kv_heads, i
 constexpr int kManyKeys = 128;  // keys of a tile on tcgen05
 
 // CTAs of a cluster that share a tile's keys there, by the same kind of cost:
-// 17 us and 2.25 a tile of keys and pair of row tiles, 16.6 and 3.1 for fp32's
-// tile.  Fitted to 2600 measurements (1 and 4 sequences, 34 to 3000 rows, 400 to
-// 30000 keys); it takes 1.0% longer than their best on average.
+// 8 us and 2.2 a tile of keys and pair of row tiles, 5.4 and 3.0 for fp32's
+// tile, 2.6 for a cluster.  Fitted to 2600 measurements (1 and 4 sequences, 34 to 3000
+// rows, 400 to 30000 keys); it takes 1.1% longer than their best on average.
 inline int many_split(long long tokens, int group, int tile_rows, int seqs, int kv_heads, int keys, bool f32, int num_sms,
                       double &least) {
     const long long clusters = even_tiles(tokens, group, tile_rows, seqs) * kv_heads;
@@ -105,7 +106,7 @@ inline int many_split(long long tokens, int group, int tile_rows, int seqs, int 
         const long long n = resident(s, false, num_sms);
         const double waves = clusters <= 3 * n ? (double)((clusters + n - 1) / n) : (double)clusters / n + 0.5;
         const int each = (tiles + s - 1) / s;
-        const double c = 3 + waves * ((f32 ? 13.6 + 3.1 * each : 14 + 2.25 * each) + (s > 1 ? 0.9 : 0));
+        const double c = 3 + waves * ((f32 ? 5.4 + 3.0 * each : 8 + 2.2 * each) + (s > 1 ? 2.6 : 0));
         if (least < 0 || c < least) best = s, least = c;
     }
     return best;
@@ -113,11 +114,11 @@ inline int many_split(long long tokens, int group, int tile_rows, int seqs, int 
 
 // How a call is made: by tiles of 128 rows on the tensor cores (`many`, with
 // clusters of `split`) or by the kernel for few rows, whichever costs less.
-// (Of 375 calls measured both ways it takes 0.5% longer than the faster on average, 78%
-// at most; by rows alone, more than 32 a sequence and head, it took up to 3.5 times as
-// long: one sequence with 2 heads, 400 rows each over 500 keys, is 29 us on tcgen05
-// and 9 here; 8 with 8 heads over 4000 keys 55 there with 32 rows and 56
-// with 48, here 44 and 83.)
+// (Of 375 calls measured both ways it takes 0.2% longer than the faster on average, 57%
+// at most.  By rows alone, more than 32 a sequence and head, it took up to twice as
+// long: one sequence with 2 heads, 400 rows each, over 500, 2600 and 8100 keys takes
+// 17.0, 22.7 and 35.7 us on tcgen05, 8.5, 18.2 and 41.3 as few rows; 4 sequences with 8
+// heads over 2500 keys with 32 rows 23.2 and 19.0, with 120 24.7 and 54.0.)
 struct AttentionPlan {
     bool many;
     int split;
