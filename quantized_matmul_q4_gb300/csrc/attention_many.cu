@@ -5,13 +5,18 @@
 //   P             = 2^(...)  into tensor memory, over S
 //   O[row][value] += P V     fp32 in tensor memory
 //
-// What bounds it is the tensor pipe (two products of 128 x 128 x D a tile and
-// 128 keys) together with the issue slots of the softmax: 256 rows a CTA take
-// 2048 cycles of the pipe per 128 keys, some 3 instructions a score in the
-// softmax 800 issue cycles of each of the SM's four schedulers, the exponentials
-// 1024 cycles of the special functions, and the codes of 256 rows of K and V
-// 400.  So two tiles of 128 rows share every dequantised key and value, and
-// while the softmax of one is computed the pipe works on the other.
+// What bounds it is the chain of a tile's softmax and the issue slots that it
+// shares with the other's.  256 rows by 128 keys take 2048 cycles of the tensor
+// pipe (two products of 128 x 128 x D a tile), 1024 of the special functions, and
+// some 2500 issue slots of each of the SM's four schedulers: a third the
+// arithmetic of the scores, a fifth the codes of K and V, the rest what each of
+// 16 warps does once a tile.  They take 4400 cycles.  So two tiles of 128
+// rows share every dequantised key and value, and while the softmax of one is
+// computed the pipe works on the other.  A prompt of 8192 tokens, 32 heads of
+// 128, 8 bits: 531 us, 1036 TFLOP/s (55% of the measured bf16 rate); 512 tokens over 8192,
+// 4 key heads of 8: 79 us, 844 TFLOP/s.  (Halves of a row that go by a maximum of their
+// own, so that each waits for 64 keys' products alone: 695 us; one warp a quarter
+// with whole rows has no exchange, but too few warps.)
 //
 // Warps of a CTA:
 //   softmax  eight a tile: a thread has half of a row's 128 scores, so that

@@ -13,6 +13,11 @@
 // all heads: their angles are computed once, and in the cache the tokens of a
 // head lie next to each other.
 //
+// Rope of 8192 x 32 x 128 bf16: 22.5 us (88% of the measured copy rate); 28000 tokens
+// of 8 heads read from 8 bits to bf16: 24.5 (77%); 8271 tokens of 32 heads rotated
+// and written from fp16 to 8 bits: 43.5 (69%), 59% of the issue slots and the loads' latency
+// (each lane holds 32 to 64 bytes of loads, 32 warps an SM).
+//
 // Angles.  p·f in radians needs some 20 bits before the point for far
 // positions and 24 behind it.  So f / 2π, in turns, is taken as a 64-bit
 // fraction, and the product with the integer p modulo 2^64 is the angle
