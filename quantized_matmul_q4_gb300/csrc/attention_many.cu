@@ -13,8 +13,8 @@
 // 16 warps does once a tile.  They take 4400 cycles.  So two tiles of 128
 // rows share every dequantised key and value, and while the softmax of one is
 // computed the pipe works on the other.  A prompt of 8192 tokens, 32 heads of
-// 128, 8 bits: 531 us, 1036 TFLOP/s (55% of the measured bf16 rate); 512 tokens over 8192,
-// 4 key heads of 8: 79 us, 844 TFLOP/s.  (Halves of a row that go by a maximum of their
+// 128, 8 bits: 527 us, 1044 TFLOP/s (55% of the measured bf16 rate); 512 tokens over 8192,
+// 4 key heads of 8: 79 us, 846 TFLOP/s.  (Halves of a row that go by a maximum of their
 // own, so that each waits for 64 keys' products alone: 695 us; one warp a quarter
 // with whole rows has no exchange, but too few warps.)
 //
@@ -444,6 +444,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         const uint32_t sum_at = tmem + lanes + L::kColSum + kDP / 2 * side;
         float M = -INFINITY, l = 0.f;
         const int n = cnt[t];
+        // Keys of this half, from the CTA's first on, that every row of the warp sees.
+        const int full = __reduce_min_sync(0xFFFFFFFFu, sees - kManyKeys * j0 - 64 * side);
         bool go = true;  // the two warps of a quarter leave together, also after a time-out
         for (int i = 0; i < n && go; ++i) {
             const int mi = i % L::kMeta;
@@ -452,8 +454,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) give_up();
             tc_fence_after();
-            const int lim = sees - kManyKeys * (j0 + i) - 64 * side;  // these keys below it are seen
-            const bool partial = __any_sync(0xFFFFFFFFu, lim < 64);
+            const bool partial = kManyKeys * i + 64 > full;
+            const int lim = partial ? sees - kManyKeys * (j0 + i) - 64 * side : 64;  // these keys below it are seen
             uint32_t x[2][32];
             tc_ld64(s_at, x[0], x[1]);
             float factor[2], vref[2], top = -INFINITY;
