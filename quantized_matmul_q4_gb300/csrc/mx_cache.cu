@@ -14,8 +14,8 @@
 // head lie next to each other.
 //
 // Rope of 8192 x 32 x 128 bf16: 22.5 us (88% of the measured copy rate); 28000 tokens
-// of 8 heads read from 8 bits to bf16: 24.5 (77%); 8271 tokens of 32 heads rotated
-// and written from fp16 to 8 bits: 43.5 (69%), 59% of the issue slots and the loads' latency
+// of 8 heads read from 8 bits to bf16: 24.1 (79%); 8271 tokens of 32 heads rotated
+// and written from fp16 to 8 bits: 43.2 (70%), 59% of the issue slots and the loads' latency
 // (each lane holds 32 to 64 bytes of loads, 32 warps an SM).
 //
 // Angles.  p·f in radians needs some 20 bits before the point for far
@@ -321,11 +321,21 @@ struct Places {
 __device__ __forceinline__ void find_places(Places &p, const MxBatchView &b, const MxCacheView &c, long long t0,
                                             int tokens, int *status) {
     for (int s = threadIdx.x / 32; s < tokens; s += kWarps) {
-        const int i = sequence_of_row(b, t0 + s);
+        int i, len = 0, end = 0;
+        if (b.seqs < 32) {  // starts and lengths by one load each, a lane each
+            const int lane = threadIdx.x & 31;
+            const int start = lane <= b.seqs ? b.starts[lane] : 0x7FFFFFFF, mine = lane < b.seqs ? b.lengths[lane] : 0;
+            i = __popc(__ballot_sync(0xFFFFFFFFu, start <= t0 + s && lane <= b.seqs)) - 1;
+            len = __shfl_sync(0xFFFFFFFFu, mine, max(i, 0)), end = __shfl_sync(0xFFFFFFFFu, start, (i + 1) & 31);
+            if (i >= b.seqs) i = -1;
+        } else {
+            i = sequence_of_row(b, t0 + s);
+            if (i >= 0) len = b.lengths[i], end = b.starts[i + 1];
+        }
         long long slot = -1;
         int pos = 0;
         if (i >= 0) {
-            pos = (int)max((long long)b.lengths[i] - b.starts[i + 1] + (t0 + s), -1LL);
+            pos = (int)max((long long)len - end + (t0 + s), -1LL);
             if (pos >= 0) {
                 const int page = page_of(b, c, i, pos / c.page, status);
                 if (page >= 0) slot = first_slot(c, page, 0) + pos % c.page;
