@@ -501,7 +501,8 @@ int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride
  *
  * mx_cache_write — k, v [tokens][kvHeads][headDim] of type dtype, strided as
  * for rope_rotate, to their places: k turned as by rope_rotate at its positions
- * (rotated = 0: as it is) in fp32 and then quantised, with no rounding between.
+ * (rotated = 0: as it is) in fp32, near a border between two codes in 64 bits,
+ * and then quantised, with no rounding between.
  * Two rows must not have the same place (pages of one table shared with
  * another sequence hold what neither writes).
  *
@@ -589,9 +590,10 @@ int q4mm_device_status(q4mm_stream_t stream, int clear);
  * q4mm_test_fail_next_wait — a test hook for the library's failure
  * detection; the pages have no counterpart.  The calling thread's next call
  * of q4k_matmul (one-token and 3-8 token kernels), q4_0_gemv, q6k_gemv,
- * q4k_ffn_swiglu, q4k_matmul_tc, mx_matmul or mx_attention (many rows) never issues
- * the copy of weight stage `stage` of each CTA (its ring stage, its 256-row weight
- * tile on the tensor cores, or its keys' tile of 128, the last if it has fewer) and bounds every in-kernel wait by `limit_cycles` SM cycles
+ * q4k_ffn_swiglu, q4k_matmul_tc, mx_matmul or mx_attention (many rows) never
+ * issues the copy of weight stage `stage` of each CTA (its ring stage, its
+ * 256-row weight tile on the tensor cores, or its tile of 128 keys, the last
+ * if it has fewer) and bounds every in-kernel wait by `limit_cycles` SM cycles
  * (about 2·10^6 per millisecond) instead of about 2·10^9.  The waits on the
  * missing stage then run out: the kernel sets the device status word, lets
  * every copy it did issue land, and exits; that call's y is undefined and

@@ -15,7 +15,7 @@
 //
 // Rope of 8192 x 32 x 128 bf16: 22.5 us (88% of the measured copy rate); 28000 tokens
 // of 8 heads read from 8 bits to bf16: 24.1 (79%); 8271 tokens of 32 heads rotated
-// and written from fp16 to 8 bits: 43.2 (70%), 59% of the issue slots and the loads' latency
+// and written from fp16 to 8 bits: 45.7 (66%), 60% of the issue slots and the loads' latency
 // (each lane holds 32 to 64 bytes of loads, 32 warps an SM).
 //
 // Angles.  p·f in radians needs some 20 bits before the point for far
@@ -346,6 +346,58 @@ __device__ __forceinline__ void find_places(Places &p, const MxBatchView &b, con
     __syncthreads();
 }
 
+// As cos_sin of a magnitude of 1, in 64 bits to some 2^-27: the last additions
+// with what they round off, the square and the rest's factor in full.
+__device__ __forceinline__ double2 cos_sin_more(uint64_t turn) {
+    const int32_t a = (int32_t)(turn >> 32), q = (a >> 29) + 1 >> 1, r = (int32_t)((uint32_t)a - ((uint32_t)q << 30));
+    constexpr float kRad = 1.46291807926715968e-9f;
+    constexpr float kRadRest = (float)(1.46291807926715968105e-9 - (double)kRad);
+    const float hi = (float)r, lo = (float)(r - (int32_t)hi) + (float)(uint32_t)turn * 0x1p-32f;
+    const float x = hi * kRad, xl = fmaf(hi, kRad, -x) + fmaf(hi, kRadRest, lo * kRad);
+    const float z = x * x, zl = fmaf(x, x, -z);
+    float s = fmaf(z, 2.75573192e-6f, -1.98412698e-4f);
+    s = fmaf(s, z, 8.33333333e-3f), s = fmaf(s, z, -1.66666667e-1f);
+    const float sl = fmaf(x * z, s, xl * fmaf(z, -0.5f, 1.f));
+    float c = fmaf(z, -2.75573192e-7f, 2.48015873e-5f);
+    c = fmaf(c, z, -1.38888889e-3f), c = fmaf(c, z, 4.16666667e-2f);
+    const float cl = fmaf(c * z, z, fmaf(zl, -0.5f, -x * xl));
+    const double co = (1.0 - 0.5 * (double)z) + (double)cl, si = (double)x + (double)sl;
+    const double u = q & 1 ? si : co, v = q & 1 ? co : si;
+    return make_double2((q & 3) == 1 || (q & 3) == 2 ? -u : u, q & 2 ? -v : v);
+}
+
+// Value d of a head, turned, rounded to odd: a code made of it is that of the
+// value before.  Out of line, for the few that need it.
+template <class T>
+__device__ __noinline__ float turned_again(const T *head, int d, const RopeView r, long long position) {
+    const int half = r.rotated / 2, i = r.interleaved ? d / 2 : d < half ? d : d - half;
+    const bool first = r.interleaved ? d % 2 == 0 : d < half;
+    const int other = r.interleaved ? d ^ 1 : first ? d + half : d - half;
+    const double2 cs = cos_sin_more((uint64_t)position * turns_of(r.frequencies[i]));
+    const double a = mx_float(head[d]), b = mx_float(head[other]);
+    const double v = r.magnitude * (first ? a * cs.x - b * cs.y : a * cs.x + b * cs.y);
+    const float f = __double2float_rz(v);
+    return (double)f == v ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
+
+// Turned values that lie within 4 units of a border between two codes, where
+// the fp32 arithmetic may fall on its other side, are taken again: nine in
+// 2^20 (8 bits) or 2^22.  (Without this 26 to 40 codes of 68 million differed from
+// those of the exact values, with it 8 to 19; 8271 tokens written take 45.7 us, 43.2 without.)  Below the codes' normal numbers the borders lie
+// elsewhere and are left as they are.
+template <int kBits, class T>
+__device__ __forceinline__ void settle(float (&f)[8], const T *head, int d, const RopeView &r, long long position, bool ok) {
+    constexpr uint32_t kMask = kBits == 8 ? 0xFFFFF : 0x3FFFFF, kBorder = kMask / 2 + 1;
+    uint32_t nearest = kMask;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) nearest = min(nearest, __float_as_uint(f[i]) - (kBorder - 4) & kMask);
+    if (nearest > 8 || !ok) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (d + i < r.rotated && (__float_as_uint(f[i]) - (kBorder - 4) & kMask) <= 8)
+            f[i] = turned_again(head, d + i, r, position);
+}
+
 // Quantises eight values of a block of four lanes into a slot: codes at
 // `codes`, the block's scale byte (and the padding's zeros) at `scales`.
 template <int kBits>
@@ -407,10 +459,13 @@ __global__ void __launch_bounds__(kThreads, kForm == 0 ? 1 : 4) mx_cache_write_k
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] = 0.f;
                     if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, f, g);
+                    settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u]);
+                    settle<kBits>(g, x + u * it.step * head, it.d + span, r, at.position[s], ok[u]);
                     put_codes<kBits>(f, c, b, it.d, D, ok[u]);
                     put_codes<kBits>(g, c, b, it.d + span, D, ok[u]);
                 } else {
                     if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, r, f);
+                    if (r.rotated) settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u]);
                     put_codes<kBits>(f, c, b, it.d, D, ok[u]);
                 }
             }
@@ -493,7 +548,7 @@ bool heads_aligned(const void *p, long long token, long long head, size_t size) 
 // Tokens a CTA takes (the most, up to 8, that leave two CTAs an SM, else 1) and
 // CTAs that share them (up to two an SM, each with work for its warps).  2048
 // tokens written, 32 heads of 128: 18.7 us with 1 token a CTA, 13.5 with 2, 12.9 with 4, 16.6
-// with 8 (256 CTAs); 8271: 67.4, 44.5, 43.1, 43.6; 28000 read, 8 heads:
+// with 8 (256 CTAs); 8271 (without settle): 67.4, 44.5, 43.1, 43.6; 28000 read, 8 heads:
 // 78, 52, 33, 24.7; rope of 1000 tokens: 4.6, 3.8, 4.8, 6.9.
 struct Shape {
     int lanes_log, tokens_log;

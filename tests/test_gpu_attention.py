@@ -319,6 +319,47 @@ def test_rows_in_pieces_and_at_once(T):
         assert torch.equal(back[0][i:i + n], some[0]) and torch.equal(back[1][i:i + n], some[1])
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("R,interleaved,D", [(128, False, 128), (64, True, 128), (36, False, 96), (64, False, 64)])
+def test_turned_keys_beside_borders_of_codes(R, interleaved, D, bits):
+    """Keys that the rotation takes to within a unit or two of the border between two codes get the code of the exact
+    value, where that is 2^-25 of it or more away from the border (the angles and what is made of them are good to 2^-26)."""
+    q, torch = _q(), _torch()
+    T = 200
+    c = Case(R + bits, [T], [T + 3000], 1, D, 16, bits)
+    pos = np.arange(3000, 3000 + T)
+    f = q.rope_frequencies(R)
+    a = pos[:, None] * f.cpu().numpy()
+    steps = 16 if bits == 8 else 4          # the significand's borders: odd multiples of 1 / steps
+    border = (1 + (2 * c.rng.integers(0, steps // 2, a.shape) + 1) / steps) * 2.0 ** c.rng.integers(0, 2, a.shape)
+    near = np.abs(np.cos(a)) >= 0.7         # which of the two parts comes to lie beside it
+    part = border / np.where(near, np.cos(a), np.sin(a))
+    swap = c.rng.random(a.shape) < 0.5      # from u or from v
+    u, v = np.where(swap, 0, part), np.where(swap, part, 0)
+    x = np.ones((T, 1, D))
+    if interleaved:
+        x[:, 0, 0:R:2], x[:, 0, 1:R:2] = u, v
+    else:
+        x[:, 0, :R // 2], x[:, 0, R // 2:R] = u, v
+    k, kv = _dev(x, "float32")
+    cache, batch = c.device_cache(), c.device_batch()
+    q.mx_cache_write(cache, k, k, *batch, rope=q.Rope(f, interleaved))
+    want = ref.turned(kv, pos, f.cpu().numpy(), interleaved)
+    codes, scales = cache.k_codes.cpu().numpy(), cache.k_scales.cpu().numpy()
+    beside = 0
+    for t, _, _, pg, at in ref.places(c.batch, 16):
+        w, unit = want[t, 0], np.repeat(np.exp2(scales[pg, 0, at][:D // 32].astype(float) - 127), 32)
+        got = mx.unpack(codes[pg, 0, at][None], bits)[0]
+        lo, hi = (mx.nearest_code(w * (1 + e) / unit, bits) for e in (-2.0 ** -25, 2.0 ** -25))
+        sure = lo == hi
+        assert np.array_equal(got[sure], lo[sure]), (t, np.flatnonzero(sure & (got != lo)))
+        wide = [mx.nearest_code(w * (1 + e) / unit, bits) for e in (-2.0 ** -22, 2.0 ** -22)]
+        beside += int((sure & (wide[0] != wide[1])).sum())
+    # It is these that are tested: an input m · 2^e is off by up to 2^-24 / m of itself, hence by more than 2^-25
+    # with probability 1 - m / 2: a quarter of the T R / 2, on average.
+    assert beside > T * R // 16
+
+
 def test_cache_write_specials():
     """A block with an infinity or a NaN reads back as NaN, its neighbours as they are."""
     q, torch = _q(), _torch()
