@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTokens = 8;    // tokens a CTA takes together
+constexpr int kMaxTokens = 16;   // tokens a CTA takes together
 constexpr int kMaxPairs = 128;   // rotated pairs of a head
 
 // f / 2π modulo 1 in units of 2^-64 turns, for the bits of a double f: its
@@ -391,7 +391,8 @@ __device__ __forceinline__ void settle(float (&f)[8], const T *head, int d, cons
     uint32_t nearest = kMask;
 #pragma unroll
     for (int i = 0; i < 8; ++i) nearest = min(nearest, __float_as_uint(f[i]) - (kBorder - 4) & kMask);
-    if (nearest > 8 || !ok) return;
+    // (Values that are not turned lie on borders often, at position 0 too: a 16-bit one in 16.)
+    if (nearest > 8 || !ok || d >= r.rotated || position == 0) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (d + i < r.rotated && (__float_as_uint(f[i]) - (kBorder - 4) & kMask) <= 8)
@@ -545,7 +546,9 @@ bool heads_aligned(const void *p, long long token, long long head, size_t size) 
            head * (long long)size % 16 == 0;
 }
 
-// Tokens a CTA takes (the most, up to 8, that leave two CTAs an SM, else 1) and
+// Tokens a CTA takes (the most, up to 8, that leave two CTAs an SM, else 1; up to 16
+// where 8 tokens' heads are less than a pass of its lanes: 28934 tokens of 2 heads
+// written 27.9 us, 35.2 with 8, read 12.0 and 16.7) and
 // CTAs that share them (up to two an SM, each with work for its warps).  2048
 // tokens written, 32 heads of 128: 18.7 us with 1 token a CTA, 13.5 with 2, 12.9 with 4, 16.6
 // with 8 (256 CTAs); 8271 (without settle): 67.4, 44.5, 43.1, 43.6; 28000 read, 8 heads:
@@ -557,7 +560,8 @@ struct Shape {
 Shape shape_of(const LaunchCtx &c, int tokens, int vectors, int D, int unroll) {
     Shape s{};
     while (8 << s.lanes_log < D) ++s.lanes_log;
-    s.tokens_log = 3;
+    const int lanes = kWarps * (32 >> s.lanes_log);  // vectors of a pass, apart from `unroll`
+    s.tokens_log = 16 <= lanes && vectors * 8 < lanes * unroll ? 4 : 3;
     while (s.tokens_log > 0 && ((long long)tokens + (1 << s.tokens_log) - 1) >> s.tokens_log < 2 * c.num_sms) --s.tokens_log;
     const int x = (tokens + (1 << s.tokens_log) - 1) >> s.tokens_log;
     const long long per_cta = (long long)kWarps * (32 >> s.lanes_log) * unroll;  // items of one pass

@@ -296,7 +296,7 @@ def test_cache_write_turns_keys(R, interleaved, D, dtype, bits):
     q.device_status()
 
 
-@pytest.mark.parametrize("T", [700, 1301, 2600])
+@pytest.mark.parametrize("T", [700, 1301, 2600, 5003])
 def test_rows_in_pieces_and_at_once(T):
     """Rotated and written rows have the same bits whatever the number of rows that a call has."""
     q, torch = _q(), _torch()
