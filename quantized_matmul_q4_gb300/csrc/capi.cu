@@ -254,6 +254,13 @@ int check_rope(const double *frequencies, int rotated, float magnitude, int D) {
     return check_mx_ptr(Span{frequencies, (size_t)rotated / 2 * 8, "frequencies"}, 8);
 }
 
+// The rows that share a key head are numbered in 32 bits (a tile's last ones may not exist).
+int check_rows(int tokens, int group) {
+    if ((long long)tokens * group <= Q4MM_MX_MAX_ROWS) return Q4MM_OK;
+    return fail(Q4MM_ERR_DIM, "tokens (%d) times heads of a key head (%d) must be at most %d rows", tokens, group,
+                Q4MM_MX_MAX_ROWS);
+}
+
 struct CacheCall {
     q4mm::MxCacheView cache;
     q4mm::MxBatchView batch;
@@ -750,6 +757,7 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
     if (heads <= 0 || heads > Q4MM_MX_MAX_HEADS || heads % kvHeads)
         return fail(Q4MM_ERR_DIM, "heads (%d) must be a positive multiple of kvHeads (%d), at most %d", heads, kvHeads,
                     Q4MM_MX_MAX_HEADS);
+    if ((rc = check_rows(tokens, heads / kvHeads))) return rc;
     if (!(scale >= 0.f && scale - scale == 0.f)) return fail(Q4MM_ERR_DIM, "scale (%g) must be finite and not negative", (double)scale);
     if (tokens == 0 || sequences == 0) return Q4MM_OK;
     if ((rc = check_head_strides(q_token_stride, q_head_stride, tokens, heads, headDim, false, "q")) ||
@@ -786,7 +794,8 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
 
 size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequences, int tableWidth, int tokens,
                               int heads) {
-    if (kvHeads <= 0 || heads <= 0 || heads % kvHeads || pageTokens <= 0 || sequences <= 0 || tableWidth < 0 || tokens <= 0)
+    if (kvHeads <= 0 || heads <= 0 || heads % kvHeads || pageTokens <= 0 || sequences <= 0 || tableWidth < 0 || tokens <= 0 ||
+        (long long)tokens * (heads / kvHeads) > Q4MM_MX_MAX_ROWS)
         return 0;
     q4mm::LaunchCtx ctx;
     if (device_ctx(nullptr, &ctx, false)) return 0;
