@@ -547,7 +547,8 @@ int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes
  *         are accepted: with less than mx_attention_workspace says the call
  *         may be slower.  Calls that may overlap in time need one each.
  * Limits: as mx_cache_write; heads a multiple of kvHeads; tokens · G at most
- *         Q4MM_MX_MAX_ROWS; scale finite, >= 0.
+ *         Q4MM_MX_MAX_ROWS; scale finite, >= 0.  Positions from 2^31 - 256 on
+ *         are beyond any table.
  * Returns Q4MM_OK or Q4MM_ERR_{DIM,NULL,ALIGN,ALIAS,CUDA}.
  */
 int mx_attention(const void *q, long long q_token_stride, long long q_head_stride, int dtype, const void *k_codes,

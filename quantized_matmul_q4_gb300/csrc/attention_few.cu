@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
 
     // Keys that any row sees, in groups, and this CTA's share of them.
     int keys = keys_of(tile, tile.first + tile.rows - 1, group, a.causal);
-    const long long room = (long long)a.batch.width * a.cache.page;
+    const int room = table_keys(a.batch.width, a.cache.page);
     if (keys > room) {
         if (threadIdx.x == 0) atomicOr(a.status, kStatusIndex);
-        keys = (int)room;
+        keys = room;
     }
     const int groups = (keys + kFewGroup - 1) / kFewGroup;
     const int share = part * S + rank, shares = parts * S;

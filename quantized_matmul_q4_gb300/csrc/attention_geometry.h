@@ -27,10 +27,13 @@ constexpr int kFewGroup = 16;     // tokens a warp takes at once
 // Tiles of 8 · nr rows, at most (see row_tile).
 inline long long few_tiles(long long tokens, int group, int nr, int seqs) { return tokens * group / (8 * nr) + seqs; }
 
-// Keys of a sequence, at most: what its table has room for (their number is the device's to know).
-inline int table_keys(int width, int page) {
+// Keys of a sequence, at most, on the host (their number is the device's to
+// know) and on the device: what its table has room for, and a tile's keys and a few
+// groups more than which can still be numbered in 32 bits.
+constexpr int kMaxKeys = 0x7FFFFF00;
+constexpr int table_keys(int width, int page) {
     const long long keys = (long long)width * page;
-    return keys < 0x7FFFFFFF ? (int)keys : 0x7FFFFFFF;
+    return keys < kMaxKeys ? (int)keys : kMaxKeys;
 }
 
 constexpr int kPartedTiles = 64;  // tiles of 8 rows and key heads, at most, that are shared by several clusters

@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
     if (tile.rows == 0) return;  // with the whole cluster
 
     // Keys that each tile of 128 rows sees, in tiles of 128, and this CTA's share of them.
-    const long long room = (long long)a.batch.width * a.cache.page;
+    const int room = table_keys(a.batch.width, a.cache.page);
     int cnt[2] = {0, 0}, keys = 0;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
         int n = rows ? keys_of(tile, tile.first + 128 * t + rows - 1, group, a.causal) : 0;
         if (n > room) {
             if (threadIdx.x == 0) atomicOr(a.status, kStatusIndex);
-            n = (int)room;
+            n = room;
         }
         keys = max(keys, n);
         cnt[t] = (n + kManyKeys - 1) / kManyKeys;

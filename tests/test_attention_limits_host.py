@@ -1,7 +1,13 @@
-"""Sizes of attention calls that its 32-bit row numbers and positions cannot hold: refused by the C ABI before any CUDA call."""
+"""Sizes of attention calls that its 32-bit row numbers and positions cannot hold: refused by the C ABI before any CUDA call, or
+counted as beyond the table."""
+import ctypes
+import os
+import subprocess
+
 import pytest
 
 DIM = -1
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A, B, C, D, E, F, G, H, I = (0x10000000 * i for i in range(1, 10))   # fake device addresses, far apart
 
 
@@ -21,3 +27,15 @@ def test_rows_of_a_key_head_stay_below_32_bits(q4mm, tokens, heads):
                               tokens, heads)
     assert e.value.code == DIM and "rows" in q4mm.last_error(), q4mm.last_error()
     assert q4mm.library().mx_attention_workspace(kv, 16, 32, 1, 4, tokens, heads) == 0
+
+
+def test_keys_of_a_table_leave_room_for_a_tile_in_32_bits(tmp_path):
+    """The kernels round the number of keys up to whole tiles, and look a tile ahead, in 32-bit integers."""
+    out = str(tmp_path / "libatt_limits.so")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC",
+                    f"-I{os.path.join(ROOT, 'quantized_matmul_q4_gb300', 'csrc')}",
+                    os.path.join(ROOT, "tests", "attention_limits_shim.cpp"), "-o", out], check=True)
+    lib = ctypes.CDLL(out)
+    for width, page in ((2 ** 31 - 1, 2 ** 24), (128, 2 ** 24), (129, 2 ** 24), (2 ** 27, 16), (2 ** 27 - 1, 16), (2 ** 31 - 1, 16)):
+        assert lib.att_table_keys(width, page) + 2 * lib.att_tile_keys() <= 2 ** 31
+    assert lib.att_table_keys(127, 2 ** 24) == 127 * 2 ** 24 and lib.att_table_keys(0, 16) == 0
