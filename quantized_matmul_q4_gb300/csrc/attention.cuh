@@ -17,6 +17,10 @@
 //   O = Σ p v',  l = Σ p · 2^-vref,  y = O / l
 //
 // M is kept while no u passes it by more than 8, so O is rarely rescaled.
+// A key whose v is far smaller than another's has a p that may be zero where its term
+// of l is not.  So vref is kept within [kVrefMin, kVrefMax], 80 apart, which is what
+// values from 2^-39 to 2^42 need (4 bits: 2^-45 to 2^36; tokens of zeros have kVrefMin).
+// Rows that met others are taken once more, by plain_row.
 // Probabilities enter the second product in fp16: one rounding to 2^-11 where
 // y is 16 bits wide, two terms (2^-22) where it is fp32.
 #pragma once
@@ -26,13 +30,15 @@
 
 #include "mx.cuh"
 #include "mx_cache.cuh"
+#include "sync.cuh"
 
 namespace q4mm {
 
 constexpr float kLog2e = 1.44269504f;
 constexpr float kPShift = 6.f;      // log2 of p at u = M
 constexpr float kPSlack = 8.f;      // u may pass M by this
-constexpr int kVrefMin = -100;      // lowest power taken out of v (2^-vref stays a normal float)
+constexpr int kVrefMin = -54;       // lowest power taken out of v
+constexpr int kVrefMax = 26;        // highest
 constexpr int kWide = 4;            // a group's tokens share a power while their largest scales are within 2^this
 constexpr int kNever = 0x7FFFFFFF;  // position of a NaN that there is not
 
@@ -44,6 +50,14 @@ __device__ __forceinline__ float ex2(float x) {
 
 // 2^e, e cut to a normal float's.
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+
+// x · 2^e, to below and above the normal floats.
+__device__ __forceinline__ float scaled(float x, int e) { return x * pow2(e) * pow2(e - min(max(e, -126), 127)); }
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 // Two E4M3 codes, or two E2M1 codes, as fp16.
 __device__ __forceinline__ uint32_t half_e4m3x2(uint32_t two) {
@@ -93,6 +107,11 @@ struct ScaleWord {
     }
 };
 
+// Whether values whose largest scale byte is `top` need another power.
+__device__ __forceinline__ bool vref_passes(int top) {
+    return top != 0 && (unsigned)(top - 134 - kVrefMin) > (unsigned)(kVrefMax - kVrefMin);
+}
+
 // A tile of `R` rows of one sequence and kv head.  Row r is token r / group of
 // the sequence's new tokens, query head r % group of the kv head.
 struct RowTile {
@@ -133,6 +152,98 @@ __device__ __forceinline__ RowTile row_tile(const MxBatchView &b, long long tile
 __device__ __forceinline__ int keys_of(const RowTile &t, int r, int group, bool causal) {
     const int seen = causal ? t.len - t.fresh + r / group + 1 : t.len;
     return max(seen, 0);
+}
+
+// Sums of one row over some of its keys: y over those, four values a lane, and the M under which they count as 1.
+struct PlainSums {
+    float4 o;
+    float m;
+};
+
+// By plain arithmetic, one row a warp: those of its first `keys` keys that lie in the groups of 16 tokens first, first +
+// step .. before last.  Two passes, the second with probabilities that add up to 1, whose powers of two
+// meet those of v before either leaves the floats.
+template <int kBits>
+__device__ __forceinline__ PlainSums plain_row(const MxAttentionArgs &a, const RowTile &tile, const int row, const int group,
+                                               const int head, const int keys, const int first, const int last,
+                                               const int step) {
+    const long long q_at = (long long)(tile.start + row / group) * a.q_token + (long long)(head * group + row % group) * a.q_head;
+    const int sees = min(keys_of(tile, row, group, a.causal), keys);
+    const int lane = threadIdx.x & 31, tok = lane & 15, half = lane >> 4;  // of K: a token, half the head
+    const int D = a.cache.D, row_bytes = D * kBits / 8, per_page = a.cache.page / 16;
+    constexpr int kWord = 32 / kBits;
+    auto query = [&](int d) {
+        return a.type == MxType::kF32   ? static_cast<const float *>(a.q)[q_at + d]
+               : a.type == MxType::kF16 ? mx_float(static_cast<const __half *>(a.q)[q_at + d])
+                                        : mx_float(static_cast<const __nv_bfloat16 *>(a.q)[q_at + d]);
+    };
+    auto slot_of = [&](int g) -> long long {  // of the group's first token, or -1
+        const int page = page_of(a.batch, a.cache, tile.seq, g / per_page, a.status);
+        return page < 0 ? -1 : first_slot(a.cache, page, head) + 16 * (g % per_page);
+    };
+    auto score = [&](int g, long long slot) {
+        if (slot < 0 || 16 * g + tok >= sees) slot = -1;
+        float s = -INFINITY;
+        if (slot >= 0) {
+            const uint8_t *codes = a.cache.k_codes + (slot + tok) * row_bytes + half * (row_bytes / 2);
+            const uint32_t scales = *reinterpret_cast<const uint32_t *>(a.cache.k_scales + (slot + tok) * 4);
+            float block = 0.f;
+            s = 0.f;
+            for (int i = 0; i < D / 2; i += kWord) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + i * kBits / 8);
+                const int d = half * (D / 2) + i;
+                float2 v[kWord / 2];
+                if constexpr (kBits == 8)
+                    v[0] = mx_from_e4m3x2<0>(w), v[1] = mx_from_e4m3x2<1>(w);
+                else
+                    v[0] = mx_from_e2m1x2<0>(w), v[1] = mx_from_e2m1x2<1>(w), v[2] = mx_from_e2m1x2<2>(w),
+                    v[3] = mx_from_e2m1x2<3>(w);
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < kWord / 2; ++k) sum += v[k].x * query(d + 2 * k) + v[k].y * query(d + 2 * k + 1);
+                block += sum;
+                if ((d + kWord) % kMxBlock == 0 || i + kWord == D / 2)
+                    s = fmaf(block, mx_scale(scales >> (8 * (d / kMxBlock)) & 0xFF), s), block = 0.f;
+            }
+        }
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+        return s * (a.scale * kLog2e);
+    };
+    float m = -INFINITY, l = 0.f;
+    for (int g = first; g < last && 16LL * g < sees; g += step) {
+        const float s = score(g, slot_of(g));
+        float top = s;
+#pragma unroll
+        for (int x = 1; x < 16; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        if (top > m) l *= m == -INFINITY ? 1.f : ex2(m - top), m = top;
+        l += ex2(s - (m == -INFINITY ? 0.f : m));
+    }
+#pragma unroll
+    for (int x = 1; x < 16; x *= 2) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    // What the keys' 2^score add up to, as a power of two: -infinity without keys, NaN where a score is.
+    PlainSums r{make_float4(0.f, 0.f, 0.f, 0.f), l == 0.f ? -INFINITY : (m == -INFINITY ? 0.f : m) + lg2(l)};
+    for (int g = first; g < last && 16LL * g < sees; g += step) {
+        const long long slot = slot_of(g);
+        const float power = score(g, slot) - r.m;
+        for (int j = 0; j < 16 && 16 * g + j < sees && slot >= 0; ++j) {
+            const float t = __shfl_sync(0xFFFFFFFFu, power, j), whole = floorf(t);
+            if (4 * lane >= D) continue;
+            const uint8_t *codes = a.cache.v_codes + (slot + j) * row_bytes + lane * kBits / 2;
+            float2 lo, hi;
+            if constexpr (kBits == 8) {
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(codes);
+                lo = mx_from_e4m3x2<0>(w), hi = mx_from_e4m3x2<1>(w);
+            } else {
+                const uint32_t w = *reinterpret_cast<const uint16_t *>(codes);
+                lo = mx_from_e2m1x2<0>(w), hi = mx_from_e2m1x2<1>(w);
+            }
+            const int b = a.cache.v_scales[(slot + j) * 4 + 4 * lane / kMxBlock], e = (int)fmaxf(whole, -999.f) + b - 127;
+            const float p = b == 255 ? __int_as_float(0x7FC00000) : ex2(t - whole);
+            r.o.x += scaled(lo.x * p, e), r.o.y += scaled(lo.y * p, e);
+            r.o.z += scaled(hi.x * p, e), r.o.w += scaled(hi.y * p, e);
+        }
+    }
+    return r;
 }
 
 // Four neighbouring outputs.

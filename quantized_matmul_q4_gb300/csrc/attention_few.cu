@@ -44,7 +44,7 @@ namespace q4mm {
 namespace {
 
 constexpr int kThreads = 32 * kFewWarps;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = kThreads;  // (few_plain has the same warps in both kernels)
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -163,9 +163,50 @@ struct FewShared {
 // for each of its rows kDP outputs, then the maximum and the sum, and at the end nan_from.
 __host__ __device__ constexpr size_t few_part_floats(int rows, int dp) { return (size_t)rows * (dp + 2) + 4; }
 
+// Sums that are not to be used: M kSpoiltMax, so that they outweigh all others, and l kSpoilt.
+constexpr float kSpoiltMax = 3e38f, kSpoilt = INFINITY;
+
+struct PlainScratch {
+    float o[kFewWarps][128], m[kFewWarps];
+};
+
+// The rows of tile and head `item` that CTA `rank` of S stores, kHere at once, by plain_row, the keys of a row
+// shared by the warps.  Some fifty times slower than the kernel.  (At the end of a kernel, and a function of its own
+// that finds its tile anew: anywhere else, or with what it needs held for it, a CTA takes 0.2 us longer.)
+template <int kBits, int kR, int kHere>
+__device__ __noinline__ void few_plain(const MxAttentionArgs &a, int group, unsigned item, int rank, int S, PlainScratch &sh) {
+    const RowTile tile = row_tile(a.batch, item / (unsigned)a.cache.heads, group, kR, a.tokens);
+    const int head = (int)(item % (unsigned)a.cache.heads), lane = threadIdx.x & 31, warp = threadIdx.x / 32, d = 4 * lane;
+    const int keys = min(keys_of(tile, tile.first + tile.rows - 1, group, a.causal), table_keys(a.batch.width, a.cache.page));
+    for (int r = rank * kHere; r < tile.rows; r = (r + 1) % kHere ? r + 1 : r + 1 + (S - 1) * kHere) {
+        const int row = tile.first + r;
+        const PlainSums own = plain_row<kBits>(a, tile, row, group, head, keys, warp, 0x7FFFFFFF, kFewWarps);
+        *reinterpret_cast<float4 *>(&sh.o[warp][d]) = own.o;
+        if (lane == 0) sh.m[warp] = own.m;
+        __syncthreads();
+        if (warp == 0 && d < a.cache.D) {
+            float top = -INFINITY, l = 0.f;
+            for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sh.m[w]);
+            for (int w = 0; w < kFewWarps; ++w) l += ex2(sh.m[w] - (top == -INFINITY ? 0.f : top));
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < kFewWarps; ++w) {
+                if (sh.m[w] == -INFINITY) continue;
+                const float4 v = *reinterpret_cast<const float4 *>(&sh.o[w][d]);
+                const float t = sh.m[w] - top - lg2(l), whole = floorf(t), by = ex2(t - whole);
+                const int e = (int)fmaxf(whole, -999.f);
+                y.x += scaled(v.x * by, e), y.y += scaled(v.y * by, e), y.z += scaled(v.z * by, e), y.w += scaled(v.w * by, e);
+            }
+            const long long at = (long long)(tile.start + row / group) * a.y_token +
+                                 (long long)(head * group + row % group) * a.y_head + d;
+            store4(a.y, a.type, at, a.vec, y);
+        }
+        __syncthreads();
+    }
+}
+
 template <int kBits, int kDP, int kNR, int kNP>
 __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
-    mx_attention_few_kernel(const MxAttentionArgs a, const int group, const int parts) {
+    mx_attention_few_kernel(const __grid_constant__ MxAttentionArgs a, const int group, const int parts) {
     using Shared = FewShared<kBits, kDP, kNR, kNP>;
     constexpr int kR = Shared::kR, kRow = Shared::kRow, kStages = Shared::kStages;
     constexpr int kSteps = kDP / 16;                 // of 16 head values
@@ -363,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         uint32_t top = max(pair & 0xFFFFu, pair >> 16);
         const bool is_v = lane >= 16;
         uint32_t any_nan = 0;  // a bit a block
-        if (__any_sync(0xFFFFFFFFu, top == 255)) {
+        if (__any_sync(0xFFFFFFFFu, top - (134 + kVrefMin) > (uint32_t)(kVrefMax - kVrefMin))) {
+            // A scale that is NaN, or one that v's powers do not reach (or that is k's).
             // NaN in v reaches the rows that see it, and no others.
             top = 0;
 #pragma unroll
@@ -373,6 +415,10 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
                 top = max(top, e == 255 ? 0u : e);
                 if (e == 255 && is_v) atomicMin(&sh.nan_from[i], base + (lane & 15));
                 if (e == 255) sw &= ~(0xFFu << (8 * i));
+            }
+            if (__any_sync(0xFFFFFFFFu, is_v && vref_passes((int)top))) {
+#pragma unroll
+                for (int n = 0; n < kNR; ++n) M[n][0] = M[n][1] = kSpoiltMax, l[n][0] = l[n][1] = kSpoilt;
             }
         }
         const int ktop = (int)__reduce_max_sync(0xFFFFFFFFu, is_v ? 0u : top);
@@ -606,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     const uint32_t o_at = smem_addr(sh.o), m_at = smem_addr(sh.m_all), l_at = smem_addr(sh.l_all),
                    n_at = smem_addr(sh.nan_from);
     float *ws = parts > 1 ? a.workspace + (size_t)(blockIdx.x / S) * few_part_floats(kR, kDP) : nullptr;
+    bool spoilt = false;
     for (int i = rank * kThreads + threadIdx.x; i < tile.rows * (kDP / 4); i += S * kThreads) {
         const int r = i / (kDP / 4), d = 4 * (i % (kDP / 4));
         if (d >= D) continue;
@@ -626,15 +673,21 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         } else {
             const int row = tile.first + r;
             sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
+            spoilt |= sum.l == kSpoilt;
         }
     }
     if (S > 1) cluster_sync_all();  // no CTA leaves while another reads its sums
+    if (__syncthreads_or(spoilt))
+        few_plain<kBits, kR, kThreads / (kDP / 4)>(a, group, blockIdx.x / cluster_size(), (int)cluster_rank(),
+                                                   (int)cluster_size(), *reinterpret_cast<PlainScratch *>(raw));
 }
 
 // Joins the parts of a tile's keys that the clusters left in the workspace.
-template <int kDP, int kNR>
-__global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const MxAttentionArgs a, const int group,
-                                                                         const int parts) {
+template <int kBits, int kDP, int kNR>
+__global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const __grid_constant__ MxAttentionArgs a,
+                                                                         const int group, const int parts) {
+    __shared__ __align__(16) PlainScratch scratch;
+    bool spoilt = false;
     constexpr int kR = 8 * kNR;
     pdl_wait();
     const int head = (int)(blockIdx.x % a.cache.heads);
@@ -659,7 +712,9 @@ __global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const M
         }
         const int row = tile.first + r;
         sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
+        spoilt |= sum.l == kSpoilt;
     }
+    if (__syncthreads_or(spoilt)) few_plain<kBits, kR, kR>(a, group, blockIdx.x, 0, 1, scratch);
 }
 
 template <int kBits, int kDP, int kNR, int kNP>
@@ -692,7 +747,7 @@ cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a, FewSplit f)
     cfg.numAttrs = c.pdl ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kernel, a, group, f.parts);
     if (e != cudaSuccess || f.parts == 1) return e;
-    return launch_kernel(c, mx_attention_join_kernel<kDP, kNR>, dim3((unsigned)(tiles * a.cache.heads)), dim3(kJoinThreads),
+    return launch_kernel(c, mx_attention_join_kernel<kBits, kDP, kNR>, dim3((unsigned)(tiles * a.cache.heads)), dim3(kJoinThreads),
                          0, a, group, f.parts);
 }
 

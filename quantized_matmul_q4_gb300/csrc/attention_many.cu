@@ -113,6 +113,7 @@ struct ManyShared {
     int nan_from[4];
     uint32_t tmem;
     int abort;
+    int spoilt;  // values that the sums cannot take were met
 };
 
 static_assert(sizeof(ManyShared) <= 15 * 1024, "");
@@ -282,9 +283,42 @@ struct RawRow {
     }
 };
 
+// The softmax warps' share of the CTA's rows, over its keys, by plain_row, to where the sums lie.  Some fifty times slower than the
+// kernel.  (A function of its own that finds rows and keys anew, so that the kernel holds nothing for it.)
+template <int kBits, int kDP, int kTiles, int kNP>
+__device__ __noinline__ void many_plain(const MxAttentionArgs &a, ManyShared &sh, uint32_t base, int group, long long tiles) {
+    using L = ManyLayout<kBits, kDP, kTiles, kNP>;
+    const int lane = threadIdx.x & 31, S = (int)cluster_size(), rank = (int)cluster_rank();
+    const unsigned item = blockIdx.x / (unsigned)S;
+    const RowTile tile = row_tile(a.batch, tiles - 1 - item / (unsigned)a.cache.heads, group, 128 * kTiles, a.tokens);
+    const int keys = min(keys_of(tile, tile.first + tile.rows - 1, group, a.causal), table_keys(a.batch.width, a.cache.page));
+    const int all = (keys + kManyKeys - 1) / kManyKeys, j0 = (int)((unsigned)all * (unsigned)rank / (unsigned)S),
+              j1 = (int)((unsigned)all * (unsigned)(rank + 1) / (unsigned)S);
+    for (int r = threadIdx.x / 32; r < tile.rows; r += L::kSoftmaxWarps) {
+        const PlainSums p = plain_row<kBits>(a, tile, tile.first + r, group, (int)(item % (unsigned)a.cache.heads), keys,
+                                             kManyKeys / 16 * j0, kManyKeys / 16 * j1, 1);
+        // M of the largest value's size, as in the kernel's own sums, with which these are joined.  (Of two
+        // CTAs' keys, values 2^180 below the others may be lost.)
+        float top = fmaxf(fmaxf(fabsf(p.o.x), fabsf(p.o.y)), fmaxf(fabsf(p.o.z), fabsf(p.o.w)));
+#pragma unroll
+        for (int x = 1; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, kVrefMin), kVrefMax);
+        const float by = pow2(-e);
+        if (lane == 0) {
+            sh.m[r] = isnan(p.m) ? -INFINITY : p.m + kPShift + (float)e;
+            sh.l[0][r] = isnan(p.m) ? p.m : p.m == -INFINITY ? 0.f : by, sh.l[1][r] = 0.f;
+        }
+        if (4 * lane < kDP)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(base + (r * L::kPitch + 4 * lane) * 4),
+                         "f"(p.o.x * by), "f"(p.o.y * by), "f"(p.o.z * by), "f"(p.o.w * by)
+                         : "memory");
+    }
+}
+
 template <int kBits, int kDP, int kTiles, int kNP>
 __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads, 1)
-    mx_attention_many_kernel(const MxAttentionArgs a, const int group, const long long tiles, const long long wait_limit, const int withhold) {
+    mx_attention_many_kernel(const __grid_constant__ MxAttentionArgs a, const int group, const long long tiles,
+                             const long long wait_limit, const int withhold) {
     using L = ManyLayout<kBits, kDP, kTiles, kNP>;
     constexpr int kRows = 128 * kTiles;
     constexpr uint32_t kHalf = kManyKeys * 128;  // bytes of 64 values of 128 rows
@@ -336,7 +370,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             mbar_init(&sh.q_full, L::kSoftmaxWarps), mbar_init(&sh.done, 1);
             mbar_init(&sh.dequant_done, L::kDequantWarps);
             fence_mbar_init();
-            sh.abort = 0;
+            sh.abort = 0, sh.spoilt = 0;
             for (int i = 0; i < 4; ++i) sh.nan_from[i] = kNever;
         }
         __syncwarp();
@@ -578,6 +612,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
              mbar_wait_prompt(&sh.dequant_done, 0, wait_limit, abort);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             give_up();
+        } else if (sh.spoilt) {
+            many_plain<kBits, kDP, kTiles, kNP>(a, sh, base, group, tiles);
         } else {
             tc_fence_after();
             sh.m[mine] = M, sh.l[side][mine] = l;
@@ -792,7 +828,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             }
             const ScaleWord sk(ks, blocks), sv(vs, blocks);
             const int kref = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sk.top) - 134;
-            const int vref = max((int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sv.top) - 134, kVrefMin);
+            const int vtop = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)sv.top), vref = max(vtop - 134, kVrefMin);
+            if (vref_passes(vtop)) sh.spoilt = 1;
             if (sv.nan) {  // NaN in v reaches the rows that see it, and no others
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
@@ -804,6 +841,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             if (wide) {
                 if (sk.top != 0) rk = sk.top - 134;
                 if (sv.top != 0) rv = max(sv.top - 134, kVrefMin);
+                if (vref_passes(sv.top)) sh.spoilt = 1;
                 sh.krefs[mi][32 * w + lane] = (short)rk, sh.vrefs[mi][32 * w + lane] = (short)rv;
                 __syncwarp();
             }
