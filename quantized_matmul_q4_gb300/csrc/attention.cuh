@@ -59,6 +59,12 @@ __device__ __forceinline__ float lg2(float x) {
     return r;
 }
 
+// Value `at` of a 16-bit type.
+__device__ __forceinline__ float wide_value(const void *p, MxType type, long long at) {
+    return type == MxType::kF16 ? mx_float(static_cast<const __half *>(p)[at])
+                                : mx_float(static_cast<const __nv_bfloat16 *>(p)[at]);
+}
+
 // Two E4M3 codes, or two E2M1 codes, as fp16.
 __device__ __forceinline__ uint32_t half_e4m3x2(uint32_t two) {
     uint32_t r;
@@ -173,9 +179,7 @@ __device__ __forceinline__ PlainSums plain_row(const MxAttentionArgs &a, const R
     const int D = a.cache.D, row_bytes = D * kBits / 8, per_page = a.cache.page / 16;
     constexpr int kWord = 32 / kBits;
     auto query = [&](int d) {
-        return a.type == MxType::kF32   ? static_cast<const float *>(a.q)[q_at + d]
-               : a.type == MxType::kF16 ? mx_float(static_cast<const __half *>(a.q)[q_at + d])
-                                        : mx_float(static_cast<const __nv_bfloat16 *>(a.q)[q_at + d]);
+        return a.type == MxType::kF32 ? static_cast<const float *>(a.q)[q_at + d] : wide_value(a.q, a.type, q_at + d);
     };
     auto slot_of = [&](int g) -> long long {  // of the group's first token, or -1
         const int page = page_of(a.batch, a.cache, tile.seq, g / per_page, a.status);

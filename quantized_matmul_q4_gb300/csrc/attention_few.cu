@@ -246,16 +246,21 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
     // The warp's query rows, on their way while the first page is looked up.
     constexpr int kEachLane = kDP / 32;
     std::conditional_t<kNP == 2, float, uint16_t> query[kNR][kEachLane];
+    const bool narrow = kNP == 2 && a.type != MxType::kF32;  // 16-bit rows as fp32 ones
 #pragma unroll
     for (int n = 0; n < kNR; ++n) {
         const int r = warp + kFewWarps * n, row = tile.first + r;
-        const auto *x = static_cast<const std::remove_reference_t<decltype(query[0][0])> *>(a.q) +
-                        ((long long)(tile.start + row / group) * a.q_token +
-                         (long long)(head * group + row % group) * a.q_head + lane);
+        const long long at = (long long)(tile.start + row / group) * a.q_token +
+                             (long long)(head * group + row % group) * a.q_head + lane;
+        const auto *x = static_cast<const std::remove_reference_t<decltype(query[0][0])> *>(a.q) + at;
 #pragma unroll
         for (int i = 0; i < kEachLane; ++i) {
             query[n][i] = 0;
-            if (r < tile.rows && lane + 32 * i < D) query[n][i] = x[32 * i];
+            if (r >= tile.rows || lane + 32 * i >= D) continue;
+            if (narrow)
+                query[n][i] = wide_value(a.q, a.type, at + 32 * i);
+            else
+                query[n][i] = x[32 * i];
         }
     }
 
@@ -718,17 +723,13 @@ __global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const _
 }
 
 template <int kBits, int kDP, int kNR, int kNP>
-cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a, FewSplit f) {
+cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f) {
     auto kernel = mx_attention_few_kernel<kBits, kDP, kNR, kNP>;
     constexpr size_t bytes = sizeof(FewShared<kBits, kDP, kNR, kNP>);
     cudaError_t e = ensure_smem(kernel, bytes);
     if (e != cudaSuccess) return e;
     const int group = a.heads / a.cache.heads;
     const long long tiles = few_tiles(a.tokens, group, kNR, a.batch.seqs);
-    // As many parts as the workspace holds.
-    const size_t part_bytes = tiles * a.cache.heads * few_part_floats(8 * kNR, kDP) * sizeof(float);
-    if ((size_t)f.parts > a.workspace_bytes / part_bytes) f.parts = (int)(a.workspace_bytes / part_bytes);
-    if (f.parts < 1 || !a.workspace) f.parts = 1;
     const long long ctas = tiles * a.cache.heads * f.parts * f.cluster;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
@@ -752,9 +753,8 @@ cudaError_t launch_few(const LaunchCtx &c, const MxAttentionArgs &a, FewSplit f)
 }
 
 template <int kBits, int kDP>
-cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f) {
-    const bool f32 = a.type == MxType::kF32;
-    if (f32) return f.rows_8 == 2 ? launch_few<kBits, kDP, 2, 2>(c, a, f) : launch_few<kBits, kDP, 1, 2>(c, a, f);
+cudaError_t launch_rows(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f, bool as_f32) {
+    if (as_f32 || a.type == MxType::kF32) return f.rows_8 == 2 ? launch_few<kBits, kDP, 2, 2>(c, a, f) : launch_few<kBits, kDP, 1, 2>(c, a, f);
     return f.rows_8 == 2 ? launch_few<kBits, kDP, 2, 1>(c, a, f) : launch_few<kBits, kDP, 1, 1>(c, a, f);
 }
 
@@ -766,10 +766,10 @@ size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, in
     return tiles * kv_heads * f.parts * few_part_floats(8 * f.rows_8, D <= 64 ? 64 : 128) * sizeof(float);
 }
 
-cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f) {
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f, bool as_f32) {
     const bool narrow = a.cache.D <= 64;
-    if (a.cache.bits == 4) return narrow ? launch_rows<4, 64>(c, a, f) : launch_rows<4, 128>(c, a, f);
-    return narrow ? launch_rows<8, 64>(c, a, f) : launch_rows<8, 128>(c, a, f);
+    if (a.cache.bits == 4) return narrow ? launch_rows<4, 64>(c, a, f, as_f32) : launch_rows<4, 128>(c, a, f, as_f32);
+    return narrow ? launch_rows<8, 64>(c, a, f, as_f32) : launch_rows<8, 128>(c, a, f, as_f32);
 }
 
 }  // namespace q4mm

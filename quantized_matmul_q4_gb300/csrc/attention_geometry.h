@@ -69,13 +69,25 @@ inline double few_cost(long long tiles, int kv_heads, long long groups, const Fe
     return more + (double)((clusters + one - 1) / one) * each;
 }
 
-// The split of least cost, as if the rows were spread evenly over the sequences and all of the table were keys.
+// Steps of 16 keys that a sum in the tensor cores has at most (0: any number).  Each
+// drops what falls below the sum's last bit, 1.7e-8 of it on average, so that 4096 leave 7e-5, a
+// third of half a step of fp16; bf16 has eight times that.  (fp32 sums are taken out
+// every few steps.)
+constexpr int kChainF16 = 4096, kChainBf16 = 8 * kChainF16;
+inline bool few_chain_passes(int keys, const FewSplit &f, int chain) {
+    const long long groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
+    return chain && groups > (long long)chain * kFewWarps * f.cluster * f.parts;
+}
+
+// The split of least cost, as if the rows were spread evenly over the sequences and all of the table were keys, of those
+// whose sums have no more steps than `chain`; least stays below 0 where there is none.
 inline FewSplit few_split(long long tokens, int group, int seqs, int kv_heads, int keys, bool f32, int num_sms,
-                          double &least) {
+                          double &least, int chain = 0) {
     const long long groups = ((long long)keys + kFewGroup - 1) / kFewGroup;
     FewSplit best = {1, 1, 1};
     least = -1;
     const auto consider = [&](long long tiles, const FewSplit &f) {
+        if (few_chain_passes(keys, f, chain)) return;
         const double c = few_cost(tiles, kv_heads, groups, f, f32, num_sms);
         if (least < 0 || c < least) best = f, least = c;
     };
@@ -99,7 +111,7 @@ constexpr int kManyKeys = 128;  // keys of a tile on tcgen05
 // tile, 2.6 for a cluster.  Fitted to 2600 measurements (1 and 4 sequences, 34 to 3000
 // rows, 400 to 30000 keys); it takes 1.1% longer than their best on average.
 inline int many_split(long long tokens, int group, int tile_rows, int seqs, int kv_heads, int keys, bool f32, int num_sms,
-                      double &least) {
+                      double &least, int chain = 0) {
     const long long clusters = even_tiles(tokens, group, tile_rows, seqs) * kv_heads;
     const int tiles = (int)(((long long)keys + kManyKeys - 1) / kManyKeys);
     int best = 1;
@@ -109,6 +121,7 @@ inline int many_split(long long tokens, int group, int tile_rows, int seqs, int 
         const long long n = resident(s, false, num_sms);
         const double waves = clusters <= 3 * n ? (double)((clusters + n - 1) / n) : (double)clusters / n + 0.5;
         const int each = (tiles + s - 1) / s;
+        if (chain && each > chain / (kManyKeys / 16)) continue;
         const double c = 3 + waves * ((f32 ? 5.4 + 3.0 * each : 8 + 2.2 * each) + (s > 1 ? 2.6 : 0));
         if (least < 0 || c < least) best = s, least = c;
     }
@@ -126,14 +139,19 @@ struct AttentionPlan {
     bool many;
     int split;
     FewSplit few;
+    bool few_as_f32, many_as_f32;  // 16-bit rows by the form for fp32, whose sums may have any length
 };
 
 inline AttentionPlan attention_plan(long long tokens, int group, int seqs, int kv_heads, int keys, bool f32,
-                                    int num_sms) {
+                                    int num_sms, int chain = 0) {
     double few = 0, many = 0;
     AttentionPlan p;
-    p.few = few_split(tokens, group, seqs, kv_heads, keys, f32, num_sms, few);
-    p.split = many_split(tokens, group, f32 ? 128 : 256, seqs, kv_heads, keys, f32, num_sms, many);
+    p.few = few_split(tokens, group, seqs, kv_heads, keys, f32, num_sms, few, chain);
+    p.few_as_f32 = few < 0;
+    if (p.few_as_f32) p.few = few_split(tokens, group, seqs, kv_heads, keys, true, num_sms, few);
+    p.split = many_split(tokens, group, f32 ? 128 : 256, seqs, kv_heads, keys, f32, num_sms, many, chain);
+    p.many_as_f32 = many < 0;
+    if (p.many_as_f32) p.split = many_split(tokens, group, 128, seqs, kv_heads, keys, true, num_sms, many);
     p.many = many < few;
     return p;
 }

@@ -94,7 +94,7 @@ struct ManyLayout {
     // fall short (one of 7500 keys by 1.6e-5 of its value, 940 steps of 16).
     // With fp32 outputs they are therefore taken every two tiles of keys, 32
     // steps, and added up by fp32 additions in other columns.  (16-bit outputs:
-    // half an fp16 step is 2.4e-4, and that many rows over that many keys are split.)
+    // kChainF16 and kChainBf16 bound their steps, by more CTAs or by this form.)
     static constexpr int kDrain = kNP == 2 ? 2 : 0;
     static constexpr uint32_t kColSum = 384;
 };
@@ -245,9 +245,12 @@ struct RawRow {
 #pragma unroll
         for (uint32_t &x : w) x = 0u;
     }
-    __device__ __forceinline__ void load(const void *p, long long at, bool vec) {
+    __device__ __forceinline__ void load(const void *p, long long at, bool vec, MxType type) {
         constexpr int kWords = kEach * kNP / 2;
-        if (vec) {
+        if (kNP == 2 && type != MxType::kF32) {  // 16-bit rows as fp32 ones
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = __float_as_uint(wide_value(p, type, at + i));
+        } else if (vec) {
             const char *q = static_cast<const char *>(p) + at * (2 * kNP);
             if constexpr (kWords == 4) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(q);
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                 rows[i].zero();
                 if (first + b + i < tile.rows && d < D)
                     rows[i].load(a.q, (long long)(tile.start + tok) * a.q_token + (long long)(head * group + row_head) * a.q_head + d,
-                                 a.vec);
+                                 a.vec, a.type);
                 if (++row_head == group) row_head = 0, ++tok;
             }
 #pragma unroll
@@ -1032,16 +1035,16 @@ cudaError_t launch_many(const LaunchCtx &c, const MxAttentionArgs &a, int S) {
 }
 
 template <int kBits, int kDP>
-cudaError_t launch_type(const LaunchCtx &c, const MxAttentionArgs &a, int split) {
-    return a.type == MxType::kF32 ? launch_many<kBits, kDP, 1, 2>(c, a, split) : launch_many<kBits, kDP, 2, 1>(c, a, split);
+cudaError_t launch_type(const LaunchCtx &c, const MxAttentionArgs &a, int split, bool as_f32) {
+    return as_f32 || a.type == MxType::kF32 ? launch_many<kBits, kDP, 1, 2>(c, a, split) : launch_many<kBits, kDP, 2, 1>(c, a, split);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split) {
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split, bool as_f32) {
     const bool narrow = a.cache.D <= 64;
-    if (a.cache.bits == 4) return narrow ? launch_type<4, 64>(c, a, split) : launch_type<4, 128>(c, a, split);
-    return narrow ? launch_type<8, 64>(c, a, split) : launch_type<8, 128>(c, a, split);
+    if (a.cache.bits == 4) return narrow ? launch_type<4, 64>(c, a, split, as_f32) : launch_type<4, 128>(c, a, split, as_f32);
+    return narrow ? launch_type<8, 64>(c, a, split, as_f32) : launch_type<8, 128>(c, a, split, as_f32);
 }
 
 }  // namespace q4mm

@@ -67,10 +67,15 @@ void take_fault(q4mm::LaunchCtx *ctx) {
 // q4mm_test_attention_kernel: 0 as planned, 1 few rows, 2 many.
 thread_local int g_test_attention = 0;
 
-q4mm::AttentionPlan plan_attention(int tokens, int heads, int kv_heads, int seqs, int width, int page, bool f32,
+int attention_chain(int dtype) {
+    return dtype == Q4MM_F16 ? q4mm::kChainF16 : dtype == Q4MM_BF16 ? q4mm::kChainBf16 : 0;
+}
+
+q4mm::AttentionPlan plan_attention(int tokens, int heads, int kv_heads, int seqs, int width, int page, int dtype,
                                    int num_sms) {
+    const int chain = attention_chain(dtype);
     q4mm::AttentionPlan p = q4mm::attention_plan(tokens, heads / kv_heads, seqs, kv_heads, q4mm::table_keys(width, page),
-                                                 f32, num_sms);
+                                                 dtype == Q4MM_F32, num_sms, chain);
     if (g_test_attention) p.many = g_test_attention == 2;
     return p;
 }
@@ -780,14 +785,20 @@ int mx_attention(const void *q, long long q_token_stride, long long q_head_strid
                      q_token_stride % 4 == 0 && q_head_stride % 4 == 0 && y_token_stride % 4 == 0 &&
                      y_head_stride % 4 == 0;
     if ((rc = device_ctx(stream, &ctx, false))) return rc;
-    const q4mm::AttentionPlan plan = plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens,
-                                                    dtype == Q4MM_F32, ctx.num_sms);
+    q4mm::AttentionPlan plan = plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens, dtype, ctx.num_sms);
+    if (!plan.many && plan.few.parts > 1) {  // as many parts as the workspace holds
+        const size_t all = q4mm::mx_attention_few_workspace(tokens, heads, kvHeads, headDim, sequences, plan.few);
+        const size_t held = workspace_bytes / (all / plan.few.parts);
+        if (held < (size_t)plan.few.parts) plan.few.parts = held ? (int)held : 1;
+        plan.few_as_f32 |= q4mm::few_chain_passes(q4mm::table_keys(tableWidth, pageTokens), plan.few, attention_chain(dtype));
+    }
     if (plan.many) take_fault(&ctx);
     const q4mm::MxAttentionArgs a{call.cache, call.batch, q, q_token_stride, q_head_stride, y, y_token_stride,
                                   y_head_stride, scale, causal != 0, tokens, heads, static_cast<q4mm::MxType>(dtype),
                                   vec, static_cast<float *>(workspace), workspace_bytes, ctx.status};
     const cudaError_t e =
-        plan.many ? q4mm::launch_mx_attention_many(ctx, a, plan.split) : q4mm::launch_mx_attention_few(ctx, a, plan.few);
+        plan.many ? q4mm::launch_mx_attention_many(ctx, a, plan.split, plan.many_as_f32)
+                  : q4mm::launch_mx_attention_few(ctx, a, plan.few, plan.few_as_f32);
     if (e != cudaSuccess) return fail_cuda(e, "mx_attention launch");
     return Q4MM_OK;
 }
@@ -800,9 +811,9 @@ size_t mx_attention_workspace(int kvHeads, int pageTokens, int headDim, int sequ
     q4mm::LaunchCtx ctx;
     if (device_ctx(nullptr, &ctx, false)) return 0;
     size_t most = 0;
-    for (int f32 = 0; f32 < 2; ++f32) {
+    for (const int dtype : {Q4MM_F32, Q4MM_F16, Q4MM_BF16}) {
         const q4mm::AttentionPlan plan =
-            plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens, f32, ctx.num_sms);
+            plan_attention(tokens, heads, kvHeads, sequences, tableWidth, pageTokens, dtype, ctx.num_sms);
         const size_t bytes =
             plan.many ? 0 : q4mm::mx_attention_few_workspace(tokens, heads, kvHeads, headDim, sequences, plan.few);
         if (bytes > most) most = bytes;

@@ -209,8 +209,9 @@ struct MxAttentionArgs {
 };
 // Bytes of workspace that a split of few rows takes.
 size_t mx_attention_few_workspace(int tokens, int heads, int kv_heads, int D, int seqs, const FewSplit &f);
-cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f);  // few rows a kv head
-cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split);  // tiles of 128, on tcgen05
+// few rows a kv head; tiles of 128, on tcgen05 (as_f32: whatever the type)
+cudaError_t launch_mx_attention_few(const LaunchCtx &c, const MxAttentionArgs &a, const FewSplit &f, bool as_f32);
+cudaError_t launch_mx_attention_many(const LaunchCtx &c, const MxAttentionArgs &a, int split, bool as_f32);
 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the
 // current device; the attribute call is made only when the limit grows, so a

@@ -29,13 +29,38 @@ def test_rows_of_a_key_head_stay_below_32_bits(q4mm, tokens, heads):
     assert q4mm.library().mx_attention_workspace(kv, 16, 32, 1, 4, tokens, heads) == 0
 
 
-def test_keys_of_a_table_leave_room_for_a_tile_in_32_bits(tmp_path):
-    """The kernels round the number of keys up to whole tiles, and look a tile ahead, in 32-bit integers."""
-    out = str(tmp_path / "libatt_limits.so")
+@pytest.fixture(scope="module")
+def limits(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("att_limits") / "libatt_limits.so")
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC",
                     f"-I{os.path.join(ROOT, 'quantized_matmul_q4_gb300', 'csrc')}",
                     os.path.join(ROOT, "tests", "attention_limits_shim.cpp"), "-o", out], check=True)
     lib = ctypes.CDLL(out)
+    lib.att_chain.argtypes = [ctypes.c_longlong] + [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_int)]
+    return lib
+
+
+def test_keys_of_a_table_leave_room_for_a_tile_in_32_bits(limits):
+    """The kernels round the number of keys up to whole tiles, and look a tile ahead, in 32-bit integers."""
     for width, page in ((2 ** 31 - 1, 2 ** 24), (128, 2 ** 24), (129, 2 ** 24), (2 ** 27, 16), (2 ** 27 - 1, 16), (2 ** 31 - 1, 16)):
-        assert lib.att_table_keys(width, page) + 2 * lib.att_tile_keys() <= 2 ** 31
-    assert lib.att_table_keys(127, 2 ** 24) == 127 * 2 ** 24 and lib.att_table_keys(0, 16) == 0
+        assert limits.att_table_keys(width, page) + 2 * limits.att_tile_keys() <= 2 ** 31
+    assert limits.att_table_keys(127, 2 ** 24) == 127 * 2 ** 24 and limits.att_table_keys(0, 16) == 0
+
+
+def test_sums_of_16_bit_rows_have_a_bounded_number_of_steps(limits):
+    """However long a table, a tensor-core sum of 16 keys a step has no more steps than drop a third of half a step of the
+    output, or the rows take the form for fp32; where all fits, plans are as without the bound."""
+    out, free = (ctypes.c_int * 7)(), (ctypes.c_int * 7)()
+    for bf16 in (0, 1):
+        chain = limits.att_chain_of(bf16)
+        assert chain * 1.7e-8 < 2.0 ** (-9 if bf16 else -12) / 3
+        for tokens, group, seqs, kv in ((1, 1, 1, 1), (1, 8, 1, 1), (64, 4, 64, 8), (2048, 4, 1, 8), (8192, 1, 1, 32), (152, 2, 152, 2), (65536, 4, 1, 8)):
+            for keys in (1000, 60000, 131072, 2 ** 19, 2 ** 20, 3000000, 2 ** 23, 2 ** 26, 2 ** 31 - 1):
+                limits.att_chain(tokens, group, seqs, kv, -(-keys // 16), 16, chain, 152, out)
+                limits.att_chain(tokens, group, seqs, kv, -(-keys // 16), 16, 0, 152, free)
+                many, split, many32, _, cluster, parts, few32 = out
+                assert few32 or -(-keys // 16) <= chain * 8 * cluster * parts
+                assert many32 or -(--(-keys // 128) // split) * 8 <= chain
+                if keys <= 16 * chain:
+                    assert list(out) == list(free) and not many32 and not few32
+                assert not free[2] and not free[6]

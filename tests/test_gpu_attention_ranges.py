@@ -107,3 +107,42 @@ def test_small_values_of_large_probability(high, low, dtype):
         x, xv = base._dev(x, dtype)
         y = q.mx_attention(x, c.device_cache(), *c.device_batch(), scale=1.0)
         base._check(c, x, y, xv, dtype, scale=1.0)
+
+
+@KERNELS
+@pytest.mark.parametrize("D,bits,keys,rows,dtype", [
+    (64, 8, 0, 152, "float16"), (128, 8, 0, 152, "float16"), (128, 4, 0, 152, "float16"), (64, 4, 0, 152, "float16"),
+    (128, 8, 1, 152, "float16"), (64, 4, 1, 152, "float16"), (128, 8, 2, 8, "bfloat16"), (96, 4, 2, 8, "bfloat16")])
+def test_long_16_bit_sums_do_not_drift(kernel, D, bits, keys, rows, dtype):
+    """Values of one over more keys than a sum in the tensor cores may hold, which drops up to 2^-23 of itself a step of 16
+    keys: outputs are one, whatever the keys that a CTA takes.  (Probabilities of 16 bits round by chance, and an fp16
+    output is one as long as its value is within 2^-12.)"""
+    q, torch = _q(), _torch()
+    keys, page = ((3_000_000, 500_000), (5_000_000, 600_000), (3_000_000, 5_000_000))[keys][kernel == "many"], 4096
+    cache = q.mx_cache(1, 2, D, page=page, bits=bits)
+    g = torch.Generator(device="cuda").manual_seed(D + bits)
+    k = torch.randn(page, 2, D, generator=g, device="cuda")
+    q.mx_cache_write(cache, k, torch.ones_like(k), base._i32([0, page]), base._i32([page]), base._i32([[0]]))
+    x = torch.randn(rows, 4, D, generator=g, device="cuda").to(getattr(torch, dtype))
+    table = torch.zeros(rows, -(-keys // page), dtype=torch.int32, device="cuda")
+    y = q.mx_attention(x, cache, torch.arange(rows + 1, dtype=torch.int32, device="cuda"),
+                       torch.full((rows,), keys, dtype=torch.int32, device="cuda"), table)
+    q.device_status()
+    assert bool((y == 1).all())
+
+
+def test_long_16_bit_sums_without_a_workspace():
+    """One row over more keys than one cluster's sums may hold, the parts' workspace left out."""
+    q, torch = _q(), _torch()
+    keys, page = 5_000_000, 4096
+    c = q.mx_cache(1, 1, 64, page=page)
+    k = torch.randn(page, 1, 64, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    q.mx_cache_write(c, k, torch.ones_like(k), base._i32([0, page]), base._i32([page]), base._i32([[0]]))
+    x = torch.randn(1, 4, 64, device="cuda").half()
+    table, starts, lengths = torch.zeros(1, -(-keys // page), dtype=torch.int32, device="cuda"), base._i32([0, 1]), base._i32([keys])
+    y = torch.empty_like(x)
+    q.mx_attention_ptr((x.data_ptr(), 256, 64), 1, (*[t.data_ptr() for t in c[:4]], 1, 1, page, 64, 8),
+                       (starts.data_ptr(), lengths.data_ptr(), table.data_ptr(), 1, table.shape[1]), 0.125, 1,
+                       (y.data_ptr(), 256, 64), 1, 4, 0, 0, torch.cuda.current_stream().cuda_stream)
+    q.device_status()
+    assert bool((y == 1).all())
