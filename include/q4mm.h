@@ -533,13 +533,15 @@ int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes
  * row's own where causal, else all lengths[i].  A row that sees none gives
  * zeros.  What a row does not see has no part in it, NaN and infinities
  * included; a block of k that is NaN makes the rows that see it NaN, a block
- * of v those rows' 32 values.
+ * of v those rows' 32 values, and so do codes that are NaN (which no call here
+ * writes), those of v their one value.
  * q, y: [tokens][heads][headDim] of type dtype, strided as for rope_rotate,
  * aligned to their elements, not overlapping each other or the cache.
  * Precision: keys and values exact (a block whose scale is 2^-17 of its
  *         token's and head's largest counts as zero; rows beside a token whose
  *         largest scale byte of v is above 160 or from 1 to 79, a value of 2^42 and
- *         more or below 2^-39, 2^36 and 2^-45 in 4 bits, are right too, but take
+ *         more or below 2^-39, 2^36 and 2^-45 in 4 bits, or with a NaN among
+ *         its codes of v, are right too, but take
  *         some fifty times as long), queries exact to 2^-22 of a
  *         row's largest value; scores, their maximum, sums and outputs in
  *         fp32; probabilities rounded to 2^-11 (2^-22 where dtype is

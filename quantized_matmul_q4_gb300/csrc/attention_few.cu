@@ -630,6 +630,11 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, x);
             const int r = 8 * n + 2 * t + j;
+            // A code of v that is NaN reaches rows that do not see it here: they have NaN among their values, but not in their sum.
+            float any = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) any += o[n][i][j] + o[n][i][2 + j];
+            if (__ballot_sync(0xFFFFFFFFu, isnan(any) && !isnan(v)) >> t & 0x11111111u) M[n][j] = kSpoiltMax, v = kSpoilt;
             if (g == 0) sh.m[warp][r] = M[n][j], sh.l[warp][r] = v;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)

@@ -113,7 +113,7 @@ struct ManyShared {
     int nan_from[4];
     uint32_t tmem;
     int abort;
-    int spoilt;  // values that the sums cannot take were met
+    int spoilt, suspect;  // values that the sums cannot take were met; NaN among a row's values
 };
 
 static_assert(sizeof(ManyShared) <= 15 * 1024, "");
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             mbar_init(&sh.q_full, L::kSoftmaxWarps), mbar_init(&sh.done, 1);
             mbar_init(&sh.dequant_done, L::kDequantWarps);
             fence_mbar_init();
-            sh.abort = 0, sh.spoilt = 0;
+            sh.abort = 0, sh.spoilt = 0, sh.suspect = 0;
             for (int i = 0; i < 4; ++i) sh.nan_from[i] = kNever;
         }
         __syncwarp();
@@ -615,10 +615,9 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
              mbar_wait_prompt(&sh.dequant_done, 0, wait_limit, abort);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
             give_up();
-        } else if (sh.spoilt) {
-            many_plain<kBits, kDP, kTiles, kNP>(a, sh, base, group, tiles);
         } else {
             tc_fence_after();
+            float any = 0.f;
             sh.m[mine] = M, sh.l[side][mine] = l;
             const uint32_t to = base + (mine * L::kPitch + kDP / 2 * side) * 4;
 #pragma unroll
@@ -638,13 +637,23 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                     for (int x = 0; x < 32; ++x) o[x] = 0u;
                 }
 #pragma unroll
-                for (int x = 0; x < 32; x += 4)
+                for (int x = 0; x < 32; x += 4) {
+                    any += __uint_as_float(o[x]) + __uint_as_float(o[x + 1]) + (__uint_as_float(o[x + 2]) + __uint_as_float(o[x + 3]));
                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * (k + x)), "r"(o[x]),
                                  "r"(o[x + 1]), "r"(o[x + 2]), "r"(o[x + 3])
                                  : "memory");
+                }
             }
             tc_fence_before();
+            if (isnan(any)) sh.suspect = 1, sh.top[0][side][mine] = any;
         }
+        // A code of v that is NaN reaches rows that do not see it here: they have NaN among their values, but not in their sum.
+        named_bar_sync(9, 32 * L::kSoftmaxWarps);
+        if (sh.suspect) {
+            if (isnan(sh.top[0][side][mine]) && !isnan(sh.l[0][mine] + sh.l[1][mine])) sh.spoilt = 1;
+            named_bar_sync(9, 32 * L::kSoftmaxWarps);
+        }
+        if (sh.spoilt && !*abort) many_plain<kBits, kDP, kTiles, kNP>(a, sh, base, group, tiles);
         meet();
         {
             // Each CTA of the cluster joins and writes its share of the rows:

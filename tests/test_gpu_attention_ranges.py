@@ -146,3 +146,30 @@ def test_long_16_bit_sums_without_a_workspace():
                        (y.data_ptr(), 256, 64), 1, 4, 0, 0, torch.cuda.current_stream().cuda_stream)
     q.device_status()
     assert bool((y == 1).all())
+
+
+@pytest.mark.filterwarnings("ignore:All-NaN slice")
+@KERNELS
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("news,lengths,D", [([5], [40], 128), ([5], [40], 64), ([1, 1], [700, 90], 96), ([150], [400], 128), ([300, 20], [300, 333], 32)])
+def test_nan_codes_stay_where_they_are_seen(news, lengths, D, dtype):
+    """Codes of v that are NaN (the format has them; no call here writes them) reach the rows that see them, in their value
+    alone; those under a NaN scale, in its block.  Codes of k reach the rows that see them whole."""
+    q, torch = _q(), _torch()
+    c = Case(sum(lengths) + D, news, lengths, 2, D, 16, 8).fill()
+    n = news[0]
+    last = int(c.lengths[0])
+    def put(what, head, p, d, code):
+        c.cache[what + "_codes"][c.table[0, p // 16], head, p % 16, d] = code
+    if n > 1:
+        put("v", 0, last - 1, 3, 0x7F), put("v", 0, last - n // 2, D - 1, 0xFF), put("v", 0, last - n // 2, 7, 0x7F)
+        put("v", 1, last - 2, 5, 0x7F)
+        c.cache["v_scales"][c.table[0, (last - 2) // 16], 1, (last - 2) % 16, 0] = 255
+        put("k", 1, last - 1, 0, 0x7F)
+    else:
+        put("v", 0, 17, 40, 0xFF), put("v", 0, last - 1, 8, 0x7F)
+    x, xv = base._dev(c.rng.normal(size=(c.T, 4, D)), dtype)
+    y = q.mx_attention(x, c.device_cache(), *c.device_batch())
+    q.device_status()
+    assert bool(torch.isnan(y).any())
+    base._check(c, x, y, xv, dtype)
