@@ -501,7 +501,7 @@ int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride
  *
  * mx_cache_write — k, v [tokens][kvHeads][headDim] of type dtype, strided as
  * for rope_rotate, to their places: k turned as by rope_rotate at its positions
- * (rotated = 0: as it is) in fp32, near a border between two codes in 64 bits,
+ * (rotated = 0: as it is) in fp32, near a border between two codes or scales in 64 bits,
  * and then quantised, with no rounding between.
  * Two rows must not have the same place (pages of one table shared with
  * another sequence hold what neither writes).

@@ -385,25 +385,33 @@ __device__ __noinline__ float turned_again(const T *head, int d, const RopeView 
 // 2^20 (8 bits) or 2^22.  (Without this 26 to 40 codes of 68 million differed from
 // those of the exact values, with it 8 to 19; 8271 tokens written take 45.7 us, 43.2 without.)  Below the codes' normal numbers the borders lie
 // elsewhere and are left as they are.
+// So are those within 4 units of a power of two where that is the block's largest value: there the
+// block's scale has its border, and all of its codes with it.  Returns the float bits of that value.
 template <int kBits, class T>
-__device__ __forceinline__ void settle(float (&f)[8], const T *head, int d, const RopeView &r, long long position, bool ok) {
+__device__ __forceinline__ uint32_t settle(float (&f)[8], const T *head, int d, const RopeView &r, long long position, bool ok) {
     constexpr uint32_t kMask = kBits == 8 ? 0xFFFFF : 0x3FFFFF, kBorder = kMask / 2 + 1;
+    const uint32_t amax = mx_block_amax(f);
     uint32_t nearest = kMask;
 #pragma unroll
     for (int i = 0; i < 8; ++i) nearest = min(nearest, __float_as_uint(f[i]) - (kBorder - 4) & kMask);
-    // (Values that are not turned lie on borders often, at position 0 too: a 16-bit one in 16.)
-    if (nearest > 8 || !ok || d >= r.rotated || position == 0) return;
+    const bool top = (amax + 4 & 0x7FFFFF) <= 8 && amax >= 0x00800000u;
+    // (Values that are not turned lie on borders often: a 16-bit one in 16.)
+    if (!__any_sync(0xFFFFFFFFu, (nearest <= 8 || top) && d < r.rotated)) return amax;
+    const bool mine = ok && (position != 0 || r.magnitude != 1.f);  // (else they are as they were)
+    const uint32_t power = top ? amax + 4 & 0x7F800000u : 0x80000000u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (d + i < r.rotated && (__float_as_uint(f[i]) - (kBorder - 4) & kMask) <= 8)
+        if (mine && d + i < r.rotated && ((__float_as_uint(f[i]) - (kBorder - 4) & kMask) <= 8 ||
+                                          (__float_as_uint(f[i]) & 0x7FFFFFFFu) + 4 - power <= 8))
             f[i] = turned_again(head, d + i, r, position);
+    return mx_block_amax(f);
 }
 
-// Quantises eight values of a block of four lanes into a slot: codes at
+// Quantises eight values of a block of four lanes, whose largest has the bits amax, into a slot: codes at
 // `codes`, the block's scale byte (and the padding's zeros) at `scales`.
 template <int kBits>
-__device__ __forceinline__ void put_codes(const float (&f)[8], uint8_t *codes, uint8_t *scales, int d, int D, bool ok) {
-    const uint32_t amax = mx_block_amax(f);
+__device__ __forceinline__ void put_codes(const float (&f)[8], uint32_t amax, uint8_t *codes, uint8_t *scales, int d, int D,
+                                          bool ok) {
     const uint32_t b = mx_quantize8(f, amax, kBits, codes, d, ok ? D : 0);
     if (ok && (d & 31) == 0) {
         const int block = d / kMxBlock, blocks = D / kMxBlock;
@@ -460,14 +468,15 @@ __global__ void __launch_bounds__(kThreads, kForm == 0 ? 1 : 4) mx_cache_write_k
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] = 0.f;
                     if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, f, g);
-                    settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u]);
-                    settle<kBits>(g, x + u * it.step * head, it.d + span, r, at.position[s], ok[u]);
-                    put_codes<kBits>(f, c, b, it.d, D, ok[u]);
-                    put_codes<kBits>(g, c, b, it.d + span, D, ok[u]);
+                    const uint32_t f_max = settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u]);
+                    put_codes<kBits>(f, f_max, c, b, it.d, D, ok[u]);
+                    const uint32_t g_max = settle<kBits>(g, x + u * it.step * head, it.d + span, r, at.position[s], ok[u]);
+                    put_codes<kBits>(g, g_max, c, b, it.d + span, D, ok[u]);
                 } else {
                     if (ok[u]) v[u].turn(table.cos[s], table.sin[s], it.d, r, f);
-                    if (r.rotated) settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u]);
-                    put_codes<kBits>(f, c, b, it.d, D, ok[u]);
+                    const uint32_t f_max = r.rotated ? settle<kBits>(f, x + u * it.step * head, it.d, r, at.position[s], ok[u])
+                                                     : mx_block_amax(f);
+                    put_codes<kBits>(f, f_max, c, b, it.d, D, ok[u]);
                 }
             }
             x += kU * it.step * head, codes += kU * apart * row_bytes, scales += kU * apart * 4;
