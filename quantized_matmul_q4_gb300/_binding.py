@@ -922,7 +922,7 @@ def mx_attention(q, cache: MxCache, starts, lengths, pages, scale: float | None 
     ba = _batch_arg(starts, lengths, pages, device)
     qa = _heads_arg(q, "q")
     T, H, D = shape = q.shape
-    if D != ca[7] or H == 0 or H % ca[5]:
+    if D != ca[7] or H == 0 or ca[5] == 0 or H % ca[5]:
         raise ValueError("q must have the cache's head_dim, and a multiple of its heads")
     at, side = _call_stream(stream, device)
     if out is None:

@@ -64,3 +64,20 @@ def test_sums_of_16_bit_rows_have_a_bounded_number_of_steps(limits):
                 if keys <= 16 * chain:
                     assert list(out) == list(free) and not many32 and not few32
                 assert not free[2] and not free[6]
+
+
+def test_a_cache_of_no_heads_is_refused(monkeypatch):
+    """Queries of any number of heads have no key heads there."""
+    import torch
+    import quantized_matmul_q4_gb300 as q
+    from quantized_matmul_q4_gb300 import _binding as b
+    b._Torch.load()
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)     # (no call here reaches a launch)
+    monkeypatch.setattr(b._Torch, "current_device", lambda: 0)
+    monkeypatch.setattr(b._Torch, "raw_stream", lambda device: 0)
+    monkeypatch.setattr(b, "_LIB", None)
+    codes, scales = torch.zeros(4, 0, 16, 64, dtype=torch.uint8), torch.zeros(4, 0, 16, 4, dtype=torch.uint8)
+    i32 = dict(dtype=torch.int32)
+    batch = torch.tensor([0, 3], **i32), torch.tensor([3], **i32), torch.zeros(1, 2, **i32)
+    with pytest.raises(ValueError):
+        q.mx_attention(torch.zeros(3, 4, 64), q.MxCache(codes, scales, codes, scales, 64, 8), *batch)
