@@ -496,8 +496,9 @@ int rope_rotate(const void *x, long long x_token_stride, long long x_head_stride
  * page number outside 0 .. pages − 1, or a position beyond the table, is not
  * accessed: q4mm_device_status then reports Q4MM_ERR_INDEX, and what that call
  * computes for the sequence is undefined.  Rows before position 0 (more rows
- * than lengths[i]) take part in nothing; rows behind the last sequence are
- * left as they were.
+ * than lengths[i]) are neither written nor read (in mx_attention they see
+ * nothing where causal, else what the sequence's other rows see); rows behind the last
+ * sequence are left as they were.
  *
  * mx_cache_write — k, v [tokens][kvHeads][headDim] of type dtype, strided as
  * for rope_rotate, to their places: k turned as by rope_rotate at its positions
@@ -537,15 +538,21 @@ int mx_cache_read(const void *k_codes, const void *k_scales, const void *v_codes
  * writes), those of v their one value.
  * q, y: [tokens][heads][headDim] of type dtype, strided as for rope_rotate,
  * aligned to their elements, not overlapping each other or the cache.
- * Precision: keys and values exact (a block whose scale is 2^-17 of its
- *         token's and head's largest counts as zero; rows beside a token whose
- *         largest scale byte of v is above 160 or from 1 to 79, a value of 2^42 and
- *         more or below 2^-39, 2^36 and 2^-45 in 4 bits, or with a NaN among
- *         its codes of v, are right too, but take
- *         some fifty times as long), queries exact to 2^-22 of a
- *         row's largest value; scores, their maximum, sums and outputs in
- *         fp32; probabilities rounded to 2^-11 (2^-22 where dtype is
- *         Q4MM_F32) of their value or 2^-30 of the row's largest.
+ * Precision: keys and values exact, but that a block whose scale is 2^-17 of
+ *         its token's and head's largest counts as zero (of v, that is 32
+ *         values of what the token adds to the output); queries exact to
+ *         2^-22 of a row's largest value; scores, their maximum, sums and
+ *         outputs in fp32 (tensor-core sums lose at most a third of half a step
+ *         of dtype with their length).  Probabilities enter the product with
+ *         v rounded to 2^-11 of their value, 2^-22 where dtype is Q4MM_F32, or
+ *         2^-30 of the row's largest product of a probability and a |v|; before
+ *         that their exponents round as fp32 numbers of the size of the score
+ *         and of log2 |v|.  With Q4MM_F16 the first of these adds a fifth to a
+ *         third to the error that the output's own rounding has.
+ *         Rows beside a token whose largest scale byte of v is above 160 or
+ *         from 1 to 79 (values of 2^42 and more or below 2^-39, in 4 bits 2^36
+ *         and 2^-45), or with NaN among its codes of v, are right too, but take
+ *         tens (single tokens) to hundreds (prompts) of times as long.
  *         The same call gives the same bits again.
  * workspace: device memory (16-byte aligned, overlapping nothing else) for the
  *         call to write to, workspace_bytes long; NULL with 0 and any length

@@ -168,7 +168,8 @@ struct PlainSums {
 
 // By plain arithmetic, one row a warp: those of its first `keys` keys that lie in the groups of 16 tokens first, first +
 // step .. before last.  Two passes, the second with probabilities that add up to 1, whose powers of two
-// meet those of v before either leaves the floats.
+// meet those of v before either leaves the floats.  Slow: decoding takes 17 times as long (16
+// sequences of 2000, 32 heads: 53 and 896 us), a prompt of 2000 with 8 heads 412 times (33 us and 13.7 ms).
 template <int kBits>
 __device__ __forceinline__ PlainSums plain_row(const MxAttentionArgs &a, const RowTile &tile, const int row, const int group,
                                                const int head, const int keys, const int first, const int last,
@@ -187,12 +188,11 @@ __device__ __forceinline__ PlainSums plain_row(const MxAttentionArgs &a, const R
     };
     auto score = [&](int g, long long slot) {
         if (slot < 0 || 16 * g + tok >= sees) slot = -1;
-        float s = -INFINITY;
+        float s = 0.f;
         if (slot >= 0) {
             const uint8_t *codes = a.cache.k_codes + (slot + tok) * row_bytes + half * (row_bytes / 2);
             const uint32_t scales = *reinterpret_cast<const uint32_t *>(a.cache.k_scales + (slot + tok) * 4);
             float block = 0.f;
-            s = 0.f;
             for (int i = 0; i < D / 2; i += kWord) {
                 const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + i * kBits / 8);
                 const int d = half * (D / 2) + i;
@@ -211,7 +211,7 @@ __device__ __forceinline__ PlainSums plain_row(const MxAttentionArgs &a, const R
             }
         }
         s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
-        return s * (a.scale * kLog2e);
+        return slot < 0 ? -INFINITY : s * (a.scale * kLog2e);  // (a scale of zero times an infinity is not one)
     };
     float m = -INFINITY, l = 0.f;
     for (int g = first; g < last && 16LL * g < sees; g += step) {

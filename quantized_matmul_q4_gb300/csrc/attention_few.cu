@@ -171,8 +171,8 @@ struct PlainScratch {
 };
 
 // The rows of tile and head `item` that CTA `rank` of S stores, kHere at once, by plain_row, the keys of a row
-// shared by the warps.  Some fifty times slower than the kernel.  (At the end of a kernel, and a function of its own
-// that finds its tile anew: anywhere else, or with what it needs held for it, a CTA takes 0.2 us longer.)
+// shared by the warps.  (At the end of a kernel, and a function of its own that finds its tile anew: anywhere else, or
+// with what it needs held for it, a CTA takes 0.2 us longer.)
 template <int kBits, int kR, int kHere>
 __device__ __noinline__ void few_plain(const MxAttentionArgs &a, int group, unsigned item, int rank, int S, PlainScratch &sh) {
     const RowTile tile = row_tile(a.batch, item / (unsigned)a.cache.heads, group, kR, a.tokens);

@@ -286,8 +286,8 @@ struct RawRow {
     }
 };
 
-// The softmax warps' share of the CTA's rows, over its keys, by plain_row, to where the sums lie.  Some fifty times slower than the
-// kernel.  (A function of its own that finds rows and keys anew, so that the kernel holds nothing for it.)
+// The softmax warps' share of the CTA's rows, over its keys, by plain_row, to where the sums lie.  (A function of its
+// own that finds rows and keys anew, so that the kernel holds nothing for it.)
 template <int kBits, int kDP, int kTiles, int kNP>
 __device__ __noinline__ void many_plain(const MxAttentionArgs &a, ManyShared &sh, uint32_t base, int group, long long tiles) {
     using L = ManyLayout<kBits, kDP, kTiles, kNP>;

@@ -173,3 +173,31 @@ def test_nan_codes_stay_where_they_are_seen(news, lengths, D, dtype):
     q.device_status()
     assert bool(torch.isnan(y).any())
     base._check(c, x, y, xv, dtype)
+
+
+@KERNELS
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("causal,scale", [(True, None), (False, 0.3), (True, 0.0)])
+@pytest.mark.parametrize("news,lengths,group,D,page,bits", [
+    ([1], [45], 1, 32, 16, 8), ([1], [3000], 4, 96, 48, 4), ([9, 0, 3], [9, 40, 1], 3, 128, 16, 8), ([40, 5], [200, 3], 2, 96, 16, 8),
+    ([150], [333], 2, 32, 64, 4), ([300], [300], 1, 128, 32, 8)])
+def test_far_values_in_every_shape(news, lengths, group, D, page, bits, causal, scale, dtype):
+    """Values that the kernels' own sums cannot take, over head sizes, groups, rows that see nothing, unaligned and
+    strided rows, with and without a mask, scores of zero among them."""
+    q, torch = _q(), _torch()
+    c = Case(sum(lengths) + D, news, lengths, 2, D, page, bits, offset=2).fill()
+    for i, n in enumerate(lengths):
+        for p in range(n):          # every fifth token tiny, some none at all; fp16 holds what the others give
+            s = c.cache["v_scales"][c.table[i, p // page], :, p % page]
+            if p % 5 == 0:
+                s[:] = np.clip(s.astype(int) - 70, 0, 250)
+            elif p % 7 == 0:
+                s[:], c.cache["v_codes"][c.table[i, p // page], :, p % page] = 0, 0
+    heads = 2 * group
+    fused, _ = base._dev(1.5 * c.rng.normal(size=(c.T + 3, heads * D + 5)), dtype)
+    x = fused[:, 3:3 + heads * D].view(c.T + 3, heads, D)
+    out = torch.full((heads, c.T + 3, D + 1), 7.0, device="cuda", dtype=x.dtype)[..., :D].transpose(0, 1)
+    q.mx_attention(x, c.device_cache(), *c.device_batch(), scale=scale, causal=causal, out=out)
+    q.device_status()
+    assert bool((out[:2] == 7).all()) and bool((out[c.T:] == 7).all())
+    base._check(c, x, out, x.double().cpu().numpy(), dtype, causal=causal, scale=scale)
