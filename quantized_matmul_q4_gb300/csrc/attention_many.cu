@@ -421,50 +421,50 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
             int tok = (tile.first + first) / group, row_head = (tile.first + first) % group;
 #pragma unroll 1
             for (int b = 0; b < 16; b += kAtOnce) {
-            RawRow<kEach, kNP> rows[kAtOnce];
+                RawRow<kEach, kNP> rows[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                rows[i].zero();
-                if (first + b + i < tile.rows && d < D)
-                    rows[i].load(a.q, (long long)(tile.start + tok) * a.q_token + (long long)(head * group + row_head) * a.q_head + d,
-                                 a.vec, a.type);
-                if (++row_head == group) row_head = 0, ++tok;
-            }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const int r = 32 * quarter + 16 * side + b + i;  // row of the slab
-                float v[kEach];
-                rows[i].values(a.type, v);
-                uint32_t top = 0;
-#pragma unroll
-                for (int k = 0; k < kEach; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                // 2^(141 - e) puts a largest value of biased exponent e at 2^14; not where it is infinite or NaN.
-                const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
-                if (lane == 0) sh.power[128 * t + r] = e - 141;
-                const float mult = __int_as_float((268 - e) << 23);
-                const uint32_t at = slab + col + r * 128 + (((d % 64) / 8) ^ (r & 7)) * 16;
-                uint32_t hi[kEach / 2];
-#pragma unroll
-                for (int k = 0; k < kEach / 2; ++k) hi[k] = half2_of(v[2 * k] * mult, v[2 * k + 1] * mult);
-                if constexpr (kEach == 4)
-                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-                else
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
-                if constexpr (kNP == 2) {
-                    uint32_t lo[kEach / 2];
-#pragma unroll
-                    for (int k = 0; k < kEach / 2; ++k) {
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
-                        lo[k] = half2_of(v[2 * k] * mult - b.x, v[2 * k + 1] * mult - b.y);
-                    }
-                    if constexpr (kEach == 4)
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kSlab), "r"(lo[0]), "r"(lo[1])
-                                     : "memory");
-                    else
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kSlab), "r"(lo[0]) : "memory");
+                for (int i = 0; i < kAtOnce; ++i) {
+                    rows[i].zero();
+                    if (first + b + i < tile.rows && d < D)
+                        rows[i].load(a.q, (long long)(tile.start + tok) * a.q_token + (long long)(head * group + row_head) * a.q_head + d,
+                                     a.vec, a.type);
+                    if (++row_head == group) row_head = 0, ++tok;
                 }
-            }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int r = 32 * quarter + 16 * side + b + i;  // row of the slab
+                    float v[kEach];
+                    rows[i].values(a.type, v);
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) top = max(top, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    // 2^(141 - e) puts a largest value of biased exponent e at 2^14; not where it is infinite or NaN.
+                    const int e = top >= 0x7F800000u ? 141 : max((int)(top >> 23), 15);
+                    if (lane == 0) sh.power[128 * t + r] = e - 141;
+                    const float mult = __int_as_float((268 - e) << 23);
+                    const uint32_t at = slab + col + r * 128 + (((d % 64) / 8) ^ (r & 7)) * 16;
+                    uint32_t hi[kEach / 2];
+#pragma unroll
+                    for (int k = 0; k < kEach / 2; ++k) hi[k] = half2_of(v[2 * k] * mult, v[2 * k + 1] * mult);
+                    if constexpr (kEach == 4)
+                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+                    else
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(hi[0]) : "memory");
+                    if constexpr (kNP == 2) {
+                        uint32_t lo[kEach / 2];
+#pragma unroll
+                        for (int k = 0; k < kEach / 2; ++k) {
+                            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
+                            lo[k] = half2_of(v[2 * k] * mult - b.x, v[2 * k + 1] * mult - b.y);
+                        }
+                        if constexpr (kEach == 4)
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + L::kSlab), "r"(lo[0]), "r"(lo[1])
+                                         : "memory");
+                        else
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + L::kSlab), "r"(lo[0]) : "memory");
+                    }
+                }
             }
         }
         fence_async_proxy();
@@ -879,137 +879,137 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
     } else {
         if constexpr (L::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         if (warp == L::kIssueWarp) {
-        // ---- issue ----
-        const bool leader = elect_lane();
-        constexpr uint32_t kIdS = f16_idesc(kManyKeys, false), kIdO = f16_idesc(kDP, true);
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, int parity) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_spin_abortable(bar, parity, wait_limit, abort));
-            tc_fence_after();
-            return ok;
-        };
-        auto scores = [&](int t, int i) {  // S of tile t and the CTA's keys i
-            const uint64_t qd = k_major_desc(base + t * kNP * L::kSlab);
-            const uint64_t kd = k_major_desc(base + L::off_ring + 2 * i % L::kSlots * L::kSlab);
-            const bool last = t == 1 || cnt[1] <= i;  // no other tile wants K
-            uint64_t *k_free = &sh.ring_free[2 * i % L::kSlots];
-            if (leader) {
+            // ---- issue ----
+            const bool leader = elect_lane();
+            constexpr uint32_t kIdS = f16_idesc(kManyKeys, false), kIdO = f16_idesc(kDP, true);
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, int parity) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_spin_abortable(bar, parity, wait_limit, abort));
+                tc_fence_after();
+                return ok;
+            };
+            auto scores = [&](int t, int i) {  // S of tile t and the CTA's keys i
+                const uint64_t qd = k_major_desc(base + t * kNP * L::kSlab);
+                const uint64_t kd = k_major_desc(base + L::off_ring + 2 * i % L::kSlots * L::kSlab);
+                const bool last = t == 1 || cnt[1] <= i;  // no other tile wants K
+                uint64_t *k_free = &sh.ring_free[2 * i % L::kSlots];
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kNP * kDP / 16; ++k) {
-                    const int in = k % (kDP / 16);
-                    const uint32_t at = in / 4 * (kHalf >> 4) + 2 * (in % 4);
-                    // (Second terms first, while there is little to cut off.)
-                    mma_ss(tmem + L::col_s(t), qd + (k < (kNP - 1) * kDP / 16 ? L::kSlab >> 4 : 0) + at, kd + at, kIdS, k != 0);
+                    for (int k = 0; k < kNP * kDP / 16; ++k) {
+                        const int in = k % (kDP / 16);
+                        const uint32_t at = in / 4 * (kHalf >> 4) + 2 * (in % 4);
+                        // (Second terms first, while there is little to cut off.)
+                        mma_ss(tmem + L::col_s(t), qd + (k < (kNP - 1) * kDP / 16 ? L::kSlab >> 4 : 0) + at, kd + at, kIdS, k != 0);
+                    }
+                    tc_commit(&sh.s_full[t]);
+                    if (last) tc_commit(k_free);
                 }
-                tc_commit(&sh.s_full[t]);
-                if (last) tc_commit(k_free);
-            }
-            __syncwarp();
-        };
-        auto outputs = [&](int t, int i) {
-            const uint64_t vd = n_major_desc(base + L::off_ring + (2 * i + 1) % L::kSlots * L::kSlab, kHalf);
-            const bool last = t == 1 || cnt[1] <= i;
-            uint64_t *v_free = &sh.ring_free[(2 * i + 1) % L::kSlots];
-            if (leader) {
+                __syncwarp();
+            };
+            auto outputs = [&](int t, int i) {
+                const uint64_t vd = n_major_desc(base + L::off_ring + (2 * i + 1) % L::kSlots * L::kSlab, kHalf);
+                const bool last = t == 1 || cnt[1] <= i;
+                uint64_t *v_free = &sh.ring_free[(2 * i + 1) % L::kSlots];
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < kNP * kManyKeys / 16; ++k) {
-                    const int in = k % (kManyKeys / 16);
-                    const uint32_t p_col = k < (kNP - 1) * kManyKeys / 16 ? L::kColLow + 8 * in : L::col_s(t) + L::col_p(in);
-                    mma_ts(tmem + L::col_o(t), tmem + p_col, vd + (2048 >> 4) * in, kIdO, (L::kDrain > 0 ? i % L::kDrain : i) != 0 || k != 0);
+                    for (int k = 0; k < kNP * kManyKeys / 16; ++k) {
+                        const int in = k % (kManyKeys / 16);
+                        const uint32_t p_col = k < (kNP - 1) * kManyKeys / 16 ? L::kColLow + 8 * in : L::col_s(t) + L::col_p(in);
+                        mma_ts(tmem + L::col_o(t), tmem + p_col, vd + (2048 >> 4) * in, kIdO, (L::kDrain > 0 ? i % L::kDrain : i) != 0 || k != 0);
+                    }
+                    if (last) tc_commit(v_free);
                 }
-                if (last) tc_commit(v_free);
-            }
-            __syncwarp();
-        };
-        auto k_ready = [&](int i) { return wait(&sh.ring_full[2 * i % L::kSlots], (2 * i / L::kSlots) & 1); };
-        auto v_ready = [&](int i) { return wait(&sh.ring_full[(2 * i + 1) % L::kSlots], ((2 * i + 1) / L::kSlots) & 1); };
-        if (steps > 0 && wait(&sh.q_full, 0) && k_ready(0)) {
+                __syncwarp();
+            };
+            auto k_ready = [&](int i) { return wait(&sh.ring_full[2 * i % L::kSlots], (2 * i / L::kSlots) & 1); };
+            auto v_ready = [&](int i) { return wait(&sh.ring_full[(2 * i + 1) % L::kSlots], ((2 * i + 1) / L::kSlots) & 1); };
+            if (steps > 0 && wait(&sh.q_full, 0) && k_ready(0)) {
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                if (cnt[t] > 0) scores(t, 0);
-            for (int i = 0; i < steps && ok; ++i) {
-                if (!v_ready(i)) break;
-                bool k_known = false;
+                for (int t = 0; t < kTiles; ++t)
+                    if (cnt[t] > 0) scores(t, 0);
+                for (int i = 0; i < steps && ok; ++i) {
+                    if (!v_ready(i)) break;
+                    bool k_known = false;
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (i >= cnt[t]) continue;
-                    if (!wait(&sh.p_full[t], i & 1)) break;
-                    outputs(t, i);
-                    if (i + 1 < cnt[t]) {
-                        if (!k_known && !k_ready(i + 1)) break;
-                        k_known = true;
-                        scores(t, i + 1);
+                    for (int t = 0; t < kTiles; ++t) {
+                        if (i >= cnt[t]) continue;
+                        if (!wait(&sh.p_full[t], i & 1)) break;
+                        outputs(t, i);
+                        if (i + 1 < cnt[t]) {
+                            if (!k_known && !k_ready(i + 1)) break;
+                            k_known = true;
+                            scores(t, i + 1);
+                        }
                     }
                 }
             }
-        }
-        if (!ok) give_up();
-        // Whatever was issued completes before tensor memory is read or freed.
-        if (leader) tc_commit(&sh.done);
-        __syncwarp();
-        if (!mbar_wait_bounded(&sh.done, 0, wait_limit)) outlast_copies();
-        __syncwarp();
-        meet();
-        leave();
-        if (*abort != 0) outlast_copies();
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-        return;
+            if (!ok) give_up();
+            // Whatever was issued completes before tensor memory is read or freed.
+            if (leader) tc_commit(&sh.done);
+            __syncwarp();
+            if (!mbar_wait_bounded(&sh.done, 0, wait_limit)) outlast_copies();
+            __syncwarp();
+            meet();
+            leave();
+            if (*abort != 0) outlast_copies();
+            tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+            return;
         }
         if (warp == L::kCopyWarp) {
-        // ---- copy ----
-        // Lane g + 8 · kind has the tile's tokens 16 g ..: kind 0 codes of K,
-        // 1 and 2 scales of K and V, 3 codes of V.
-        const int kind = lane / 8, g16 = lane % 8, row_bytes = D * kBits / 8, per_page = a.cache.page / 16;
-        int piece = (8 * j0 + g16) / per_page, within = (8 * j0 + g16) % per_page;
-        const uint8_t *from = kind == 0 ? a.cache.k_codes : kind == 1 ? a.cache.k_scales : kind == 2 ? a.cache.v_scales
-                                                                                           : a.cache.v_codes;
-        const int token_bytes = kind == 1 || kind == 2 ? 4 : row_bytes;
-        const uint32_t bytes = 16 * token_bytes;
-        auto next_page = [&](int i) {
-            return i < steps && kManyKeys * (j0 + i) + 16 * g16 < keys ? page_of(a.batch, a.cache, tile.seq, piece, a.status)
-                                                                       : -1;
-        };
-        int page = next_page(0), unit = 0;
-        bool ok = true;
-        auto slot_free = [&](int u) {
-            if (u >= L::kCodeSlots)
-                ok = mbar_wait_prompt(&sh.code_free[u % L::kCodeSlots], (u / L::kCodeSlots - 1) & 1, wait_limit, abort);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            return ok;
-        };
-        const int held = withhold < 0 ? -1 : min(withhold, steps - 1);
-        for (int i = 0; i < steps; ++i) {
-            const uint8_t *at = from + (first_slot(a.cache, page, head) + 16 * within) * token_bytes;
-            const bool mine = page >= 0;
-            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine) & 0xFF;
-            const int groups = __popc(valid);
-            within += 8 % per_page, piece += 8 / per_page;
-            if (within >= per_page) within -= per_page, ++piece;
-            page = next_page(i + 1);
-            for (int v = 0; v < 2; ++v, ++unit) {
-                if (!slot_free(unit)) break;
-                uint64_t *full = &sh.code_full[unit % L::kCodeSlots];
-                if (lane == 0) {
-                    sh.valid[i % L::kMeta] = valid;
-                    if (i != held) mbar_arrive_expect_tx(full, groups * 16 * (row_bytes + (v ? 0 : 8)));
+            // ---- copy ----
+            // Lane g + 8 · kind has the tile's tokens 16 g ..: kind 0 codes of K,
+            // 1 and 2 scales of K and V, 3 codes of V.
+            const int kind = lane / 8, g16 = lane % 8, row_bytes = D * kBits / 8, per_page = a.cache.page / 16;
+            int piece = (8 * j0 + g16) / per_page, within = (8 * j0 + g16) % per_page;
+            const uint8_t *from = kind == 0 ? a.cache.k_codes : kind == 1 ? a.cache.k_scales : kind == 2 ? a.cache.v_scales
+                                                                                               : a.cache.v_codes;
+            const int token_bytes = kind == 1 || kind == 2 ? 4 : row_bytes;
+            const uint32_t bytes = 16 * token_bytes;
+            auto next_page = [&](int i) {
+                return i < steps && kManyKeys * (j0 + i) + 16 * g16 < keys ? page_of(a.batch, a.cache, tile.seq, piece, a.status)
+                                                                           : -1;
+            };
+            int page = next_page(0), unit = 0;
+            bool ok = true;
+            auto slot_free = [&](int u) {
+                if (u >= L::kCodeSlots)
+                    ok = mbar_wait_prompt(&sh.code_free[u % L::kCodeSlots], (u / L::kCodeSlots - 1) & 1, wait_limit, abort);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                return ok;
+            };
+            const int held = withhold < 0 ? -1 : min(withhold, steps - 1);
+            for (int i = 0; i < steps; ++i) {
+                const uint8_t *at = from + (first_slot(a.cache, page, head) + 16 * within) * token_bytes;
+                const bool mine = page >= 0;
+                const uint32_t valid = __ballot_sync(0xFFFFFFFFu, mine) & 0xFF;
+                const int groups = __popc(valid);
+                within += 8 % per_page, piece += 8 / per_page;
+                if (within >= per_page) within -= per_page, ++piece;
+                page = next_page(i + 1);
+                for (int v = 0; v < 2; ++v, ++unit) {
+                    if (!slot_free(unit)) break;
+                    uint64_t *full = &sh.code_full[unit % L::kCodeSlots];
+                    if (lane == 0) {
+                        sh.valid[i % L::kMeta] = valid;
+                        if (i != held) mbar_arrive_expect_tx(full, groups * 16 * (row_bytes + (v ? 0 : 8)));
+                    }
+                    __syncwarp();
+                    if (mine && i != held && (v ? kind == 3 : kind < 3)) {
+                        const uint32_t to = kind == 1 || kind == 2
+                                                ? base + L::off_scales + i % 2 * 1024 + (kind - 1) * 512 + 64 * g16
+                                                : base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 16 * g16 * row_bytes;
+                        bulk_copy(to, at, bytes, full);
+                    }
                 }
-                __syncwarp();
-                if (mine && i != held && (v ? kind == 3 : kind < 3)) {
-                    const uint32_t to = kind == 1 || kind == 2
-                                            ? base + L::off_scales + i % 2 * 1024 + (kind - 1) * 512 + 64 * g16
-                                            : base + L::off_codes + unit % L::kCodeSlots * L::kCodes + 16 * g16 * row_bytes;
-                    bulk_copy(to, at, bytes, full);
-                }
+                if (!ok) break;
             }
-            if (!ok) break;
-        }
-        if (!ok) {
-            give_up();
-            // No copy may still be writing shared memory at exit.
-            outlast_copies();
-        }
-        __syncwarp();
+            if (!ok) {
+                give_up();
+                // No copy may still be writing shared memory at exit.
+                outlast_copies();
+            }
+            __syncwarp();
         }
         meet();
         leave();
