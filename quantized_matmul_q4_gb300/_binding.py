@@ -883,7 +883,9 @@ def mx_cache_write(cache: MxCache, k, v, starts, lengths, pages, rope: Rope | No
 
 def mx_cache_read(cache: MxCache, starts, lengths, pages, tokens: int | None = None, dtype=None, out=None, stream=None):
     """The values (k, v), each [tokens, kv heads, head_dim], of a batch's rows
-    (float32 unless dtype or out = (k, v) says otherwise)."""
+    (float32 unless dtype or out = (k, v) says otherwise).  Rows that are not in
+    the cache, and those behind the last sequence, are left as they were (without
+    `out`: as the allocator gave them)."""
     device = _cuda_device(cache[0], "cache")
     ca = _cache_arg(cache, device)
     ba = _batch_arg(starts, lengths, pages, device)
@@ -915,7 +917,8 @@ def mx_attention(q, cache: MxCache, starts, lengths, pages, scale: float | None 
     """softmax(scale·q·kᵀ)·v of a batch's queries [tokens, heads, head_dim]
     over their sequences' cached tokens (causal: up to their own), heads a
     multiple of the cache's; scale is head_dim^-1/2 unless given.  A row that
-    sees nothing gives zeros; rows behind the last sequence are left as they were."""
+    sees nothing gives zeros; rows behind the last sequence are left as they were
+    (without `out`: as the allocator gave them)."""
     device = _cuda_device(q, "q")
     dtype = _mx_dtype(q.dtype, "q")
     ca = _cache_arg(cache, device)

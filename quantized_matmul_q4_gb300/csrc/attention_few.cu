@@ -4,9 +4,9 @@
 // Every byte of the cache is read once by the tile that needs it, so the
 // kernel is meant to be bound by HBM: 8-bit heads of 128 bring an SM some 23
 // values per clock, of which each costs 3.6 instructions of a lane here.  64 sequences to
-// 4096 tokens, 32 heads of 128: 8 bits 229 us (88% of the measured copy rate),
-// where 4 bits are bound by those instructions; one row over 1000 tokens 7.4 us,
-// launch, lookups and one round; over 131072, 5 key heads, 4 bits 37.9.  A tensor-core
+// 4096 tokens, 32 heads of 128: 8 bits 233 us (87% of the measured copy rate),
+// where 4 bits are bound by those instructions; one row over 1000 tokens 7.6 us,
+// launch, lookups and one round; over 131072, 5 key heads, 4 bits 38.9.  A tensor-core
 // tile of 128 rows would be empty but for 8, so the products are mma.sync's
 // (m16n8k16, fp16 in, fp32 out), with the tokens or head values on M and the
 // rows on N:
@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
 // row 2t or 2t + 1 at a time, in the g-th of eight runs of the row: rows and
 // runs all begin in the same banks, so pairs within a run are permuted by
 // t and g, and 16 lanes meet in no bank (stored as they come they all did: one
-// row over 1000 tokens 7.7 us, now 7.4; 64 sequences to 4096 234, now 229).
+// row over 1000 tokens 7.7 us, so 7.4; 64 sequences to 4096 234, so 229).
 template <int kDP>
 __device__ __forceinline__ int sum_swizzle(int r, int g) {
     return kDP == 128 ? (r >> 1 & 3) | (g >> 1 & 1) << 2 : r >> 1 & 3;

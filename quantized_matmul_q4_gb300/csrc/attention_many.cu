@@ -13,8 +13,8 @@
 // 16 warps does once a tile.  They take 4400 cycles.  So two tiles of 128
 // rows share every dequantised key and value, and while the softmax of one is
 // computed the pipe works on the other.  A prompt of 8192 tokens, 32 heads of
-// 128, 8 bits: 527 us, 1044 TFLOP/s (55% of the measured bf16 rate); 512 tokens over 8192,
-// 8 key heads: 79 us, 846 TFLOP/s.  (Halves of a row that go by a maximum of their
+// 128, 8 bits: 536 us, 1025 TFLOP/s (54% of the measured bf16 rate); 512 tokens over 8192,
+// 8 key heads: 80 us, 828 TFLOP/s.  (Halves of a row that go by a maximum of their
 // own, so that each waits for 64 keys' products alone: 695 us; one warp a quarter
 // with whole rows has no exchange, but too few warps.)
 //

@@ -13,10 +13,10 @@
 // all heads: their angles are computed once, and in the cache the tokens of a
 // head lie next to each other.
 //
-// Rope of 8192 x 32 x 128 bf16: 22.5 us (88% of the measured copy rate); 28000 tokens
-// of 8 heads read from 8 bits to bf16: 24.1 (79%); 8271 tokens of 32 heads rotated
-// and written from fp16 to 8 bits: 45.7 (66%), 60% of the issue slots and the loads' latency
-// (each lane holds 32 to 64 bytes of loads, 32 warps an SM).
+// Rope of 8192 x 32 x 128 bf16: 22.5 us in a chain of calls (88% of the measured copy rate),
+// 25.7 a call (77%); 20748 tokens of 8 heads read from 8 bits to bf16: 24.1 (78%); 8272
+// tokens of 32 heads rotated and written from fp16 to 8 bits: 46.4 (65%), 64% of the issue
+// slots and the loads' latency (each lane holds 32 to 64 bytes of loads, 32 warps an SM).
 //
 // Angles.  p·f in radians needs some 20 bits before the point for far
 // positions and 24 behind it.  So f / 2π, in turns, is taken as a 64-bit
@@ -383,10 +383,11 @@ __device__ __noinline__ float turned_again(const T *head, int d, const RopeView 
 // Turned values that lie within 4 units of a border between two codes, where
 // the fp32 arithmetic may fall on its other side, are taken again: nine in
 // 2^20 (8 bits) or 2^22.  (Without this 26 to 40 codes of 68 million differed from
-// those of the exact values, with it 8 to 19; 8271 tokens written take 45.7 us, 43.2 without.)  Below the codes' normal numbers the borders lie
-// elsewhere and are left as they are.
-// So are those within 4 units of a power of two where that is the block's largest value: there the
-// block's scale has its border, and all of its codes with it.  Returns the float bits of that value.
+// those of the exact values, with it 9 to 19; 8272 tokens written take 46.4 us, 43.2 without.)
+// Below the codes' normal numbers the borders lie elsewhere and are left as they are.
+// So are those within 4 units of a power of two where that is the block's largest value: there
+// the block's scale has its border, and all of its codes with it.  Returns the float bits of
+// the block's largest value.
 template <int kBits, class T>
 __device__ __forceinline__ uint32_t settle(float (&f)[8], const T *head, int d, const RopeView &r, long long position, bool ok) {
     constexpr uint32_t kMask = kBits == 8 ? 0xFFFFF : 0x3FFFFF, kBorder = kMask / 2 + 1;
@@ -560,7 +561,7 @@ bool heads_aligned(const void *p, long long token, long long head, size_t size) 
 // written 27.9 us, 35.2 with 8, read 12.0 and 16.7) and
 // CTAs that share them (up to two an SM, each with work for its warps).  2048
 // tokens written, 32 heads of 128: 18.7 us with 1 token a CTA, 13.5 with 2, 12.9 with 4, 16.6
-// with 8 (256 CTAs); 8271 (without settle): 67.4, 44.5, 43.1, 43.6; 28000 read, 8 heads:
+// with 8 (256 CTAs); 8272 (without settle): 67.4, 44.5, 43.1, 43.6; 20748 read, 8 heads:
 // 78, 52, 33, 24.7; rope of 1000 tokens: 4.6, 3.8, 4.8, 6.9.
 struct Shape {
     int lanes_log, tokens_log;
