@@ -18,9 +18,10 @@
 //
 // M is kept while no u passes it by more than 8, so O is rarely rescaled.
 // A key whose v is far smaller than another's has a p that may be zero where its term
-// of l is not.  So vref is kept within [kVrefMin, kVrefMax], 80 apart, which is what
-// values from 2^-39 to 2^42 need (4 bits: 2^-45 to 2^36; tokens of zeros have kVrefMin).
-// Rows that met others are taken once more, by plain_row.
+// of l is not.  So vref is kept within [kVrefLow, kVrefMax], 80 apart, which is what
+// values from 2^-39 to 2^42 need (4 bits: 2^-45 to 2^36).  Rows that met others are taken
+// once more, by plain_row.  Groups of zeros have kVrefMin, so that they raise M only where they are
+// 2^60 and more times as probable as the rest.
 // Probabilities enter the second product in fp16: one rounding to 2^-11 where y is 16 bits
 // wide, two terms where it is fp32 (2^-22, of those above 2^-9 of the largest; the second
 // term of smaller ones is below fp16's normal numbers).  A second term for 16-bit y as well would be
@@ -41,8 +42,9 @@ namespace q4mm {
 constexpr float kLog2e = 1.44269504f;
 constexpr float kPShift = 6.f;      // log2 of p at u = M
 constexpr float kPSlack = 8.f;      // u may pass M by this
-constexpr int kVrefMin = -54;       // lowest power taken out of v
+constexpr int kVrefLow = -54;       // lowest power taken out of v
 constexpr int kVrefMax = 26;        // highest
+constexpr int kVrefMin = -80;       // that of zeros
 constexpr int kWide = 4;            // a group's tokens share a power while their largest scales are within 2^this
 constexpr int kNever = 0x7FFFFFFF;  // position of a NaN that there is not
 
@@ -119,7 +121,7 @@ struct ScaleWord {
 
 // Whether values whose largest scale byte is `top` need another power.
 __device__ __forceinline__ bool vref_passes(int top) {
-    return top != 0 && (unsigned)(top - 134 - kVrefMin) > (unsigned)(kVrefMax - kVrefMin);
+    return top != 0 && (unsigned)(top - 134 - kVrefLow) > (unsigned)(kVrefMax - kVrefLow);
 }
 
 // A tile of `R` rows of one sequence and kv head.  Row r is token r / group of

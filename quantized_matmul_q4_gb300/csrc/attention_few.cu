@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
         uint32_t top = max(pair & 0xFFFFu, pair >> 16);
         const bool is_v = lane >= 16;
         uint32_t any_nan = 0;  // a bit a block
-        if (__any_sync(0xFFFFFFFFu, top - (134 + kVrefMin) > (uint32_t)(kVrefMax - kVrefMin))) {
+        if (__any_sync(0xFFFFFFFFu, top - (134 + kVrefLow) > (uint32_t)(kVrefMax - kVrefLow))) {
             // A scale that is NaN, or one that v's powers do not reach (or that is k's).
             // NaN in v reaches the rows that see it, and no others.
             top = 0;

@@ -201,3 +201,25 @@ def test_far_values_in_every_shape(news, lengths, group, D, page, bits, causal, 
     q.device_status()
     assert bool((out[:2] == 7).all()) and bool((out[c.T:] == 7).all())
     base._check(c, x, out, x.double().cpu().numpy(), dtype, causal=causal, scale=scale)
+
+
+@KERNELS
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("gap", [20, 50, 65, 80])
+def test_tokens_of_zeros_that_outweigh_all_others(gap, dtype):
+    """Keys without values, 2^gap times as probable as the others: they shrink the output, and leave it its precision."""
+    q = _q()
+    for n, m in ((1, 700), (140, 600)):
+        c = Case(18, [n], [m], 1, 64, 16, 8).fill()
+        for p in range(m):
+            pg, at = c.table[0, p // 16], p % 16
+            codes, byte = ref.head_codes(np.concatenate([[16 if p // 32 % 4 == 0 else 0], np.zeros(63)]), 8)
+            c.cache["k_codes"][pg, 0, at], c.cache["k_scales"][pg, 0, at] = codes, byte
+            if p // 32 % 4 == 0:
+                c.cache["v_codes"][pg, 0, at], c.cache["v_scales"][pg, 0, at] = 0, 0
+        x = np.zeros((n, 2, 64))
+        x[..., 0] = gap * np.log(2) / 16
+        x, xv = base._dev(x, dtype)
+        y = q.mx_attention(x, c.device_cache(), *c.device_batch(), scale=1.0)
+        q.device_status()
+        base._check(c, x, y, xv, dtype, scale=1.0)
