@@ -128,12 +128,14 @@ struct Joined {
         l += mi == -INFINITY ? li : by * li;
         o.x = fmaf(by, v.x, o.x), o.y = fmaf(by, v.y, o.y), o.z = fmaf(by, v.z, o.z), o.w = fmaf(by, v.w, o.w);
     }
-    // Four outputs from value d on; a row that sees nothing has no sum: zeros.
+    // Four outputs from value d on.  A row that sees nothing has no sum: zeros.  One that does, and has none, has scores
+    // of minus infinity alone, whose softmax is NaN.
     __device__ __forceinline__ void store(const MxAttentionArgs &a, const RowTile &tile, int row, int head, int group,
-                                          int d, bool nan) const {
+                                          int d, int nan_from) const {
         const long long at = (long long)(tile.start + row / group) * a.y_token +
                              (long long)(head * group + row % group) * a.y_head + d;
-        const float by = nan ? __int_as_float(0x7FC00000) : l == 0.f ? 0.f : 1.f / l;
+        const int sees = keys_of(tile, row, group, a.causal);
+        const float by = nan_from < sees || (l == 0.f && sees > 0) ? __int_as_float(0x7FC00000) : l == 0.f ? 0.f : 1.f / l;
         store4(a.y, a.type, at, a.vec, make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
     }
 };
@@ -188,7 +190,8 @@ __device__ __noinline__ void few_plain(const MxAttentionArgs &a, int group, unsi
             float top = -INFINITY, l = 0.f;
             for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, sh.m[w]);
             for (int w = 0; w < kFewWarps; ++w) l += ex2(sh.m[w] - (top == -INFINITY ? 0.f : top));
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float none = l == 0.f && keys_of(tile, row, group, a.causal) > 0 ? __int_as_float(0x7FC00000) : 0.f;
+            float4 y = make_float4(none, none, none, none);
             for (int w = 0; w < kFewWarps; ++w) {
                 if (sh.m[w] == -INFINITY) continue;
                 const float4 v = *reinterpret_cast<const float4 *>(&sh.o[w][d]);
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, kNR == 1 && kNP == 1 ? 2 : 1)
             if (r == 0 && d % kMxBlock == 0) ws[kR * (kDP + 2) + d / kMxBlock] = __int_as_float(nan_from);
         } else {
             const int row = tile.first + r;
-            sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
+            sum.store(a, tile, row, head, group, d, nan_from);
             spoilt |= sum.l == kSpoilt;
         }
     }
@@ -721,7 +724,7 @@ __global__ void __launch_bounds__(kJoinThreads) mx_attention_join_kernel(const _
             sum.add(w[kR * kDP + r], m, w[kR * (kDP + 1) + r], *reinterpret_cast<const float4 *>(w + r * kDP + d));
         }
         const int row = tile.first + r;
-        sum.store(a, tile, row, head, group, d, nan_from < keys_of(tile, row, group, a.causal));
+        sum.store(a, tile, row, head, group, d, nan_from);
         spoilt |= sum.l == kSpoilt;
     }
     if (__syncthreads_or(spoilt)) few_plain<kBits, kR, kR>(a, group, blockIdx.x, 0, 1, scratch);

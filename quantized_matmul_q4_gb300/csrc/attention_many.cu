@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(ManyLayout<kBits, kDP, kTiles, kNP>::kThreads,
                     o.by[s] = m[s] == -INFINITY ? 0.f : ex2(m[s] - top);
                     ls += m[s] == -INFINITY ? l[s] : o.by[s] * l[s];
                 }
-                // A row that sees nothing has no sum: zeros.
-                o.scale = ls == 0.f ? 0.f : 1.f / ls;
+                // A row that sees nothing has no sum: zeros.  (One that does: scores of minus infinity alone, whose softmax is NaN.)
+                o.scale = ls != 0.f ? 1.f / ls : sees > 0 ? __int_as_float(0x7FC00000) : 0.f;
                 o.at = (long long)(tile.start + tok) * a.y_token + (long long)(head * group + row - tok * group) * a.y_head;
                 out[threadIdx.x] = o;
             }

@@ -223,3 +223,28 @@ def test_tokens_of_zeros_that_outweigh_all_others(gap, dtype):
         y = q.mx_attention(x, c.device_cache(), *c.device_batch(), scale=1.0)
         q.device_status()
         base._check(c, x, y, xv, dtype, scale=1.0)
+
+
+@KERNELS
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("far", [False, True])
+@pytest.mark.parametrize("n,m", [(1, 50), (5, 700), (150, 300)])
+def test_rows_whose_scores_are_all_minus_infinity(n, m, far, dtype):
+    """The softmax of such scores is NaN; those of rows that see no keys stay zeros, other rows as they are."""
+    q, torch = _q(), _torch()
+    c = Case(19, [n, 2], [m, 0], 1, 64, 16, 8).fill()
+    c.cache["k_codes"] &= 0x7F          # k is positive,
+    c.cache["k_codes"][..., 0] |= 0x38  # and not zero where the infinity is
+    c.cache["k_codes"] = np.where(c.cache["k_codes"] == 0x7F, 0x78, c.cache["k_codes"]).astype(np.uint8)
+    c.cache["k_scales"] = np.where(c.cache["k_scales"] > 140, 120, c.cache["k_scales"]).astype(np.uint8)
+    if far:
+        c.cache["v_scales"][c.table[0, 0], 0, 3] = 70
+    x, xv = base._dev(c.rng.normal(size=(c.T, 2, 64)), dtype)
+    x[0, 1, 0] = xv[0, 1, 0] = -np.inf
+    y = q.mx_attention(x, c.device_cache(), *c.device_batch())
+    assert bool(torch.isnan(y[0, 1]).all()) and int(torch.isnan(y).sum()) == 64 and bool((y[n:] == 0).all())
+    xv[0, 1, 0] = 0
+    x, xv = base._dev(xv, dtype)
+    other = q.mx_attention(x, c.device_cache(), *c.device_batch())
+    keep = ~torch.isnan(y)
+    assert bool((y[keep] == other[keep]).all())
